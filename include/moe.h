@@ -75,8 +75,9 @@ extern "C" {
 #define MOE_FLAG_BAD_EXPERT 1 /* expert id outside [0, E) */
 #define MOE_FLAG_NONFINITE 2  /* NaN or Inf router logit   */
 #define MOE_FLAG_TIMEOUT 4    /* a kernel wait gave up     */
+#define MOE_FLAG_BAD_INDEX 8  /* sequence bounds or cache slot out of range */
 
-/* wgrad output types */
+/* element types (weight gradients, optimizer tensors) */
 #define MOE_DTYPE_F32 0
 #define MOE_DTYPE_BF16 1
 
@@ -87,6 +88,10 @@ extern "C" {
 #define MOE_OP_SHARED_SWIGLU_BWD 4
 #define MOE_OP_ROUTE_TOPK_BWD 5
 #define MOE_OP_ROUTER_AUX 6
+#define MOE_OP_LINATTN_FWD 7
+#define MOE_OP_LINATTN_BWD 8
+#define MOE_OP_ADAMW_PLAN 9
+#define MOE_OP_ADAMW_STEP 10
 
 int moe_version(void);
 const char* moe_status_string(int status);
@@ -387,6 +392,113 @@ int moe_route_topk_bwd(const float* d_row_w, const int32_t* slot_of, const int32
                        const float* aux_bias, const float* aux_p_mean, float aux_scale,
                        const uint16_t* dz, const uint16_t* W_dn, int l, void* ws,
                        size_t ws_bytes, int32_t* err_flag, void* stream);
+
+/* ---------------------------------------------------------------- sequence mixer */
+
+/* Linear attention with a decay for each state head. Hs state heads, each shared
+ * by r query heads (query head h*r + a reads state head h), so Hq = Hs * r. With
+ * lam = exp(log_decay[h]), for the tokens of one sequence in order:
+ *   S_t     = lam S_{t-1} + k_t v_t^T              (Dk x Dv, fp32)
+ *   o_t^(a) = scale * S_t^T q_t^(a)
+ * log_decay is a constant of the head (fp32 [Hs], <= 0; 0 keeps everything, -inf
+ * keeps nothing): it gets no gradient. A NaN or positive entry sets
+ * MOE_FLAG_NONFINITE and counts as 0.
+ * Tensors: q [T][Hq][Dk], k [T][Hs][Dk], v [T][Hs][Dv], o [T][Hq][Dv], bf16; the heads
+ * of one token are contiguous and ld* elements lie between tokens (ld* >= heads *
+ * width), so q, k and v may be slices of one fused projection's rows. Dk and Dv are
+ * multiples of 8 up to 128; ld* are multiples of 8. States are fp32 [N][Hs][Dk][Dv].
+ * Sequences: N of them packed on the token axis; sequence n is the tokens
+ * cu_seqlens[n] .. cu_seqlens[n+1]-1 (int32 [N+1], device) and may be empty.
+ * max_seqlen is an upper bound of their lengths, known on the host. A sequence
+ * that is out of order, past T or longer than max_seqlen sets MOE_FLAG_BAD_INDEX and is
+ * skipped: nothing of it is written. cu_seqlens == NULL means N sequences of T / N
+ * tokens (T divisible by N).
+ * state_in (nullable: zeros) is each sequence's state before its first token,
+ * state_out (nullable) its state after the last; an empty sequence copies one to
+ * the other. state_out may be state_in. Sums and states are fp32 throughout.
+ * Workspace: moe_workspace_size(MOE_OP_LINATTN_FWD, max_seqlen, Dk, Dv, Hs, r, 0, N). */
+int moe_linattn_fwd(const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                    const float* log_decay, const int32_t* cu_seqlens, const float* state_in,
+                    int N, int T, int max_seqlen, int Hs, int r, int Dk, int Dv, int ldq, int ldk,
+                    int ldv, int ldo, float scale, uint16_t* o, float* state_out, void* ws,
+                    size_t ws_bytes, int32_t* err_flag, void* stream);
+
+/* Backward of moe_linattn_fwd for dout = d loss / d o and d_state_out = d loss / d
+ * state_out (nullable: zeros), from the forward's inputs alone. With X the
+ * gradient that reaches a state from the later tokens (X = d_state_out after the
+ * last token):
+ *   R_t = X + scale * sum_a q_t^(a) (dout_t^(a))^T
+ *   dq_t^(a) = scale * S_t dout_t^(a);  dk_t = R_t v_t;  dv_t = R_t^T k_t;  then X = lam R_t
+ * dk and dv are the sums over the r query heads. d_state_in (nullable) is X before the
+ * first token; it must not be d_state_out. dq, dk, dv are bf16 with lddq, lddk, lddv elements between
+ * tokens. Workspace: moe_workspace_size(MOE_OP_LINATTN_BWD, max_seqlen, Dk, Dv, Hs, r, 0, N). */
+int moe_linattn_bwd(const uint16_t* dout, const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                    const float* log_decay, const int32_t* cu_seqlens, const float* state_in,
+                    const float* d_state_out, int N, int T, int max_seqlen, int Hs, int r, int Dk,
+                    int Dv, int lddo, int ldq, int ldk, int ldv, float scale, uint16_t* dq,
+                    uint16_t* dk, uint16_t* dv, int lddq, int lddk, int lddv, float* d_state_in,
+                    void* ws, size_t ws_bytes, int32_t* err_flag, void* stream);
+
+/* One token for each of B rows: the recurrent form, for decoding. Row b updates
+ * the state cache [n_slots][Hs][Dk][Dv] (fp32) in place at slot state_idx[b]
+ * (int32 [B]; NULL: slot b) and writes o[b]. A negative slot is an empty row: its o is
+ * zero and no state changes. A slot >= n_slots sets MOE_FLAG_BAD_INDEX and counts
+ * as empty. The slots of one call must differ from one another. */
+int moe_linattn_step(const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                     const float* log_decay, float* state, const int32_t* state_idx, int n_slots,
+                     int B, int Hs, int r, int Dk, int Dv, int ldq, int ldk, int ldv, int ldo,
+                     float scale, uint16_t* o, int32_t* err_flag, void* stream);
+
+/* ---------------------------------------------------------------- optimizer */
+
+/* One tensor of an AdamW step. p, g, m, v hold n values each (device). p and g are
+ * fp32 or bf16 (MOE_DTYPE_*). With master (fp32 [n], nullable, p in bf16) the update
+ * runs on master and p is its rounded copy; without it a bf16 p is rounded
+ * stochastically. States in 32 bits: m and v fp32. In 8 bits: blocks of 256
+ * consecutive values (the last one shorter); m holds E4M3 bytes of m / m_scale[block], v E4M3
+ * bytes of sqrt(v) / v_scale[block], scales fp32 [ceil(n / 256)] = the block's largest
+ * magnitude / 448, rounded stochastically. Zeroed states are a fresh start. */
+typedef struct {
+  void* p;
+  const void* g;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  float* master;
+  long long n;
+  float weight_decay;
+  int p_dtype;
+  int g_dtype;
+} moe_adamw_tensor;
+
+#define MOE_ADAMW_CTL_BYTES 64
+
+/* Checks n_tensors tensors (host array, device pointers in it) and writes the
+ * step's plan to `plan` (host memory, plan_bytes >= moe_workspace_size(MOE_OP_ADAMW_PLAN,
+ * n_tensors, 0, ...)), which the caller copies to the device once; *chunks is the
+ * amount of work that moe_adamw_step takes. Arrays aligned to 32 bytes (fp32), 16
+ * (bf16) and 8 (codes) take whole vector accesses, others are walked by value. n may be 0. */
+int moe_adamw_plan(const moe_adamw_tensor* tensors, int n_tensors, int state_bits, void* plan,
+                   size_t plan_bytes, long long* chunks);
+
+/* One AdamW step over every tensor of `plan` (device copy), t = steps taken + 1,
+ * beta = 1 - rate (the rates are passed because 1 - beta in fp32 would lose digits):
+ *   c = min(1, max_norm / (|g| + 1e-6)) over all tensors (1 when max_norm <= 0)
+ *   m = beta1 m + (1 - beta1) c g;  v = beta2 v + (1 - beta2) (c g)^2
+ *   p = p (1 - lr weight_decay) - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
+ * ctl (device, MOE_ADAMW_CTL_BYTES, zeroed before the first step) holds the number
+ * of steps taken (int64 at byte 0), the last gradient norm (fp32 at byte 8) and the
+ * clip factor (byte 12), so a captured step counts by itself; lr_dev (device fp32,
+ * nullable) takes the place of lr. With max_norm > 0 a gradient norm that is not
+ * finite leaves every tensor and the count as they are and sets MOE_FLAG_NONFINITE;
+ * with max_norm <= 0 no norm is computed and such values pass into the tensors. Stochastic
+ * rounding depends on (seed, t, tensor, index) alone; results do not depend on
+ * timing. Workspace: moe_workspace_size(MOE_OP_ADAMW_STEP, 0, ...). */
+int moe_adamw_step(const void* plan, int n_tensors, long long chunks, int state_bits, float lr,
+                   const float* lr_dev, float rate1, float rate2, float eps, float max_norm,
+                   int seed, void* ctl, void* ws, size_t ws_bytes, int32_t* err_flag,
+                   void* stream);
 
 /* ---------------------------------------------------------------- diagnostics */
 

@@ -23,6 +23,7 @@ MOE_ERR_CUDA = -5
 MOE_FLAG_BAD_EXPERT = 1
 MOE_FLAG_NONFINITE = 2
 MOE_FLAG_TIMEOUT = 4
+MOE_FLAG_BAD_INDEX = 8
 MOE_DTYPE_F32 = 0
 MOE_DTYPE_BF16 = 1
 MOE_OP_ROUTE_TOPK = 1
@@ -31,11 +32,17 @@ MOE_OP_GROUPED_SWIGLU_BWD = 3
 MOE_OP_SHARED_SWIGLU_BWD = 4
 MOE_OP_ROUTE_TOPK_BWD = 5
 MOE_OP_ROUTER_AUX = 6
+MOE_OP_LINATTN_FWD = 7
+MOE_OP_LINATTN_BWD = 8
+MOE_OP_ADAMW_PLAN = 9
+MOE_OP_ADAMW_STEP = 10
+MOE_ADAMW_CTL_BYTES = 64
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _Z = ctypes.c_size_t
 _F = ctypes.c_float
+_L = ctypes.c_longlong
 
 # name -> argument types (pointer args are _P; the last one is always the stream)
 SIGNATURES = {
@@ -76,6 +83,12 @@ SIGNATURES = {
     "moe_expert_buckets": ([_P, _I, _P, _P, _P], _I),
     "moe_grouped_swiglu_ordered": ([_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P],
                                    _I),
+    "moe_linattn_fwd": ([_P] * 6 + [_I] * 11 + [_F, _P, _P, _P, _Z, _P, _P], _I),
+    "moe_linattn_bwd": ([_P] * 8 + [_I] * 11 + [_F] + [_P] * 3 + [_I] * 3 + [_P, _P, _Z, _P, _P],
+                        _I),
+    "moe_linattn_step": ([_P] * 6 + [_I] * 10 + [_F, _P, _P, _P], _I),
+    "moe_adamw_plan": ([_P, _I, _I, _P, _Z, _P], _I),
+    "moe_adamw_step": ([_P, _I, _L, _I, _F, _P, _F, _F, _F, _F, _I, _P, _P, _Z, _P, _P], _I),
     "moe_diag_wait_timeout": ([ctypes.c_longlong, _P, _P, _P], _I),
     "moe_timing_enable": ([_I], _I),
     "moe_timing_report": ([ctypes.c_char_p, _Z], _I),
@@ -84,6 +97,12 @@ SIGNATURES = {
 
 class MoEError(RuntimeError):
     pass
+
+
+class AdamWTensor(ctypes.Structure):
+    """moe_adamw_tensor of the header."""
+    _fields_ = [("p", _P), ("g", _P), ("m", _P), ("v", _P), ("m_scale", _P), ("v_scale", _P),
+                ("master", _P), ("n", _L), ("weight_decay", _F), ("p_dtype", _I), ("g_dtype", _I)]
 
 
 _lib = None
@@ -281,6 +300,39 @@ def moe_route_topk_bwd(d_row_w, slot_of, topk_idx, topk_w, topk_s, x, Wr, T, d, 
 
 def moe_router_aux_loss(logits, bias, T, E, p_mean, loss, ws, ws_bytes, stream=None):
     _call("moe_router_aux_loss", logits, bias, T, E, p_mean, loss, ws, ws_bytes, stream)
+
+
+def moe_linattn_fwd(q, k, v, log_decay, cu_seqlens, state_in, N, T, max_seqlen, Hs, r, Dk, Dv, ldq,
+                    ldk, ldv, ldo, scale, o, state_out, ws, ws_bytes, err_flag=None, stream=None):
+    _call("moe_linattn_fwd", q, k, v, log_decay, cu_seqlens, state_in, N, T, max_seqlen, Hs, r, Dk,
+          Dv, ldq, ldk, ldv, ldo, scale, o, state_out, ws, ws_bytes, err_flag, stream)
+
+
+def moe_linattn_bwd(dout, q, k, v, log_decay, cu_seqlens, state_in, d_state_out, N, T, max_seqlen,
+                    Hs, r, Dk, Dv, lddo, ldq, ldk, ldv, scale, dq, dk, dv, lddq, lddk, lddv,
+                    d_state_in, ws, ws_bytes, err_flag=None, stream=None):
+    _call("moe_linattn_bwd", dout, q, k, v, log_decay, cu_seqlens, state_in, d_state_out, N, T,
+          max_seqlen, Hs, r, Dk, Dv, lddo, ldq, ldk, ldv, scale, dq, dk, dv, lddq, lddk, lddv,
+          d_state_in, ws, ws_bytes, err_flag, stream)
+
+
+def moe_linattn_step(q, k, v, log_decay, state, state_idx, n_slots, B, Hs, r, Dk, Dv, ldq, ldk, ldv,
+                     ldo, scale, o, err_flag=None, stream=None):
+    _call("moe_linattn_step", q, k, v, log_decay, state, state_idx, n_slots, B, Hs, r, Dk, Dv, ldq,
+          ldk, ldv, ldo, scale, o, err_flag, stream)
+
+
+def moe_adamw_plan(tensors, n_tensors, state_bits, plan, plan_bytes, chunks):
+    """Host call: `tensors` an array of AdamWTensor, `plan` a host buffer's address,
+    `chunks` a ctypes.c_longlong."""
+    _check(load().moe_adamw_plan(tensors, n_tensors, state_bits, plan, plan_bytes,
+                                 ctypes.byref(chunks)), "moe_adamw_plan")
+
+
+def moe_adamw_step(plan, n_tensors, chunks, state_bits, lr, lr_dev, rate1, rate2, eps, max_norm, seed,
+                   ctl, ws, ws_bytes, err_flag=None, stream=None):
+    _call("moe_adamw_step", plan, n_tensors, chunks, state_bits, lr, lr_dev, rate1, rate2, eps,
+          max_norm, seed, ctl, ws, ws_bytes, err_flag, stream)
 
 
 def moe_diag_wait_timeout(limit_ns, err_flag, waited_ns, stream=None):

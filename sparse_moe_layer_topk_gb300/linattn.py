@@ -1,0 +1,126 @@
+"""Linear attention with a decay for each state head, the sequence mixer of a
+block, as libmoe calls: chunked forward over packed prompts, its backward, and
+the one-token step of decoding.
+
+    S_t = exp(log_decay[h]) S_{t-1} + k_t v_t^T;   o_t = scale S_t^T q_t
+
+Hs state heads, each read by r query heads. PyTorch only provides the device
+buffers and the stream. One instance holds the outputs, workspaces and gradients
+for a fixed number of packed tokens T, so a call allocates nothing.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import _lib as M
+
+BF16 = torch.bfloat16
+
+
+class LinearAttention:
+    def __init__(self, log_decay, T: int, Dk: int, Dv: int, r: int = 1, N: int = 1,
+                 max_seqlen: int | None = None, scale: float | None = None, backward: bool = True):
+        """log_decay: fp32 [Hs] on the device, <= 0. T packed tokens of N sequences, none
+        longer than max_seqlen (default: T / N where the sequences are of one length, else T
+        has to be given). scale: Dk ** -0.5 if not given."""
+        if log_decay.dtype != torch.float32 or log_decay.dim() != 1:
+            raise ValueError("log_decay is an fp32 vector with one entry for each state head")
+        self.log_decay = log_decay.contiguous()
+        self.Hs, self.r, self.Dk, self.Dv, self.T, self.N = log_decay.numel(), r, Dk, Dv, T, N
+        self.max_seqlen = (T // N if N else 0) if max_seqlen is None else max_seqlen
+        self.scale = Dk ** -0.5 if scale is None else scale
+        dev = log_decay.device
+        e = lambda *shape, dt=BF16: torch.empty(shape, dtype=dt, device=dev)  # noqa: E731
+        Hq = self.Hs * r
+        self.o = e(T, Hq, Dv)
+        self.err = torch.zeros(1, dtype=torch.int32, device=dev)
+        self._state_out = None
+        if backward:
+            self.dq, self.dk, self.dv = e(T, Hq, Dk), e(T, self.Hs, Dk), e(T, self.Hs, Dv)
+        self._d_state_in = None
+        dims = dict(T=self.max_seqlen, d=Dk, l=Dv, E=self.Hs, k=r, S=N)
+        self.ws_bytes = max(M.moe_workspace_size(M.MOE_OP_LINATTN_FWD, **dims),
+                            M.moe_workspace_size(M.MOE_OP_LINATTN_BWD, **dims) if backward else 0)
+        self.ws = torch.empty(max(self.ws_bytes, 256), dtype=torch.uint8, device=dev)
+        self.saved = None
+
+    # buffers that only some callers want are made when first asked for
+    @property
+    def state_out(self):
+        if self._state_out is None:
+            self._state_out = torch.empty(self.N, self.Hs, self.Dk, self.Dv, device=self.o.device)
+        return self._state_out
+
+    @property
+    def d_state_in(self):
+        if self._d_state_in is None:
+            self._d_state_in = torch.empty(self.N, self.Hs, self.Dk, self.Dv, device=self.o.device)
+        return self._d_state_in
+
+    def _rows(self, name, x, heads, width):
+        """Checks a [T][heads][width] bf16 operand; returns the elements between tokens."""
+        if tuple(x.shape) != (self.T, heads, width) or x.dtype != BF16:
+            raise ValueError(f"{name} is bf16 [{self.T}, {heads}, {width}], got {x.dtype} "
+                             f"{list(x.shape)}")
+        if x.numel() and (x.stride(2) != 1 or (heads > 1 and x.stride(1) != width)):
+            raise ValueError(f"{name}: the heads of a token have to be contiguous")
+        return x.stride(0) if self.T > 1 else max(x.stride(0), heads * width)
+
+    def _state(self, name, x):
+        want = (self.N, self.Hs, self.Dk, self.Dv)
+        if x is not None and (tuple(x.shape) != want or x.dtype != torch.float32
+                              or not x.is_contiguous()):
+            raise ValueError(f"{name} is fp32 {list(want)}, contiguous")
+        return x
+
+    def forward(self, q, k, v, cu_seqlens=None, state_in=None, want_state: bool = False,
+                stream=None):
+        """o [T, Hs * r, Dv] (bf16, this instance's buffer) for q [T, Hs * r, Dk],
+        k [T, Hs, Dk], v [T, Hs, Dv]: slices of one projection's rows will do. With
+        want_state, state_out holds each sequence's state after its last token."""
+        Hq = self.Hs * self.r
+        ld = [self._rows(n, x, h, w) for n, x, h, w in (("q", q, Hq, self.Dk), ("k", k, self.Hs, self.Dk),
+                                                        ("v", v, self.Hs, self.Dv))]
+        self._state("state_in", state_in)
+        self.saved = (q, k, v, cu_seqlens, state_in)
+        M.moe_linattn_fwd(q, k, v, self.log_decay, cu_seqlens, state_in, self.N, self.T,
+                          self.max_seqlen, self.Hs, self.r, self.Dk, self.Dv, *ld, Hq * self.Dv,
+                          self.scale, self.o, self.state_out if want_state else None, self.ws,
+                          self.ws_bytes, self.err, stream)
+        return self.o
+
+    def backward(self, dout, d_state_out=None, stream=None):
+        """(dq, dk, dv) of the last forward call for dout = d loss / d o and d_state_out = d
+        loss / d state_out; where the forward was given a state or d_state_out is given,
+        d_state_in holds d loss / d state_in."""
+        if self.saved is None:
+            raise ValueError("backward needs a forward before it")
+        q, k, v, cu_seqlens, state_in = self.saved
+        Hs, Hq, Dk, Dv = self.Hs, self.Hs * self.r, self.Dk, self.Dv
+        ld = [self._rows(n, x, h, w) for n, x, h, w in (("dout", dout, Hq, Dv), ("q", q, Hq, Dk),
+                                                        ("k", k, Hs, Dk), ("v", v, Hs, Dv))]
+        self._state("d_state_out", d_state_out)
+        want = state_in is not None or d_state_out is not None
+        M.moe_linattn_bwd(dout, q, k, v, self.log_decay, cu_seqlens, state_in, d_state_out, self.N,
+                          self.T, self.max_seqlen, Hs, self.r, Dk, Dv, *ld, self.scale, self.dq,
+                          self.dk, self.dv, Hq * Dk, Hs * Dk, Hs * Dv,
+                          self.d_state_in if want else None, self.ws, self.ws_bytes, self.err,
+                          stream)
+        return self.dq, self.dk, self.dv
+
+    def step(self, q, k, v, state, state_idx=None, stream=None):
+        """One token for each of T rows: updates the state cache [slots, Hs, Dk, Dv] (fp32) in
+        place at slot state_idx[row] (int32, negative for an empty row; default: the row) and
+        returns o."""
+        Hq = self.Hs * self.r
+        ld = [self._rows(n, x, h, w) for n, x, h, w in (("q", q, Hq, self.Dk), ("k", k, self.Hs, self.Dk),
+                                                        ("v", v, self.Hs, self.Dv))]
+        if (state.dim() != 4 or tuple(state.shape[1:]) != (self.Hs, self.Dk, self.Dv)
+                or state.dtype != torch.float32 or not state.is_contiguous()):
+            raise ValueError(f"state is fp32 [slots, {self.Hs}, {self.Dk}, {self.Dv}], contiguous")
+        if state_idx is not None and (state_idx.dtype != torch.int32 or tuple(state_idx.shape) != (self.T,)):
+            raise ValueError(f"state_idx is int32 [{self.T}]")
+        M.moe_linattn_step(q, k, v, self.log_decay, state, state_idx, state.shape[0], self.T, self.Hs,
+                           self.r, self.Dk, self.Dv, *ld, Hq * self.Dv, self.scale, self.o, self.err,
+                           stream)
+        return self.o
