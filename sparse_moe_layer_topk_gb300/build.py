@@ -17,7 +17,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe.so")
 SOURCES = ["gemm_tc.cu", "route_permute.cu", "abi.cu", "timing.cu", "permute_noalloc.cu", "diag.cu",
-           "abi_block.cu", "linattn.cu", "optim.cu"]
+           "abi_block.cu", "linattn.cu", "linattn_chunk.cu", "optim.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include")]
 

@@ -80,8 +80,8 @@ int moe_linattn_fwd(const uint16_t* q, const uint16_t* k, const uint16_t* v,
   const size_t need = moe_workspace_size(MOE_OP_LINATTN_FWD, max_seqlen, Dk, Dv, Hs, r, 0, N);
   MOE_REQUIRE(need == 0 || (ws != nullptr && ws_bytes >= need), MOE_ERR_WORKSPACE);
   const LinShape s{cu_seqlens, log_decay, N, T, max_seqlen, Hs, err_flag};
-  const LinProblem p{q, k, v, ldq, ldk, ldv, ldo, o, r, 1, Dk, Dv, 0, 1.0f, scale, state_in, state_out, Dv, 1};
-  return cuda_status(launch_linattn_token(p, s, S(stream)));
+  const LinProblem p{q, k, v, ldq, ldk, ldv, ldo, o, r, 1, Dk, Dv, 0, 1.0f, scale, state_in, state_out, Dv, 1, -1};
+  return linattn_run(&p, 1, s, ws, S(stream));
 }
 
 int moe_linattn_bwd(const uint16_t* dout, const uint16_t* q, const uint16_t* k, const uint16_t* v,
@@ -110,13 +110,12 @@ int moe_linattn_bwd(const uint16_t* dout, const uint16_t* q, const uint16_t* k, 
   MOE_REQUIRE(need == 0 || (ws != nullptr && ws_bytes >= need), MOE_ERR_WORKSPACE);
   const LinShape s{cu_seqlens, log_decay, N, T, max_seqlen, Hs, err_flag};
   // dq_t = scale S_t dout_t: the forward's recurrence with k and v exchanged
-  const LinProblem pq{dout, v, k, lddo, ldv, ldk, lddq, dq, r, 1, Dv, Dk, 0, 1.0f, scale, state_in, nullptr, 1, Dv};
+  const LinProblem pq{dout, v, k, lddo, ldv, ldk, lddq, dq, r, 1, Dv, Dk, 0, 1.0f, scale, state_in, nullptr, 1, Dv, -1};
   // dv_t = R_t^T k_t and dk_t = R_t v_t: from the last token to the first
-  const LinProblem pv{k, q, dout, ldk, ldq, lddo, lddv, dv, 1, r, Dk, Dv, 1, scale, 1.0f, d_state_out, d_state_in, Dv, 1};
-  const LinProblem pk{v, dout, q, ldv, lddo, ldq, lddk, dk, 1, r, Dv, Dk, 1, scale, 1.0f, d_state_out, nullptr, 1, Dv};
-  MOE_CHECK(cuda_status(launch_linattn_token(pq, s, S(stream))));
-  MOE_CHECK(cuda_status(launch_linattn_token(pv, s, S(stream))));
-  return cuda_status(launch_linattn_token(pk, s, S(stream)));
+  const LinProblem pv{k, q, dout, ldk, ldq, lddo, lddv, dv, 1, r, Dk, Dv, 1, scale, 1.0f, d_state_out, d_state_in, Dv, 1, -1};
+  const LinProblem pk{v, dout, q, ldv, lddo, ldq, lddk, dk, 1, r, Dv, Dk, 1, scale, 1.0f, d_state_out, nullptr, 1, Dv, 1};
+  const LinProblem p[3] = {pq, pv, pk};  // (dk's states are dv's transposed)
+  return linattn_run(p, 3, s, ws, S(stream));
 }
 
 int moe_linattn_step(const uint16_t* q, const uint16_t* k, const uint16_t* v,

@@ -127,6 +127,12 @@ int gemm_launch(const GemmLaunch& L, cudaStream_t stream);
 // partials per row and n tile (dw_nparts = 2 * n tiles).
 int gemm_epilogue_warps(const GemmLaunch& L);
 
+// 3-D tensor map of a bf16 [d2][d1][d0] tensor (d0 contiguous; ld1, ld2 elements between
+// rows and between slices) with boxes of 64 x box_rows x 1, 128-byte swizzle. The map is written
+// to `map` (128 bytes, 64-byte aligned). False when the driver refuses it.
+bool make_rows_map(void* map, const void* ptr, long long d0, long long d1, long long d2,
+                   long long ld1, long long ld2, int box_rows);
+
 int num_sms();
 void record_cuda_error(cudaError_t e);
 

@@ -1,5 +1,5 @@
-// Linear attention with a decay for each state head: the recurrence token by
-// token, and the step of a decoding batch.
+// Linear attention with a decay for each state head: the step of a decoding batch
+// (linattn_chunk.cu has the chunked form).
 #include "common.cuh"
 #include "linattn.h"
 #include "timing.h"
@@ -16,68 +16,6 @@ __device__ __forceinline__ float head_log_decay(const float* log_decay, int h, i
   if (g <= 0.0f) return g;
   set_flag(err_flag, MOE_FLAG_NONFINITE);
   return 0.0f;
-}
-
-// ------------------------------------------------------------------ token by token
-
-// One CTA per sequence and state head, thread j holds column j of the state.
-__global__ void __launch_bounds__(128) linattn_token_kernel(LinProblem p, LinShape s) {
-  const int n = blockIdx.x / s.Hs, h = blockIdx.x % s.Hs;
-  int start, len;
-  lin_sequence(s, n, start, len);
-  if (len < 0) {
-    if (threadIdx.x == 0 && h == 0) set_flag(s.err_flag, MOE_FLAG_BAD_INDEX);
-    return;
-  }
-  const int j = threadIdx.x;
-  const bool mine = j < p.dv;
-  const float lam = expf(head_log_decay(s.log_decay, h, j == 0 ? s.err_flag : nullptr));
-  __shared__ float sq[128], sk[128];
-  float S[128];
-  const long long base = (static_cast<long long>(n) * s.Hs + h) * p.dk * p.dv;
-#pragma unroll
-  for (int i = 0; i < 128; ++i)
-    S[i] = p.s_in && mine && i < p.dk
-               ? p.s_in[base + static_cast<long long>(i) * p.s_row + static_cast<long long>(j) * p.s_col]
-               : 0.0f;
-  for (int x = 0; x < len; ++x) {
-    const long long t = start + (p.rev ? len - 1 - x : x);
-    if (!p.rev) {
-#pragma unroll
-      for (int i = 0; i < 128; ++i) S[i] *= lam;
-    }
-    for (int b = 0; b < p.nkv; ++b) {
-      const int hk = h * p.nkv + b;
-      __syncthreads();
-      sk[j] = j < p.dk ? __bfloat162float(static_cast<const bf16*>(p.k)[t * p.ldk + hk * p.dk + j]) : 0.0f;
-      __syncthreads();
-      const float vj =
-          mine ? p.upd * __bfloat162float(static_cast<const bf16*>(p.v)[t * p.ldv + hk * p.dv + j]) : 0.0f;
-#pragma unroll
-      for (int i = 0; i < 128; ++i) S[i] = fmaf(sk[i], vj, S[i]);
-    }
-    for (int a = 0; a < p.nq; ++a) {
-      const int hq = h * p.nq + a;
-      __syncthreads();
-      sq[j] = j < p.dk ? __bfloat162float(static_cast<const bf16*>(p.q)[t * p.ldq + hq * p.dk + j]) : 0.0f;
-      __syncthreads();
-      float o = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 128; ++i) o = fmaf(sq[i], S[i], o);
-      if (mine)
-        static_cast<bf16*>(p.o)[t * p.ldo + hq * p.dv + j] = __float2bfloat16_rn(p.inter * o);
-    }
-    if (p.rev) {
-#pragma unroll
-      for (int i = 0; i < 128; ++i) S[i] *= lam;
-    }
-  }
-  if (p.s_out && mine) {
-#pragma unroll
-    for (int i = 0; i < 128; ++i)
-      if (i < p.dk)
-        p.s_out[base + static_cast<long long>(i) * p.s_row + static_cast<long long>(j) * p.s_col] = S[i];
-  }
 }
 
 // ------------------------------------------------------------------ decoding step
@@ -172,12 +110,6 @@ __global__ void __launch_bounds__(kStepThreads)
 }
 
 }  // namespace
-
-cudaError_t launch_linattn_token(const LinProblem& p, const LinShape& s, cudaStream_t st) {
-  LaunchTimer lt(p.rev ? "linattn_token_rev" : "linattn_token", st);
-  linattn_token_kernel<<<s.N * s.Hs, 128, 0, st>>>(p, s);
-  return cudaGetLastError();
-}
 
 cudaError_t launch_linattn_step(const void* q, const void* k, const void* v,
                                 const float* log_decay, float* state, const int* state_idx,

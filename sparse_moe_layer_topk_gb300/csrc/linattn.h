@@ -23,6 +23,7 @@ struct LinProblem {
   const float* s_in;
   float* s_out;
   int s_row, s_col;
+  int shares;  // index of the problem whose states are this one's transposed; -1: none
 };
 
 struct LinShape {
@@ -45,7 +46,11 @@ __device__ __forceinline__ void lin_sequence(const LinShape& s, int n, int& star
   len = (start < 0 || end > s.T || d < 0 || d > s.max_seqlen) ? -1 : static_cast<int>(d);
 }
 
-cudaError_t launch_linattn_token(const LinProblem& p, const LinShape& s, cudaStream_t st);
+// Runs np (1 to 3) recurrences over the same sequences. ws: linattn_workspace bytes (device); an MOE_*
+// status.
+size_t linattn_workspace(int max_seqlen, int Dk, int Dv, int Hs, int N, bool backward);
+int linattn_run(const LinProblem* p, int np, const LinShape& s, void* ws, cudaStream_t st);
+
 cudaError_t launch_linattn_step(const void* q, const void* k, const void* v,
                                 const float* log_decay, float* state, const int* state_idx,
                                 int n_slots, int B, int Hs, int r, int Dk, int Dv, long long ldq,

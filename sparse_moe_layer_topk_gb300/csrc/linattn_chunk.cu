@@ -1,0 +1,991 @@
+// Linear attention with a decay for each state head in chunks of 128 tokens, on
+// the tcgen05 tensor cores: the forward and the three products of the backward
+// are runs of one recurrence (linattn.h). With lam the head's decay, for a
+// chunk of n tokens and the state S before it (forward order):
+//   P   = (Q K^T) . L,  L_ij = lam^(i-j) for j <= i, else 0
+//   O   = inter lam^(i+1) (Q S) + inter upd (P V)
+//   S'  = lam^n S + upd sum_j (lam^(n-1-j) k_j) v_j^T
+// and in reverse L_ij = lam^(j-i) for j >= i, lam^(n-1-i) for the rows, lam^(j+1)
+// for the state's weights.
+//
+// One CTA walks the chunks of one sequence and state head (or of a segment of
+// them), so the state never leaves the SM: per chunk it reads q, k, v and writes o once.
+// Tokens arrive by TMA in tiles of 128 x width (128-byte swizzle). Warp roles:
+//   warp 0       TMA producer over a ring of tile slots
+//   warp 1       MMA issue: QK^T, QS, PV, K~^T V into four accumulators that fill
+//                tensor memory (512 columns at width 128)
+//   warps 4-11   scores: P out of tensor memory, times the decay factors, back as the
+//                bf16 A operand of PV (in place); then the output rows
+//   warps 12-19  state: the decayed keys K~ into shared memory; S in registers (fp32), its
+//                bf16 copy as the B operand of QS
+// Rounding: P and the copy of S that QS reads are bf16 (their error is that of the
+// output's own rounding; with keys of up to 64 values, two bf16 terms); the state itself is summed in fp32 and K~ enters the product
+// as two bf16 terms (16 bits and a sign: 2.7e-6 of the state, rms), because the state is an
+// output of the call and is carried over thousands of chunks. A chunk's sum starts from zero and
+// is added in fp32 registers, not in tensor memory, whose accumulation truncates.
+#include <cuda.h>
+
+#include <cmath>
+#include <cstring>
+
+#include "common.cuh"
+#include "gemm.h"
+#include "linattn.h"
+#include "timing.h"
+
+namespace moe {
+namespace {
+
+constexpr int C = 128;  // tokens of a chunk
+constexpr int kScoreWarps = 8, kStateWarps = 8;
+constexpr int kThreads = 128 + 32 * (kScoreWarps + kStateWarps);
+// Registers a thread of each warpgroup; together no more than what the block is launched with
+// (640 threads of 96).
+constexpr int kIssueRegs = 80, kScoreRegs = 80, kStateRegs = 120;
+static_assert(kIssueRegs + 2 * kScoreRegs + 2 * kStateRegs <= 5 * 96, "register split");
+
+template <int DK, int DV>
+struct Cfg {
+  static constexpr int TK = C * DK * 2, TV = C * DV * 2;  // bytes of a q / k and of a v tile
+  static constexpr int SLOT = TK > TV ? TK : TV;
+  // P and the state's copy in two bf16 terms for keys of up to 64 values: the fewer values a product
+  // sums, the less their rounding errors average out, and QS is short then.
+  static constexpr int TERMS = DK <= 64 ? 2 : 1;
+  static constexpr int COPY = DK * DV * 2;  // a term of the state's copy
+  static constexpr int MISC = 256 + 1024 + 768;  // barriers; decay factors and powers
+  static constexpr int LIMIT = 232448 - 1024;
+  // slots of the ring: what fits beside the state's copy
+  static constexpr int FIT = (LIMIT - MISC - TERMS * COPY) / SLOT;
+  static constexpr int SLOTS = FIT > 9 ? 9 : FIT;
+  static constexpr int SMEM = SLOTS * SLOT + TERMS * COPY + MISC + 1024;
+  static_assert(SLOTS >= 6, "a chunk's three tiles and the next one's");
+  // tensor memory columns
+  static constexpr int P = 0, Z = 128, O1 = 256, O2 = 384;
+};
+
+struct Problem {
+  CUtensorMap q, k, v, o;
+  LinProblem p;
+  // states at the segments' starts, [sequence][head][segment][dk * dv], element (i, j) at
+  // i * seg_row + j * seg_col (null: one segment)
+  float* seg;
+  int seg_row, seg_col;
+};
+
+struct Args {
+  Problem prob[3];
+  LinShape s;
+  int nprob;
+  int nseg;         // segments a sequence may have
+  int seg_chunks;   // chunks of one
+  int states_only;  // the segments' own sums alone, for the scan
+};
+
+// ------------------------------------------------------------------ powers of the decay
+
+// exp(e * g) with the product's rounding error added back.
+__device__ __forceinline__ float power(float g, int e) {
+  if (e == 0) return 1.0f;
+  const float fe = static_cast<float>(e);
+  const float y = fe * g;
+  const float x = expf(y);
+  return x > 0.0f ? fmaf(x, fmaf(fe, g, -y), x) : 0.0f;
+}
+
+// The same as hi + lo: a state is multiplied by it once a chunk, and a rounding error
+// of a factor near 1 would grow with the number of chunks.
+__device__ __forceinline__ void power2(float g, int e, float& hi, float& lo) {
+  const float fe = static_cast<float>(e);
+  const float y = fe * g;
+  if (!(y > -0.3f) || e == 0) {
+    hi = power(g, e);
+    lo = 0.0f;
+    return;
+  }
+  float m = expm1f(y);
+  m = fmaf(1.0f + m, fmaf(fe, g, -y), m);
+  hi = 1.0f + m;
+  lo = m - (hi - 1.0f);
+}
+
+__device__ __forceinline__ void store32(void* p, uint4 a, uint4 b) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x),
+               "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
+}
+
+// What a CTA works on.
+struct Work {
+  int prob, n, h, seg;
+  int start, len;   // the sequence's tokens
+  int chunks;       // of the whole sequence
+  int c0, c1;       // this CTA's, in processing order
+  bool last;        // it holds the sequence's last state
+};
+
+__device__ __forceinline__ bool find_work(const Args& a, Work& w) {
+  int b = blockIdx.x;
+  w.prob = b % a.nprob;
+  b /= a.nprob;
+  const int segs = a.states_only ? a.nseg - 1 : a.nseg;
+  w.seg = b % segs;
+  b /= segs;
+  w.h = b % a.s.Hs;
+  w.n = b / a.s.Hs;
+  lin_sequence(a.s, w.n, w.start, w.len);
+  // (what follows from them is then uniform to the compiler, the MMA descriptors above all)
+  w.start = __shfl_sync(0xFFFFFFFFu, w.start, 0);
+  w.len = __shfl_sync(0xFFFFFFFFu, w.len, 0);
+  if (w.len < 0) {
+    if (threadIdx.x == 0 && w.seg == 0 && w.h == 0) set_flag(a.s.err_flag, MOE_FLAG_BAD_INDEX);
+    return false;
+  }
+  w.chunks = (w.len + C - 1) / C;
+  w.c0 = w.seg * a.seg_chunks;
+  w.c1 = min(w.chunks, w.c0 + a.seg_chunks);
+  w.last = w.c1 == w.chunks;
+  if (a.states_only) return w.c0 + a.seg_chunks < w.chunks;  // a later segment starts from it
+  return w.c0 < w.chunks || w.seg == 0;
+}
+
+// First token and token count of the c-th chunk in processing order.
+__device__ __forceinline__ void chunk_at(const Work& w, int rev, int c, int& tok, int& n) {
+  const int i = rev ? w.chunks - 1 - c : c;
+  tok = w.start + i * C;
+  n = min(C, w.len - i * C);
+}
+
+// The group's heads of each chunk in turn.
+struct Item {
+  int i = 0, sub = 0, c, group;
+  __device__ __forceinline__ Item(const Work& w, int g) : c(w.c0), group(g) {}
+  __device__ __forceinline__ void next() {
+    ++i;
+    if (++sub == group) {
+      sub = 0;
+      ++c;
+    }
+  }
+};
+
+struct Ring {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int slots) {
+    if (++slot == slots) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+// K~: rows 32 b0 .. 32 b1 - 1 of a k tile times the powers of the decay, as two bf16 terms in the
+// places of k and of q (256 threads).
+template <int DK>
+__device__ __forceinline__ void decay_keys(uint8_t* tk, uint8_t* tq, const float* power_of, int rev, int n,
+                                           int tid, int b0, int b1) {
+  const int row0 = tid >> 3;  // a thread takes 16 bytes of rows row0 + 32 b
+  const uint32_t at0 = row0 * 128 + (((tid & 7) ^ (row0 & 7)) << 4);
+  const f32x2 minus = pack2(-1.0f, -1.0f);
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b) {
+    const int j = row0 + 32 * b;
+    const float wt = j < n ? power_of[rev ? j + 1 : n - 1 - j] : 0.0f;
+    const f32x2 wt2 = pack2(wt, wt);
+    const uint32_t at = at0 + b * 4096;
+    uint4 x[DK / 64];
+#pragma unroll
+    for (int c = 0; c < DK / 64; ++c) x[c] = *reinterpret_cast<const uint4*>(tk + at + c * C * 128);
+#pragma unroll
+    for (int c = 0; c < DK / 64; ++c) {
+      if (j >= n) x[c] = make_uint4(0, 0, 0, 0);  // (possibly NaN)
+      const uint32_t in[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+      uint32_t t0[4], t1[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const f32x2 v = mul2(pack2(bf16_lo(in[e]), bf16_hi(in[e])), wt2);
+        t0[e] = pack_bf16(v);
+        t1[e] = pack_bf16(fma2(pack2(bf16_lo(t0[e]), bf16_hi(t0[e])), minus, v));
+      }
+      *reinterpret_cast<uint4*>(tk + at + c * C * 128) = make_uint4(t0[0], t0[1], t0[2], t0[3]);
+      *reinterpret_cast<uint4*>(tq + at + c * C * 128) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
+    }
+  }
+}
+
+template <int DK, int DV>
+__global__ void __launch_bounds__(kThreads, 1)
+    linattn_chunk_kernel(const __grid_constant__ Args a) {
+  using F = Cfg<DK, DV>;
+  extern __shared__ uint8_t smem_raw[];
+  Work w;
+  if (!find_work(a, w)) return;
+  const LinProblem& p = a.prob[w.prob].p;
+
+  uint8_t* const smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* const copy = smem + F::SLOTS * F::SLOT;  // the state in bf16
+  uint64_t* const full = reinterpret_cast<uint64_t*>(copy + F::TERMS * F::COPY);
+  uint64_t* const empty = full + F::SLOTS;
+  uint64_t* const p_full = empty + F::SLOTS;   // QK^T done
+  uint64_t* const qs_done = p_full + 1;        // QS done: the q tile may be overwritten
+  uint64_t* const p_ready = p_full + 2;        // P back in tensor memory
+  uint64_t* const o_full = p_full + 3;
+  uint64_t* const o_empty = p_full + 4;
+  uint64_t* const k_ready = p_full + 5;        // decayed keys written
+  uint64_t* const z_full = p_full + 6;
+  uint64_t* const s_ready = p_full + 7;        // the state's copy written, Z read
+  uint64_t* const v_clean = p_full + 8;        // a short chunk's v rows of other sequences cleared
+  uint64_t* const o_gone = p_full + 9;         // the output has left its staging place
+  uint64_t* const drain = p_full + 10;
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(p_full + 11);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  // factor[128 + j - i] is L_ij, zero outside the mask; power_of[m] = lam^m, 0 <= m <= 128;
+  // falling[m] = lam^(15-m), 0 <= m < 16
+  float* const factor = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(full) + 256);
+  float* const power_of = factor + 2 * C;
+  float* const falling = power_of + C + 4;
+
+  const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);  // (uniform to the compiler)
+  const int lane = static_cast<int>(lane_id());
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < F::SLOTS; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(p_full, 1);
+    mbar_init(qs_done, 1);
+    mbar_init(p_ready, kScoreWarps);
+    mbar_init(o_full, 1);
+    mbar_init(o_empty, kScoreWarps);
+    mbar_init(k_ready, a.states_only ? kStateWarps : kStateWarps + kScoreWarps);
+    mbar_init(z_full, 1);
+    mbar_init(s_ready, kStateWarps);
+    mbar_init(v_clean, kStateWarps);
+    mbar_init(o_gone, DV / 64);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&a.prob[w.prob].q);
+    tma_prefetch_desc(&a.prob[w.prob].k);
+    tma_prefetch_desc(&a.prob[w.prob].v);
+    tma_prefetch_desc(&a.prob[w.prob].o);
+  }
+  const float log_decay = __ldg(a.s.log_decay + w.h);
+  if (threadIdx.x >= kThreads - C) {
+    const int m = threadIdx.x - (kThreads - C);
+    const float g = fminf(log_decay, 0.0f);
+    const float x = power(g, m);
+    power_of[m] = x;
+    factor[p.rev ? C + m : C - m] = x;
+    if (m > 0) factor[p.rev ? C - m : C + m] = 0.0f;
+    if (m < 16) falling[15 - m] = x;
+    if (m == 0) {
+      factor[0] = 0.0f;
+      power_of[C] = power(g, C);
+      if (!(log_decay <= 0.0f)) set_flag(a.s.err_flag, MOE_FLAG_NONFINITE);
+    }
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
+
+  // Items: the group's query heads (or key / value heads) of each chunk in turn.
+  const bool so = a.states_only != 0;
+  const int group = so ? p.nkv : max(p.nq, p.nkv);
+  const bool many_q = group > 1 && p.nq > 1;
+  const int items = (w.c1 - w.c0) * group;
+  // per item: QS and a new PV sum start with the first of a shared output, the
+  // output ends with the last; the keys of a shared state enter with the last query head
+  const auto first_q = [&](int sub) { return many_q || sub == 0; };
+  const auto last_q = [&](int sub) { return many_q || sub == group - 1; };
+  const auto adds_k = [&](int sub) { return !many_q || sub == group - 1; };
+  // A whole chunk's output rows leave through the place of the state's copy, which is idle from QS
+  // to the next state (with several query heads the next one's QS reads it): stores of one row a
+  // lane took 1,024 clocks of the shared-memory pipe a chunk. It has room for DK >= C rows.
+  const auto staged = [&](int n) { return DK == C && !many_q && n == C; };
+  const auto fail = [&]() {
+    *abort_flag = 1;
+    set_flag(a.s.err_flag, MOE_FLAG_TIMEOUT);
+  };
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+    if (warp == 0) {
+      if (elect_one()) {
+        Ring r;
+        long long issued = 0;
+        bool ok = true;
+        for (Item it(w, group); it.i < items && ok; it.next()) {
+          const int sub = it.sub;
+          int tok, n;
+          chunk_at(w, p.rev, it.c, tok, n);
+          const int hq = p.nq > 1 ? w.h * p.nq + sub : w.h;
+          const int hk = p.nkv > 1 ? w.h * p.nkv + sub : w.h;
+          for (int t = 0; t < 3; ++t) {
+            if (!mbar_wait_short(&empty[r.slot], r.phase ^ 1u)) {
+              fail();
+              ok = false;
+              break;
+            }
+            if (t == 0 && so) {
+              mbar_arrive(&full[r.slot]);  // (the q slot only takes a key term)
+            } else {
+              const CUtensorMap* m = t == 0 ? &a.prob[w.prob].q : t == 1 ? &a.prob[w.prob].k : &a.prob[w.prob].v;
+              const int width = t == 2 ? DV : DK;
+              const uint32_t dst = smem_u32(smem + r.slot * F::SLOT);
+              mbar_arrive_expect_tx(&full[r.slot], C * width * 2);
+              for (int c = 0; c < width / 64; ++c)
+                tma_load_3d(dst + c * C * 128, m, &full[r.slot], 64 * c, tok, t == 0 ? hq : hk);
+            }
+            ++issued;
+            r.next(F::SLOTS);
+          }
+        }
+        if (ok) {
+          // the last commits must not reach this CTA's barriers after it left
+          for (int i = 0; i < F::SLOTS; ++i) {
+            if (!mbar_wait_short(&empty[r.slot], r.phase ^ 1u)) {
+              fail();
+              break;
+            }
+            r.next(F::SLOTS);
+          }
+        } else {
+          // nothing may land in shared memory after the CTA left
+          int s = r.slot;
+          uint32_t ph = r.phase;
+          for (long long i = 0; i < issued && i < F::SLOTS; ++i) {
+            if (--s < 0) {
+              s = F::SLOTS - 1;
+              ph ^= 1u;
+            }
+            mbar_wait_short(&full[s], ph);
+          }
+        }
+      }
+    } else if (warp == 1) {
+      // The whole warp walks the items and one lane issues, batch by batch: the descriptors then
+      // stay in uniform registers and an MMA of 128 x 128 x 16 issues in 67 clocks (a single
+      // thread's loop took over 100).
+      {
+        const uint32_t i_qk = make_idesc_bf16(C, C, 0, 0), i_qs = make_idesc_bf16(C, DV, 0, 1);
+        const uint32_t i_pv = make_idesc_bf16(C, DV, 0, 1), i_kv = make_idesc_bf16(DK, DV, 1, 1);
+        Ring r, rn;  // the item's first slot, and that of the next one's q
+        uint32_t n_o = 0, n_s = 0, n_k = 0, n_v = 0;  // outputs, states, key sets, cleared tiles so far
+        bool ok = true;
+        const auto wait = [&](uint64_t* b, uint32_t parity) {
+          if (ok && !__all_sync(0xFFFFFFFFu, mbar_wait_short(b, parity & 1u))) {
+            fail();
+            ok = false;
+          }
+        };
+        const auto scores = [&]() {  // QK^T of the item whose q is in slot rn
+          const uint32_t sq = smem_u32(smem + rn.slot * F::SLOT);
+          wait(&full[rn.slot], rn.phase);
+          rn.next(F::SLOTS);
+          const uint32_t sk = smem_u32(smem + rn.slot * F::SLOT);
+          wait(&full[rn.slot], rn.phase);
+          rn.next(F::SLOTS);
+          rn.next(F::SLOTS);
+          if (!ok) return;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < DK / 16; ++kk) {
+              const uint32_t off = (kk >> 2) * C * 128 + (kk & 3) * 32;
+              mma_bf16_ss(tmem + F::P, make_sdesc(sq + off, 16, 1024), make_sdesc(sk + off, 16, 1024),
+                          i_qk, kk != 0);
+            }
+            mma_commit(p_full);
+          }
+          __syncwarp();
+        };
+        if (!so && items > 0) scores();
+        for (Item it(w, group); it.i < items && ok; it.next()) {
+          const int i = it.i, sub = it.sub;
+          bool early = false;
+          int tok, n;
+          chunk_at(w, p.rev, it.c, tok, n);
+          const Ring rq = r;
+          r.next(F::SLOTS);
+          const Ring rk = r;
+          r.next(F::SLOTS);
+          const Ring rv = r;
+          r.next(F::SLOTS);
+          const uint32_t sq = smem_u32(smem + rq.slot * F::SLOT), sk = smem_u32(smem + rk.slot * F::SLOT),
+                         sv = smem_u32(smem + rv.slot * F::SLOT);
+          if (!so) {
+            if (first_q(sub)) {
+              wait(s_ready, n_s);       // the state before this chunk
+              wait(o_empty, n_o ^ 1u);  // the previous output read
+              if (!ok) break;
+              tc_fence_after();
+              if (elect_one()) {
+#pragma unroll
+                for (int t = 0; t < F::TERMS; ++t)
+#pragma unroll
+                  for (int kk = 0; kk < DK / 16; ++kk)
+                    mma_bf16_ss(tmem + F::O1, make_sdesc(sq + (kk >> 2) * C * 128 + (kk & 3) * 32, 16, 1024),
+                                make_sdesc(smem_u32(copy) + t * F::COPY + kk * 2048, DK * 128, 1024), i_qs,
+                                t != 0 || kk != 0);
+              }
+              __syncwarp();
+            }
+            if (elect_one()) mma_commit(qs_done);
+            __syncwarp();
+            wait(&full[rv.slot], rv.phase);
+            if (n < C) wait(v_clean, n_v++);
+            wait(p_ready, i);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int t = 0; t < F::TERMS; ++t)
+#pragma unroll
+                for (int kk = 0; kk < C / 16; ++kk)
+                  mma_bf16_ts(tmem + F::O2, tmem + F::P + kk * 16 + t * 8, make_sdesc(sv + kk * 2048, C * 128, 1024),
+                              i_pv, t != 0 || kk != 0 || !first_q(sub));
+              if (last_q(sub)) mma_commit(o_full);
+            }
+            __syncwarp();
+            if (last_q(sub)) ++n_o;
+            // the next item's scores before this one's keys enter, if its tiles are there
+            if (i + 1 < items) {
+              Ring x = rn;
+              x.next(F::SLOTS);
+              early = __all_sync(0xFFFFFFFFu, mbar_test(&full[rn.slot], rn.phase) && mbar_test(&full[x.slot], x.phase));
+              if (early) scores();
+            }
+          }
+          if (adds_k(sub)) {
+            if (so) wait(&full[rv.slot], rv.phase);
+            if (so && n < C) wait(v_clean, n_v++);
+            wait(s_ready, n_s);  // (the sum of the chunk before was read)
+            wait(k_ready, n_k);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < 2 * C / 16; ++kk)
+                mma_bf16_ss(tmem + F::Z, make_sdesc((kk < C / 16 ? sk : sq) + (kk & 7) * 2048, C * 128, 1024),
+                            make_sdesc(sv + (kk & 7) * 2048, C * 128, 1024), i_kv, kk != 0 || !(many_q || sub == 0));
+              mma_commit(z_full);
+            }
+            __syncwarp();
+            ++n_k;
+          }
+          if (sub == group - 1) ++n_s;
+          if (elect_one()) {
+            mma_commit(&empty[rq.slot]);
+            mma_commit(&empty[rk.slot]);
+            mma_commit(&empty[rv.slot]);
+          }
+          __syncwarp();
+          if (!so && !early && i + 1 < items) scores();
+        }
+        if (*abort_flag) {
+          // every issued MMA ends before tensor memory is released
+          if (elect_one()) mma_commit(drain);
+          __syncwarp();
+          mbar_wait_short(drain, 0);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp < 4 + kScoreWarps) {
+    // ---------------------------------------------------------------- score warps
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kScoreRegs));
+    const int qd = warp & 3;  // tensor memory lanes 32 qd .. 32 qd + 31: rows of the chunk
+    const int half = (warp - 4) >> 2;  // half of the scores' and of the output's columns
+    const int row = 32 * qd + lane;
+    const uint32_t trow = tmem + (static_cast<uint32_t>(32 * qd) << 16);
+    const f32x2 intra = pack2(p.inter * p.upd, p.inter * p.upd);
+    const bool wide = (p.ldo % 16 == 0) && (p.dv % 16 == 0) && (reinterpret_cast<uintptr_t>(p.o) & 31u) == 0;
+    const int tid = threadIdx.x - 128;
+    uint32_t n_o = 0;
+    Ring r;
+    for (Item it(w, group); it.i < items && !so; it.next()) {
+      const int i = it.i, sub = it.sub;
+      int tok, n;
+      chunk_at(w, p.rev, it.c, tok, n);
+      const int rq = r.slot;
+      r.next(F::SLOTS);
+      const int rk = r.slot;
+      r.next(F::SLOTS);
+      r.next(F::SLOTS);
+      if (!mbar_wait_short(p_full, i & 1)) {
+        fail();
+        break;
+      }
+      tc_fence_after();
+      // P: 16 fp32 columns become 8 of bf16 pairs, and 8 of their second term, in place
+#pragma unroll 1
+      for (int b = 0; b < 4; ++b) {
+        const int c0 = 64 * half + 16 * b;
+        uint32_t out[F::TERMS][8];
+        if (p.rev ? c0 + 16 > 32 * qd : c0 < 32 * qd + 32) {
+          uint32_t x[16];
+          tmem_ld_32x32b_x16(trow + F::P + c0, x);
+          tmem_ld_wait();
+          float y[16];
+          if (c0 >> 5 == qd) {
+            // selected, not multiplied by zero: what lies outside the mask may be NaN
+            const float* const f = factor + C - row + c0;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float fj = f[j];
+              y[j] = fj > 0.0f ? __uint_as_float(x[j]) * fj : 0.0f;
+            }
+          } else {
+            // beside the diagonal blocks lam^|i-j| is the power of the row's distance from the 16
+            // columns' near edge times that of the column's
+            const float d = power_of[p.rev ? c0 - row : row - c0 - 15];
+            const f32x2 d2 = pack2(d, d);
+            const float4* const e = reinterpret_cast<const float4*>(p.rev ? power_of : falling);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float4 e4 = e[j];
+              unpack2(mul2(mul2(pack2(__uint_as_float(x[4 * j]), __uint_as_float(x[4 * j + 1])), d2), pack2(e4.x, e4.y)),
+                      y[4 * j], y[4 * j + 1]);
+              unpack2(mul2(mul2(pack2(__uint_as_float(x[4 * j + 2]), __uint_as_float(x[4 * j + 3])), d2), pack2(e4.z, e4.w)),
+                      y[4 * j + 2], y[4 * j + 3]);
+            }
+          }
+          if (p.rev && c0 + 16 > n) {  // keys past the chunk's tokens
+#pragma unroll
+            for (int j = 0; j < 16; ++j) y[j] = c0 + j < n ? y[j] : 0.0f;
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            out[0][j] = pack_bf16(y[2 * j], y[2 * j + 1]);
+            if (F::TERMS == 2)
+              out[F::TERMS - 1][j] = pack_bf16(y[2 * j] - bf16_lo(out[0][j]), y[2 * j + 1] - bf16_hi(out[0][j]));
+          }
+        } else {
+#pragma unroll
+          for (int t = 0; t < F::TERMS; ++t)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) out[t][j] = 0u;
+        }
+#pragma unroll
+        for (int t = 0; t < F::TERMS; ++t) tmem_st_32x32b_x8(trow + F::P + c0 + 8 * t, out[t]);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_ready);
+      // half of the keys (QS has read the q tile; every item's phase is waited for in turn)
+      if (!mbar_wait_short(qs_done, i & 1)) {
+        fail();
+        break;
+      }
+      if (adds_k(sub)) {
+        decay_keys<DK>(smem + rk * F::SLOT, smem + rq * F::SLOT, power_of, p.rev, n, tid, 2, 4);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(k_ready);
+      }
+      if (!last_q(sub)) continue;
+      if (!mbar_wait_short(o_full, n_o & 1)) {
+        fail();
+        break;
+      }
+      ++n_o;
+      tc_fence_after();
+      const float rsf = p.inter * power_of[p.rev ? max(n - 1 - row, 0) : row + 1];
+      const f32x2 rs = pack2(rsf, rsf);
+      const int hq = p.nq > 1 ? w.h * p.nq + sub : w.h;
+      bf16* const orow = static_cast<bf16*>(p.o) + (static_cast<long long>(tok) + row) * p.ldo +
+                         static_cast<long long>(hq) * p.dv;
+#pragma unroll 1
+      for (int b = 0; b < DV / 32; ++b) {
+        const int c0 = half * (DV / 2) + 16 * b;
+        uint32_t x1[16], x2[16];
+        tmem_ld_32x32b_x16(trow + F::O1 + c0, x1);
+        tmem_ld_32x32b_x16(trow + F::O2 + c0, x2);
+        tmem_ld_wait();
+        if (b == DV / 32 - 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(o_empty);
+        }
+        uint32_t u[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          u[j] = pack_bf16(fma2(rs, pack2(__uint_as_float(x1[2 * j]), __uint_as_float(x1[2 * j + 1])),
+                                mul2(intra, pack2(__uint_as_float(x2[2 * j]), __uint_as_float(x2[2 * j + 1])))));
+        const uint4 lo4 = make_uint4(u[0], u[1], u[2], u[3]), hi4 = make_uint4(u[4], u[5], u[6], u[7]);
+        if (staged(n)) {
+          uint8_t* const line = copy + (c0 >> 6) * C * 128 + row * 128;
+          const int at = (c0 & 63) >> 3, sw = row & 7;
+          *reinterpret_cast<uint4*>(line + ((at ^ sw) << 4)) = lo4;
+          *reinterpret_cast<uint4*>(line + (((at + 1) ^ sw) << 4)) = hi4;
+        } else if (row < n) {
+          if (wide && c0 + 16 <= p.dv) {
+            store32(orow + c0, lo4, hi4);
+          } else {
+            if (c0 + 8 <= p.dv) *reinterpret_cast<uint4*>(orow + c0) = lo4;
+            if (c0 + 16 <= p.dv) *reinterpret_cast<uint4*>(orow + c0 + 8) = hi4;
+          }
+        }
+      }
+      if (staged(n)) {
+        // the warps that share a 64-column block (its upper and its lower half where there is one block)
+        fence_proxy_async_smem();
+        if (DV == 128) asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
+        else asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (qd == 0 && (DV == 128 || half == 0)) {
+          if (elect_one()) {
+            tma_store_3d(&a.prob[w.prob].o, smem_u32(copy) + half * C * 128, 64 * half, tok, hq);
+            bulk_commit();
+            bulk_wait_read_all();
+            mbar_arrive(o_gone);
+          }
+          __syncwarp();
+        }
+      }
+    }
+    if (qd == 0) {
+      if (elect_one()) bulk_wait_all();
+      __syncwarp();
+    }
+  } else {
+    // ---------------------------------------------------------------- state warps
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kStateRegs));
+    const int tid = threadIdx.x - 128 - 32 * kScoreWarps;
+    const float g = fminf(log_decay, 0.0f);
+    constexpr int NC = DV / 2;  // columns of a thread
+    const int qd = warp & 3, half = (warp - 4 - kScoreWarps) >> 2;
+    const bool mine = DK == 128 || lane < 16;
+    const int row = DK == 128 ? 32 * qd + lane : 16 * qd + (lane & 15);
+    const uint32_t trow = tmem + (static_cast<uint32_t>(32 * qd) << 16) + F::Z + half * NC;
+    f32x2 S[NC / 2];
+    const long long state = (static_cast<long long>(w.n) * a.s.Hs + w.h) * p.dk * p.dv;
+    const Problem& pr = a.prob[w.prob];
+    float* const seg = pr.seg == nullptr ? nullptr
+        : pr.seg + ((static_cast<long long>(w.n) * a.s.Hs + w.h) * a.nseg + w.seg) * p.dk * p.dv;
+    {
+      const float* in = so ? nullptr : seg ? seg : p.s_in ? p.s_in + state : nullptr;
+      const int sr = seg ? pr.seg_row : p.s_row, sc = seg ? pr.seg_col : p.s_col;
+      const auto at = [&](int c) {
+        return in && mine && row < p.dk && c < p.dv
+                   ? in[static_cast<long long>(row) * sr + static_cast<long long>(c) * sc] : 0.0f;
+      };
+#pragma unroll
+      for (int j = 0; j < NC / 2; ++j) S[j] = pack2(at(half * NC + 2 * j), at(half * NC + 2 * j + 1));
+    }
+    // row `row` of the K x N operand of QS, 64 columns to a 128-byte line: columns c .. c + 7
+    const auto copy8 = [&](int j) {
+      const int c = half * NC + 8 * j;
+      uint8_t* const at = copy + (c >> 6) * DK * 128 + row * 128 + ((((c & 63) >> 3) ^ (row & 7)) << 4);
+      const uint4 t0 = make_uint4(pack_bf16(S[4 * j]), pack_bf16(S[4 * j + 1]), pack_bf16(S[4 * j + 2]), pack_bf16(S[4 * j + 3]));
+      if (mine) *reinterpret_cast<uint4*>(at) = t0;
+      if (F::TERMS == 2) {
+        const f32x2 minus = pack2(-1.0f, -1.0f);
+        const auto rest = [&](uint32_t u, f32x2 x) { return pack_bf16(fma2(pack2(bf16_lo(u), bf16_hi(u)), minus, x)); };
+        if (mine)
+          *reinterpret_cast<uint4*>(at + F::COPY) =
+              make_uint4(rest(t0.x, S[4 * j]), rest(t0.y, S[4 * j + 1]), rest(t0.z, S[4 * j + 2]), rest(t0.w, S[4 * j + 3]));
+      }
+    };
+    const auto copied = [&]() {
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(s_ready);
+    };
+#pragma unroll
+    for (int j = 0; j < NC / 8; ++j) copy8(j);
+    copied();
+    float hi = 0.0f, lo = 0.0f;
+    int n_was = -1;
+    uint32_t n_k = 0, n_out = 0;
+    const f32x2 upd = pack2(p.upd, p.upd);
+    Ring r;
+    for (Item it(w, group); it.i < items; it.next()) {
+      const int i = it.i;
+      int tok, n;
+      chunk_at(w, p.rev, it.c, tok, n);
+      const Ring rq = r;
+      r.next(F::SLOTS);
+      const Ring rk = r;
+      r.next(F::SLOTS);
+      const Ring rv = r;
+      r.next(F::SLOTS);
+      if (n < C) {
+        // rows of v past the chunk's tokens are another sequence's, possibly NaN
+        if (!mbar_wait_short(&full[rv.slot], rv.phase)) {
+          fail();
+          break;
+        }
+        uint8_t* const tv = smem + rv.slot * F::SLOT;
+#pragma unroll 1
+        for (int x = n * 8 + tid; x < C * 8; x += 32 * kStateWarps) {
+#pragma unroll
+          for (int c = 0; c < DV / 64; ++c)
+            *reinterpret_cast<uint4*>(tv + c * C * 128 + x * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(v_clean);
+      }
+      // QS has read the q tile (and QK^T the keys): both may be overwritten. (Every item's phase is
+      // waited for in turn: a parity tells one phase from the next alone.)
+      if (!so && !mbar_wait_short(qs_done, i & 1)) {
+        fail();
+        break;
+      }
+      if (!adds_k(it.sub)) continue;
+      if (n != n_was) {
+        n_was = n;
+        power2(g, n, hi, lo);
+      }
+      if (!mbar_wait_short(&full[rk.slot], rk.phase)) {
+        fail();
+        break;
+      }
+      decay_keys<DK>(smem + rk.slot * F::SLOT, smem + rq.slot * F::SLOT, power_of, p.rev, n, tid, 0, so ? 4 : 2);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (so && n_k > 0 && !mbar_wait_short(z_full, (n_k - 1) & 1)) {  // (no more than one set ahead)
+        fail();
+        break;
+      }
+      if (lane == 0) mbar_arrive(k_ready);
+      if (!mbar_wait_short(z_full, n_k & 1)) {
+        fail();
+        break;
+      }
+      ++n_k;
+      if (it.sub != group - 1) continue;
+      tc_fence_after();
+      if (!so && staged(n) && !mbar_wait_short(o_gone, n_out++ & 1)) {
+        fail();
+        break;
+      }
+      const f32x2 hi2 = pack2(hi, hi), lo2 = pack2(lo, lo);
+#pragma unroll
+      for (int cb = 0; cb < NC / 32; ++cb) {
+        uint32_t x[2][16];
+        tmem_ld_32x32b_x16(trow + cb * 32, x[0]);
+        tmem_ld_32x32b_x16(trow + cb * 32 + 16, x[1]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          f32x2& s = S[16 * cb + j];
+          const uint32_t* const z = &x[j >> 3][2 * (j & 7)];
+          s = fma2(hi2, s, fma2(lo2, s, mul2(upd, pack2(__uint_as_float(z[0]), __uint_as_float(z[1])))));
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) copy8(4 * cb + j);
+      }
+      copied();
+    }
+    if (so || (w.last && p.s_out)) {
+      // the segment's own sum goes where the scan turns it into the next one's start
+      float* const out = so ? seg + static_cast<long long>(p.dk) * p.dv : p.s_out + state;
+      const int sr = so ? p.dv : p.s_row, sc = so ? 1 : p.s_col;
+      const auto put = [&](int c, float x) {
+        if (mine && row < p.dk && c < p.dv)
+          out[static_cast<long long>(row) * sr + static_cast<long long>(c) * sc] = x;
+      };
+#pragma unroll
+      for (int j = 0; j < NC / 2; ++j) {
+        float x, y;
+        unpack2(S[j], x, y);
+        put(half * NC + 2 * j, x);
+        put(half * NC + 2 * j + 1, y);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------ segments
+
+// The states at the segments' starts from their own sums (written by a states_only launch one slot
+// further): slot 0 is the sequence's first state, slot s + 1 = lam^(tokens of s) slot s + the sum of s.
+__global__ void __launch_bounds__(256) segment_scan_kernel(LinProblem p, LinShape s, float* seg, int nseg, int seg_chunks) {
+  const int h = blockIdx.x % s.Hs, n = blockIdx.x / s.Hs;
+  int start, len;
+  lin_sequence(s, n, start, len);
+  if (len < 0) return;
+  const int chunks = (len + C - 1) / C;
+  const int used = (chunks + seg_chunks - 1) / seg_chunks;
+  const float g = fminf(__ldg(s.log_decay + h), 0.0f);
+  const int size = p.dk * p.dv;
+  const long long base = static_cast<long long>(n) * s.Hs + h;
+  float* const out = seg + base * nseg * size;
+  // (a reverse recurrence starts with the sequence's last, short chunk)
+  float hi0, lo0, hi, lo;
+  power2(g, p.rev ? len - (chunks - seg_chunks) * C : seg_chunks * C, hi0, lo0);
+  power2(g, seg_chunks * C, hi, lo);
+  for (int e = blockIdx.y * blockDim.x + threadIdx.x; e < size; e += gridDim.y * blockDim.x) {
+    const int i = e / p.dv, j = e - i * p.dv;
+    float x = p.s_in ? p.s_in[base * size + static_cast<long long>(i) * p.s_row + static_cast<long long>(j) * p.s_col] : 0.0f;
+    out[e] = x;
+    for (int k = 1; k < used; ++k) {
+      float& y = out[static_cast<long long>(k) * size + e];
+      x = k == 1 ? fmaf(hi0, x, fmaf(lo0, x, y)) : fmaf(hi, x, fmaf(lo, x, y));
+      y = x;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ host side
+
+int status(cudaError_t e) {
+  if (e == cudaSuccess) return MOE_OK;
+  record_cuda_error(e);
+  return MOE_ERR_CUDA;
+}
+
+template <int DK, int DV>
+int launch(const char* name, const Args& a, cudaStream_t st) {
+  using F = Cfg<DK, DV>;
+  const auto kernel = linattn_chunk_kernel<DK, DV>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, F::SMEM);
+  if (e != cudaSuccess) return status(e);
+  const long long grid = static_cast<long long>(a.nprob) * a.s.N * a.s.Hs * (a.states_only ? a.nseg - 1 : a.nseg);
+  if (grid >= (1ll << 31)) return MOE_ERR_ARG;
+  {
+    LaunchTimer lt(name, st);
+    kernel<<<static_cast<unsigned>(grid), kThreads, F::SMEM, st>>>(a);
+  }
+  return status(cudaGetLastError());
+}
+
+// One launch over problems of one width class.
+int launch_problems(const char* name, const Problem* const* probs, int np, const LinShape& s, int nseg,
+                    int seg_chunks, bool states_only, cudaStream_t st) {
+  Args a;
+  std::memset(static_cast<void*>(&a), 0, sizeof a);
+  for (int i = 0; i < np; ++i) a.prob[i] = *probs[i];
+  a.s = s;
+  a.nprob = np;
+  a.nseg = nseg;
+  a.seg_chunks = seg_chunks;
+  a.states_only = states_only ? 1 : 0;
+  const bool k64 = a.prob[0].p.dk <= 64, v64 = a.prob[0].p.dv <= 64;
+  if (k64 && v64) return launch<64, 64>(name, a, st);
+  if (k64) return launch<64, 128>(name, a, st);
+  if (v64) return launch<128, 64>(name, a, st);
+  return launch<128, 128>(name, a, st);
+}
+
+struct Split {
+  int nseg, seg_chunks;
+};
+
+// Segments of the time axis for `units` recurrences of at most `chunks` chunks. A CTA takes about 4 us a
+// chunk, 2 us where it sums the state alone, and the two more launches 8 us (measured at widths of 128):
+// the split with the shortest estimate of rounds over the SMs is taken. At 32 heads of 32,768 tokens
+// one segment took 1,036 us and the split 334.
+Split split(long long units, int chunks) {
+  Split best{1, chunks > 0 ? chunks : 1};
+  const long long sms = num_sms();
+  const auto rounds = [&](long long ctas) { return static_cast<double>((ctas + sms - 1) / sms); };
+  double least = 4.0 * chunks * rounds(units);
+  for (int n = 2; n <= 64 && n <= chunks && units * n <= 8 * sms; ++n) {
+    const int per = (chunks + n - 1) / n;
+    const int used = (chunks + per - 1) / per;
+    const double t = 4.0 * per * rounds(units * used) + 2.0 * per * rounds(units * (used - 1)) + 8.0;
+    if (t < least) {
+      least = t;
+      best = Split{used, per};
+    }
+  }
+  return best;
+}
+
+size_t slots_bytes(const LinShape& s, const Split& sp, int dk, int dv) {
+  return static_cast<size_t>(s.N) * s.Hs * sp.nseg * dk * dv * 4;
+}
+
+}  // namespace
+
+size_t linattn_workspace(int max_seqlen, int Dk, int Dv, int Hs, int N, bool backward) {
+  if (max_seqlen <= 0 || N <= 0 || Hs <= 0 || Dk <= 0 || Dv <= 0) return 0;
+  const Split sp = split(static_cast<long long>(backward ? 3 : 1) * N * Hs, (max_seqlen + C - 1) / C);
+  if (sp.nseg == 1) return 0;
+  LinShape s{};
+  s.N = N;
+  s.Hs = Hs;
+  return (slots_bytes(s, sp, Dk, Dv) * (backward ? 2 : 1) + 255) & ~static_cast<size_t>(255);
+}
+
+int linattn_run(const LinProblem* p, int np, const LinShape& s, void* ws, cudaStream_t st) {
+  const Split sp = split(static_cast<long long>(np) * s.N * s.Hs, (s.max_seqlen + C - 1) / C);
+  Problem prob[3];
+  const long long T = s.T > 0 ? s.T : 1;
+  float* slots = static_cast<float*>(ws);
+  for (int i = 0; i < np; ++i) {
+    Problem& x = prob[i];
+    std::memset(static_cast<void*>(&x), 0, sizeof x);
+    x.p = p[i];
+    const long long hq = static_cast<long long>(s.Hs) * p[i].nq, hk = static_cast<long long>(s.Hs) * p[i].nkv;
+    if (!make_rows_map(&x.q, p[i].q, p[i].dk, T, hq, p[i].ldq, p[i].dk, C) ||
+        !make_rows_map(&x.k, p[i].k, p[i].dk, T, hk, p[i].ldk, p[i].dk, C) ||
+        !make_rows_map(&x.v, p[i].v, p[i].dv, T, hk, p[i].ldv, p[i].dv, C) ||
+        !make_rows_map(&x.o, p[i].o, p[i].dv, T, hq, p[i].ldo, p[i].dv, C))
+      return MOE_ERR_CUDA;
+    if (sp.nseg > 1) {
+      if (p[i].shares < 0) {
+        x.seg = slots;
+        x.seg_row = p[i].dv;
+        x.seg_col = 1;
+        slots += slots_bytes(s, sp, p[i].dk, p[i].dv) / 4;
+      } else {  // the transposed states of another problem
+        x.seg = prob[p[i].shares].seg;
+        x.seg_row = 1;
+        x.seg_col = p[i].dk;
+      }
+    }
+  }
+  // problems of one width class run in one launch
+  const auto same = [&](int i, int j) {
+    return (p[i].dk <= 64) == (p[j].dk <= 64) && (p[i].dv <= 64) == (p[j].dv <= 64);
+  };
+  for (int pass = sp.nseg > 1 ? 0 : 1; pass < 2; ++pass) {
+    bool done[3] = {false, false, false};
+    for (int i = 0; i < np; ++i) {
+      if (done[i]) continue;
+      const Problem* some[3];
+      int n = 0;
+      for (int j = i; j < np; ++j) {
+        if (done[j] || !same(i, j)) continue;
+        done[j] = true;
+        if (pass == 1 || p[j].shares < 0) some[n++] = &prob[j];
+      }
+      if (n == 0) continue;
+      const int e = launch_problems(pass == 0 ? "linattn_segments" : np == 1 ? "linattn_fwd" : "linattn_bwd", some, n, s,
+                                    sp.nseg, sp.seg_chunks, pass == 0, st);
+      if (e != MOE_OK) return e;
+    }
+    if (pass == 0) {
+      for (int i = 0; i < np; ++i) {
+        if (p[i].shares >= 0) continue;
+        LaunchTimer lt("linattn_scan", st);
+        const dim3 grid(static_cast<unsigned>(s.N) * s.Hs, (p[i].dk * p[i].dv + 2047) / 2048);
+        segment_scan_kernel<<<grid, 256, 0, st>>>(p[i], s, prob[i].seg, sp.nseg, sp.seg_chunks);
+        const int e = status(cudaGetLastError());
+        if (e != MOE_OK) return e;
+      }
+    }
+  }
+  return MOE_OK;
+}
+
+}  // namespace moe

@@ -177,11 +177,12 @@ def test_slices_of_a_fused_projection():
         _close(n, t, ref[n], mag[n], 8)
 
 
+@pytest.mark.parametrize("r", [1, 3])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
-def test_other_sequences_values_stay_out(bad):
+def test_other_sequences_values_stay_out(bad, r):
     """A sequence of NaN or infinities leaves its neighbours in the same tiles as they were."""
     lens = [70, 50, 75]
-    x = _make(lens, 1, 1, 64, 64)
+    x = _make(lens, 1, r, 64, 64)
     ref, mag = _ref(x)
     for n in ("q", "k", "v", "do"):
         x[n][70:120] = bad
