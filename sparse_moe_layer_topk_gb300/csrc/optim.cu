@@ -6,8 +6,7 @@
 //
 // Nothing is reused, so the step is bound by HBM: p, m, v in and out and g in.
 // Each warp takes runs of blocks of 256 values (a prefix of the tensors' chunk
-// counts, searched where a run enters a tensor, says whose), eight consecutive values a lane: 32-byte loads and stores of fp32, 16-byte of bf16, 8-byte of codes, a block's loads under
-// way while the one before it is worked on. A block is also what shares a scale in the 8-bit states:
+// counts, searched where a run enters a tensor, says whose), eight consecutive values a lane: 32-byte loads and stores of fp32, 16-byte of bf16, 8-byte of codes. A block is also what shares a scale in the 8-bit states:
 // its largest magnitude is one warp reduction. The 8-bit step moves 10 bytes a value (bf16 weights and
 // gradients), so its instructions weigh as much as its bytes: arithmetic runs two values to an
 // instruction, and types are told apart once a run.
@@ -230,15 +229,16 @@ __global__ void __launch_bounds__(kThreads)
     grad_norm_kernel(const AdamwEntry* entries, int n_tensors, long long chunks, float max_norm,
                      double* partial, AdamwControl* ctl) {
   f32x2 acc[4] = {{0}, {0}, {0}, {0}};
-  for (long long c = blockIdx.x; c < chunks; c += gridDim.x) {
-    const int t = find_tensor(entries, n_tensors, c);
-    const AdamwEntry& e = entries[t];
+  const auto load = [&](long long c, f32x2 (&g)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) g[i] = pack2(0.0f, 0.0f);
+    if (c >= chunks) return;
+    const AdamwEntry& e = entries[find_tensor(entries, n_tensors, c)];
     const long long at = (c - e.chunk0) * kAdamwChunk + threadIdx.x * kPerLane;
     const long long left = e.n - at;
-    if (left <= 0) continue;
+    if (left <= 0) return;
     const int n = static_cast<int>(left < 8 ? left : 8);
     const bool whole = e.vec && n == 8;
-    f32x2 g[4];
     if (e.g_dtype == MOE_DTYPE_F32) {
       uint32_t raw[8];
       load_raw(static_cast<const char*>(e.g) + at * 4, n, whole, raw);
@@ -248,8 +248,15 @@ __global__ void __launch_bounds__(kThreads)
       load_raw(static_cast<const char*>(e.g) + at * 2, n, whole, raw);
       to_f32(raw, g);
     }
+  };
+  for (long long c = blockIdx.x; c < chunks; c += 2 * gridDim.x) {
+    f32x2 g0[4], g1[4];
+    load(c, g0);
+    load(c + gridDim.x, g1);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] = fma2(g[i], g[i], acc[i]);
+    for (int i = 0; i < 4; ++i) acc[i] = fma2(g0[i], g0[i], acc[i]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] = fma2(g1[i], g1[i], acc[i]);
   }
   double s = 0.0;
 #pragma unroll
@@ -356,18 +363,15 @@ struct Lane {
   uint32_t m[Q8 ? 2 : 8], v[Q8 ? 2 : 8];
   float m_scale, v_scale;
 
-  // AHEAD: of the block after `a`
-  template <int AHEAD>
   __device__ __forceinline__ void load(const At& a, bool vec) {
-    const int n = a.left - AHEAD * kBlock;
-    const bool whole = vec && n >= 8;
-    load_raw(a.g + AHEAD * kBlock * At::GS, n, whole, g);
-    load_raw(a.p + AHEAD * kBlock * At::PS, n, whole, p);
-    load_raw(a.m + AHEAD * kBlock * At::SS, n, whole, m);
-    load_raw(a.v + AHEAD * kBlock * At::SS, n, whole, v);
+    const bool whole = vec && a.left >= 8;
+    load_raw(a.g, a.left, whole, g);
+    load_raw(a.p, a.left, whole, p);
+    load_raw(a.m, a.left, whole, m);
+    load_raw(a.v, a.left, whole, v);
     if (Q8) {
-      m_scale = a.m_scale[AHEAD];
-      v_scale = a.v_scale[AHEAD];
+      m_scale = *a.m_scale;
+      v_scale = *a.v_scale;
     }
   }
 
@@ -454,10 +458,10 @@ struct Lane {
   }
 };
 
-// `count` blocks of a tensor from value `at` (the lane's first) on, by one warp. With 32-bit states a
-// block's loads are under way while the one before it is worked on; the 8-bit step has enough
-// instructions for four CTAs an SM to cover them. Out of line: each pair of types has its own
-// registers (inlined into one kernel, six of them spilled 950 bytes a thread).
+// `count` blocks of a tensor from value `at` (the lane's first) on, by one warp. The warps of three or
+// four CTAs an SM cover one another's loads (a block's loads issued ahead of the one before it took the
+// registers of a CTA and 2% more time). Out of line: each pair of types has its own registers
+// (inlined into one kernel, six of them spilled 950 bytes a thread).
 template <bool Q8, int W, bool GB>
 __device__ __noinline__ void run_blocks(const AdamwEntry* entry, long long at, int count, uint32_t key,
                                         const StepConsts* consts) {
@@ -468,14 +472,11 @@ __device__ __noinline__ void run_blocks(const AdamwEntry* entry, long long at, i
   // (a lane's eight values share all but the last three bits of their index)
   uint32_t high = mix32(static_cast<uint32_t>(at >> 32) + key);
   uint32_t low = static_cast<uint32_t>(at);
-  Lane<Q8, W, GB> now, next;
-  if (!Q8) now.template load<0>(a, vec);
 #pragma unroll 1
   for (int k = 0; k < count; ++k) {
-    if (Q8) now.template load<0>(a, vec);
-    else if (k + 1 < count) next.template load<1>(a, vec);
-    now.update(a, vec, decay, low ^ high, s);
-    if (!Q8) now = next;
+    Lane<Q8, W, GB> x;
+    x.load(a, vec);
+    x.update(a, vec, decay, low ^ high, s);
     a.next_block();
     low += kBlock;
     at += kBlock;
@@ -484,7 +485,7 @@ __device__ __noinline__ void run_blocks(const AdamwEntry* entry, long long at, i
 }
 
 template <bool Q8>
-__global__ void __launch_bounds__(kThreads, Q8 ? 4 : 2)
+__global__ void __launch_bounds__(kThreads, Q8 ? 4 : 3)
     adamw_step_kernel(const AdamwEntry* entries, int n_tensors, long long chunks, AdamwHyper h,
                       const float* lr_dev, AdamwControl* ctl, int clipped, long long run, int* err_flag) {
   __shared__ StepConsts sc;
@@ -510,7 +511,10 @@ __global__ void __launch_bounds__(kThreads, Q8 ? 4 : 2)
     // runs of blocks (a tensor's last chunk counts whole), one warp each in turn
     const long long blocks = chunks * kChunkBlocks;
     const long long warps = static_cast<long long>(gridDim.x) * (kThreads / 32);
-    for (long long r = (static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5)) * run; r < blocks; r += warps * run) {
+    const long long runs = (blocks + run - 1) / run;
+    for (long long i = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); i < runs; i += warps) {
+      // (last to first after a norm, whose last gradients are still in L2)
+      const long long r = (clipped ? runs - 1 - i : i) * run;
       const long long b1 = r + run < blocks ? r + run : blocks;
       for (long long b0 = r; b0 < b1;) {
         const int t = find_tensor(entries, n_tensors, b0 / kChunkBlocks);
@@ -566,8 +570,8 @@ cudaError_t launch_grad_norm(const AdamwEntry* entries, int n, long long chunks,
 cudaError_t launch_adamw_step(const AdamwEntry* entries, int n, long long chunks, int state_bits,
                               const AdamwHyper& h, const float* lr_dev, AdamwControl* ctl,
                               bool clipped, int* err_flag, cudaStream_t st) {
-  // Four or two CTAs an SM (8- and 32-bit states), fewer where there is not a block for every warp.
-  const long long ctas = (state_bits == 8 ? 4ll : 2ll) * num_sms();
+  // Four or three CTAs an SM (8- and 32-bit states), fewer where there is not a block for every warp.
+  const long long ctas = (state_bits == 8 ? 4ll : 3ll) * num_sms();
   const int grid = static_cast<int>(chunks < ctas ? chunks : ctas);
   // A warp's run: an equal share of all blocks with 8-bit states, whose instructions have to be spread
   // evenly (67 M bf16 values: 175 us, in runs of 8 blocks 194); at most 8 blocks with 32-bit ones, which
