@@ -443,7 +443,8 @@ int moe_linattn_bwd(const uint16_t* dout, const uint16_t* q, const uint16_t* k, 
  * the state cache [n_slots][Hs][Dk][Dv] (fp32) in place at slot state_idx[b]
  * (int32 [B]; NULL: slot b) and writes o[b]. A negative slot is an empty row: its o is
  * zero and no state changes. A slot >= n_slots sets MOE_FLAG_BAD_INDEX and counts
- * as empty. The slots of one call must differ from one another. */
+ * as empty. The slots of one call must differ from one another. state is 32-byte
+ * aligned; B * Hs < 2^28. */
 int moe_linattn_step(const uint16_t* q, const uint16_t* k, const uint16_t* v,
                      const float* log_decay, float* state, const int32_t* state_idx, int n_slots,
                      int B, int Hs, int r, int Dk, int Dv, int ldq, int ldk, int ldv, int ldo,

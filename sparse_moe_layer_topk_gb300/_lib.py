@@ -144,13 +144,14 @@ def _ptr(x):
             if x.numel():
                 raise MoEError("libmoe takes device tensors")
             return None
-        return x.data_ptr() if x.numel() else _empty_ptr(x.device)
+        return x.data_ptr() or _empty_ptr(x.device)
     return int(x)
 
 
 def _stream(s):
     if s is None:
-        return torch.cuda.current_stream().cuda_stream
+        # (the raw handle: making a torch.cuda.Stream for it takes longer than the call below)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(s, torch.cuda.Stream):
         return s.cuda_stream
     return int(s)
@@ -165,14 +166,25 @@ def _check(status: int, name: str):
         raise MoEError(f"{name} failed: {msg}{extra}")
 
 
+_BOUND = {}
+
+
+def _bind(name):
+    """The entry point and the places of its pointer arguments (the last one, the stream, apart)."""
+    types = SIGNATURES[name][0]
+    _BOUND[name] = getattr(load(), name), [i for i, t in enumerate(types[:-1]) if t is _P]
+    return _BOUND[name]
+
+
 def _call(name, *args):
-    lib = load()
-    argtypes = SIGNATURES[name][0]
-    conv = []
-    for a, t in zip(args[:-1], argtypes[:-1]):
-        conv.append(_ptr(a) if t is _P else a)
-    conv.append(_stream(args[-1]))
-    _check(getattr(lib, name)(*conv), name)
+    fn, pointers = _BOUND.get(name) or _bind(name)
+    conv = list(args)
+    for i in pointers:
+        conv[i] = _ptr(conv[i])
+    conv[-1] = _stream(conv[-1])
+    status = fn(*conv)
+    if status != MOE_OK:
+        _check(status, name)
 
 
 def moe_version() -> int:

@@ -125,13 +125,13 @@ int moe_linattn_step(const uint16_t* q, const uint16_t* k, const uint16_t* v,
   MOE_REQUIRE(log_decay != nullptr && state != nullptr && B >= 0 && n_slots >= 0, MOE_ERR_ARG);
   MOE_REQUIRE(state_idx != nullptr || B <= n_slots, MOE_ERR_ARG);
   MOE_CHECK(check_heads(Hs, r, Dk, Dv));
-  MOE_REQUIRE(static_cast<long long>(B) * Hs < (1ll << 31), MOE_ERR_ARG);
+  MOE_REQUIRE(static_cast<long long>(B) * Hs < (1ll << 28), MOE_ERR_ARG);
   const long long Hq = static_cast<long long>(Hs) * r;
   MOE_CHECK(check_rows(q, Hq, Dk, ldq));
   MOE_CHECK(check_rows(k, Hs, Dk, ldk));
   MOE_CHECK(check_rows(v, Hs, Dv, ldv));
   MOE_CHECK(check_rows(o, Hq, Dv, ldo));
-  MOE_REQUIRE(aligned(state, 16), MOE_ERR_ALIGN);
+  MOE_REQUIRE(aligned(state, 32), MOE_ERR_ALIGN);
   if (B == 0) return MOE_OK;
   return cuda_status(launch_linattn_step(q, k, v, log_decay, state, state_idx, n_slots, B, Hs, r,
                                          Dk, Dv, ldq, ldk, ldv, ldo, scale, o, err_flag, S(stream)));

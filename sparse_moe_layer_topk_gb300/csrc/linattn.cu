@@ -22,20 +22,40 @@ __device__ __forceinline__ float head_log_decay(const float* log_decay, int h, i
 //
 // S = lam S + k v^T and o = scale S^T q for one token of a row: every state value
 // is read and written once, 8 bytes for 2 + r multiply-adds, so HBM bounds it. A CTA
-// takes `cols` columns of one row's state head (128 threads: cols / 4 float4
-// columns x the state's rows in turn), which cuts a state into up to four pieces
-// when the batch is too small to fill the GPU; the partial sums of o are joined
-// in shared memory in a fixed order.
+// takes COLS columns of one row's state head, a lane 8 columns (32-byte accesses) of Dk / (256 * 8 / COLS)
+// rows, all of whose loads are under way before the first is used; four CTAs an SM hold 128 KB in
+// flight. The partial sums of o over the rows are joined by shuffles and in shared memory, in a fixed
+// order. Where the batch leaves SMs without work, tiles of 32 columns instead of 64.
 constexpr int kStepThreads = 256;
+constexpr int kStepHeads = 4;  // query heads whose partial sums share one exchange
 
-__global__ void __launch_bounds__(kStepThreads)
+__device__ __forceinline__ void ld8(const float* p, float (&v)[8]) {
+  asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+               : "l"(p));
+}
+
+__device__ __forceinline__ void st8(float* p, const float (&v)[8]) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+
+template <int COLS>
+__global__ void __launch_bounds__(kStepThreads, 4)
     linattn_step_kernel(const bf16* q, const bf16* k, const bf16* v, const float* log_decay,
                         float* state, const int* state_idx, int n_slots, int Hs, int r, int Dk,
                         int Dv, long long ldq, long long ldk, long long ldv, long long ldo,
-                        float scale, bf16* o, int* err_flag, int cols) {
-  const int h = blockIdx.x % Hs, b = blockIdx.x / Hs;
-  const int col0 = blockIdx.y * cols;
-  const int nc = min(cols, Dv - col0);  // columns of this CTA, a multiple of 8
+                        float scale, bf16* o, int* err_flag) {
+  constexpr int GROUPS = COLS / 8;               // lanes side by side
+  constexpr int ROWS = kStepThreads / GROUPS;    // rows at a time
+  constexpr int N = 128 / ROWS;                  // rows of a lane
+  constexpr int WARPS = kStepThreads / 32;
+  const int tiles = (Dv + COLS - 1) / COLS;
+  const int tile = blockIdx.x % tiles;
+  const int h = blockIdx.x / tiles % Hs, b = blockIdx.x / tiles / Hs;
+  const int col0 = tile * COLS;
+  const int nc = min(COLS, Dv - col0);  // columns of this CTA, a multiple of 8
   const int tid = threadIdx.x;
   int slot = state_idx ? __ldg(state_idx + b) : b;
   if (slot >= n_slots) {
@@ -48,63 +68,80 @@ __global__ void __launch_bounds__(kStepThreads)
       orow[static_cast<long long>(i / nc) * Dv + i % nc] = __float2bfloat16_rn(0.0f);
     return;
   }
-  const float lam = expf(head_log_decay(log_decay, h, tid == 0 ? err_flag : nullptr));
-  __shared__ float sk[128], sq[128];
-  __shared__ float4 part[kStepThreads];
-  const int groups = cols / 4;            // float4 columns side by side
-  const int rows = kStepThreads / groups;  // rows at a time
-  const int c = tid % groups, row0 = tid / groups;
-  const bool mine = c * 4 < nc;
-  float* const S = state + (static_cast<long long>(slot) * Hs + h) * Dk * Dv + col0 + 4 * c;
-  if (tid < Dk) sk[tid] = __bfloat162float(k[b * ldk + static_cast<long long>(h) * Dk + tid]);
-  float4 vv = make_float4(0, 0, 0, 0);
-  if (mine) {
-    const uint2 w = *reinterpret_cast<const uint2*>(v + b * ldv + static_cast<long long>(h) * Dv + col0 + 4 * c);
-    vv = make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
-  }
-  // at most 16 rows a thread (128 rows, 8 at a time for 128 columns)
-  float4 x[16];
+  const int c = tid % GROUPS, row0 = tid / GROUPS;
+  const bool mine = c * 8 < nc;
+  float* const S = state + (static_cast<long long>(slot) * Hs + h) * Dk * Dv + col0 + 8 * c;
+  float x[N][8];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int row = row0 + i * rows;
-    if (mine && row < Dk) x[i] = *reinterpret_cast<const float4*>(S + static_cast<long long>(row) * Dv);
+  for (int i = 0; i < N; ++i) {
+    const int row = row0 + i * ROWS;
+    if (mine && row < Dk) {
+      ld8(S + row * Dv, x[i]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[i][j] = 0.0f;
+    }
   }
+  __shared__ float sk[128], sq[kStepHeads][128];
+  __shared__ float part[kStepHeads][WARPS][COLS];
+  if (tid < Dk) sk[tid] = __bfloat162float(k[b * ldk + static_cast<long long>(h) * Dk + tid]);
+  float vv[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (mine) {
+    const uint4 w = *reinterpret_cast<const uint4*>(v + b * ldv + static_cast<long long>(h) * Dv + col0 + 8 * c);
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      vv[2 * j] = bf16_lo(u[j]);
+      vv[2 * j + 1] = bf16_hi(u[j]);
+    }
+  }
+  const float lam = expf(head_log_decay(log_decay, h, tid == 0 ? err_flag : nullptr));
+  const bf16* const qrow = q + b * ldq + static_cast<long long>(h) * r * Dk;
+  for (int i = tid; i < min(kStepHeads, r) * Dk; i += kStepThreads) sq[i / Dk][i % Dk] = __bfloat162float(qrow[i]);
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int row = row0 + i * rows;
+  for (int i = 0; i < N; ++i) {
+    const int row = row0 + i * ROWS;
     if (mine && row < Dk) {
       const float kr = sk[row];
-      x[i].x = fmaf(lam, x[i].x, kr * vv.x);
-      x[i].y = fmaf(lam, x[i].y, kr * vv.y);
-      x[i].z = fmaf(lam, x[i].z, kr * vv.z);
-      x[i].w = fmaf(lam, x[i].w, kr * vv.w);
-      *reinterpret_cast<float4*>(S + static_cast<long long>(row) * Dv) = x[i];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[i][j] = fmaf(lam, x[i][j], kr * vv[j]);
+      st8(S + row * Dv, x[i]);
     }
   }
-  for (int a = 0; a < r; ++a) {
-    if (tid < Dk)
-      sq[tid] = __bfloat162float(q[b * ldq + (static_cast<long long>(h) * r + a) * Dk + tid]);
-    __syncthreads();
-    float4 acc = make_float4(0, 0, 0, 0);
+  for (int a0 = 0; a0 < r; a0 += kStepHeads) {
+    const int heads = min(kStepHeads, r - a0);
+    if (a0 > 0) {
+      __syncthreads();
+      for (int i = tid; i < heads * Dk; i += kStepThreads)
+        sq[i / Dk][i % Dk] = __bfloat162float(qrow[static_cast<long long>(a0) * Dk + i]);
+      __syncthreads();
+    }
+    for (int a = 0; a < heads; ++a) {
+      float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int row = row0 + i * rows;
-      if (mine && row < Dk) {
-        const float qr = sq[row];
-        acc.x = fmaf(qr, x[i].x, acc.x);
-        acc.y = fmaf(qr, x[i].y, acc.y);
-        acc.z = fmaf(qr, x[i].z, acc.z);
-        acc.w = fmaf(qr, x[i].w, acc.w);
+      for (int i = 0; i < N; ++i) {
+        const int row = row0 + i * ROWS;
+        const float qr = row < Dk ? sq[a][row] : 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] = fmaf(qr, x[i][j], acc[j]);
+      }
+#pragma unroll
+      for (int d = GROUPS; d < 32; d <<= 1)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] += __shfl_xor_sync(0xFFFFFFFFu, acc[j], d);
+      if ((tid & 31) < GROUPS) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) part[a][tid >> 5][8 * c + j] = acc[j];
       }
     }
-    part[tid] = acc;
     __syncthreads();
-    if (tid < nc) {
+    for (int i = tid; i < heads * nc; i += kStepThreads) {
+      const int a = i / nc, j = i - a * nc;
       float sum = 0.0f;
-      for (int i = 0; i < rows; ++i)
-        sum += reinterpret_cast<const float*>(part)[(i * groups + (tid >> 2)) * 4 + (tid & 3)];
-      orow[static_cast<long long>(a) * Dv + tid] = __float2bfloat16_rn(scale * sum);
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) sum += part[a][w][j];
+      orow[static_cast<long long>(a0 + a) * Dv + j] = __float2bfloat16_rn(scale * sum);
     }
   }
 }
@@ -116,15 +153,15 @@ cudaError_t launch_linattn_step(const void* q, const void* k, const void* v,
                                 int n_slots, int B, int Hs, int r, int Dk, int Dv, long long ldq,
                                 long long ldk, long long ldv, long long ldo, float scale, void* o,
                                 int* err_flag, cudaStream_t st) {
-  int cols = 128;
-  while (cols > 32 && static_cast<long long>(B) * Hs * ((Dv + cols - 1) / cols) < 2ll * num_sms())
-    cols /= 2;
+  const auto tiles = [&](int cols) { return static_cast<unsigned>((Dv + cols - 1) / cols) * B * Hs; };
   LaunchTimer lt("linattn_step", st);
-  const dim3 grid(static_cast<unsigned>(B) * Hs, (Dv + cols - 1) / cols);
-  linattn_step_kernel<<<grid, kStepThreads, 0, st>>>(
-      static_cast<const bf16*>(q), static_cast<const bf16*>(k), static_cast<const bf16*>(v),
-      log_decay, state, state_idx, n_slots, Hs, r, Dk, Dv, ldq, ldk, ldv, ldo, scale,
-      static_cast<bf16*>(o), err_flag, cols);
+  const auto run = [&](auto kernel, unsigned grid) {
+    kernel<<<grid, kStepThreads, 0, st>>>(static_cast<const bf16*>(q), static_cast<const bf16*>(k),
+                                          static_cast<const bf16*>(v), log_decay, state, state_idx, n_slots, Hs, r, Dk,
+                                          Dv, ldq, ldk, ldv, ldo, scale, static_cast<bf16*>(o), err_flag);
+  };
+  if (tiles(64) >= 2u * num_sms()) run(linattn_step_kernel<64>, tiles(64));
+  else run(linattn_step_kernel<32>, tiles(32));
   return cudaGetLastError();
 }
 

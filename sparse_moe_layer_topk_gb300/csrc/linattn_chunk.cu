@@ -25,6 +25,7 @@
 // is added in fp32 registers, not in tensor memory, whose accumulation truncates.
 #include <cuda.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstring>
 
@@ -856,8 +857,15 @@ template <int DK, int DV>
 int launch(const char* name, const Args& a, cudaStream_t st) {
   using F = Cfg<DK, DV>;
   const auto kernel = linattn_chunk_kernel<DK, DV>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, F::SMEM);
+  static std::atomic<bool> ready[64];  // by device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return status(e);
+  if (dev < 0 || dev >= 64 || !ready[dev].load()) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, F::SMEM);
+    if (e != cudaSuccess) return status(e);
+    if (dev >= 0 && dev < 64) ready[dev].store(true);
+  }
   const long long grid = static_cast<long long>(a.nprob) * a.s.N * a.s.Hs * (a.states_only ? a.nseg - 1 : a.nseg);
   if (grid >= (1ll << 31)) return MOE_ERR_ARG;
   {

@@ -59,19 +59,22 @@ class LinearAttention:
 
     def _rows(self, name, x, heads, width):
         """Checks a [T][heads][width] bf16 operand; returns the elements between tokens."""
-        if tuple(x.shape) != (self.T, heads, width) or x.dtype != BF16:
+        if x.shape != (self.T, heads, width) or x.dtype != BF16:
             raise ValueError(f"{name} is bf16 [{self.T}, {heads}, {width}], got {x.dtype} "
                              f"{list(x.shape)}")
-        if x.numel() and (x.stride(2) != 1 or (heads > 1 and x.stride(1) != width)):
+        token, head, value = x.stride()
+        if (value != 1 or (heads > 1 and head != width)) and x.numel():
             raise ValueError(f"{name}: the heads of a token have to be contiguous")
-        return x.stride(0) if self.T > 1 else max(x.stride(0), heads * width)
+        return token if self.T > 1 else max(token, heads * width)
+
+    def _operands(self, q, k, v):
+        return (self._rows("q", q, self.Hs * self.r, self.Dk), self._rows("k", k, self.Hs, self.Dk),
+                self._rows("v", v, self.Hs, self.Dv))
 
     def _state(self, name, x):
-        want = (self.N, self.Hs, self.Dk, self.Dv)
-        if x is not None and (tuple(x.shape) != want or x.dtype != torch.float32
-                              or not x.is_contiguous()):
-            raise ValueError(f"{name} is fp32 {list(want)}, contiguous")
-        return x
+        if x is not None and (x.shape != (self.N, self.Hs, self.Dk, self.Dv)
+                              or x.dtype != torch.float32 or not x.is_contiguous()):
+            raise ValueError(f"{name} is fp32 {[self.N, self.Hs, self.Dk, self.Dv]}, contiguous")
 
     def forward(self, q, k, v, cu_seqlens=None, state_in=None, want_state: bool = False,
                 stream=None):
@@ -79,8 +82,7 @@ class LinearAttention:
         k [T, Hs, Dk], v [T, Hs, Dv]: slices of one projection's rows will do. With
         want_state, state_out holds each sequence's state after its last token."""
         Hq = self.Hs * self.r
-        ld = [self._rows(n, x, h, w) for n, x, h, w in (("q", q, Hq, self.Dk), ("k", k, self.Hs, self.Dk),
-                                                        ("v", v, self.Hs, self.Dv))]
+        ld = self._operands(q, k, v)
         self._state("state_in", state_in)
         self.saved = (q, k, v, cu_seqlens, state_in)
         M.moe_linattn_fwd(q, k, v, self.log_decay, cu_seqlens, state_in, self.N, self.T,
@@ -97,8 +99,7 @@ class LinearAttention:
             raise ValueError("backward needs a forward before it")
         q, k, v, cu_seqlens, state_in = self.saved
         Hs, Hq, Dk, Dv = self.Hs, self.Hs * self.r, self.Dk, self.Dv
-        ld = [self._rows(n, x, h, w) for n, x, h, w in (("dout", dout, Hq, Dv), ("q", q, Hq, Dk),
-                                                        ("k", k, Hs, Dk), ("v", v, Hs, Dv))]
+        ld = [self._rows("dout", dout, Hq, Dv), *self._operands(q, k, v)]
         self._state("d_state_out", d_state_out)
         want = state_in is not None or d_state_out is not None
         M.moe_linattn_bwd(dout, q, k, v, self.log_decay, cu_seqlens, state_in, d_state_out, self.N,
@@ -113,12 +114,11 @@ class LinearAttention:
         place at slot state_idx[row] (int32, negative for an empty row; default: the row) and
         returns o."""
         Hq = self.Hs * self.r
-        ld = [self._rows(n, x, h, w) for n, x, h, w in (("q", q, Hq, self.Dk), ("k", k, self.Hs, self.Dk),
-                                                        ("v", v, self.Hs, self.Dv))]
-        if (state.dim() != 4 or tuple(state.shape[1:]) != (self.Hs, self.Dk, self.Dv)
+        ld = self._operands(q, k, v)
+        if (state.dim() != 4 or state.shape[1:] != (self.Hs, self.Dk, self.Dv)
                 or state.dtype != torch.float32 or not state.is_contiguous()):
             raise ValueError(f"state is fp32 [slots, {self.Hs}, {self.Dk}, {self.Dv}], contiguous")
-        if state_idx is not None and (state_idx.dtype != torch.int32 or tuple(state_idx.shape) != (self.T,)):
+        if state_idx is not None and (state_idx.dtype != torch.int32 or state_idx.shape != (self.T,)):
             raise ValueError(f"state_idx is int32 [{self.T}]")
         M.moe_linattn_step(q, k, v, self.log_decay, state, state_idx, state.shape[0], self.T, self.Hs,
                            self.r, self.Dk, self.Dv, *ld, Hq * self.Dv, self.scale, self.o, self.err,
