@@ -406,7 +406,8 @@ int moe_route_topk_bwd(const float* d_row_w, const int32_t* slot_of, const int32
  * Tensors: q [T][Hq][Dk], k [T][Hs][Dk], v [T][Hs][Dv], o [T][Hq][Dv], bf16; the heads
  * of one token are contiguous and ld* elements lie between tokens (ld* >= heads *
  * width), so q, k and v may be slices of one fused projection's rows. Dk and Dv are
- * multiples of 8 up to 128; ld* are multiples of 8. States are fp32 [N][Hs][Dk][Dv].
+ * multiples of 8 up to 128; ld* are multiples of 8. States are fp32 [N][Hs][Dk][Dv],
+ * 32-byte aligned.
  * Sequences: N of them packed on the token axis; sequence n is the tokens
  * cu_seqlens[n] .. cu_seqlens[n+1]-1 (int32 [N+1], device) and may be empty.
  * max_seqlen is an upper bound of their lengths, known on the host. A sequence
@@ -416,7 +417,7 @@ int moe_route_topk_bwd(const float* d_row_w, const int32_t* slot_of, const int32
  * state_in (nullable: zeros) is each sequence's state before its first token,
  * state_out (nullable) its state after the last; an empty sequence copies one to
  * the other. state_out may be state_in. Sums and states are fp32 throughout.
- * Workspace: moe_workspace_size(MOE_OP_LINATTN_FWD, max_seqlen, Dk, Dv, Hs, r, 0, N). */
+ * Workspace: moe_workspace_size(MOE_OP_LINATTN_FWD, max_seqlen, Dk, Dv, Hs, r, T, N). */
 int moe_linattn_fwd(const uint16_t* q, const uint16_t* k, const uint16_t* v,
                     const float* log_decay, const int32_t* cu_seqlens, const float* state_in,
                     int N, int T, int max_seqlen, int Hs, int r, int Dk, int Dv, int ldq, int ldk,
@@ -431,7 +432,7 @@ int moe_linattn_fwd(const uint16_t* q, const uint16_t* k, const uint16_t* v,
  *   dq_t^(a) = scale * S_t dout_t^(a);  dk_t = R_t v_t;  dv_t = R_t^T k_t;  then X = lam R_t
  * dk and dv are the sums over the r query heads. d_state_in (nullable) is X before the
  * first token; it must not be d_state_out. dq, dk, dv are bf16 with lddq, lddk, lddv elements between
- * tokens. Workspace: moe_workspace_size(MOE_OP_LINATTN_BWD, max_seqlen, Dk, Dv, Hs, r, 0, N). */
+ * tokens. Workspace: moe_workspace_size(MOE_OP_LINATTN_BWD, max_seqlen, Dk, Dv, Hs, r, T, N). */
 int moe_linattn_bwd(const uint16_t* dout, const uint16_t* q, const uint16_t* k, const uint16_t* v,
                     const float* log_decay, const int32_t* cu_seqlens, const float* state_in,
                     const float* d_state_out, int N, int T, int max_seqlen, int Hs, int r, int Dk,

@@ -169,8 +169,8 @@ size_t moe_workspace_size(int op, int T, int d, int l, int E, int k, int f, int 
     case MOE_OP_SHARED_SWIGLU_BWD: return shared_bwd_ws(T, l, f, S);
     case MOE_OP_ROUTE_TOPK_BWD: return up256(static_cast<size_t>(T) * E * 2);
     case MOE_OP_ROUTER_AUX: return up256(static_cast<size_t>(aux_partial_warps(T)) * E * 4);
-    case MOE_OP_LINATTN_FWD: return linattn_workspace(T, d, l, E, S, false);
-    case MOE_OP_LINATTN_BWD: return linattn_workspace(T, d, l, E, S, true);
+    case MOE_OP_LINATTN_FWD: return linattn_workspace(T, d, l, E, k, f, S, false);
+    case MOE_OP_LINATTN_BWD: return linattn_workspace(T, d, l, E, k, f, S, true);
     case MOE_OP_ADAMW_PLAN: return up256(static_cast<size_t>(T) * sizeof(AdamwEntry));
     case MOE_OP_ADAMW_STEP: return up256(static_cast<size_t>(adamw_norm_ctas()) * 8);
     default: return 0;

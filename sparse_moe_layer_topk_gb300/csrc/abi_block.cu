@@ -75,9 +75,9 @@ int moe_linattn_fwd(const uint16_t* q, const uint16_t* k, const uint16_t* v,
   MOE_CHECK(check_rows(k, Hs, Dk, ldk));
   MOE_CHECK(check_rows(v, Hs, Dv, ldv));
   MOE_CHECK(check_rows(o, Hq, Dv, ldo));
-  MOE_REQUIRE(aligned(state_in, 16) && aligned(state_out, 16), MOE_ERR_ALIGN);
+  MOE_REQUIRE(aligned(state_in, 32) && aligned(state_out, 32), MOE_ERR_ALIGN);
   if (N == 0) return MOE_OK;
-  const size_t need = moe_workspace_size(MOE_OP_LINATTN_FWD, max_seqlen, Dk, Dv, Hs, r, 0, N);
+  const size_t need = moe_workspace_size(MOE_OP_LINATTN_FWD, max_seqlen, Dk, Dv, Hs, r, T, N);
   MOE_REQUIRE(need == 0 || (ws != nullptr && ws_bytes >= need), MOE_ERR_WORKSPACE);
   const LinShape s{cu_seqlens, log_decay, N, T, max_seqlen, Hs, err_flag};
   const LinProblem p{q, k, v, ldq, ldk, ldv, ldo, o, r, 1, Dk, Dv, 0, 1.0f, scale, state_in, state_out, Dv, 1, -1};
@@ -103,10 +103,10 @@ int moe_linattn_bwd(const uint16_t* dout, const uint16_t* q, const uint16_t* k, 
   MOE_CHECK(check_rows(dv, Hs, Dv, lddv));
   // dk's recurrence reads d_state_out while dv's writes d_state_in
   MOE_REQUIRE(d_state_in == nullptr || d_state_in != d_state_out, MOE_ERR_ARG);
-  MOE_REQUIRE(aligned(state_in, 16) && aligned(d_state_out, 16) && aligned(d_state_in, 16),
+  MOE_REQUIRE(aligned(state_in, 32) && aligned(d_state_out, 32) && aligned(d_state_in, 32),
               MOE_ERR_ALIGN);
   if (N == 0) return MOE_OK;
-  const size_t need = moe_workspace_size(MOE_OP_LINATTN_BWD, max_seqlen, Dk, Dv, Hs, r, 0, N);
+  const size_t need = moe_workspace_size(MOE_OP_LINATTN_BWD, max_seqlen, Dk, Dv, Hs, r, T, N);
   MOE_REQUIRE(need == 0 || (ws != nullptr && ws_bytes >= need), MOE_ERR_WORKSPACE);
   const LinShape s{cu_seqlens, log_decay, N, T, max_seqlen, Hs, err_flag};
   // dq_t = scale S_t dout_t: the forward's recurrence with k and v exchanged

@@ -558,6 +558,20 @@ __device__ __forceinline__ uint32_t pack_bf16(f32x2 x) {
   return pack_bf16(a, b);
 }
 
+// Eight fp32 values in one 32-byte access.
+__device__ __forceinline__ void load_f32x8(const float* p, float (&v)[8]) {
+  asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+                 "=f"(v[7])
+               : "l"(p));
+}
+
+__device__ __forceinline__ void store_f32x8(float* p, const float (&v)[8]) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]),
+               "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+
 // ---------------------------------------------------------------- FP8 (E4M3)
 
 // Two fp32 values -> an E4M3 pair (round to nearest even, saturating at

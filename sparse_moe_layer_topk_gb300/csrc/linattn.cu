@@ -29,18 +29,6 @@ __device__ __forceinline__ float head_log_decay(const float* log_decay, int h, i
 constexpr int kStepThreads = 256;
 constexpr int kStepHeads = 4;  // query heads whose partial sums share one exchange
 
-__device__ __forceinline__ void ld8(const float* p, float (&v)[8]) {
-  asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
-               : "l"(p));
-}
-
-__device__ __forceinline__ void st8(float* p, const float (&v)[8]) {
-  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
-               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
-               : "memory");
-}
-
 template <int COLS>
 __global__ void __launch_bounds__(kStepThreads, 4)
     linattn_step_kernel(const bf16* q, const bf16* k, const bf16* v, const float* log_decay,
@@ -76,7 +64,7 @@ __global__ void __launch_bounds__(kStepThreads, 4)
   for (int i = 0; i < N; ++i) {
     const int row = row0 + i * ROWS;
     if (mine && row < Dk) {
-      ld8(S + row * Dv, x[i]);
+      load_f32x8(S + row * Dv, x[i]);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[i][j] = 0.0f;
@@ -106,7 +94,7 @@ __global__ void __launch_bounds__(kStepThreads, 4)
       const float kr = sk[row];
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[i][j] = fmaf(lam, x[i][j], kr * vv[j]);
-      st8(S + row * Dv, x[i]);
+      store_f32x8(S + row * Dv, x[i]);
     }
   }
   for (int a0 = 0; a0 < r; a0 += kStepHeads) {

@@ -48,7 +48,7 @@ __device__ __forceinline__ void lin_sequence(const LinShape& s, int n, int& star
 
 // Runs np (1 to 3) recurrences over the same sequences. ws: linattn_workspace bytes (device); an MOE_*
 // status.
-size_t linattn_workspace(int max_seqlen, int Dk, int Dv, int Hs, int N, bool backward);
+size_t linattn_workspace(int max_seqlen, int Dk, int Dv, int Hs, int r, int T, int N, bool backward);
 int linattn_run(const LinProblem* p, int np, const LinShape& s, void* ws, cudaStream_t st);
 
 cudaError_t launch_linattn_step(const void* q, const void* k, const void* v,

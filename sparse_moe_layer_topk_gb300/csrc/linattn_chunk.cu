@@ -25,6 +25,7 @@
 // is added in fp32 registers, not in tensor memory, whose accumulation truncates.
 #include <cuda.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstring>
@@ -214,7 +215,20 @@ __device__ __forceinline__ void decay_keys(uint8_t* tk, uint8_t* tq, const float
   }
 }
 
-template <int DK, int DV>
+// Rows of a v tile past the chunk's n tokens are another sequence's, possibly NaN: zeros (256 threads).
+template <int DV>
+__device__ __forceinline__ void clear_values(uint8_t* tv, int n, int tid) {
+#pragma unroll 1
+  for (int x = n * 8 + tid; x < C * 8; x += 256) {
+#pragma unroll
+    for (int c = 0; c < DV / 64; ++c) *reinterpret_cast<uint4*>(tv + c * C * 128 + x * 16) = make_uint4(0, 0, 0, 0);
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
+// SO: the states alone (the segments' own sums).
+template <int DK, int DV, bool SO>
 __global__ void __launch_bounds__(kThreads, 1)
     linattn_chunk_kernel(const __grid_constant__ Args a) {
   using F = Cfg<DK, DV>;
@@ -259,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(p_ready, kScoreWarps);
     mbar_init(o_full, 1);
     mbar_init(o_empty, kScoreWarps);
-    mbar_init(k_ready, a.states_only ? kStateWarps : kStateWarps + kScoreWarps);
+    mbar_init(k_ready, SO ? kScoreWarps : kStateWarps + kScoreWarps);
     mbar_init(z_full, 1);
     mbar_init(s_ready, kStateWarps);
     mbar_init(v_clean, kStateWarps);
@@ -297,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
 
   // Items: the group's query heads (or key / value heads) of each chunk in turn.
-  const bool so = a.states_only != 0;
+  constexpr bool so = SO;
   const int group = so ? p.nkv : max(p.nq, p.nkv);
   const bool many_q = group > 1 && p.nq > 1;
   const int items = (w.c1 - w.c0) * group;
@@ -511,6 +525,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x - 128;
     uint32_t n_o = 0;
     Ring r;
+    if (so) {
+      // the segments' own sums: these warps prepare the keys, the state warps sum
+      uint32_t n_k = 0;
+      for (Item it(w, group); it.i < items; it.next()) {
+        int tok, n;
+        chunk_at(w, p.rev, it.c, tok, n);
+        const Ring rq = r;
+        r.next(F::SLOTS);
+        const Ring rk = r;
+        r.next(F::SLOTS);
+        const Ring rv = r;
+        r.next(F::SLOTS);
+        bool ok = mbar_wait_short(&full[rk.slot], rk.phase);
+        if (ok && n < C) {
+          ok = mbar_wait_short(&full[rv.slot], rv.phase);
+          clear_values<DV>(smem + rv.slot * F::SLOT, n, tid);
+          if (lane == 0) mbar_arrive(v_clean);
+        }
+        if (ok) decay_keys<DK>(smem + rk.slot * F::SLOT, smem + rq.slot * F::SLOT, power_of, p.rev, n, tid, 0, 4);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (ok && n_k > 0) ok = mbar_wait_short(z_full, (n_k - 1) & 1);  // (no more than one set ahead)
+        if (!ok) {
+          fail();
+          break;
+        }
+        if (lane == 0) mbar_arrive(k_ready);
+        ++n_k;
+      }
+    }
     for (Item it(w, group); it.i < items && !so; it.next()) {
       const int i = it.i, sub = it.sub;
       int tok, n;
@@ -674,12 +718,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     {
       const float* in = so ? nullptr : seg ? seg : p.s_in ? p.s_in + state : nullptr;
       const int sr = seg ? pr.seg_row : p.s_row, sc = seg ? pr.seg_col : p.s_col;
-      const auto at = [&](int c) {
-        return in && mine && row < p.dk && c < p.dv
-                   ? in[static_cast<long long>(row) * sr + static_cast<long long>(c) * sc] : 0.0f;
-      };
+      const float* const at = in + static_cast<long long>(row) * sr;
+      const bool have = in && mine && row < p.dk;
+      if (sc == 1) {
 #pragma unroll
-      for (int j = 0; j < NC / 2; ++j) S[j] = pack2(at(half * NC + 2 * j), at(half * NC + 2 * j + 1));
+        for (int j = 0; j < NC / 8; ++j) {
+          float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+          const int c = half * NC + 8 * j;
+          if (have && c < p.dv) load_f32x8(at + c, x);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) S[4 * j + e] = pack2(x[2 * e], x[2 * e + 1]);
+        }
+      } else {  // (transposed: the lanes' values are neighbours)
+#pragma unroll
+        for (int j = 0; j < NC / 2; ++j) {
+          const int c = half * NC + 2 * j;
+          const bool real = have && c < p.dv;
+          S[j] = pack2(real ? at[static_cast<long long>(c) * sc] : 0.0f, real ? at[static_cast<long long>(c + 1) * sc] : 0.0f);
+        }
+      }
     }
     // row `row` of the K x N operand of QS, 64 columns to a 128-byte line: columns c .. c + 7
     const auto copy8 = [&](int j) {
@@ -701,8 +758,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(s_ready);
     };
+    if (!so) {
 #pragma unroll
-    for (int j = 0; j < NC / 8; ++j) copy8(j);
+      for (int j = 0; j < NC / 8; ++j) copy8(j);
+    }
     copied();
     float hi = 0.0f, lo = 0.0f;
     int n_was = -1;
@@ -719,21 +778,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       r.next(F::SLOTS);
       const Ring rv = r;
       r.next(F::SLOTS);
-      if (n < C) {
-        // rows of v past the chunk's tokens are another sequence's, possibly NaN
+      if (n < C && !so) {
         if (!mbar_wait_short(&full[rv.slot], rv.phase)) {
           fail();
           break;
         }
-        uint8_t* const tv = smem + rv.slot * F::SLOT;
-#pragma unroll 1
-        for (int x = n * 8 + tid; x < C * 8; x += 32 * kStateWarps) {
-#pragma unroll
-          for (int c = 0; c < DV / 64; ++c)
-            *reinterpret_cast<uint4*>(tv + c * C * 128 + x * 16) = make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
+        clear_values<DV>(smem + rv.slot * F::SLOT, n, tid);
         if (lane == 0) mbar_arrive(v_clean);
       }
       // QS has read the q tile (and QK^T the keys): both may be overwritten. (Every item's phase is
@@ -747,18 +797,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         n_was = n;
         power2(g, n, hi, lo);
       }
-      if (!mbar_wait_short(&full[rk.slot], rk.phase)) {
-        fail();
-        break;
+      if (!so) {
+        if (!mbar_wait_short(&full[rk.slot], rk.phase)) {
+          fail();
+          break;
+        }
+        decay_keys<DK>(smem + rk.slot * F::SLOT, smem + rq.slot * F::SLOT, power_of, p.rev, n, tid, 0, 2);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(k_ready);
       }
-      decay_keys<DK>(smem + rk.slot * F::SLOT, smem + rq.slot * F::SLOT, power_of, p.rev, n, tid, 0, so ? 4 : 2);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (so && n_k > 0 && !mbar_wait_short(z_full, (n_k - 1) & 1)) {  // (no more than one set ahead)
-        fail();
-        break;
-      }
-      if (lane == 0) mbar_arrive(k_ready);
       if (!mbar_wait_short(z_full, n_k & 1)) {
         fail();
         break;
@@ -784,24 +832,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           s = fma2(hi2, s, fma2(lo2, s, mul2(upd, pack2(__uint_as_float(z[0]), __uint_as_float(z[1])))));
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) copy8(4 * cb + j);
+        for (int j = 0; j < 4; ++j)
+          if (!so) copy8(4 * cb + j);
       }
       copied();
     }
     if (so || (w.last && p.s_out)) {
       // the segment's own sum goes where the scan turns it into the next one's start
-      float* const out = so ? seg + static_cast<long long>(p.dk) * p.dv : p.s_out + state;
-      const int sr = so ? p.dv : p.s_row, sc = so ? 1 : p.s_col;
-      const auto put = [&](int c, float x) {
-        if (mine && row < p.dk && c < p.dv)
-          out[static_cast<long long>(row) * sr + static_cast<long long>(c) * sc] = x;
-      };
+      // (a call's state_out is never transposed)
+      float* const out = (so ? seg + static_cast<long long>(p.dk) * p.dv : p.s_out + state) + static_cast<long long>(row) * p.dv;
 #pragma unroll
-      for (int j = 0; j < NC / 2; ++j) {
-        float x, y;
-        unpack2(S[j], x, y);
-        put(half * NC + 2 * j, x);
-        put(half * NC + 2 * j + 1, y);
+      for (int j = 0; j < NC / 8; ++j) {
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) unpack2(S[4 * j + e], x[2 * e], x[2 * e + 1]);
+        const int c = half * NC + 8 * j;
+        if (mine && row < p.dk && c < p.dv) store_f32x8(out + c, x);
       }
     }
   }
@@ -818,7 +864,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // The states at the segments' starts from their own sums (written by a states_only launch one slot
 // further): slot 0 is the sequence's first state, slot s + 1 = lam^(tokens of s) slot s + the sum of s.
-__global__ void __launch_bounds__(256) segment_scan_kernel(LinProblem p, LinShape s, float* seg, int nseg, int seg_chunks) {
+__global__ void __launch_bounds__(128) segment_scan_kernel(LinProblem p, LinShape s, float* seg, int nseg, int seg_chunks) {
   const int h = blockIdx.x % s.Hs, n = blockIdx.x / s.Hs;
   int start, len;
   lin_sequence(s, n, start, len);
@@ -828,19 +874,35 @@ __global__ void __launch_bounds__(256) segment_scan_kernel(LinProblem p, LinShap
   const float g = fminf(__ldg(s.log_decay + h), 0.0f);
   const int size = p.dk * p.dv;
   const long long base = static_cast<long long>(n) * s.Hs + h;
-  float* const out = seg + base * nseg * size;
   // (a reverse recurrence starts with the sequence's last, short chunk)
   float hi0, lo0, hi, lo;
   power2(g, p.rev ? len - (chunks - seg_chunks) * C : seg_chunks * C, hi0, lo0);
   power2(g, seg_chunks * C, hi, lo);
-  for (int e = blockIdx.y * blockDim.x + threadIdx.x; e < size; e += gridDim.y * blockDim.x) {
+  const int e = (blockIdx.y * blockDim.x + threadIdx.x) * 8;  // eight values of one row
+  if (e >= size) return;
+  float* const out = seg + base * nseg * size + e;
+  float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (p.s_in) {
+    const float* const in = p.s_in + base * size;
     const int i = e / p.dv, j = e - i * p.dv;
-    float x = p.s_in ? p.s_in[base * size + static_cast<long long>(i) * p.s_row + static_cast<long long>(j) * p.s_col] : 0.0f;
-    out[e] = x;
-    for (int k = 1; k < used; ++k) {
-      float& y = out[static_cast<long long>(k) * size + e];
-      x = k == 1 ? fmaf(hi0, x, fmaf(lo0, x, y)) : fmaf(hi, x, fmaf(lo, x, y));
-      y = x;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) x[u] = in[static_cast<long long>(i) * p.s_row + static_cast<long long>(j + u) * p.s_col];
+  }
+  store_f32x8(out, x);
+  constexpr int AHEAD = 4;  // slots read at a time
+  for (int k0 = 1; k0 < used; k0 += AHEAD) {
+    float y[AHEAD][8];
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u)
+      if (k0 + u < used) load_f32x8(out + static_cast<long long>(k0 + u) * size, y[u]);
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) {
+      if (k0 + u >= used) continue;
+      const bool first = k0 + u == 1;
+#pragma unroll
+      for (int v = 0; v < 8; ++v)
+        x[v] = first ? fmaf(hi0, x[v], fmaf(lo0, x[v], y[u][v])) : fmaf(hi, x[v], fmaf(lo, x[v], y[u][v]));
+      store_f32x8(out + static_cast<long long>(k0 + u) * size, x);
     }
   }
 }
@@ -853,10 +915,10 @@ int status(cudaError_t e) {
   return MOE_ERR_CUDA;
 }
 
-template <int DK, int DV>
+template <int DK, int DV, bool SO>
 int launch(const char* name, const Args& a, cudaStream_t st) {
   using F = Cfg<DK, DV>;
-  const auto kernel = linattn_chunk_kernel<DK, DV>;
+  const auto kernel = linattn_chunk_kernel<DK, DV, SO>;
   static std::atomic<bool> ready[64];  // by device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -887,30 +949,40 @@ int launch_problems(const char* name, const Problem* const* probs, int np, const
   a.seg_chunks = seg_chunks;
   a.states_only = states_only ? 1 : 0;
   const bool k64 = a.prob[0].p.dk <= 64, v64 = a.prob[0].p.dv <= 64;
-  if (k64 && v64) return launch<64, 64>(name, a, st);
-  if (k64) return launch<64, 128>(name, a, st);
-  if (v64) return launch<128, 64>(name, a, st);
-  return launch<128, 128>(name, a, st);
+  if (k64 && v64) return states_only ? launch<64, 64, true>(name, a, st) : launch<64, 64, false>(name, a, st);
+  if (k64) return states_only ? launch<64, 128, true>(name, a, st) : launch<64, 128, false>(name, a, st);
+  if (v64) return states_only ? launch<128, 64, true>(name, a, st) : launch<128, 64, false>(name, a, st);
+  return states_only ? launch<128, 128, true>(name, a, st) : launch<128, 128, false>(name, a, st);
 }
 
 struct Split {
   int nseg, seg_chunks;
 };
 
-// Segments of the time axis for `units` recurrences of at most `chunks` chunks. A CTA takes about 4 us a
-// chunk, 2 us where it sums the state alone, and the two more launches 8 us (measured at widths of 128):
-// the split with the shortest estimate of rounds over the SMs is taken. At 32 heads of 32,768 tokens
-// one segment took 1,036 us and the split 334.
-Split split(long long units, int chunks) {
+// Segments of the time axis. Estimated from what was measured (us, widths of 128): a CTA takes 6 and
+// 3.4 a chunk and head of its group, one that sums the state alone 5 and 2, one that finds nothing to do
+// 1; the scan moves every segment's state twice at 5 GB a ms; two more launches 8. Each is a round over the
+// SMs. The ragged sequences' segments are counted from the tokens alone, for their lengths are on the
+// device. The split with the shortest estimate is taken: at 32 heads of 32,768 tokens one segment took
+// 1,036 us and the split 371; at 4 x 4,096 tokens of 32 heads, backward, one segment is best.
+Split split(int N, int T, int max_seqlen, int Hs, int np, int group, int Dk, int Dv) {
+  const int chunks = (max_seqlen + C - 1) / C;
   Split best{1, chunks > 0 ? chunks : 1};
-  const long long sms = num_sms();
-  const auto rounds = [&](long long ctas) { return static_cast<double>((ctas + sms - 1) / sms); };
-  double least = 4.0 * chunks * rounds(units);
-  for (int n = 2; n <= 64 && n <= chunks && units * n <= 8 * sms; ++n) {
+  const double sms = num_sms(), heads = static_cast<double>(Hs) * np;
+  const double chunk = Dk <= 64 && Dv <= 64 ? 2.7 : 3.4;
+  const auto rounds = [&](double ctas) { return std::ceil(ctas / sms); };
+  double least = 0.0;
+  for (int n = 1; n <= 64 && n <= chunks && (n == 1 || heads * N * n <= 16 * sms); ++n) {
     const int per = (chunks + n - 1) / n;
     const int used = (chunks + per - 1) / per;
-    const double t = 4.0 * per * rounds(units * used) + 2.0 * per * rounds(units * (used - 1)) + 8.0;
-    if (t < least) {
+    if (used != n) continue;
+    const double all = heads * N * used;
+    const double busy = std::min(all, heads * (static_cast<double>(T) / (per * C) + N));
+    double t = rounds(busy) * (6.0 + chunk * per * group) + (all - busy) / sms;
+    if (n > 1)
+      t += rounds(busy * (used - 1) / used) * (5.0 + 2.0 * per * group) + (all - busy) / sms +
+           busy * Dk * Dv * 8.0 / 5.0e6 + 8.0;
+    if (n == 1 || t < least) {
       least = t;
       best = Split{used, per};
     }
@@ -924,9 +996,10 @@ size_t slots_bytes(const LinShape& s, const Split& sp, int dk, int dv) {
 
 }  // namespace
 
-size_t linattn_workspace(int max_seqlen, int Dk, int Dv, int Hs, int N, bool backward) {
+size_t linattn_workspace(int max_seqlen, int Dk, int Dv, int Hs, int r, int T, int N, bool backward) {
   if (max_seqlen <= 0 || N <= 0 || Hs <= 0 || Dk <= 0 || Dv <= 0) return 0;
-  const Split sp = split(static_cast<long long>(backward ? 3 : 1) * N * Hs, (max_seqlen + C - 1) / C);
+  if (T <= 0) T = static_cast<int>(std::min(static_cast<long long>(N) * max_seqlen, 0x7FFFFFFFll));
+  const Split sp = split(N, T, max_seqlen, Hs, backward ? 3 : 1, r, Dk, Dv);
   if (sp.nseg == 1) return 0;
   LinShape s{};
   s.N = N;
@@ -935,7 +1008,7 @@ size_t linattn_workspace(int max_seqlen, int Dk, int Dv, int Hs, int N, bool bac
 }
 
 int linattn_run(const LinProblem* p, int np, const LinShape& s, void* ws, cudaStream_t st) {
-  const Split sp = split(static_cast<long long>(np) * s.N * s.Hs, (s.max_seqlen + C - 1) / C);
+  const Split sp = split(s.N, s.T, s.max_seqlen, s.Hs, np, std::max(p[0].nq, p[0].nkv), p[0].dk, p[0].dv);
   Problem prob[3];
   const long long T = s.T > 0 ? s.T : 1;
   float* slots = static_cast<float*>(ws);
@@ -986,8 +1059,8 @@ int linattn_run(const LinProblem* p, int np, const LinShape& s, void* ws, cudaSt
       for (int i = 0; i < np; ++i) {
         if (p[i].shares >= 0) continue;
         LaunchTimer lt("linattn_scan", st);
-        const dim3 grid(static_cast<unsigned>(s.N) * s.Hs, (p[i].dk * p[i].dv + 2047) / 2048);
-        segment_scan_kernel<<<grid, 256, 0, st>>>(p[i], s, prob[i].seg, sp.nseg, sp.seg_chunks);
+        const dim3 grid(static_cast<unsigned>(s.N) * s.Hs, (p[i].dk * p[i].dv + 1023) / 1024);
+        segment_scan_kernel<<<grid, 128, 0, st>>>(p[i], s, prob[i].seg, sp.nseg, sp.seg_chunks);
         const int e = status(cudaGetLastError());
         if (e != MOE_OK) return e;
       }

@@ -91,9 +91,7 @@ __device__ __forceinline__ void store8_f32(char* at, int n, bool whole, const f3
 #pragma unroll
   for (int i = 0; i < 4; ++i) unpack2(x[i], v[2 * i], v[2 * i + 1]);
   if (whole) {
-    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]),
-                 "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
-                 : "memory");
+    store_f32x8(p, v);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)

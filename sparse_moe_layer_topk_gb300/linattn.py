@@ -38,7 +38,7 @@ class LinearAttention:
         if backward:
             self.dq, self.dk, self.dv = e(T, Hq, Dk), e(T, self.Hs, Dk), e(T, self.Hs, Dv)
         self._d_state_in = None
-        dims = dict(T=self.max_seqlen, d=Dk, l=Dv, E=self.Hs, k=r, S=N)
+        dims = dict(T=self.max_seqlen, d=Dk, l=Dv, E=self.Hs, k=r, f=T, S=N)
         self.ws_bytes = max(M.moe_workspace_size(M.MOE_OP_LINATTN_FWD, **dims),
                             M.moe_workspace_size(M.MOE_OP_LINATTN_BWD, **dims) if backward else 0)
         self.ws = torch.empty(max(self.ws_bytes, 256), dtype=torch.uint8, device=dev)
