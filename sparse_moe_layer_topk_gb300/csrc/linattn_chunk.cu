@@ -227,14 +227,10 @@ __device__ __forceinline__ void clear_values(uint8_t* tv, int n, int tid) {
   __syncwarp();
 }
 
-// SO: the states alone (the segments' own sums).
+// A CTA's chunks. SO: the states alone (the segments' own sums).
 template <int DK, int DV, bool SO>
-__global__ void __launch_bounds__(kThreads, 1)
-    linattn_chunk_kernel(const __grid_constant__ Args a) {
+__device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t* smem_raw) {
   using F = Cfg<DK, DV>;
-  extern __shared__ uint8_t smem_raw[];
-  Work w;
-  if (!find_work(a, w)) return;
   const LinProblem& p = a.prob[w.prob].p;
 
   uint8_t* const smem = reinterpret_cast<uint8_t*>(
@@ -860,6 +856,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// Width classes of keys and values, the smaller first: one kernel runs the forward's and the
+// backward's problems, half of which have keys and values exchanged.
+template <int D0, int D1, bool SO>
+__global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid_constant__ Args a) {
+  extern __shared__ uint8_t smem_raw[];
+  Work w;
+  if (!find_work(a, w)) return;
+  if (D0 == D1 || a.prob[w.prob].p.dk <= 64) run_chunks<D0, D1, SO>(a, w, smem_raw);
+  else run_chunks<D1, D0, SO>(a, w, smem_raw);
+}
+
 // ------------------------------------------------------------------ segments
 
 // The states at the segments' starts from their own sums (written by a states_only launch one slot
@@ -915,44 +922,34 @@ int status(cudaError_t e) {
   return MOE_ERR_CUDA;
 }
 
-template <int DK, int DV, bool SO>
+template <int D0, int D1, bool SO>
 int launch(const char* name, const Args& a, cudaStream_t st) {
-  using F = Cfg<DK, DV>;
-  const auto kernel = linattn_chunk_kernel<DK, DV, SO>;
+  constexpr int SMEM = std::max(Cfg<D0, D1>::SMEM, Cfg<D1, D0>::SMEM);
+  const auto kernel = linattn_chunk_kernel<D0, D1, SO>;
   static std::atomic<bool> ready[64];  // by device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return status(e);
   if (dev < 0 || dev >= 64 || !ready[dev].load()) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, F::SMEM);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e != cudaSuccess) return status(e);
     if (dev >= 0 && dev < 64) ready[dev].store(true);
   }
-  const long long grid = static_cast<long long>(a.nprob) * a.s.N * a.s.Hs * (a.states_only ? a.nseg - 1 : a.nseg);
+  const long long grid = static_cast<long long>(a.nprob) * a.s.N * a.s.Hs * (SO ? a.nseg - 1 : a.nseg);
   if (grid >= (1ll << 31)) return MOE_ERR_ARG;
   {
     LaunchTimer lt(name, st);
-    kernel<<<static_cast<unsigned>(grid), kThreads, F::SMEM, st>>>(a);
+    kernel<<<static_cast<unsigned>(grid), kThreads, SMEM, st>>>(a);
   }
   return status(cudaGetLastError());
 }
 
-// One launch over problems of one width class.
-int launch_problems(const char* name, const Problem* const* probs, int np, const LinShape& s, int nseg,
-                    int seg_chunks, bool states_only, cudaStream_t st) {
-  Args a;
-  std::memset(static_cast<void*>(&a), 0, sizeof a);
-  for (int i = 0; i < np; ++i) a.prob[i] = *probs[i];
-  a.s = s;
-  a.nprob = np;
-  a.nseg = nseg;
-  a.seg_chunks = seg_chunks;
-  a.states_only = states_only ? 1 : 0;
+template <bool SO>
+int launch_widths(const char* name, const Args& a, cudaStream_t st) {
   const bool k64 = a.prob[0].p.dk <= 64, v64 = a.prob[0].p.dv <= 64;
-  if (k64 && v64) return states_only ? launch<64, 64, true>(name, a, st) : launch<64, 64, false>(name, a, st);
-  if (k64) return states_only ? launch<64, 128, true>(name, a, st) : launch<64, 128, false>(name, a, st);
-  if (v64) return states_only ? launch<128, 64, true>(name, a, st) : launch<128, 64, false>(name, a, st);
-  return states_only ? launch<128, 128, true>(name, a, st) : launch<128, 128, false>(name, a, st);
+  if (k64 && v64) return launch<64, 64, SO>(name, a, st);
+  if (k64 != v64) return launch<64, 128, SO>(name, a, st);
+  return launch<128, 128, SO>(name, a, st);
 }
 
 struct Split {
@@ -1009,12 +1006,16 @@ size_t linattn_workspace(int max_seqlen, int Dk, int Dv, int Hs, int r, int T, i
 
 int linattn_run(const LinProblem* p, int np, const LinShape& s, void* ws, cudaStream_t st) {
   const Split sp = split(s.N, s.T, s.max_seqlen, s.Hs, np, std::max(p[0].nq, p[0].nkv), p[0].dk, p[0].dv);
-  Problem prob[3];
+  Args a;
+  std::memset(static_cast<void*>(&a), 0, sizeof a);
+  a.s = s;
+  a.nprob = np;
+  a.nseg = sp.nseg;
+  a.seg_chunks = sp.seg_chunks;
   const long long T = s.T > 0 ? s.T : 1;
   float* slots = static_cast<float*>(ws);
   for (int i = 0; i < np; ++i) {
-    Problem& x = prob[i];
-    std::memset(static_cast<void*>(&x), 0, sizeof x);
+    Problem& x = a.prob[i];
     x.p = p[i];
     const long long hq = static_cast<long long>(s.Hs) * p[i].nq, hk = static_cast<long long>(s.Hs) * p[i].nkv;
     if (!make_rows_map(&x.q, p[i].q, p[i].dk, T, hq, p[i].ldq, p[i].dk, C) ||
@@ -1029,44 +1030,27 @@ int linattn_run(const LinProblem* p, int np, const LinShape& s, void* ws, cudaSt
         x.seg_col = 1;
         slots += slots_bytes(s, sp, p[i].dk, p[i].dv) / 4;
       } else {  // the transposed states of another problem
-        x.seg = prob[p[i].shares].seg;
+        x.seg = a.prob[p[i].shares].seg;
         x.seg_row = 1;
         x.seg_col = p[i].dk;
       }
     }
   }
-  // problems of one width class run in one launch
-  const auto same = [&](int i, int j) {
-    return (p[i].dk <= 64) == (p[j].dk <= 64) && (p[i].dv <= 64) == (p[j].dv <= 64);
-  };
-  for (int pass = sp.nseg > 1 ? 0 : 1; pass < 2; ++pass) {
-    bool done[3] = {false, false, false};
-    for (int i = 0; i < np; ++i) {
-      if (done[i]) continue;
-      const Problem* some[3];
-      int n = 0;
-      for (int j = i; j < np; ++j) {
-        if (done[j] || !same(i, j)) continue;
-        done[j] = true;
-        if (pass == 1 || p[j].shares < 0) some[n++] = &prob[j];
-      }
-      if (n == 0) continue;
-      const int e = launch_problems(pass == 0 ? "linattn_segments" : np == 1 ? "linattn_fwd" : "linattn_bwd", some, n, s,
-                                    sp.nseg, sp.seg_chunks, pass == 0, st);
-      if (e != MOE_OK) return e;
-    }
-    if (pass == 0) {
-      for (int i = 0; i < np; ++i) {
-        if (p[i].shares >= 0) continue;
-        LaunchTimer lt("linattn_scan", st);
-        const dim3 grid(static_cast<unsigned>(s.N) * s.Hs, (p[i].dk * p[i].dv + 1023) / 1024);
-        segment_scan_kernel<<<grid, 128, 0, st>>>(p[i], s, prob[i].seg, sp.nseg, sp.seg_chunks);
-        const int e = status(cudaGetLastError());
-        if (e != MOE_OK) return e;
-      }
+  if (sp.nseg > 1) {
+    Args own = a;  // (the problems with states of their own come first)
+    own.states_only = 1;
+    while (p[own.nprob - 1].shares >= 0) --own.nprob;
+    const int e = launch_widths<true>("linattn_segments", own, st);
+    if (e != MOE_OK) return e;
+    for (int i = 0; i < own.nprob; ++i) {
+      LaunchTimer lt("linattn_scan", st);
+      const dim3 grid(static_cast<unsigned>(s.N) * s.Hs, (p[i].dk * p[i].dv + 1023) / 1024);
+      segment_scan_kernel<<<grid, 128, 0, st>>>(p[i], s, a.prob[i].seg, sp.nseg, sp.seg_chunks);
+      const int se = status(cudaGetLastError());
+      if (se != MOE_OK) return se;
     }
   }
-  return MOE_OK;
+  return launch_widths<false>(np == 1 ? "linattn_fwd" : "linattn_bwd", a, st);
 }
 
 }  // namespace moe
