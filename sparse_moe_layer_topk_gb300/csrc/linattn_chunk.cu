@@ -236,20 +236,22 @@ __device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t
   uint8_t* const smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* const copy = smem + F::SLOTS * F::SLOT;  // the state in bf16
+  // A wait tells a phase from the next one alone, so no barrier may complete twice before each of its
+  // waiters has returned: every phase is waited for, and the next one needs an arrival made after that.
   uint64_t* const full = reinterpret_cast<uint64_t*>(copy + F::TERMS * F::COPY);
   uint64_t* const empty = full + F::SLOTS;
   uint64_t* const p_full = empty + F::SLOTS;   // QK^T done
-  uint64_t* const qs_done = p_full + 1;        // QS done: the q tile may be overwritten
+  // QS done: the q tile may be overwritten (with each set of keys; states alone: a set has entered)
+  uint64_t* const qs_done = p_full + 1;
   uint64_t* const p_ready = p_full + 2;        // P back in tensor memory
   uint64_t* const o_full = p_full + 3;
   uint64_t* const o_empty = p_full + 4;
   uint64_t* const k_ready = p_full + 5;        // decayed keys written
-  uint64_t* const z_full = p_full + 6;
+  uint64_t* const z_full = p_full + 6;         // the chunk's sum of keys and values
   uint64_t* const s_ready = p_full + 7;        // the state's copy written, Z read
-  uint64_t* const v_clean = p_full + 8;        // a short chunk's v rows of other sequences cleared
-  uint64_t* const o_gone = p_full + 9;         // the output has left its staging place
-  uint64_t* const drain = p_full + 10;
-  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(p_full + 11);
+  uint64_t* const o_gone = p_full + 8;         // the output has left its staging place
+  uint64_t* const drain = p_full + 9;
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(p_full + 10);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   // factor[128 + j - i] is L_ij, zero outside the mask; power_of[m] = lam^m, 0 <= m <= 128;
   // falling[m] = lam^(15-m), 0 <= m < 16
@@ -272,7 +274,6 @@ __device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t
     mbar_init(k_ready, SO ? kScoreWarps : kStateWarps + kScoreWarps);
     mbar_init(z_full, 1);
     mbar_init(s_ready, kStateWarps);
-    mbar_init(v_clean, kStateWarps);
     mbar_init(o_gone, DV / 64);
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -388,7 +389,7 @@ __device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t
         const uint32_t i_qk = make_idesc_bf16(C, C, 0, 0), i_qs = make_idesc_bf16(C, DV, 0, 1);
         const uint32_t i_pv = make_idesc_bf16(C, DV, 0, 1), i_kv = make_idesc_bf16(DK, DV, 1, 1);
         Ring r, rn;  // the item's first slot, and that of the next one's q
-        uint32_t n_o = 0, n_s = 0, n_k = 0, n_v = 0;  // outputs, states, key sets, cleared tiles so far
+        uint32_t n_o = 0, n_s = 0, n_k = 0;  // outputs, states, key sets so far
         bool ok = true;
         const auto wait = [&](uint64_t* b, uint32_t parity) {
           if (ok && !__all_sync(0xFFFFFFFFu, mbar_wait_short(b, parity & 1u))) {
@@ -421,8 +422,6 @@ __device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t
         for (Item it(w, group); it.i < items && ok; it.next()) {
           const int i = it.i, sub = it.sub;
           bool early = false;
-          int tok, n;
-          chunk_at(w, p.rev, it.c, tok, n);
           const Ring rq = r;
           r.next(F::SLOTS);
           const Ring rk = r;
@@ -448,10 +447,9 @@ __device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t
               }
               __syncwarp();
             }
-            if (elect_one()) mma_commit(qs_done);
+            if (adds_k(sub) && elect_one()) mma_commit(qs_done);
             __syncwarp();
             wait(&full[rv.slot], rv.phase);
-            if (n < C) wait(v_clean, n_v++);
             wait(p_ready, i);
             if (!ok) break;
             tc_fence_after();
@@ -476,7 +474,6 @@ __device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t
           }
           if (adds_k(sub)) {
             if (so) wait(&full[rv.slot], rv.phase);
-            if (so && n < C) wait(v_clean, n_v++);
             wait(s_ready, n_s);  // (the sum of the chunk before was read)
             wait(k_ready, n_k);
             if (!ok) break;
@@ -486,7 +483,8 @@ __device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t
               for (int kk = 0; kk < 2 * C / 16; ++kk)
                 mma_bf16_ss(tmem + F::Z, make_sdesc((kk < C / 16 ? sk : sq) + (kk & 7) * 2048, C * 128, 1024),
                             make_sdesc(sv + (kk & 7) * 2048, C * 128, 1024), i_kv, kk != 0 || !(many_q || sub == 0));
-              mma_commit(z_full);
+              if (so) mma_commit(qs_done);
+              if (sub == group - 1) mma_commit(z_full);
             }
             __syncwarp();
             ++n_k;
@@ -519,11 +517,10 @@ __device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t
     const f32x2 intra = pack2(p.inter * p.upd, p.inter * p.upd);
     const bool wide = (p.ldo % 16 == 0) && (p.dv % 16 == 0) && (reinterpret_cast<uintptr_t>(p.o) & 31u) == 0;
     const int tid = threadIdx.x - 128;
-    uint32_t n_o = 0;
+    uint32_t n_o = 0, n_k = 0;
     Ring r;
     if (so) {
       // the segments' own sums: these warps prepare the keys, the state warps sum
-      uint32_t n_k = 0;
       for (Item it(w, group); it.i < items; it.next()) {
         int tok, n;
         chunk_at(w, p.rev, it.c, tok, n);
@@ -536,13 +533,12 @@ __device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t
         bool ok = mbar_wait_short(&full[rk.slot], rk.phase);
         if (ok && n < C) {
           ok = mbar_wait_short(&full[rv.slot], rv.phase);
-          clear_values<DV>(smem + rv.slot * F::SLOT, n, tid);
-          if (lane == 0) mbar_arrive(v_clean);
+          if (ok) clear_values<DV>(smem + rv.slot * F::SLOT, n, tid);
         }
         if (ok) decay_keys<DK>(smem + rk.slot * F::SLOT, smem + rq.slot * F::SLOT, power_of, p.rev, n, tid, 0, 4);
         fence_proxy_async_smem();
         __syncwarp();
-        if (ok && n_k > 0) ok = mbar_wait_short(z_full, (n_k - 1) & 1);  // (no more than one set ahead)
+        if (ok && n_k > 0) ok = mbar_wait_short(qs_done, (n_k - 1) & 1);  // (no more than one set ahead)
         if (!ok) {
           fail();
           break;
@@ -559,7 +555,15 @@ __device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t
       r.next(F::SLOTS);
       const int rk = r.slot;
       r.next(F::SLOTS);
+      const Ring rv = r;
       r.next(F::SLOTS);
+      if (n < C) {
+        if (!mbar_wait_short(&full[rv.slot], rv.phase)) {
+          fail();
+          break;
+        }
+        clear_values<DV>(smem + rv.slot * F::SLOT, n, tid);
+      }
       if (!mbar_wait_short(p_full, i & 1)) {
         fail();
         break;
@@ -621,12 +625,12 @@ __device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(p_ready);
-      // half of the keys (QS has read the q tile; every item's phase is waited for in turn)
-      if (!mbar_wait_short(qs_done, i & 1)) {
-        fail();
-        break;
-      }
+      // half of the keys, once QS has read the q tile
       if (adds_k(sub)) {
+        if (!mbar_wait_short(qs_done, n_k++ & 1)) {
+          fail();
+          break;
+        }
         decay_keys<DK>(smem + rk * F::SLOT, smem + rq * F::SLOT, power_of, p.rev, n, tid, 2, 4);
         fence_proxy_async_smem();
         __syncwarp();
@@ -761,40 +765,25 @@ __device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t
     copied();
     float hi = 0.0f, lo = 0.0f;
     int n_was = -1;
-    uint32_t n_k = 0, n_out = 0;
+    uint32_t n_k = 0, n_z = 0, n_out = 0;
     const f32x2 upd = pack2(p.upd, p.upd);
     Ring r;
     for (Item it(w, group); it.i < items; it.next()) {
-      const int i = it.i;
       int tok, n;
       chunk_at(w, p.rev, it.c, tok, n);
       const Ring rq = r;
       r.next(F::SLOTS);
       const Ring rk = r;
       r.next(F::SLOTS);
-      const Ring rv = r;
       r.next(F::SLOTS);
-      if (n < C && !so) {
-        if (!mbar_wait_short(&full[rv.slot], rv.phase)) {
-          fail();
-          break;
-        }
-        clear_values<DV>(smem + rv.slot * F::SLOT, n, tid);
-        if (lane == 0) mbar_arrive(v_clean);
-      }
-      // QS has read the q tile (and QK^T the keys): both may be overwritten. (Every item's phase is
-      // waited for in turn: a parity tells one phase from the next alone.)
-      if (!so && !mbar_wait_short(qs_done, i & 1)) {
-        fail();
-        break;
-      }
       if (!adds_k(it.sub)) continue;
       if (n != n_was) {
         n_was = n;
         power2(g, n, hi, lo);
       }
       if (!so) {
-        if (!mbar_wait_short(&full[rk.slot], rk.phase)) {
+        // QS has read the q tile, and QK^T the keys: both may be overwritten
+        if (!mbar_wait_short(&full[rk.slot], rk.phase) || !mbar_wait_short(qs_done, n_k++ & 1)) {
           fail();
           break;
         }
@@ -803,12 +792,11 @@ __device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t
         __syncwarp();
         if (lane == 0) mbar_arrive(k_ready);
       }
-      if (!mbar_wait_short(z_full, n_k & 1)) {
+      if (it.sub != group - 1) continue;
+      if (!mbar_wait_short(z_full, n_z++ & 1)) {
         fail();
         break;
       }
-      ++n_k;
-      if (it.sub != group - 1) continue;
       tc_fence_after();
       if (!so && staged(n) && !mbar_wait_short(o_gone, n_out++ & 1)) {
         fail();

@@ -115,6 +115,14 @@ def test_grouped_heads(Hs, r, Dk, Dv):
     _check(_make([131, 1, 140], Hs, r, Dk, Dv, seed=Hs * 10 + r))
 
 
+@pytest.mark.parametrize("Dk,Dv", [(64, 64), (64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("lens,Hs,r", [([127, 255, 126, 383], 3, 2), ([255, 127, 1, 127], 2, 4),
+                                       ([4095], 1, 2), ([2047, 127, 1663], 1, 3)], ids=str)
+def test_grouped_heads_of_nearly_whole_chunks(lens, Hs, r, Dk, Dv):
+    """Chunks short of a token, for each head of a group in turn; the long ones in segments."""
+    _check(_make(lens, Hs, r, Dk, Dv, seed=sum(lens) + r))
+
+
 def test_without_states():
     x = _make([200, 90], 2, 2, 64, 64, states=False)
     la = _check(x)
