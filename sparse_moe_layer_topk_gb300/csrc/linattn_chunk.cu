@@ -945,31 +945,36 @@ struct Split {
 };
 
 // Segments of the time axis. Estimated from what was measured (us, widths of 128): a CTA takes 6 and
-// 3.4 a chunk and head of its group, one that sums the state alone 5 and 2, one that finds nothing to do
-// 1; the scan moves every segment's state twice at 5 GB a ms; two more launches 8. Each is a round over the
-// SMs. The ragged sequences' segments are counted from the tokens alone, for their lengths are on the
-// device. The split with the shortest estimate is taken: at 32 heads of 32,768 tokens one segment took
-// 1,036 us and the split 371; at 4 x 4,096 tokens of 32 heads, backward, one segment is best.
-Split split(int N, int T, int max_seqlen, int Hs, int np, int group, int Dk, int Dv) {
+// 3.4 a chunk and head of its group, one that sums the state alone 5 and 1.7 a chunk and head of the keys,
+// one that finds nothing to do 1; the scan moves every segment's state twice at 5 GB a ms; two more
+// launches 8. The lengths of ragged sequences are on the device: the CTAs with a whole segment are
+// counted as if every sequence but for its last chunk were full of them, and run in rounds over the SMs
+// unless the chunks spread over all SMs take longer. The split with the shortest estimate is taken.
+Split split(int N, int T, int max_seqlen, int Hs, int np, int group, int keys, int Dk, int Dv) {
   const int chunks = (max_seqlen + C - 1) / C;
+  // (a workspace may be asked for before the tokens are counted)
+  if (T <= 0) T = static_cast<int>(std::min(static_cast<long long>(N) * max_seqlen, 0x7FFFFFFFll));
   Split best{1, chunks > 0 ? chunks : 1};
   const double sms = num_sms(), heads = static_cast<double>(Hs) * np;
-  const double chunk = Dk <= 64 && Dv <= 64 ? 2.7 : 3.4;
-  const auto rounds = [&](double ctas) { return std::ceil(ctas / sms); };
+  const double chunk = (Dk <= 64 && Dv <= 64 ? 2.7 : 3.4) * group, sum = 1.7 * keys;
+  const double all_chunks = std::min(static_cast<double>(N) * chunks, static_cast<double>(T / C) + N);
   double least = 0.0;
   for (int n = 1; n <= 64 && n <= chunks && (n == 1 || heads * N * n <= 16 * sms); ++n) {
     const int per = (chunks + n - 1) / n;
-    const int used = (chunks + per - 1) / per;
-    if (used != n) continue;
-    const double all = heads * N * used;
-    const double busy = std::min(all, heads * (static_cast<double>(T) / (per * C) + N));
-    double t = rounds(busy) * (6.0 + chunk * per * group) + (all - busy) / sms;
-    if (n > 1)
-      t += rounds(busy * (used - 1) / used) * (5.0 + 2.0 * per * group) + (all - busy) / sms +
-           busy * Dk * Dv * 8.0 / 5.0e6 + 8.0;
+    if ((chunks + per - 1) / per != n) continue;
+    const double all = heads * N * n;
+    const double busy = std::min(all, heads * (std::floor(all_chunks / per) + N));
+    const double whole = heads * (N == 1 ? n : std::max(1.0, std::floor(all_chunks / per)));
+    const double idle = (all - busy) / sms;
+    const auto pass = [&](double part, double cta, double per_chunk) {
+      return std::max(std::ceil(whole * part / sms) * (cta + per_chunk * per),
+                      (busy * part * cta + heads * all_chunks * part * per_chunk) / sms) + idle;
+    };
+    double t = pass(1.0, 6.0, chunk);
+    if (n > 1) t += pass((n - 1.0) / n, 5.0, sum) + busy * Dk * Dv * 8.0 / 5.0e6 + 8.0;
     if (n == 1 || t < least) {
       least = t;
-      best = Split{used, per};
+      best = Split{n, per};
     }
   }
   return best;
@@ -983,8 +988,7 @@ size_t slots_bytes(const LinShape& s, const Split& sp, int dk, int dv) {
 
 size_t linattn_workspace(int max_seqlen, int Dk, int Dv, int Hs, int r, int T, int N, bool backward) {
   if (max_seqlen <= 0 || N <= 0 || Hs <= 0 || Dk <= 0 || Dv <= 0) return 0;
-  if (T <= 0) T = static_cast<int>(std::min(static_cast<long long>(N) * max_seqlen, 0x7FFFFFFFll));
-  const Split sp = split(N, T, max_seqlen, Hs, backward ? 3 : 1, r, Dk, Dv);
+  const Split sp = split(N, T, max_seqlen, Hs, backward ? 3 : 1, r, backward ? r : 1, Dk, Dv);
   if (sp.nseg == 1) return 0;
   LinShape s{};
   s.N = N;
@@ -993,7 +997,8 @@ size_t linattn_workspace(int max_seqlen, int Dk, int Dv, int Hs, int r, int T, i
 }
 
 int linattn_run(const LinProblem* p, int np, const LinShape& s, void* ws, cudaStream_t st) {
-  const Split sp = split(s.N, s.T, s.max_seqlen, s.Hs, np, std::max(p[0].nq, p[0].nkv), p[0].dk, p[0].dv);
+  const int r = std::max(p[0].nq, p[0].nkv);
+  const Split sp = split(s.N, s.T, s.max_seqlen, s.Hs, np, r, np > 1 ? r : 1, p[0].dk, p[0].dv);
   Args a;
   std::memset(static_cast<void*>(&a), 0, sizeof a);
   a.s = s;

@@ -123,6 +123,13 @@ def test_grouped_heads_of_nearly_whole_chunks(lens, Hs, r, Dk, Dv):
     _check(_make(lens, Hs, r, Dk, Dv, seed=sum(lens) + r))
 
 
+@pytest.mark.parametrize("N,max_seqlen", [(1, 20000), (3, 5000)])
+def test_empty_sequences_where_long_ones_were_expected(N, max_seqlen):
+    from sparse_moe_layer_topk_gb300.linattn import LinearAttention
+    x = _make([0] * N, 2, 2, 64, 128)
+    _check(x, LinearAttention(x["ld"].cuda(), 0, 64, 128, r=2, N=N, max_seqlen=max_seqlen, scale=x["scale"]))
+
+
 def test_without_states():
     x = _make([200, 90], 2, 2, 64, 64, states=False)
     la = _check(x)
