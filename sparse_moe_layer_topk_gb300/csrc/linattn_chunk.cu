@@ -716,6 +716,7 @@ __device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t
     float* const seg = pr.seg == nullptr ? nullptr
         : pr.seg + ((static_cast<long long>(w.n) * a.s.Hs + w.h) * a.nseg + w.seg) * p.dk * p.dv;
     {
+      if (!so && seg) wait_for_last_kernel();  // (until here the CTA needs no state)
       const float* in = so ? nullptr : seg ? seg : p.s_in ? p.s_in + state : nullptr;
       const int sr = seg ? pr.seg_row : p.s_row, sc = seg ? pr.seg_col : p.s_col;
       const float* const at = in + static_cast<long long>(row) * sr;
@@ -849,8 +850,12 @@ __device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t
 template <int D0, int D1, bool SO>
 __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid_constant__ Args a) {
   extern __shared__ uint8_t smem_raw[];
+  if (SO) allow_next_kernel();
   Work w;
-  if (!find_work(a, w)) return;
+  if (!find_work(a, w)) {
+    if (!SO && a.nseg > 1) wait_for_last_kernel();  // (no call ends before its kernels)
+    return;
+  }
   if (D0 == D1 || a.prob[w.prob].p.dk <= 64) run_chunks<D0, D1, SO>(a, w, smem_raw);
   else run_chunks<D1, D0, SO>(a, w, smem_raw);
 }
@@ -861,6 +866,8 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
 // further): slot 0 is the sequence's first state, slot s + 1 = lam^(tokens of s) slot s + the sum of s.
 __global__ void __launch_bounds__(128) segment_scan_kernel(LinProblem p, LinShape s, float* seg, int nseg, int seg_chunks) {
   const int h = blockIdx.x % s.Hs, n = blockIdx.x / s.Hs;
+  allow_next_kernel();
+  wait_for_last_kernel();
   int start, len;
   lin_sequence(s, n, start, len);
   if (len < 0) return;
@@ -911,7 +918,7 @@ int status(cudaError_t e) {
 }
 
 template <int D0, int D1, bool SO>
-int launch(const char* name, const Args& a, cudaStream_t st) {
+int launch(const char* name, const Args& a, bool behind, cudaStream_t st) {
   constexpr int SMEM = std::max(Cfg<D0, D1>::SMEM, Cfg<D1, D0>::SMEM);
   const auto kernel = linattn_chunk_kernel<D0, D1, SO>;
   static std::atomic<bool> ready[64];  // by device
@@ -927,17 +934,18 @@ int launch(const char* name, const Args& a, cudaStream_t st) {
   if (grid >= (1ll << 31)) return MOE_ERR_ARG;
   {
     LaunchTimer lt(name, st);
-    kernel<<<static_cast<unsigned>(grid), kThreads, SMEM, st>>>(a);
+    if (behind) e = launch_behind(kernel, static_cast<unsigned>(grid), kThreads, SMEM, st, a);
+    else kernel<<<static_cast<unsigned>(grid), kThreads, SMEM, st>>>(a);
   }
-  return status(cudaGetLastError());
+  return status(e == cudaSuccess ? cudaGetLastError() : e);
 }
 
 template <bool SO>
-int launch_widths(const char* name, const Args& a, cudaStream_t st) {
+int launch_widths(const char* name, const Args& a, bool behind, cudaStream_t st) {
   const bool k64 = a.prob[0].p.dk <= 64, v64 = a.prob[0].p.dv <= 64;
-  if (k64 && v64) return launch<64, 64, SO>(name, a, st);
-  if (k64 != v64) return launch<64, 128, SO>(name, a, st);
-  return launch<128, 128, SO>(name, a, st);
+  if (k64 && v64) return launch<64, 64, SO>(name, a, behind, st);
+  if (k64 != v64) return launch<64, 128, SO>(name, a, behind, st);
+  return launch<128, 128, SO>(name, a, behind, st);
 }
 
 struct Split {
@@ -947,7 +955,7 @@ struct Split {
 // Segments of the time axis. Estimated from what was measured (us, widths of 128): a CTA takes 6 and
 // 3.4 a chunk and head of its group, one that sums the state alone 5 and 1.7 a chunk and head of the keys,
 // one that finds nothing to do 1; the scan moves every segment's state twice at 5 GB a ms; two more
-// launches 8. The lengths of ragged sequences are on the device: the CTAs with a whole segment are
+// launches 4. The lengths of ragged sequences are on the device: the CTAs with a whole segment are
 // counted as if every sequence but for its last chunk were full of them, and run in rounds over the SMs
 // unless the chunks spread over all SMs take longer. The split with the shortest estimate is taken.
 Split split(int N, int T, int max_seqlen, int Hs, int np, int group, int keys, int Dk, int Dv) {
@@ -971,7 +979,7 @@ Split split(int N, int T, int max_seqlen, int Hs, int np, int group, int keys, i
                       (busy * part * cta + heads * all_chunks * part * per_chunk) / sms) + idle;
     };
     double t = pass(1.0, 6.0, chunk);
-    if (n > 1) t += pass((n - 1.0) / n, 5.0, sum) + busy * Dk * Dv * 8.0 / 5.0e6 + 8.0;
+    if (n > 1) t += pass((n - 1.0) / n, 5.0, sum) + busy * Dk * Dv * 8.0 / 5.0e6 + 4.0;
     if (n == 1 || t < least) {
       least = t;
       best = Split{n, per};
@@ -1033,17 +1041,16 @@ int linattn_run(const LinProblem* p, int np, const LinShape& s, void* ws, cudaSt
     Args own = a;  // (the problems with states of their own come first)
     own.states_only = 1;
     while (p[own.nprob - 1].shares >= 0) --own.nprob;
-    const int e = launch_widths<true>("linattn_segments", own, st);
+    const int e = launch_widths<true>("linattn_segments", own, false, st);
     if (e != MOE_OK) return e;
     for (int i = 0; i < own.nprob; ++i) {
       LaunchTimer lt("linattn_scan", st);
       const dim3 grid(static_cast<unsigned>(s.N) * s.Hs, (p[i].dk * p[i].dv + 1023) / 1024);
-      segment_scan_kernel<<<grid, 128, 0, st>>>(p[i], s, a.prob[i].seg, sp.nseg, sp.seg_chunks);
-      const int se = status(cudaGetLastError());
+      const int se = status(launch_behind(segment_scan_kernel, grid, 128, 0, st, p[i], s, a.prob[i].seg, sp.nseg, sp.seg_chunks));
       if (se != MOE_OK) return se;
     }
   }
-  return launch_widths<false>(np == 1 ? "linattn_fwd" : "linattn_bwd", a, st);
+  return launch_widths<false>(np == 1 ? "linattn_fwd" : "linattn_bwd", a, sp.nseg > 1, st);
 }
 
 }  // namespace moe

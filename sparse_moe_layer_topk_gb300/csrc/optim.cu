@@ -226,6 +226,7 @@ __device__ __forceinline__ int find_tensor(const AdamwEntry* e, int n, long long
 __global__ void __launch_bounds__(kThreads)
     grad_norm_kernel(const AdamwEntry* entries, int n_tensors, long long chunks, float max_norm,
                      double* partial, AdamwControl* ctl) {
+  allow_next_kernel();
   f32x2 acc[4] = {{0}, {0}, {0}, {0}};
   const auto load = [&](long long c, f32x2 (&g)[4]) {
 #pragma unroll
@@ -487,6 +488,7 @@ __global__ void __launch_bounds__(kThreads, Q8 ? 4 : 3)
     adamw_step_kernel(const AdamwEntry* entries, int n_tensors, long long chunks, AdamwHyper h,
                       const float* lr_dev, AdamwControl* ctl, int clipped, long long run, int* err_flag) {
   __shared__ StepConsts sc;
+  if (clipped) wait_for_last_kernel();
   if (threadIdx.x == 0) {
     const long long t = ctl->step + 1;
     sc.lr = lr_dev ? *lr_dev : h.lr;
@@ -578,12 +580,11 @@ cudaError_t launch_adamw_step(const AdamwEntry* entries, int n, long long chunks
   long long run = (chunks * kChunkBlocks + warps - 1) / warps;
   if (state_bits == 32 && run > kChunkBlocks) run = kChunkBlocks;
   LaunchTimer lt(state_bits == 8 ? "adamw_step8" : "adamw_step32", st);
-  if (state_bits == 8)
-    adamw_step_kernel<true><<<grid, kThreads, 0, st>>>(entries, n, chunks, h, lr_dev, ctl,
-                                                       clipped ? 1 : 0, run, err_flag);
-  else
-    adamw_step_kernel<false><<<grid, kThreads, 0, st>>>(entries, n, chunks, h, lr_dev, ctl,
-                                                        clipped ? 1 : 0, run, err_flag);
+  // (behind the norm, if there is one: its CTAs are then in place when it ends)
+  const auto kernel = state_bits == 8 ? adamw_step_kernel<true> : adamw_step_kernel<false>;
+  if (clipped)
+    return launch_behind(kernel, grid, kThreads, 0, st, entries, n, chunks, h, lr_dev, ctl, 1, run, err_flag);
+  kernel<<<grid, kThreads, 0, st>>>(entries, n, chunks, h, lr_dev, ctl, 0, run, err_flag);
   return cudaGetLastError();
 }
 
