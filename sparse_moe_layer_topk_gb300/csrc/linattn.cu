@@ -21,11 +21,13 @@ __device__ __forceinline__ float head_log_decay(const float* log_decay, int h, i
 // ------------------------------------------------------------------ decoding step
 //
 // S = lam S + k v^T and o = scale S^T q for one token of a row: every state value
-// is read and written once, 8 bytes for 2 + r multiply-adds, so HBM bounds it. A CTA
-// takes COLS columns of one row's state head, a lane 8 columns (32-byte accesses) of Dk / (256 * 8 / COLS)
-// rows, all of whose loads are under way before the first is used; four CTAs an SM hold 128 KB in
-// flight. The partial sums of o over the rows are joined by shuffles and in shared memory, in a fixed
-// order. Where the batch leaves SMs without work, tiles of 32 columns instead of 64.
+// is read and written once, 8 bytes for 2 + r multiply-adds, so HBM bounds it. A CTA takes COLS
+// columns of one row's state head, a lane 8 columns (32-byte accesses) of Dk / (256 * 8 / COLS) rows, all
+// of whose loads are under way before the first is used; four CTAs an SM hold 128 KB in flight. The
+// partial sums of o over the rows are joined by shuffles and in shared memory, in a fixed order.
+// Where the batch leaves SMs without work, tiles of 32 columns instead of 64.
+// Measured: 256 rows x 32 heads, 128 x 128 (1.08 GB): 185 us, 5.8 TB/s, 0.86 of a plain copy's rate;
+// with 16-byte accesses and three CTAs an SM 246. One row: 10 us, the call and the launch.
 constexpr int kStepThreads = 256;
 constexpr int kStepHeads = 4;  // query heads whose partial sums share one exchange
 

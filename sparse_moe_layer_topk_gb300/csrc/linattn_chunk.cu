@@ -18,11 +18,17 @@
 //                bf16 A operand of PV (in place); then the output rows
 //   warps 12-19  state: the decayed keys K~ into shared memory; S in registers (fp32), its
 //                bf16 copy as the B operand of QS
-// Rounding: P and the copy of S that QS reads are bf16 (their error is that of the
-// output's own rounding; with keys of up to 64 values, two bf16 terms); the state itself is summed in fp32 and K~ enters the product
-// as two bf16 terms (16 bits and a sign: 2.7e-6 of the state, rms), because the state is an
-// output of the call and is carried over thousands of chunks. A chunk's sum starts from zero and
-// is added in fp32 registers, not in tensor memory, whose accumulation truncates.
+// Rounding: P and the copy of S that QS reads are bf16 (their error is that of the output's own
+// rounding; with keys of up to 64 values, two bf16 terms). The state itself is summed in fp32 and K~
+// enters the product as two bf16 terms (16 bits and a sign: 2.7e-6 of the state, rms; one term 1.7e-3),
+// because the state is an output of the call and is carried over thousands of chunks. A chunk's sum
+// starts from zero and is added in fp32 registers, not in tensor memory, whose accumulation truncates.
+//
+// Measured: 152 heads x 4,096 tokens, 128 wide (637 MB): 114 us, 5.6 TB/s, 0.82 of a plain copy's rate.
+// 3.4 us a chunk: of its 6,300 clocks the shared-memory pipe is taken for 4,800 (operands 2,304, TMA in
+// 768, K~ 768, the state's copy, the scores' tables and the output), the tensor cores work for 2,700, and
+// the chain from a state to the next one (QS, keys, K~^T V, sum, copy) fills the rest.
+
 #include <cuda.h>
 
 #include <algorithm>

@@ -4,12 +4,16 @@
 //   g' = c g;  m = b1 m + (1 - b1) g';  v = b2 v + (1 - b2) g'^2
 //   p  = p (1 - lr wd) - lr (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps)
 //
-// Nothing is reused, so the step is bound by HBM: p, m, v in and out and g in.
-// Each warp takes runs of blocks of 256 values (a prefix of the tensors' chunk
-// counts, searched where a run enters a tensor, says whose), eight consecutive values a lane: 32-byte loads and stores of fp32, 16-byte of bf16, 8-byte of codes. A block is also what shares a scale in the 8-bit states:
-// its largest magnitude is one warp reduction. The 8-bit step moves 10 bytes a value (bf16 weights and
-// gradients), so its instructions weigh as much as its bytes: arithmetic runs two values to an
-// instruction, and types are told apart once a run.
+// Nothing is reused, so the 32-bit step is bound by HBM: p, m, v in and out and g in. Each warp takes
+// runs of blocks of 256 values (a prefix of the tensors' chunk counts, searched where a run enters a
+// tensor, says whose), eight consecutive values a lane: 32-byte loads and stores of fp32, 16-byte of
+// bf16, 8-byte of codes. A block is also what shares a scale in the 8-bit states: its largest magnitude
+// is one warp reduction. The 8-bit step moves 10 bytes a value (bf16 weights and gradients) with 73
+// instructions, which weigh more than its bytes: arithmetic runs two values to an instruction, and
+// types are told apart once a run.
+// Measured: 67 M values, bf16 weights with a master copy, fp32 gradients: 325 us, 6.2 TB/s (0.91 of a
+// plain copy's rate); 8-bit states, bf16 weights and gradients: 181 us, 3.7 TB/s, issue slots 73% taken.
+
 #include "common.cuh"
 #include "optim.h"
 #include "timing.h"
