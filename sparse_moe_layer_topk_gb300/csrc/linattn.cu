@@ -25,9 +25,8 @@ __device__ __forceinline__ float head_log_decay(const float* log_decay, int h, i
 // columns of one row's state head, a lane 8 columns (32-byte accesses) of Dk / (256 * 8 / COLS) rows, all
 // of whose loads are under way before the first is used; four CTAs an SM hold 128 KB in flight. The
 // partial sums of o over the rows are joined by shuffles and in shared memory, in a fixed order.
-// Where the batch leaves SMs without work, tiles of 32 columns instead of 64.
 // Measured: 256 rows x 32 heads, 128 x 128 (1.08 GB): 185 us, 5.8 TB/s, 0.86 of a plain copy's rate;
-// with 16-byte accesses and three CTAs an SM 246. One row: 10 us, the call and the launch.
+// with 16-byte accesses and three CTAs an SM 246. One row: 10 us a call from Python, 2.5 in a graph.
 constexpr int kStepThreads = 256;
 constexpr int kStepHeads = 4;  // query heads whose partial sums share one exchange
 
@@ -150,7 +149,9 @@ cudaError_t launch_linattn_step(const void* q, const void* k, const void* v,
                                           static_cast<const bf16*>(v), log_decay, state, state_idx, n_slots, Hs, r, Dk,
                                           Dv, ldq, ldk, ldv, ldo, scale, static_cast<bf16*>(o), err_flag);
   };
-  if (tiles(64) >= 2u * num_sms()) run(linattn_step_kernel<64>, tiles(64));
+  // Tiles of 64 columns where they fill the SMs twice over (32 heads of 128 x 128, in a graph: 64 rows
+  // 49.2 us, in tiles of 32 columns 51.9), of 32 where there are fewer (5 rows 4.95 us, in tiles of 64 5.39).
+  if (tiles(64) >= 8u * num_sms()) run(linattn_step_kernel<64>, tiles(64));
   else run(linattn_step_kernel<32>, tiles(32));
   return cudaGetLastError();
 }
