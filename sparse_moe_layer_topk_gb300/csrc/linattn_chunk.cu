@@ -14,6 +14,7 @@
 //   warp 0       TMA producer over a ring of tile slots
 //   warp 1       MMA issue: QK^T, QS, PV, K~^T V into four accumulators that fill
 //                tensor memory (512 columns at width 128)
+//   warp 2       stores of the output tiles that the score warps leave in shared memory
 //   warps 4-11   scores: P out of tensor memory, times the decay factors, back as the
 //                bf16 A operand of PV (in place); then the output rows
 //   warps 12-19  state: the decayed keys K~ into shared memory; S in registers (fp32), its
@@ -24,10 +25,11 @@
 // because the state is an output of the call and is carried over thousands of chunks. A chunk's sum
 // starts from zero and is added in fp32 registers, not in tensor memory, whose accumulation truncates.
 //
-// Measured: 152 heads x 4,096 tokens, 128 wide (637 MB): 114 us, 5.6 TB/s, 0.82 of a plain copy's rate.
-// 3.4 us a chunk: of its 6,300 clocks the shared-memory pipe is taken for 4,800 (operands 2,304, TMA in
+// Measured: 152 heads x 4,096 tokens, 128 wide (637 MB): 111 us, 5.7 TB/s, 0.85 of a plain copy's rate.
+// 3.3 us a chunk: of its 6,200 clocks the shared-memory pipe is taken for 4,800 (operands 2,304, TMA in
 // 768, K~ 768, the state's copy, the scores' tables and the output), the tensor cores work for 2,700, and
-// the chain from a state to the next one (QS, keys, K~^T V, sum, copy) fills the rest.
+// the chain from a state to the next one (QS 830, keys 1,600, K~^T V 1,340, sum 600, copy 700, the waits
+// between them) takes nearly all of them.
 
 #include <cuda.h>
 
@@ -257,7 +259,8 @@ __device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t
   uint64_t* const s_ready = p_full + 7;        // the state's copy written, Z read
   uint64_t* const o_gone = p_full + 8;         // the output has left its staging place
   uint64_t* const drain = p_full + 9;
-  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(p_full + 10);
+  uint64_t* const o_staged = p_full + 10;      // three, used in turn
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(p_full + 13);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   // factor[128 + j - i] is L_ij, zero outside the mask; power_of[m] = lam^m, 0 <= m <= 128;
   // falling[m] = lam^(15-m), 0 <= m < 16
@@ -280,7 +283,8 @@ __device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t
     mbar_init(k_ready, SO ? kScoreWarps : kStateWarps + kScoreWarps);
     mbar_init(z_full, 1);
     mbar_init(s_ready, kStateWarps);
-    mbar_init(o_gone, DV / 64);
+    mbar_init(o_gone, 1);
+    for (int i = 0; i < 3; ++i) mbar_init(&o_staged[i], kScoreWarps);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -323,10 +327,16 @@ __device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t
   const auto first_q = [&](int sub) { return many_q || sub == 0; };
   const auto last_q = [&](int sub) { return many_q || sub == group - 1; };
   const auto adds_k = [&](int sub) { return !many_q || sub == group - 1; };
-  // A whole chunk's output rows leave through the place of the state's copy, which is idle from QS
-  // to the next state (with several query heads the next one's QS reads it): stores of one row a
-  // lane took 1,024 clocks of the shared-memory pipe a chunk. It has room for DK >= C rows.
-  const auto staged = [&](int n) { return DK == C && !many_q && n == C; };
+  // At widths of 128 a whole chunk's output rows leave through shared memory and a TMA store (stores of one
+  // row a lane take 1,024 clocks of the shared-memory pipe a chunk): through the place of the state's
+  // copy, which is idle from the chunk's last QS to the next state, or, while another query head's QS is
+  // to read that, through the item's q tile. (At narrower widths the copy is sooner done and would wait
+  // for the store: 152 heads x 4,096 tokens, 64 wide, 84 us, staged 87; 16 x 2 heads, 64 / 128 wide, backward
+  // 119, staged 124.)
+  constexpr bool STAGED = DK == C && DV == C;
+  static_assert(!STAGED || F::COPY >= C * DV * 2, "room for an output tile");
+  const auto staged = [&](int n) { return STAGED && n == C; };
+  const auto in_q = [&](int sub, int n) { return staged(n) && many_q && sub < group - 1; };
   const auto fail = [&]() {
     *abort_flag = 1;
     set_flag(a.s.err_flag, MOE_FLAG_TIMEOUT);
@@ -387,6 +397,34 @@ __device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t
           }
         }
       }
+    } else if (warp == 2) {
+      // Stores the staged outputs. (Before the fourth is staged the first one's place was given back.)
+      if (!so && STAGED && elect_one()) {
+        Ring r;
+        int n_st = 0;
+        for (Item it(w, group); it.i < items; it.next()) {
+          const int rq = r.slot;
+          r.next(F::SLOTS);
+          r.next(F::SLOTS);
+          r.next(F::SLOTS);
+          int tok, n;
+          chunk_at(w, p.rev, it.c, tok, n);
+          if (!last_q(it.sub) || !staged(n)) continue;
+          if (!mbar_wait_short(&o_staged[n_st % 3], n_st / 3 & 1)) {
+            fail();
+            break;
+          }
+          ++n_st;
+          const bool q_place = in_q(it.sub, n);
+          const uint32_t from = smem_u32(q_place ? smem + rq * F::SLOT : copy);
+          const int hq = p.nq > 1 ? w.h * p.nq + it.sub : w.h;
+          for (int c = 0; c < DV / 64; ++c) tma_store_3d(&a.prob[w.prob].o, from + c * C * 128, 64 * c, tok, hq);
+          bulk_commit();
+          bulk_wait_read_all();
+          mbar_arrive(q_place ? &empty[rq] : o_gone);
+        }
+        bulk_wait_all();
+      }
     } else if (warp == 1) {
       // The whole warp walks the items and one lane issues, batch by batch: the descriptors then
       // stay in uniform registers and an MMA of 128 x 128 x 16 issues in 67 clocks (a single
@@ -428,6 +466,8 @@ __device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t
         for (Item it(w, group); it.i < items && ok; it.next()) {
           const int i = it.i, sub = it.sub;
           bool early = false;
+          int tok, n;
+          chunk_at(w, p.rev, it.c, tok, n);
           const Ring rq = r;
           r.next(F::SLOTS);
           const Ring rk = r;
@@ -497,7 +537,7 @@ __device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t
           }
           if (sub == group - 1) ++n_s;
           if (elect_one()) {
-            mma_commit(&empty[rq.slot]);
+            if (so || !in_q(sub, n)) mma_commit(&empty[rq.slot]);
             mma_commit(&empty[rk.slot]);
             mma_commit(&empty[rv.slot]);
           }
@@ -524,6 +564,7 @@ __device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t
     const bool wide = (p.ldo % 16 == 0) && (p.dv % 16 == 0) && (reinterpret_cast<uintptr_t>(p.o) & 31u) == 0;
     const int tid = threadIdx.x - 128;
     uint32_t n_o = 0, n_k = 0;
+    int n_st = 0;
     Ring r;
     if (so) {
       // the segments' own sums: these warps prepare the keys, the state warps sum
@@ -673,7 +714,7 @@ __device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t
                                 mul2(intra, pack2(__uint_as_float(x2[2 * j]), __uint_as_float(x2[2 * j + 1])))));
         const uint4 lo4 = make_uint4(u[0], u[1], u[2], u[3]), hi4 = make_uint4(u[4], u[5], u[6], u[7]);
         if (staged(n)) {
-          uint8_t* const line = copy + (c0 >> 6) * C * 128 + row * 128;
+          uint8_t* const line = (in_q(sub, n) ? smem + rq * F::SLOT : copy) + (c0 >> 6) * C * 128 + row * 128;
           const int at = (c0 & 63) >> 3, sw = row & 7;
           *reinterpret_cast<uint4*>(line + ((at ^ sw) << 4)) = lo4;
           *reinterpret_cast<uint4*>(line + (((at + 1) ^ sw) << 4)) = hi4;
@@ -687,24 +728,11 @@ __device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t
         }
       }
       if (staged(n)) {
-        // the warps that share a 64-column block (its upper and its lower half where there is one block)
         fence_proxy_async_smem();
-        if (DV == 128) asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
-        else asm volatile("bar.sync 1, 256;" ::: "memory");
-        if (qd == 0 && (DV == 128 || half == 0)) {
-          if (elect_one()) {
-            tma_store_3d(&a.prob[w.prob].o, smem_u32(copy) + half * C * 128, 64 * half, tok, hq);
-            bulk_commit();
-            bulk_wait_read_all();
-            mbar_arrive(o_gone);
-          }
-          __syncwarp();
-        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&o_staged[n_st % 3]);
+        ++n_st;
       }
-    }
-    if (qd == 0) {
-      if (elect_one()) bulk_wait_all();
-      __syncwarp();
     }
   } else {
     // ---------------------------------------------------------------- state warps
@@ -805,10 +833,6 @@ __device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t
         break;
       }
       tc_fence_after();
-      if (!so && staged(n) && !mbar_wait_short(o_gone, n_out++ & 1)) {
-        fail();
-        break;
-      }
       const f32x2 hi2 = pack2(hi, hi), lo2 = pack2(lo, lo);
 #pragma unroll
       for (int cb = 0; cb < NC / 32; ++cb) {
@@ -824,7 +848,15 @@ __device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          if (!so) copy8(4 * cb + j);
+          if (!so && !STAGED) copy8(4 * cb + j);
+      }
+      if (!so && STAGED) {  // (an output may stand in the copy's place; the sum need not wait for it)
+        if (staged(n) && !mbar_wait_short(o_gone, n_out++ & 1)) {
+          fail();
+          break;
+        }
+#pragma unroll
+        for (int j = 0; j < NC / 8; ++j) copy8(j);
       }
       copied();
     }
@@ -959,7 +991,7 @@ struct Split {
 };
 
 // Segments of the time axis. Estimated from what was measured (us, widths of 128): a CTA takes 6 and
-// 3.4 a chunk and head of its group, one that sums the state alone 5 and 1.7 a chunk and head of the keys,
+// 3.3 a chunk and head of its group, one that sums the state alone 5 and 1.7 a chunk and head of the keys,
 // one that finds nothing to do 1; the scan moves every segment's state twice at 5 GB a ms; two more
 // launches 4. The lengths of ragged sequences are on the device: the CTAs with a whole segment are
 // counted as if every sequence but for its last chunk were full of them, and run in rounds over the SMs
@@ -970,7 +1002,7 @@ Split split(int N, int T, int max_seqlen, int Hs, int np, int group, int keys, i
   if (T <= 0) T = static_cast<int>(std::min(static_cast<long long>(N) * max_seqlen, 0x7FFFFFFFll));
   Split best{1, chunks > 0 ? chunks : 1};
   const double sms = num_sms(), heads = static_cast<double>(Hs) * np;
-  const double chunk = (Dk <= 64 && Dv <= 64 ? 2.7 : 3.4) * group, sum = 1.7 * keys;
+  const double chunk = (Dk <= 64 && Dv <= 64 ? 2.7 : 3.3) * group, sum = 1.7 * keys;
   const double all_chunks = std::min(static_cast<double>(N) * chunks, static_cast<double>(T / C) + N);
   double least = 0.0;
   for (int n = 1; n <= 64 && n <= chunks && (n == 1 || heads * N * n <= 16 * sms); ++n) {
