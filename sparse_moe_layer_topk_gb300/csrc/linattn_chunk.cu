@@ -624,30 +624,32 @@ __device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t
         if (p.rev ? c0 + 16 > 32 * qd : c0 < 32 * qd + 32) {
           uint32_t x[16];
           tmem_ld_32x32b_x16(trow + F::P + c0, x);
-          tmem_ld_wait();
-          float y[16];
+          float y[16];  // (the factors are read while the scores are on their way)
           if (c0 >> 5 == qd) {
             // selected, not multiplied by zero: what lies outside the mask may be NaN
             const float* const f = factor + C - row + c0;
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const float fj = f[j];
-              y[j] = fj > 0.0f ? __uint_as_float(x[j]) * fj : 0.0f;
-            }
+            for (int j = 0; j < 16; ++j) y[j] = f[j];
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) y[j] = y[j] > 0.0f ? __uint_as_float(x[j]) * y[j] : 0.0f;
           } else {
             // beside the diagonal blocks lam^|i-j| is the power of the row's distance from the 16
             // columns' near edge times that of the column's
             const float d = power_of[p.rev ? c0 - row : row - c0 - 15];
             const f32x2 d2 = pack2(d, d);
             const float4* const e = reinterpret_cast<const float4*>(p.rev ? power_of : falling);
+            f32x2 f[8];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const float4 e4 = e[j];
-              unpack2(mul2(mul2(pack2(__uint_as_float(x[4 * j]), __uint_as_float(x[4 * j + 1])), d2), pack2(e4.x, e4.y)),
-                      y[4 * j], y[4 * j + 1]);
-              unpack2(mul2(mul2(pack2(__uint_as_float(x[4 * j + 2]), __uint_as_float(x[4 * j + 3])), d2), pack2(e4.z, e4.w)),
-                      y[4 * j + 2], y[4 * j + 3]);
+              f[2 * j] = mul2(pack2(e4.x, e4.y), d2);
+              f[2 * j + 1] = mul2(pack2(e4.z, e4.w), d2);
             }
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              unpack2(mul2(pack2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), f[j]), y[2 * j], y[2 * j + 1]);
           }
           if (p.rev && c0 + 16 > n) {  // keys past the chunk's tokens
 #pragma unroll

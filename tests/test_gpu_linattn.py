@@ -272,6 +272,32 @@ def test_same_result_on_a_side_stream_and_in_a_graph():
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("lens,r,Dk,Dv", [([4000], 2, 128, 128), ([2900, 0, 513], 1, 64, 128)], ids=str)
+def test_segments_in_a_graph(lens, r, Dk, Dv):
+    """Several launches a call, each behind the one before it: the same bits in a graph and a second time."""
+    x = _make(lens, 1, r, Dk, Dv, seed=9)
+    la = _check(x)
+    assert la.ws_bytes > 0  # (in segments)
+    y, cu = _cuda(x), _cu(lens)
+
+    def both():
+        la.forward(y["q"], y["k"], y["v"], cu, y["S0"], want_state=True)
+        la.backward(y["do"], y["X"])
+
+    keep = lambda: [t.clone() for t in (la.o, la.state_out, la.dq, la.dk, la.dv, la.d_state_in)]  # noqa: E731
+    want = keep()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        both()
+        both()
+    for t in (la.o, la.dq, la.dk, la.dv, la.ws):
+        t.zero_()
+    for _ in range(2):
+        graph.replay()
+        for a, b in zip(keep(), want):
+            assert torch.equal(a, b)
+
+
 def test_states_in_place():
     """state_out may be state_in."""
     x = _make([200, 0, 15], 2, 1, 64, 64)
