@@ -67,7 +67,11 @@ struct Cfg {
   // slots of the ring: what fits beside the state's copy
   static constexpr int FIT = (LIMIT - MISC - TERMS * COPY) / SLOT;
   static constexpr int SLOTS = FIT > 9 ? 9 : FIT;
-  static constexpr int SMEM = SLOTS * SLOT + TERMS * COPY + MISC + 1024;
+  // the states alone: two places for second terms of the keys, the rest a ring of k and v
+  static constexpr int SUM_FIT = (LIMIT - MISC) / SLOT;
+  static constexpr int SUM_SLOTS = (SUM_FIT > 11 ? 11 : SUM_FIT) - 2;
+  template <bool SO>
+  static constexpr int SMEM = (SO ? (SUM_SLOTS + 2) * SLOT : SLOTS * SLOT + TERMS * COPY) + MISC + 1024;
   static_assert(SLOTS >= 6, "a chunk's three tiles and the next one's");
   // tensor memory columns
   static constexpr int P = 0, Z = 128, O1 = 256, O2 = 384;
@@ -235,7 +239,9 @@ __device__ __forceinline__ void clear_values(uint8_t* tv, int n, int tid) {
   __syncwarp();
 }
 
-// A CTA's chunks. SO: the states alone (the segments' own sums).
+// A CTA's chunks. SO: the states alone (the segments' own sums): the score warps decay the keys, with two
+// places for their second terms, and k and v have the rest of shared memory (five tiles and not the four of a
+// ring with q's place: 64 chunks of 96 CTAs 99 us instead of 111).
 template <int DK, int DV, bool SO>
 __device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t* smem_raw) {
   using F = Cfg<DK, DV>;
@@ -243,12 +249,13 @@ __device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t
 
   uint8_t* const smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint8_t* const copy = smem + F::SLOTS * F::SLOT;  // the state in bf16
+  constexpr int SLOTS = SO ? F::SUM_SLOTS : F::SLOTS;
+  uint8_t* const copy = smem + SLOTS * F::SLOT;  // the state in bf16 (the states alone: second terms of the keys)
   // A wait tells a phase from the next one alone, so no barrier may complete twice before each of its
   // waiters has returned: every phase is waited for, and the next one needs an arrival made after that.
-  uint64_t* const full = reinterpret_cast<uint64_t*>(copy + F::TERMS * F::COPY);
-  uint64_t* const empty = full + F::SLOTS;
-  uint64_t* const p_full = empty + F::SLOTS;   // QK^T done
+  uint64_t* const full = reinterpret_cast<uint64_t*>(copy + (SO ? 2 * F::SLOT : F::TERMS * F::COPY));
+  uint64_t* const empty = full + SLOTS;
+  uint64_t* const p_full = empty + SLOTS;   // QK^T done
   // QS done: the q tile may be overwritten (with each set of keys; states alone: a set has entered)
   uint64_t* const qs_done = p_full + 1;
   uint64_t* const p_ready = p_full + 2;        // P back in tensor memory
@@ -271,7 +278,7 @@ __device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t
   const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);  // (uniform to the compiler)
   const int lane = static_cast<int>(lane_id());
   if (threadIdx.x == 0) {
-    for (int i = 0; i < F::SLOTS; ++i) {
+    for (int i = 0; i < SLOTS; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
@@ -355,42 +362,38 @@ __device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t
           chunk_at(w, p.rev, it.c, tok, n);
           const int hq = p.nq > 1 ? w.h * p.nq + sub : w.h;
           const int hk = p.nkv > 1 ? w.h * p.nkv + sub : w.h;
-          for (int t = 0; t < 3; ++t) {
+          for (int t = so ? 1 : 0; t < 3; ++t) {
             if (!mbar_wait_short(&empty[r.slot], r.phase ^ 1u)) {
               fail();
               ok = false;
               break;
             }
-            if (t == 0 && so) {
-              mbar_arrive(&full[r.slot]);  // (the q slot only takes a key term)
-            } else {
-              const CUtensorMap* m = t == 0 ? &a.prob[w.prob].q : t == 1 ? &a.prob[w.prob].k : &a.prob[w.prob].v;
-              const int width = t == 2 ? DV : DK;
-              const uint32_t dst = smem_u32(smem + r.slot * F::SLOT);
-              mbar_arrive_expect_tx(&full[r.slot], C * width * 2);
-              for (int c = 0; c < width / 64; ++c)
-                tma_load_3d(dst + c * C * 128, m, &full[r.slot], 64 * c, tok, t == 0 ? hq : hk);
-            }
+            const CUtensorMap* m = t == 0 ? &a.prob[w.prob].q : t == 1 ? &a.prob[w.prob].k : &a.prob[w.prob].v;
+            const int width = t == 2 ? DV : DK;
+            const uint32_t dst = smem_u32(smem + r.slot * F::SLOT);
+            mbar_arrive_expect_tx(&full[r.slot], C * width * 2);
+            for (int c = 0; c < width / 64; ++c)
+              tma_load_3d(dst + c * C * 128, m, &full[r.slot], 64 * c, tok, t == 0 ? hq : hk);
             ++issued;
-            r.next(F::SLOTS);
+            r.next(SLOTS);
           }
         }
         if (ok) {
           // the last commits must not reach this CTA's barriers after it left
-          for (int i = 0; i < F::SLOTS; ++i) {
+          for (int i = 0; i < SLOTS; ++i) {
             if (!mbar_wait_short(&empty[r.slot], r.phase ^ 1u)) {
               fail();
               break;
             }
-            r.next(F::SLOTS);
+            r.next(SLOTS);
           }
         } else {
           // nothing may land in shared memory after the CTA left
           int s = r.slot;
           uint32_t ph = r.phase;
-          for (long long i = 0; i < issued && i < F::SLOTS; ++i) {
+          for (long long i = 0; i < issued && i < SLOTS; ++i) {
             if (--s < 0) {
-              s = F::SLOTS - 1;
+              s = SLOTS - 1;
               ph ^= 1u;
             }
             mbar_wait_short(&full[s], ph);
@@ -404,9 +407,9 @@ __device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t
         int n_st = 0;
         for (Item it(w, group); it.i < items; it.next()) {
           const int rq = r.slot;
-          r.next(F::SLOTS);
-          r.next(F::SLOTS);
-          r.next(F::SLOTS);
+          r.next(SLOTS);
+          r.next(SLOTS);
+          r.next(SLOTS);
           int tok, n;
           chunk_at(w, p.rev, it.c, tok, n);
           if (!last_q(it.sub) || !staged(n)) continue;
@@ -444,11 +447,11 @@ __device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t
         const auto scores = [&]() {  // QK^T of the item whose q is in slot rn
           const uint32_t sq = smem_u32(smem + rn.slot * F::SLOT);
           wait(&full[rn.slot], rn.phase);
-          rn.next(F::SLOTS);
+          rn.next(SLOTS);
           const uint32_t sk = smem_u32(smem + rn.slot * F::SLOT);
           wait(&full[rn.slot], rn.phase);
-          rn.next(F::SLOTS);
-          rn.next(F::SLOTS);
+          rn.next(SLOTS);
+          rn.next(SLOTS);
           if (!ok) return;
           tc_fence_after();
           if (elect_one()) {
@@ -469,12 +472,13 @@ __device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t
           int tok, n;
           chunk_at(w, p.rev, it.c, tok, n);
           const Ring rq = r;
-          r.next(F::SLOTS);
+          if (!so) r.next(SLOTS);
           const Ring rk = r;
-          r.next(F::SLOTS);
+          r.next(SLOTS);
           const Ring rv = r;
-          r.next(F::SLOTS);
-          const uint32_t sq = smem_u32(smem + rq.slot * F::SLOT), sk = smem_u32(smem + rk.slot * F::SLOT),
+          r.next(SLOTS);
+          // (the second terms of the keys take the place of q)
+          const uint32_t sq = smem_u32(so ? copy + (i & 1) * F::SLOT : smem + rq.slot * F::SLOT), sk = smem_u32(smem + rk.slot * F::SLOT),
                          sv = smem_u32(smem + rv.slot * F::SLOT);
           if (!so) {
             if (first_q(sub)) {
@@ -513,7 +517,7 @@ __device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t
             // the next item's scores before this one's keys enter, if its tiles are there
             if (i + 1 < items) {
               Ring x = rn;
-              x.next(F::SLOTS);
+              x.next(SLOTS);
               early = __all_sync(0xFFFFFFFFu, mbar_test(&full[rn.slot], rn.phase) && mbar_test(&full[x.slot], x.phase));
               if (early) scores();
             }
@@ -537,7 +541,7 @@ __device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t
           }
           if (sub == group - 1) ++n_s;
           if (elect_one()) {
-            if (so || !in_q(sub, n)) mma_commit(&empty[rq.slot]);
+            if (!so && !in_q(sub, n)) mma_commit(&empty[rq.slot]);
             mma_commit(&empty[rk.slot]);
             mma_commit(&empty[rv.slot]);
           }
@@ -571,18 +575,16 @@ __device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t
       for (Item it(w, group); it.i < items; it.next()) {
         int tok, n;
         chunk_at(w, p.rev, it.c, tok, n);
-        const Ring rq = r;
-        r.next(F::SLOTS);
         const Ring rk = r;
-        r.next(F::SLOTS);
+        r.next(SLOTS);
         const Ring rv = r;
-        r.next(F::SLOTS);
+        r.next(SLOTS);
         bool ok = mbar_wait_short(&full[rk.slot], rk.phase);
         if (ok && n < C) {
           ok = mbar_wait_short(&full[rv.slot], rv.phase);
           if (ok) clear_values<DV>(smem + rv.slot * F::SLOT, n, tid);
         }
-        if (ok) decay_keys<DK>(smem + rk.slot * F::SLOT, smem + rq.slot * F::SLOT, power_of, p.rev, n, tid, 0, 4);
+        if (ok) decay_keys<DK>(smem + rk.slot * F::SLOT, copy + (it.i & 1) * F::SLOT, power_of, p.rev, n, tid, 0, 4);
         fence_proxy_async_smem();
         __syncwarp();
         if (ok && n_k > 0) ok = mbar_wait_short(qs_done, (n_k - 1) & 1);  // (no more than one set ahead)
@@ -599,11 +601,11 @@ __device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t
       int tok, n;
       chunk_at(w, p.rev, it.c, tok, n);
       const int rq = r.slot;
-      r.next(F::SLOTS);
+      r.next(SLOTS);
       const int rk = r.slot;
-      r.next(F::SLOTS);
+      r.next(SLOTS);
       const Ring rv = r;
-      r.next(F::SLOTS);
+      r.next(SLOTS);
       if (n < C) {
         if (!mbar_wait_short(&full[rv.slot], rv.phase)) {
           fail();
@@ -809,10 +811,10 @@ __device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t
       int tok, n;
       chunk_at(w, p.rev, it.c, tok, n);
       const Ring rq = r;
-      r.next(F::SLOTS);
+      r.next(SLOTS);
       const Ring rk = r;
-      r.next(F::SLOTS);
-      r.next(F::SLOTS);
+      r.next(SLOTS);
+      r.next(SLOTS);
       if (!adds_k(it.sub)) continue;
       if (n != n_was) {
         n_was = n;
@@ -959,7 +961,7 @@ int status(cudaError_t e) {
 
 template <int D0, int D1, bool SO>
 int launch(const char* name, const Args& a, bool behind, cudaStream_t st) {
-  constexpr int SMEM = std::max(Cfg<D0, D1>::SMEM, Cfg<D1, D0>::SMEM);
+  constexpr int SMEM = std::max(Cfg<D0, D1>::template SMEM<SO>, Cfg<D1, D0>::template SMEM<SO>);
   const auto kernel = linattn_chunk_kernel<D0, D1, SO>;
   static std::atomic<bool> ready[64];  // by device
   int dev = 0;
@@ -993,8 +995,8 @@ struct Split {
 };
 
 // Segments of the time axis. Estimated from what was measured (us, widths of 128): a CTA takes 6 and
-// 3.3 a chunk and head of its group, one that sums the state alone 5 and 1.7 a chunk and head of the keys,
-// one that finds nothing to do 1; the scan moves every segment's state twice at 5 GB a ms; two more
+// 3.2 a chunk and head of its group (64 wide 2.5), one that sums the state alone 5 and 1.4 (1.0) a chunk and
+// head of the keys, one that finds nothing to do 1; the scan moves every segment's state twice at 5 GB a ms; two more
 // launches 4. The lengths of ragged sequences are on the device: the CTAs with a whole segment are
 // counted as if every sequence but for its last chunk were full of them, and run in rounds over the SMs
 // unless the chunks spread over all SMs take longer. The split with the shortest estimate is taken.
@@ -1004,7 +1006,8 @@ Split split(int N, int T, int max_seqlen, int Hs, int np, int group, int keys, i
   if (T <= 0) T = static_cast<int>(std::min(static_cast<long long>(N) * max_seqlen, 0x7FFFFFFFll));
   Split best{1, chunks > 0 ? chunks : 1};
   const double sms = num_sms(), heads = static_cast<double>(Hs) * np;
-  const double chunk = (Dk <= 64 && Dv <= 64 ? 2.7 : 3.3) * group, sum = 1.7 * keys;
+  const bool narrow = Dk <= 64 && Dv <= 64;
+  const double chunk = (narrow ? 2.5 : 3.2) * group, sum = (narrow ? 1.0 : 1.4) * keys;
   const double all_chunks = std::min(static_cast<double>(N) * chunks, static_cast<double>(T / C) + N);
   double least = 0.0;
   for (int n = 1; n <= 64 && n <= chunks && (n == 1 || heads * N * n <= 16 * sms); ++n) {
