@@ -37,6 +37,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstring>
+#include <utility>
 
 #include "common.cuh"
 #include "gemm.h"
@@ -86,6 +87,8 @@ struct Problem {
   int seg_row, seg_col;
 };
 
+constexpr int kEven = 320;  // CTAs of an even split
+
 struct Args {
   Problem prob[3];
   LinShape s;
@@ -93,6 +96,9 @@ struct Args {
   int nseg;         // segments a sequence may have
   int seg_chunks;   // chunks of one
   int states_only;  // the segments' own sums alone, for the scan
+  // even split: CTA i's state head << 8 | segment (n_even of them; 0: equal segments of every head)
+  int n_even, even_chunks;
+  uint16_t even[kEven];
 };
 
 // ------------------------------------------------------------------ powers of the decay
@@ -128,6 +134,12 @@ __device__ __forceinline__ void store32(void* p, uint4 a, uint4 b) {
                : "memory");
 }
 
+// Chunks that the first segment of state head h is short of: an even split (of one sequence) cuts the heads'
+// chunks, laid one behind the other, into parts of seg_chunks.
+__device__ __forceinline__ int first_short(int n_even, int even_chunks, int seg_chunks, int h) {
+  return n_even ? static_cast<int>(static_cast<long long>(h) * even_chunks % seg_chunks) : 0;
+}
+
 // What a CTA works on.
 struct Work {
   int prob, n, h, seg;
@@ -139,13 +151,19 @@ struct Work {
 
 __device__ __forceinline__ bool find_work(const Args& a, Work& w) {
   int b = blockIdx.x;
-  w.prob = b % a.nprob;
-  b /= a.nprob;
-  const int segs = a.states_only ? a.nseg - 1 : a.nseg;
-  w.seg = b % segs;
-  b /= segs;
-  w.h = b % a.s.Hs;
-  w.n = b / a.s.Hs;
+  if (a.n_even) {
+    w.prob = w.n = 0;
+    w.h = a.even[b] >> 8;
+    w.seg = a.even[b] & 255;
+  } else {
+    w.prob = b % a.nprob;
+    b /= a.nprob;
+    const int segs = a.states_only ? a.nseg - 1 : a.nseg;
+    w.seg = b % segs;
+    b /= segs;
+    w.h = b % a.s.Hs;
+    w.n = b / a.s.Hs;
+  }
   lin_sequence(a.s, w.n, w.start, w.len);
   // (what follows from them is then uniform to the compiler, the MMA descriptors above all)
   w.start = __shfl_sync(0xFFFFFFFFu, w.start, 0);
@@ -155,10 +173,11 @@ __device__ __forceinline__ bool find_work(const Args& a, Work& w) {
     return false;
   }
   w.chunks = (w.len + C - 1) / C;
-  w.c0 = w.seg * a.seg_chunks;
-  w.c1 = min(w.chunks, w.c0 + a.seg_chunks);
+  const int c0 = w.seg * a.seg_chunks - first_short(a.n_even, a.even_chunks, a.seg_chunks, w.h);
+  w.c0 = max(c0, 0);
+  w.c1 = min(w.chunks, c0 + a.seg_chunks);
   w.last = w.c1 == w.chunks;
-  if (a.states_only) return w.c0 + a.seg_chunks < w.chunks;  // a later segment starts from it
+  if (a.states_only) return c0 + a.seg_chunks < w.chunks;  // a later segment starts from it
   return w.c0 < w.chunks || w.seg == 0;
 }
 
@@ -906,7 +925,8 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
 
 // The states at the segments' starts from their own sums (written by a states_only launch one slot
 // further): slot 0 is the sequence's first state, slot s + 1 = lam^(tokens of s) slot s + the sum of s.
-__global__ void __launch_bounds__(128) segment_scan_kernel(LinProblem p, LinShape s, float* seg, int nseg, int seg_chunks) {
+__global__ void __launch_bounds__(128) segment_scan_kernel(LinProblem p, LinShape s, float* seg, int nseg, int seg_chunks,
+                                                           int n_even, int even_chunks) {
   const int h = blockIdx.x % s.Hs, n = blockIdx.x / s.Hs;
   allow_next_kernel();
   wait_for_last_kernel();
@@ -914,13 +934,14 @@ __global__ void __launch_bounds__(128) segment_scan_kernel(LinProblem p, LinShap
   lin_sequence(s, n, start, len);
   if (len < 0) return;
   const int chunks = (len + C - 1) / C;
-  const int used = (chunks + seg_chunks - 1) / seg_chunks;
+  const int lack = first_short(n_even, even_chunks, seg_chunks, h), first_chunks = seg_chunks - lack;
+  const int used = (chunks + lack + seg_chunks - 1) / seg_chunks;
   const float g = fminf(__ldg(s.log_decay + h), 0.0f);
   const int size = p.dk * p.dv;
   const long long base = static_cast<long long>(n) * s.Hs + h;
   // (a reverse recurrence starts with the sequence's last, short chunk)
   float hi0, lo0, hi, lo;
-  power2(g, p.rev ? len - (chunks - seg_chunks) * C : seg_chunks * C, hi0, lo0);
+  power2(g, p.rev ? len - (chunks - first_chunks) * C : first_chunks * C, hi0, lo0);
   power2(g, seg_chunks * C, hi, lo);
   const int e = (blockIdx.y * blockDim.x + threadIdx.x) * 8;  // eight values of one row
   if (e >= size) return;
@@ -972,7 +993,7 @@ int launch(const char* name, const Args& a, bool behind, cudaStream_t st) {
     if (e != cudaSuccess) return status(e);
     if (dev >= 0 && dev < 64) ready[dev].store(true);
   }
-  const long long grid = static_cast<long long>(a.nprob) * a.s.N * a.s.Hs * (SO ? a.nseg - 1 : a.nseg);
+  const long long grid = a.n_even ? a.n_even : static_cast<long long>(a.nprob) * a.s.N * a.s.Hs * (SO ? a.nseg - 1 : a.nseg);
   if (grid >= (1ll << 31)) return MOE_ERR_ARG;
   {
     LaunchTimer lt(name, st);
@@ -992,7 +1013,33 @@ int launch_widths(const char* name, const Args& a, bool behind, cudaStream_t st)
 
 struct Split {
   int nseg, seg_chunks;
+  int n_even;  // CTAs of an even split, or 0
 };
+
+// Segments of state head h in an even split.
+int segments_of(int h, int chunks, int per) {
+  const int lack = static_cast<int>(static_cast<long long>(h) * chunks % per);
+  return (chunks + lack + per - 1) / per;
+}
+
+// The CTAs of an even split: whole segments, then the others, the longer first: an SM that ends one of
+// those early takes the longest of the rest.
+void even_order(const Split& sp, int Hs, int chunks, uint16_t* order) {
+  int n = 0, parts = 0;
+  std::pair<int, uint16_t> part[2 * kEven];
+  for (int h = 0; h < Hs; ++h) {
+    const int lack = static_cast<int>(static_cast<long long>(h) * chunks % sp.seg_chunks);
+    const int segs = segments_of(h, chunks, sp.seg_chunks);
+    for (int k = 0; k < segs; ++k) {
+      const int c0 = std::max(k * sp.seg_chunks - lack, 0), c1 = std::min(chunks, (k + 1) * sp.seg_chunks - lack);
+      const uint16_t id = static_cast<uint16_t>(h << 8 | k);
+      if (c1 - c0 == sp.seg_chunks) order[n++] = id;
+      else part[parts++] = {c0 - c1, id};
+    }
+  }
+  std::sort(part, part + parts);
+  for (int i = 0; i < parts; ++i) order[n++] = part[i].second;
+}
 
 // Segments of the time axis. Estimated from what was measured (us, widths of 128): a CTA takes 6 and
 // 3.2 a chunk and head of its group (64 wide 2.5), one that sums the state alone 5 and 1.4 (1.0) a chunk and
@@ -1004,7 +1051,7 @@ Split split(int N, int T, int max_seqlen, int Hs, int np, int group, int keys, i
   const int chunks = (max_seqlen + C - 1) / C;
   // (a workspace may be asked for before the tokens are counted)
   if (T <= 0) T = static_cast<int>(std::min(static_cast<long long>(N) * max_seqlen, 0x7FFFFFFFll));
-  Split best{1, chunks > 0 ? chunks : 1};
+  Split best{1, chunks > 0 ? chunks : 1, 0};
   const double sms = num_sms(), heads = static_cast<double>(Hs) * np;
   const bool narrow = Dk <= 64 && Dv <= 64;
   const double chunk = (narrow ? 2.5 : 3.2) * group, sum = (narrow ? 1.0 : 1.4) * keys;
@@ -1025,8 +1072,19 @@ Split split(int N, int T, int max_seqlen, int Hs, int np, int group, int keys, i
     if (n > 1) t += pass((n - 1.0) / n, 5.0, sum) + busy * Dk * Dv * 8.0 / 5.0e6 + 4.0;
     if (n == 1 || t < least) {
       least = t;
-      best = Split{n, per};
+      best = Split{n, per, 0};
     }
+  }
+  // One sequence: the heads' chunks laid one behind the other and cut evenly over the SMs. A part that holds
+  // the end of one head and the start of the next is two CTAs, which fill an SM one after the other. (32 heads
+  // of 32,768 tokens: 280 us, in four equal segments on 128 of 152 SMs 304.)
+  if (N == 1 && np == 1 && Hs < sms && chunks > 1) {
+    const int per = static_cast<int>(std::ceil(static_cast<double>(Hs) * chunks / sms));
+    const int slots = (chunks + per - 2) / per + 1;  // of a head, at most
+    int ctas = 0;
+    for (int h = 0; h < Hs; ++h) ctas += segments_of(h, chunks, per);
+    const double t = 12.0 + chunk * per + 10.0 + sum * per + static_cast<double>(Hs) * slots * Dk * Dv * 8.0 / 5.0e6 + 4.0;
+    if (per < chunks && slots < 256 && Hs < 256 && ctas <= kEven && t < least) best = Split{slots, per, ctas};
   }
   return best;
 }
@@ -1056,6 +1114,11 @@ int linattn_run(const LinProblem* p, int np, const LinShape& s, void* ws, cudaSt
   a.nprob = np;
   a.nseg = sp.nseg;
   a.seg_chunks = sp.seg_chunks;
+  a.n_even = sp.n_even;
+  if (sp.n_even) {
+    a.even_chunks = (s.max_seqlen + C - 1) / C;
+    even_order(sp, s.Hs, a.even_chunks, a.even);
+  }
   const long long T = s.T > 0 ? s.T : 1;
   float* slots = static_cast<float*>(ws);
   for (int i = 0; i < np; ++i) {
@@ -1089,7 +1152,7 @@ int linattn_run(const LinProblem* p, int np, const LinShape& s, void* ws, cudaSt
     for (int i = 0; i < own.nprob; ++i) {
       LaunchTimer lt("linattn_scan", st);
       const dim3 grid(static_cast<unsigned>(s.N) * s.Hs, (p[i].dk * p[i].dv + 1023) / 1024);
-      const int se = status(launch_behind(segment_scan_kernel, grid, 128, 0, st, p[i], s, a.prob[i].seg, sp.nseg, sp.seg_chunks));
+      const int se = status(launch_behind(segment_scan_kernel, grid, 128, 0, st, p[i], s, a.prob[i].seg, sp.nseg, sp.seg_chunks, a.n_even, a.even_chunks));
       if (se != MOE_OK) return se;
     }
   }

@@ -335,6 +335,26 @@ def test_long_axis(T, lens_of):
     _check(_make(lens_of, 1, 1, 128, 128, decays=[-2e-3]))
 
 
+@pytest.mark.parametrize("Hs,r,T,most", [(80, 1, 8190, 8192), (80, 2, 8192, 8192), (32, 1, 16300, 16384),
+                                         (80, 1, 3001, 8192), (80, 1, 0, 8192), (151, 1, 20000, 20000)])
+def test_long_axis_of_many_heads(Hs, r, T, most):
+    """One sequence of heads that do not divide the SMs: segments of unequal lengths (151 heads fill the SMs
+    and are not split)."""
+    from sparse_moe_layer_topk_gb300.linattn import LinearAttention
+    x = _make([T], Hs, r, 8, 16, decays=(-0.3 * 1000.0 ** (-np.arange(Hs) / Hs)).tolist(), seed=T + Hs)
+    la = LinearAttention(x["ld"].cuda(), T, 8, 16, r=r, max_seqlen=most, scale=x["scale"], backward=False)
+    assert (la.ws_bytes > 0) == (Hs < 151)
+    y = _cuda(x)
+    o = la.forward(y["q"], y["k"], y["v"], _cu([T]), y["S0"], want_state=True)
+    torch.cuda.synchronize()
+    d = {n: f64(x[n]) for n in ("q", "k", "v", "S0", "ld")}
+    run = lambda f: O.linattn_forward(f(d["q"]), f(d["k"]), f(d["v"]), d["ld"], [T], x["scale"], f(d["S0"]))  # noqa: E731
+    ref, mag = run(lambda a: a), run(np.abs)
+    _close("o", o, ref[0], mag[0], 8)
+    _close("state_out", la.state_out, ref[1], mag[1], 16)
+    assert int(la.err) == 0
+
+
 def test_offsets_past_32_bits():
     """Tokens 2^20 elements apart: the last ones lie past 2^31 elements."""
     T, ld = 2100, 1 << 20
