@@ -151,7 +151,7 @@ def _ptr(x):
 def _stream(s):
     if s is None:
         # (the raw handle: making a torch.cuda.Stream for it takes longer than the call below)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(s, torch.cuda.Stream):
         return s.cuda_stream
     return int(s)
@@ -180,7 +180,9 @@ def _call(name, *args):
     fn, pointers = _BOUND.get(name) or _bind(name)
     conv = list(args)
     for i in pointers:
-        conv[i] = _ptr(conv[i])
+        x = conv[i]
+        if x is not None:  # (the usual tensor without a call of _ptr: a small call's time is the host's)
+            conv[i] = type(x) is torch.Tensor and x.is_cuda and x.data_ptr() or _ptr(x)
     conv[-1] = _stream(conv[-1])
     status = fn(*conv)
     if status != MOE_OK:

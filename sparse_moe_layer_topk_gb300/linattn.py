@@ -63,7 +63,7 @@ class LinearAttention:
             raise ValueError(f"{name} is bf16 [{self.T}, {heads}, {width}], got {x.dtype} "
                              f"{list(x.shape)}")
         token, head, value = x.stride()
-        if (value != 1 or (heads > 1 and head != width)) and x.numel():
+        if (value != 1 or (head != width and heads > 1)) and x.numel():
             raise ValueError(f"{name}: the heads of a token have to be contiguous")
         return token if self.T > 1 else max(token, heads * width)
 
@@ -115,12 +115,13 @@ class LinearAttention:
         returns o."""
         Hq = self.Hs * self.r
         ld = self._operands(q, k, v)
-        if (state.dim() != 4 or state.shape[1:] != (self.Hs, self.Dk, self.Dv)
-                or state.dtype != torch.float32 or not state.is_contiguous()):
+        slots = state.shape[0] if state.dim() else 0
+        if (state.shape != (slots, self.Hs, self.Dk, self.Dv) or state.dtype != torch.float32
+                or not state.is_contiguous()):
             raise ValueError(f"state is fp32 [slots, {self.Hs}, {self.Dk}, {self.Dv}], contiguous")
         if state_idx is not None and (state_idx.dtype != torch.int32 or state_idx.shape != (self.T,)):
             raise ValueError(f"state_idx is int32 [{self.T}]")
-        M.moe_linattn_step(q, k, v, self.log_decay, state, state_idx, state.shape[0], self.T, self.Hs,
+        M.moe_linattn_step(q, k, v, self.log_decay, state, state_idx, slots, self.T, self.Hs,
                            self.r, self.Dk, self.Dv, *ld, Hq * self.Dv, self.scale, self.o, self.err,
                            stream)
         return self.o
