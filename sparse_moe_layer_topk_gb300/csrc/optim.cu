@@ -225,41 +225,46 @@ __device__ __forceinline__ int find_tensor(const AdamwEntry* e, int n, long long
 
 // ------------------------------------------------------------------ gradient norm
 
-// Sum of squares of all gradients. Each CTA writes one partial; the last one to
-// finish adds them in a fixed order, so the norm does not depend on timing.
+constexpr int kNormRun = 4;  // blocks that a warp loads at a time
+static_assert(kChunkBlocks % kNormRun == 0, "a run lies in one tensor");
+
+// Squares of kNormRun blocks of a gradient from byte `at` (the lane's first) on, added to acc; `left`
+// values of the tensor are there from the lane's first on.
+template <int BYTES>
+__device__ __forceinline__ void add_squares(const char* at, long long left, bool vec, f32x2 (&acc)[4]) {
+  uint32_t raw[kNormRun][2 * BYTES];
+#pragma unroll
+  for (int u = 0; u < kNormRun; ++u) {
+    const long long here = left - u * kBlock;
+    const int n = here > 0 ? static_cast<int>(here < 8 ? here : 8) : 0;
+    load_raw(at + u * kBlock * BYTES, n, vec && n == 8, raw[u]);
+  }
+#pragma unroll
+  for (int u = 0; u < kNormRun; ++u) {
+    f32x2 g[4];
+    to_f32(raw[u], g);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] = fma2(g[i], g[i], acc[i]);
+  }
+}
+
+// Sum of squares of all gradients, from the first to the last, each warp a run of blocks in turn. Each CTA
+// writes one partial; the last one to finish adds them in a fixed order, so the norm does not depend
+// on timing. Four blocks a warp are loaded at once, and a small step has few CTAs, whose tickets and partials
+// are its time: a clipped step of 1 M values in a graph 12.2 us, with two blocks and a CTA a chunk 17.0.
 __global__ void __launch_bounds__(kThreads)
-    grad_norm_kernel(const AdamwEntry* entries, int n_tensors, long long chunks, float max_norm,
-                     double* partial, AdamwControl* ctl) {
+    grad_norm_kernel(const AdamwEntry* entries, int n_tensors, long long chunks, float max_norm, double* partial,
+                     AdamwControl* ctl) {
   allow_next_kernel();
   f32x2 acc[4] = {{0}, {0}, {0}, {0}};
-  const auto load = [&](long long c, f32x2 (&g)[4]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) g[i] = pack2(0.0f, 0.0f);
-    if (c >= chunks) return;
-    const AdamwEntry& e = entries[find_tensor(entries, n_tensors, c)];
-    const long long at = (c - e.chunk0) * kAdamwChunk + threadIdx.x * kPerLane;
-    const long long left = e.n - at;
-    if (left <= 0) return;
-    const int n = static_cast<int>(left < 8 ? left : 8);
-    const bool whole = e.vec && n == 8;
-    if (e.g_dtype == MOE_DTYPE_F32) {
-      uint32_t raw[8];
-      load_raw(static_cast<const char*>(e.g) + at * 4, n, whole, raw);
-      to_f32(raw, g);
-    } else {
-      uint32_t raw[4];
-      load_raw(static_cast<const char*>(e.g) + at * 2, n, whole, raw);
-      to_f32(raw, g);
-    }
-  };
-  for (long long c = blockIdx.x; c < chunks; c += 2 * gridDim.x) {
-    f32x2 g0[4], g1[4];
-    load(c, g0);
-    load(c + gridDim.x, g1);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] = fma2(g0[i], g0[i], acc[i]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] = fma2(g1[i], g1[i], acc[i]);
+  const long long blocks = chunks * kChunkBlocks, step = static_cast<long long>(gridDim.x) * (kThreads / 32) * kNormRun;
+  for (long long from = (static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5)) * kNormRun;
+       from < blocks; from += step) {
+    // (a tensor's blocks are a multiple of a run's: a run lies in one)
+    const AdamwEntry& e = entries[find_tensor(entries, n_tensors, from / kChunkBlocks)];
+    const long long at = (from - e.chunk0 * kChunkBlocks) * kBlock + (threadIdx.x & 31) * kPerLane;
+    if (e.g_dtype == MOE_DTYPE_F32) add_squares<4>(static_cast<const char*>(e.g) + at * 4, e.n - at, e.vec, acc);
+    else add_squares<2>(static_cast<const char*>(e.g) + at * 2, e.n - at, e.vec, acc);
   }
   double s = 0.0;
 #pragma unroll
@@ -492,7 +497,6 @@ __global__ void __launch_bounds__(kThreads, Q8 ? 4 : 3)
     adamw_step_kernel(const AdamwEntry* entries, int n_tensors, long long chunks, AdamwHyper h,
                       const float* lr_dev, AdamwControl* ctl, int clipped, long long run, int* err_flag) {
   __shared__ StepConsts sc;
-  if (clipped) wait_for_last_kernel();
   if (threadIdx.x == 0) {
     const long long t = ctl->step + 1;
     sc.lr = lr_dev ? *lr_dev : h.lr;
@@ -501,14 +505,15 @@ __global__ void __launch_bounds__(kThreads, Q8 ? 4 : 3)
     const float bc2 = -expm1f(static_cast<float>(h.log_b2 * static_cast<double>(t)));
     sc.step_size = sc.lr / bc1;
     sc.inv_sqrt_bc2 = 1.0f / sqrtf(bc2);
-    sc.clip = clipped ? ctl->clip : 1.0f;
-    sc.skip = clipped ? ctl->skip : 0;
     sc.b1 = h.b1;
     sc.b2 = h.b2;
     sc.rate1 = h.rate1;
     sc.rate2 = h.rate2;
     sc.eps = h.eps;
     sc.key = mix32(h.seed ^ mix32(static_cast<uint32_t>(t)));
+    if (clipped) wait_for_last_kernel();  // (the norm's; what stands above is the step's before it)
+    sc.clip = clipped ? ctl->clip : 1.0f;
+    sc.skip = clipped ? ctl->skip : 0;
   }
   __syncthreads();
   if (!sc.skip) {
@@ -564,8 +569,9 @@ int adamw_norm_ctas() { return 4 * num_sms(); }
 
 cudaError_t launch_grad_norm(const AdamwEntry* entries, int n, long long chunks, float max_norm,
                              double* partial, AdamwControl* ctl, cudaStream_t st) {
-  const long long most = adamw_norm_ctas();
-  const int grid = static_cast<int>(chunks < most ? chunks : most);
+  const long long most = adamw_norm_ctas(), of_cta = kThreads / 32 * kNormRun;
+  const long long want = (chunks * kChunkBlocks + of_cta - 1) / of_cta;
+  const int grid = static_cast<int>(want < most ? want : most);
   LaunchTimer lt("grad_norm", st);
   grad_norm_kernel<<<grid, kThreads, 0, st>>>(entries, n, chunks, max_norm, partial, ctl);
   return cudaGetLastError();
