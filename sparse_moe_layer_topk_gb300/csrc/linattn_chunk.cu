@@ -62,6 +62,10 @@ struct Cfg {
   // P and the state's copy in two bf16 terms for keys of up to 64 values: the fewer values a product
   // sums, the less their rounding errors average out, and QS is short then.
   static constexpr int TERMS = DK <= 64 ? 2 : 1;
+  // The state's sum has the wider of keys and values as its rows (the tensor memory's lanes, a thread
+  // each): with 64 rows half of the lanes would be idle and the others have twice the columns.
+  static constexpr bool BY_VALUE = DK < DV;
+  static constexpr int ROWS = BY_VALUE ? DV : DK, COLS = BY_VALUE ? DK : DV;
   static constexpr int COPY = DK * DV * 2;  // a term of the state's copy
   static constexpr int MISC = 256 + 1024 + 768;  // barriers; decay factors and powers
   static constexpr int LIMIT = 232448 - 1024;
@@ -452,8 +456,8 @@ __device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t
       // stay in uniform registers and an MMA of 128 x 128 x 16 issues in 67 clocks (a single
       // thread's loop took over 100).
       {
-        const uint32_t i_qk = make_idesc_bf16(C, C, 0, 0), i_qs = make_idesc_bf16(C, DV, 0, 1);
-        const uint32_t i_pv = make_idesc_bf16(C, DV, 0, 1), i_kv = make_idesc_bf16(DK, DV, 1, 1);
+        const uint32_t i_qk = make_idesc_bf16(C, C, 0, 0), i_qs = make_idesc_bf16(C, DV, 0, F::BY_VALUE ? 0 : 1);
+        const uint32_t i_pv = make_idesc_bf16(C, DV, 0, 1), i_kv = make_idesc_bf16(F::ROWS, F::COLS, 1, 1);
         Ring r, rn;  // the item's first slot, and that of the next one's q
         uint32_t n_o = 0, n_s = 0, n_k = 0;  // outputs, states, key sets so far
         bool ok = true;
@@ -511,7 +515,8 @@ __device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t
 #pragma unroll
                   for (int kk = 0; kk < DK / 16; ++kk)
                     mma_bf16_ss(tmem + F::O1, make_sdesc(sq + (kk >> 2) * C * 128 + (kk & 3) * 32, 16, 1024),
-                                make_sdesc(smem_u32(copy) + t * F::COPY + kk * 2048, DK * 128, 1024), i_qs,
+                                F::BY_VALUE ? make_sdesc(smem_u32(copy) + t * F::COPY + kk * 32, 16, 1024)
+                                            : make_sdesc(smem_u32(copy) + t * F::COPY + kk * 2048, DK * 128, 1024), i_qs,
                                 t != 0 || kk != 0);
               }
               __syncwarp();
@@ -549,9 +554,12 @@ __device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
-              for (int kk = 0; kk < 2 * C / 16; ++kk)
-                mma_bf16_ss(tmem + F::Z, make_sdesc((kk < C / 16 ? sk : sq) + (kk & 7) * 2048, C * 128, 1024),
-                            make_sdesc(sv + (kk & 7) * 2048, C * 128, 1024), i_kv, kk != 0 || !(many_q || sub == 0));
+              for (int kk = 0; kk < 2 * C / 16; ++kk) {
+                const uint64_t keys = make_sdesc((kk < C / 16 ? sk : sq) + (kk & 7) * 2048, C * 128, 1024);
+                const uint64_t values = make_sdesc(sv + (kk & 7) * 2048, C * 128, 1024);
+                mma_bf16_ss(tmem + F::Z, F::BY_VALUE ? values : keys, F::BY_VALUE ? keys : values, i_kv,
+                            kk != 0 || !(many_q || sub == 0));
+              }
               if (so) mma_commit(qs_done);
               if (sub == group - 1) mma_commit(z_full);
             }
@@ -762,10 +770,11 @@ __device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kStateRegs));
     const int tid = threadIdx.x - 128 - 32 * kScoreWarps;
     const float g = fminf(log_decay, 0.0f);
-    constexpr int NC = DV / 2;  // columns of a thread
+    constexpr int NC = F::COLS / 2;  // columns of a thread
     const int qd = warp & 3, half = (warp - 4 - kScoreWarps) >> 2;
-    const bool mine = DK == 128 || lane < 16;
-    const int row = DK == 128 ? 32 * qd + lane : 16 * qd + (lane & 15);
+    const bool mine = F::ROWS == 128 || lane < 16;
+    const int row = F::ROWS == 128 ? 32 * qd + lane : 16 * qd + (lane & 15);
+    const int rows = F::BY_VALUE ? p.dv : p.dk, cols = F::BY_VALUE ? p.dk : p.dv;
     const uint32_t trow = tmem + (static_cast<uint32_t>(32 * qd) << 16) + F::Z + half * NC;
     f32x2 S[NC / 2];
     const long long state = (static_cast<long long>(w.n) * a.s.Hs + w.h) * p.dk * p.dv;
@@ -775,31 +784,32 @@ __device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t
     {
       if (!so && seg) wait_for_last_kernel();  // (until here the CTA needs no state)
       const float* in = so ? nullptr : seg ? seg : p.s_in ? p.s_in + state : nullptr;
-      const int sr = seg ? pr.seg_row : p.s_row, sc = seg ? pr.seg_col : p.s_col;
+      const int sk = seg ? pr.seg_row : p.s_row, sv = seg ? pr.seg_col : p.s_col;
+      const int sr = F::BY_VALUE ? sv : sk, sc = F::BY_VALUE ? sk : sv;
       const float* const at = in + static_cast<long long>(row) * sr;
-      const bool have = in && mine && row < p.dk;
+      const bool have = in && mine && row < rows;
       if (sc == 1) {
 #pragma unroll
         for (int j = 0; j < NC / 8; ++j) {
           float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
           const int c = half * NC + 8 * j;
-          if (have && c < p.dv) load_f32x8(at + c, x);
+          if (have && c < cols) load_f32x8(at + c, x);
 #pragma unroll
           for (int e = 0; e < 4; ++e) S[4 * j + e] = pack2(x[2 * e], x[2 * e + 1]);
         }
-      } else {  // (transposed: the lanes' values are neighbours)
+      } else {  // (the lanes' values are neighbours)
 #pragma unroll
         for (int j = 0; j < NC / 2; ++j) {
           const int c = half * NC + 2 * j;
-          const bool real = have && c < p.dv;
+          const bool real = have && c < cols;
           S[j] = pack2(real ? at[static_cast<long long>(c) * sc] : 0.0f, real ? at[static_cast<long long>(c + 1) * sc] : 0.0f);
         }
       }
     }
-    // row `row` of the K x N operand of QS, 64 columns to a 128-byte line: columns c .. c + 7
+    // row `row` of QS' operand, 64 columns to a 128-byte line: columns c .. c + 7
     const auto copy8 = [&](int j) {
       const int c = half * NC + 8 * j;
-      uint8_t* const at = copy + (c >> 6) * DK * 128 + row * 128 + ((((c & 63) >> 3) ^ (row & 7)) << 4);
+      uint8_t* const at = copy + (c >> 6) * F::ROWS * 128 + row * 128 + ((((c & 63) >> 3) ^ (row & 7)) << 4);
       const uint4 t0 = make_uint4(pack_bf16(S[4 * j]), pack_bf16(S[4 * j + 1]), pack_bf16(S[4 * j + 2]), pack_bf16(S[4 * j + 3]));
       if (mine) *reinterpret_cast<uint4*>(at) = t0;
       if (F::TERMS == 2) {
@@ -886,14 +896,20 @@ __device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t
     if (so || (w.last && p.s_out)) {
       // the segment's own sum goes where the scan turns it into the next one's start
       // (a call's state_out is never transposed)
-      float* const out = (so ? seg + static_cast<long long>(p.dk) * p.dv : p.s_out + state) + static_cast<long long>(row) * p.dv;
+      float* const out = so ? seg + static_cast<long long>(p.dk) * p.dv : p.s_out + state;
 #pragma unroll
       for (int j = 0; j < NC / 8; ++j) {
         float x[8];
 #pragma unroll
         for (int e = 0; e < 4; ++e) unpack2(S[4 * j + e], x[2 * e], x[2 * e + 1]);
         const int c = half * NC + 8 * j;
-        if (mine && row < p.dk && c < p.dv) store_f32x8(out + c, x);
+        if (!(mine && row < rows && c < cols)) continue;
+        if (F::BY_VALUE) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) out[static_cast<long long>(c + e) * p.dv + row] = x[e];
+        } else {
+          store_f32x8(out + static_cast<long long>(row) * p.dv + c, x);
+        }
       }
     }
   }
