@@ -361,8 +361,7 @@ __device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t
   // row a lane take 1,024 clocks of the shared-memory pipe a chunk): through the place of the state's
   // copy, which is idle from the chunk's last QS to the next state, or, while another query head's QS is
   // to read that, through the item's q tile. (At narrower widths the copy is sooner done and would wait
-  // for the store: 152 heads x 4,096 tokens, 64 wide, 84 us, staged 87; 16 x 2 heads, 64 / 128 wide, backward
-  // 119, staged 124.)
+  // for the store: 152 heads x 4,096 tokens, 64 wide, 84 us, staged 87.)
   constexpr bool STAGED = DK == C && DV == C;
   static_assert(!STAGED || F::COPY >= C * DV * 2, "room for an output tile");
   const auto staged = [&](int n) { return STAGED && n == C; };
@@ -688,7 +687,8 @@ __device__ __forceinline__ void run_chunks(const Args& a, const Work& w, uint8_t
           for (int j = 0; j < 8; ++j) {
             out[0][j] = pack_bf16(y[2 * j], y[2 * j + 1]);
             if (F::TERMS == 2)
-              out[F::TERMS - 1][j] = pack_bf16(y[2 * j] - bf16_lo(out[0][j]), y[2 * j + 1] - bf16_hi(out[0][j]));
+              out[F::TERMS - 1][j] = pack_bf16(fma2(pack2(bf16_lo(out[0][j]), bf16_hi(out[0][j])), pack2(-1.0f, -1.0f),
+                                                    pack2(y[2 * j], y[2 * j + 1])));
           }
         } else {
 #pragma unroll
