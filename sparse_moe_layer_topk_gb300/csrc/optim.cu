@@ -25,7 +25,7 @@ constexpr int kThreads = 256;
 constexpr int kPerLane = 8;
 constexpr int kBlock = 32 * kPerLane;  // values of one warp, and of one 8-bit block
 constexpr int kChunkBlocks = kAdamwChunk / kBlock;
-static_assert(kThreads * kPerLane == kAdamwChunk, "the norm takes a chunk at once");
+static_assert(kAdamwChunk % kBlock == 0, "chunk");
 static_assert(kBlock == kAdamwBlock, "block");
 
 // ------------------------------------------------------------------ random numbers
