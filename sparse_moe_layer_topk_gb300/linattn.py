@@ -35,6 +35,7 @@ class LinearAttention:
         self.o = e(T, Hq, Dv)
         self.err = torch.zeros(1, dtype=torch.int32, device=dev)
         self._state_out = None
+        self.trains = backward
         if backward:
             self.dq, self.dk, self.dv = e(T, Hq, Dk), e(T, self.Hs, Dk), e(T, self.Hs, Dv)
         self._d_state_in = None
@@ -42,6 +43,7 @@ class LinearAttention:
         self.ws_bytes = max(M.moe_workspace_size(M.MOE_OP_LINATTN_FWD, **dims),
                             M.moe_workspace_size(M.MOE_OP_LINATTN_BWD, **dims) if backward else 0)
         self.ws = torch.empty(max(self.ws_bytes, 256), dtype=torch.uint8, device=dev)
+        self._state_first = None
         self.saved = None
 
     # buffers that only some callers want are made when first asked for
@@ -76,15 +78,30 @@ class LinearAttention:
                               or x.dtype != torch.float32 or not x.is_contiguous()):
             raise ValueError(f"{name} is fp32 {[self.N, self.Hs, self.Dk, self.Dv]}, contiguous")
 
+    def _keep_first(self, state, stream):
+        """A copy, made on the call's stream, of states that the call is about to overwrite."""
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=state.device)
+        with torch.cuda.stream(stream):  # (None: the current one)
+            if self._state_first is None:
+                self._state_first = torch.empty_like(state)
+            return self._state_first.copy_(state)
+
     def forward(self, q, k, v, cu_seqlens=None, state_in=None, want_state: bool = False,
                 stream=None):
         """o [T, Hs * r, Dv] (bf16, this instance's buffer) for q [T, Hs * r, Dk],
         k [T, Hs, Dk], v [T, Hs, Dv]: slices of one projection's rows will do. With
-        want_state, state_out holds each sequence's state after its last token."""
+        want_state, state_out holds each sequence's state after its last token. state_in may be
+        state_out: the states are then updated in place, and backward still starts from those that
+        were there before (this instance keeps a copy). What else was given to this call has to
+        stay as it is until backward."""
         Hq = self.Hs * self.r
         ld = self._operands(q, k, v)
         self._state("state_in", state_in)
-        self.saved = (q, k, v, cu_seqlens, state_in)
+        first = state_in
+        if self.trains and want_state and state_in is not None and state_in.data_ptr() == self.state_out.data_ptr():
+            first = self._keep_first(state_in, stream)
+        self.saved = (q, k, v, cu_seqlens, first)
         M.moe_linattn_fwd(q, k, v, self.log_decay, cu_seqlens, state_in, self.N, self.T,
                           self.max_seqlen, self.Hs, self.r, self.Dk, self.Dv, *ld, Hq * self.Dv,
                           self.scale, self.o, self.state_out if want_state else None, self.ws,

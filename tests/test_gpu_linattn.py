@@ -309,6 +309,41 @@ def test_states_in_place():
     assert torch.equal(la.state_out, want)
 
 
+@pytest.mark.parametrize("how", ["current", "stream", "handle", "graph"])
+@pytest.mark.parametrize("lens,Hs,r", [([200, 0, 15], 2, 1), ([4000], 1, 2)], ids=str)
+def test_backward_of_a_forward_in_place(lens, Hs, r, how):
+    """Consecutive segments by one instance, the states handed on in place: each segment's backward starts from
+    the states before that segment."""
+    parts = [_make(lens, Hs, r, 64, 64, seed=s) for s in (1, 2, 3)]
+    la, cu = _layer(parts[0]), _cu(lens)
+    ys = [_cuda(x) for x in parts]
+    side = torch.cuda.Stream() if how in ("stream", "handle") else None
+    stream = side.cuda_stream if how == "handle" else side
+
+    def segment(y, state):
+        la.forward(y["q"], y["k"], y["v"], cu, state, want_state=True, stream=stream)
+        la.backward(y["do"], y["X"], stream=stream)
+
+    for i, x in enumerate(parts):
+        parts[i] = x = {**x, "ld": parts[0]["ld"], "S0": x["S0"] if i == 0 else la.state_out.clone().cpu()}
+        state = ys[0]["S0"] if i == 0 else la.state_out
+        torch.cuda.synchronize()
+        if how == "graph" and i > 0:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                segment(ys[i], state)
+            graph.replay()
+        else:
+            segment(ys[i], state)
+        torch.cuda.synchronize()
+        ref, mag = _ref(x)
+        _close("o", la.o, ref["o"], mag["o"], 8)
+        for n, t in (("dq", la.dq), ("dk", la.dk), ("dv", la.dv)):
+            _close(n, t, ref[n], mag[n], 8)
+        _close("state_out", la.state_out, ref["S"], mag["S"], 16)
+        _close("d_state_in", la.d_state_in, ref["dS"], mag["dS"], 16)
+
+
 def test_prompt_in_parts_and_tokens_resume_the_state():
     """A prompt at once, in two parts with the state handed on, and its last tokens by the step form
     give the same state and outputs."""
