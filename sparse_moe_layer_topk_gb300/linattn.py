@@ -81,7 +81,9 @@ class LinearAttention:
     def _keep_first(self, state, stream):
         """A copy, made on the call's stream, of states that the call is about to overwrite."""
         if stream is not None and not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=state.device)
+            # (ExternalStream takes a handle of 0, the default stream, for none and makes a new one)
+            stream = (torch.cuda.ExternalStream(int(stream), device=state.device) if int(stream) else
+                      torch.cuda.default_stream(state.device))
         with torch.cuda.stream(stream):  # (None: the current one)
             if self._state_first is None:
                 self._state_first = torch.empty_like(state)

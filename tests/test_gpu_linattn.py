@@ -344,6 +344,23 @@ def test_backward_of_a_forward_in_place(lens, Hs, r, how):
         _close("d_state_in", la.d_state_in, ref["dS"], mag["dS"], 16)
 
 
+@pytest.mark.parametrize("stream", [0, None])
+def test_a_forward_in_place_keeps_states_that_are_still_being_written(stream):
+    """The states come from work that is still under way on the call's stream, the default one."""
+    x = _make([150], 1, 1, 64, 64)
+    la, y, cu = _layer(x), _cuda(x), _cu(x["lens"])
+    la.state_out.zero_()
+    la.forward(y["q"], y["k"], y["v"], cu, la.state_out, want_state=True)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(40_000_000)
+    la.state_out.copy_(y["S0"])
+    la.forward(y["q"], y["k"], y["v"], cu, la.state_out, want_state=True, stream=stream)
+    dq, _, _ = la.backward(y["do"], y["X"], stream=stream)
+    torch.cuda.synchronize()
+    ref, mag = _ref(x)
+    _close("dq", dq, ref["dq"], mag["dq"], 8)
+
+
 def test_prompt_in_parts_and_tokens_resume_the_state():
     """A prompt at once, in two parts with the state handed on, and its last tokens by the step form
     give the same state and outputs."""
