@@ -431,8 +431,9 @@ int moe_linattn_fwd(const uint16_t* q, const uint16_t* k, const uint16_t* v,
  *   R_t = X + scale * sum_a q_t^(a) (dout_t^(a))^T
  *   dq_t^(a) = scale * S_t dout_t^(a);  dk_t = R_t v_t;  dv_t = R_t^T k_t;  then X = lam R_t
  * dk and dv are the sums over the r query heads. d_state_in (nullable) is X before the
- * first token; it must not be d_state_out. dq, dk, dv are bf16 with lddq, lddk, lddv elements between
- * tokens. Workspace: moe_workspace_size(MOE_OP_LINATTN_BWD, max_seqlen, Dk, Dv, Hs, r, T, N). */
+ * first token; it must not share memory with d_state_out or state_in. dq, dk, dv are bf16 with lddq,
+ * lddk, lddv elements between tokens and share no memory with the inputs.
+ * Workspace: moe_workspace_size(MOE_OP_LINATTN_BWD, max_seqlen, Dk, Dv, Hs, r, T, N). */
 int moe_linattn_bwd(const uint16_t* dout, const uint16_t* q, const uint16_t* k, const uint16_t* v,
                     const float* log_decay, const int32_t* cu_seqlens, const float* state_in,
                     const float* d_state_out, int N, int T, int max_seqlen, int Hs, int r, int Dk,

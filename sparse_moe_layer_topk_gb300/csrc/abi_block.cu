@@ -49,6 +49,13 @@ int check_rows(const void* p, long long heads, int width, int ld) {
   return MOE_OK;
 }
 
+// Whether two fp32 arrays of n values share memory.
+bool overlap(const float* a, const float* b, long long n) {
+  if (a == nullptr || b == nullptr) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return (x > y ? x - y : y - x) < static_cast<uintptr_t>(n) * 4;
+}
+
 int check_sequences(const int32_t* cu_seqlens, int N, int T, int max_seqlen) {
   MOE_REQUIRE(N >= 0 && T >= 0 && max_seqlen >= 0, MOE_ERR_ARG);
   if (N > 0 && cu_seqlens == nullptr)
@@ -101,8 +108,10 @@ int moe_linattn_bwd(const uint16_t* dout, const uint16_t* q, const uint16_t* k, 
   MOE_CHECK(check_rows(dq, Hq, Dk, lddq));
   MOE_CHECK(check_rows(dk, Hs, Dk, lddk));
   MOE_CHECK(check_rows(dv, Hs, Dv, lddv));
-  // dk's recurrence reads d_state_out while dv's writes d_state_in
+  // dk's recurrence reads d_state_out, and dq's state_in, while dv's writes d_state_in
+  const long long states = static_cast<long long>(N) * Hs * Dk * Dv;
   MOE_REQUIRE(d_state_in == nullptr || d_state_in != d_state_out, MOE_ERR_ARG);
+  MOE_REQUIRE(!overlap(d_state_in, d_state_out, states) && !overlap(d_state_in, state_in, states), MOE_ERR_ARG);
   MOE_REQUIRE(aligned(state_in, 32) && aligned(d_state_out, 32) && aligned(d_state_in, 32),
               MOE_ERR_ALIGN);
   if (N == 0) return MOE_OK;

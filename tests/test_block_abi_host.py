@@ -55,6 +55,16 @@ def test_backward_refusals(lib, change, want):
     assert _status(lib, "moe_linattn_bwd", BWD, **change) == want
 
 
+@pytest.mark.parametrize("name", ["state_in", "d_state_out"])
+@pytest.mark.parametrize("behind", [0, 32, 65536 - 32, -32, 32 - 65536])
+def test_backward_refuses_a_state_gradient_over_states_that_it_reads(lib, name, behind):
+    """One recurrence of the call reads these states while another writes d_state_in."""
+    assert 65536 == BWD["N"] * BWD["Hs"] * BWD["Dk"] * BWD["Dv"] * 4
+    at = 1 << 20
+    change = {name: at, "d_state_in": at + behind}
+    assert _status(lib, "moe_linattn_bwd", BWD, **change) == M.MOE_ERR_ARG
+
+
 @pytest.mark.parametrize("change,want", COMMON + [
     (dict(state=None), M.MOE_ERR_ARG), (dict(o=None), M.MOE_ERR_ARG), (dict(B=5), M.MOE_ERR_ARG),
     (dict(B=-1), M.MOE_ERR_ARG), (dict(state=P + 8), M.MOE_ERR_ALIGN), (dict(B=0), M.MOE_OK)], ids=str)
