@@ -416,7 +416,8 @@ int moe_route_topk_bwd(const float* d_row_w, const int32_t* slot_of, const int32
  * tokens (T divisible by N).
  * state_in (nullable: zeros) is each sequence's state before its first token,
  * state_out (nullable) its state after the last; an empty sequence copies one to
- * the other. state_out may be state_in. Sums and states are fp32 throughout.
+ * the other. state_out may be state_in, but not overlap it in part; o shares no memory with
+ * the inputs. Sums and states are fp32 throughout.
  * Workspace: moe_workspace_size(MOE_OP_LINATTN_FWD, max_seqlen, Dk, Dv, Hs, r, T, N). */
 int moe_linattn_fwd(const uint16_t* q, const uint16_t* k, const uint16_t* v,
                     const float* log_decay, const int32_t* cu_seqlens, const float* state_in,

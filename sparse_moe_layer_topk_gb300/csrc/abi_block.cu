@@ -83,6 +83,9 @@ int moe_linattn_fwd(const uint16_t* q, const uint16_t* k, const uint16_t* v,
   MOE_CHECK(check_rows(v, Hs, Dv, ldv));
   MOE_CHECK(check_rows(o, Hq, Dv, ldo));
   MOE_REQUIRE(aligned(state_in, 32) && aligned(state_out, 32), MOE_ERR_ALIGN);
+  // in place, or apart: a sequence's last state may not fall on another's first
+  MOE_REQUIRE(state_out == state_in || !overlap(state_out, state_in, static_cast<long long>(N) * Hs * Dk * Dv),
+              MOE_ERR_ARG);
   if (N == 0) return MOE_OK;
   const size_t need = moe_workspace_size(MOE_OP_LINATTN_FWD, max_seqlen, Dk, Dv, Hs, r, T, N);
   MOE_REQUIRE(need == 0 || (ws != nullptr && ws_bytes >= need), MOE_ERR_WORKSPACE);

@@ -65,6 +65,12 @@ def test_backward_refuses_a_state_gradient_over_states_that_it_reads(lib, name, 
     assert _status(lib, "moe_linattn_bwd", BWD, **change) == M.MOE_ERR_ARG
 
 
+@pytest.mark.parametrize("behind", [32, 65536 - 32, -32, 32 - 65536])
+def test_forward_refuses_states_that_overlap_in_part(lib, behind):
+    at = 1 << 20
+    assert _status(lib, "moe_linattn_fwd", FWD, state_in=at, state_out=at + behind) == M.MOE_ERR_ARG
+
+
 @pytest.mark.parametrize("change,want", COMMON + [
     (dict(state=None), M.MOE_ERR_ARG), (dict(o=None), M.MOE_ERR_ARG), (dict(B=5), M.MOE_ERR_ARG),
     (dict(B=-1), M.MOE_ERR_ARG), (dict(state=P + 8), M.MOE_ERR_ALIGN), (dict(B=0), M.MOE_OK)], ids=str)
