@@ -92,13 +92,18 @@ class LinearAttention:
     def forward(self, q, k, v, cu_seqlens=None, state_in=None, want_state: bool = False,
                 stream=None):
         """o [T, Hs * r, Dv] (bf16, this instance's buffer) for q [T, Hs * r, Dk],
-        k [T, Hs, Dk], v [T, Hs, Dv]: slices of one projection's rows will do. With
+        k [T, Hs, Dk], v [T, Hs, Dv]: slices of one projection's rows will do. cu_seqlens (int32
+        [N + 1]): sequence n is the tokens cu_seqlens[n] .. cu_seqlens[n + 1] - 1; without it all
+        have T / N tokens. With
         want_state, state_out holds each sequence's state after its last token. state_in may be
         state_out: the states are then updated in place, and backward still starts from those that
         were there before (this instance keeps a copy). What else was given to this call has to
         stay as it is until backward."""
         Hq = self.Hs * self.r
         ld = self._operands(q, k, v)
+        if cu_seqlens is not None and (cu_seqlens.dtype != torch.int32 or cu_seqlens.shape != (self.N + 1,)
+                                       or not cu_seqlens.is_contiguous()):
+            raise ValueError(f"cu_seqlens is int32 [{self.N + 1}], contiguous")
         self._state("state_in", state_in)
         first = state_in
         if self.trains and want_state and state_in is not None and state_in.data_ptr() == self.state_out.data_ptr():

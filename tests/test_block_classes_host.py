@@ -1,0 +1,35 @@
+"""What the classes of the mixer and the optimizer refuse, before any call of the library reaches a GPU:
+every operand here lies in host memory."""
+import pytest
+import torch
+
+from sparse_moe_layer_topk_gb300 import _lib as M
+from sparse_moe_layer_topk_gb300 import build as B
+from sparse_moe_layer_topk_gb300.linattn import LinearAttention
+
+BF = torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    B.build_library()
+    M.load()
+
+
+def _mixer(T=8, N=2, Hs=2, r=1, Dk=64, Dv=64, **kw):
+    la = LinearAttention(torch.zeros(Hs), T, Dk, Dv, r=r, N=N, **kw)
+    return la, [torch.zeros(T, n, w, dtype=BF) for n, w in ((Hs * r, Dk), (Hs, Dk), (Hs, Dv))]
+
+
+@pytest.mark.parametrize("cu", [
+    torch.tensor([0, 3, 8]),                                     # int64, as cumsum makes it of int32 lengths
+    torch.tensor([3, 5], dtype=torch.int32).cumsum(0),
+    torch.tensor([3, 8], dtype=torch.int32),                     # N entries
+    torch.tensor([0, 3, 5, 8], dtype=torch.int32),
+    torch.tensor([[0, 3, 8]], dtype=torch.int32),
+    torch.tensor([0, 9, 3, 9, 8], dtype=torch.int32)[::2],       # every other entry
+    torch.tensor([0.0, 3.0, 8.0])], ids=str)
+def test_sequence_bounds_of_another_form(cu):
+    la, qkv = _mixer(max_seqlen=8)
+    with pytest.raises(ValueError, match="cu_seqlens"):
+        la.forward(*qkv, cu)
