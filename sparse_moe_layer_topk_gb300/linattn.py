@@ -143,8 +143,9 @@ class LinearAttention:
         if (state.shape != (slots, self.Hs, self.Dk, self.Dv) or state.dtype != torch.float32
                 or not state.is_contiguous()):
             raise ValueError(f"state is fp32 [slots, {self.Hs}, {self.Dk}, {self.Dv}], contiguous")
-        if state_idx is not None and (state_idx.dtype != torch.int32 or state_idx.shape != (self.T,)):
-            raise ValueError(f"state_idx is int32 [{self.T}]")
+        if state_idx is not None and (state_idx.dtype != torch.int32 or state_idx.shape != (self.T,)
+                                      or not state_idx.is_contiguous()):
+            raise ValueError(f"state_idx is int32 [{self.T}], contiguous")
         M.moe_linattn_step(q, k, v, self.log_decay, state, state_idx, slots, self.T, self.Hs,
                            self.r, self.Dk, self.Dv, *ld, Hq * self.Dv, self.scale, self.o, self.err,
                            stream)

@@ -33,3 +33,10 @@ def test_sequence_bounds_of_another_form(cu):
     la, qkv = _mixer(max_seqlen=8)
     with pytest.raises(ValueError, match="cu_seqlens"):
         la.forward(*qkv, cu)
+
+
+def test_slots_that_are_not_contiguous():
+    la, qkv = _mixer(T=3, N=3)
+    state = torch.zeros(6, 2, 64, 64)
+    with pytest.raises(ValueError, match="state_idx"):
+        la.step(*qkv, state, torch.tensor([0, 9, 1, 9, 2, 9], dtype=torch.int32)[::2])
