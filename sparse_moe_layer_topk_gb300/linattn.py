@@ -67,7 +67,7 @@ class LinearAttention:
         token, head, value = x.stride()
         if (value != 1 or (head != width and heads > 1)) and x.numel():
             raise ValueError(f"{name}: the heads of a token have to be contiguous")
-        return token if self.T > 1 else max(token, heads * width)
+        return token if self.T > 1 else heads * width  # (the stride of a single token means nothing)
 
     def _operands(self, q, k, v):
         return (self._rows("q", q, self.Hs * self.r, self.Dk), self._rows("k", k, self.Hs, self.Dk),

@@ -40,3 +40,10 @@ def test_slots_that_are_not_contiguous():
     state = torch.zeros(6, 2, 64, 64)
     with pytest.raises(ValueError, match="state_idx"):
         la.step(*qkv, state, torch.tensor([0, 9, 1, 9, 2, 9], dtype=torch.int32)[::2])
+
+
+@pytest.mark.parametrize("stride", [0, 1, 128, 1001, (1 << 32) + 136])
+def test_the_stride_of_a_single_token_means_nothing(stride):
+    la, _ = _mixer(T=1, N=1)
+    x = torch.zeros(128, dtype=BF).as_strided((1, 2, 64), (stride, 64, 1))
+    assert la._rows("q", x, 2, 64) == 128
