@@ -67,6 +67,8 @@ class LinearAttention:
         token, head, value = x.stride()
         if (value != 1 or (head != width and heads > 1)) and x.numel():
             raise ValueError(f"{name}: the heads of a token have to be contiguous")
+        if token > 0x7FFFFFFF and self.T > 1:
+            raise ValueError(f"{name}: tokens lie less than 2^31 values apart")
         return token if self.T > 1 else heads * width  # (the stride of a single token means nothing)
 
     def _operands(self, q, k, v):

@@ -47,3 +47,12 @@ def test_the_stride_of_a_single_token_means_nothing(stride):
     la, _ = _mixer(T=1, N=1)
     x = torch.zeros(128, dtype=BF).as_strided((1, 2, 64), (stride, 64, 1))
     assert la._rows("q", x, 2, 64) == 128
+
+
+@pytest.mark.parametrize("stride", [1 << 31, (1 << 32) + 128])
+def test_tokens_too_far_apart(stride):
+    """The library takes the stride as a 32-bit number."""
+    la, _ = _mixer(T=2, N=1)
+    x = torch.empty_strided((2, 2, 64), (stride, 64, 1), dtype=BF, device="meta")
+    with pytest.raises(ValueError, match="apart"):
+        la._rows("q", x, 2, 64)
