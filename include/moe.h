@@ -410,7 +410,8 @@ int moe_route_topk_bwd(const float* d_row_w, const int32_t* slot_of, const int32
  * 32-byte aligned.
  * Sequences: N of them packed on the token axis; sequence n is the tokens
  * cu_seqlens[n] .. cu_seqlens[n+1]-1 (int32 [N+1], device) and may be empty.
- * max_seqlen is an upper bound of their lengths, known on the host. A sequence
+ * max_seqlen is an upper bound of their lengths, known on the host (any int32; the time axis is
+ * split by it, so a loose one costs time and workspace). A sequence
  * that is out of order, past T or longer than max_seqlen sets MOE_FLAG_BAD_INDEX and is
  * skipped: nothing of it is written. cu_seqlens == NULL means N sequences of T / N
  * tokens (T divisible by N).

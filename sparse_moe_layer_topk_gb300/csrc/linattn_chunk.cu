@@ -48,6 +48,9 @@ namespace moe {
 namespace {
 
 constexpr int C = 128;  // tokens of a chunk
+
+// (unsigned: a length, or a bound given as "any", may lie within a chunk of 2^31)
+__host__ __device__ constexpr int chunks_of(int tokens) { return static_cast<int>((static_cast<unsigned>(tokens) + C - 1) / C); }
 constexpr int kScoreWarps = 8, kStateWarps = 8;
 constexpr int kThreads = 128 + 32 * (kScoreWarps + kStateWarps);
 // Registers a thread of each warpgroup; together no more than what the block is launched with
@@ -176,7 +179,7 @@ __device__ __forceinline__ bool find_work(const Args& a, Work& w) {
     if (threadIdx.x == 0 && w.seg == 0 && w.h == 0) set_flag(a.s.err_flag, MOE_FLAG_BAD_INDEX);
     return false;
   }
-  w.chunks = (w.len + C - 1) / C;
+  w.chunks = chunks_of(w.len);
   const int c0 = w.seg * a.seg_chunks - first_short(a.n_even, a.even_chunks, a.seg_chunks, w.h);
   w.c0 = max(c0, 0);
   w.c1 = min(w.chunks, c0 + a.seg_chunks);
@@ -949,7 +952,7 @@ __global__ void __launch_bounds__(128) segment_scan_kernel(LinProblem p, LinShap
   int start, len;
   lin_sequence(s, n, start, len);
   if (len < 0) return;
-  const int chunks = (len + C - 1) / C;
+  const int chunks = chunks_of(len);
   const int lack = first_short(n_even, even_chunks, seg_chunks, h), first_chunks = seg_chunks - lack;
   const int used = (chunks + lack + seg_chunks - 1) / seg_chunks;
   const float g = fminf(__ldg(s.log_decay + h), 0.0f);
@@ -1064,7 +1067,7 @@ void even_order(const Split& sp, int Hs, int chunks, uint16_t* order) {
 // counted as if every sequence but for its last chunk were full of them, and run in rounds over the SMs
 // unless the chunks spread over all SMs take longer. The split with the shortest estimate is taken.
 Split split(int N, int T, int max_seqlen, int Hs, int np, int group, int keys, int Dk, int Dv) {
-  const int chunks = (max_seqlen + C - 1) / C;
+  const int chunks = chunks_of(max_seqlen);
   // (a workspace may be asked for before the tokens are counted)
   if (T <= 0) T = static_cast<int>(std::min(static_cast<long long>(N) * max_seqlen, 0x7FFFFFFFll));
   Split best{1, chunks > 0 ? chunks : 1, 0};
@@ -1132,7 +1135,7 @@ int linattn_run(const LinProblem* p, int np, const LinShape& s, void* ws, cudaSt
   a.seg_chunks = sp.seg_chunks;
   a.n_even = sp.n_even;
   if (sp.n_even) {
-    a.even_chunks = (s.max_seqlen + C - 1) / C;
+    a.even_chunks = chunks_of(s.max_seqlen);
     even_order(sp, s.Hs, a.even_chunks, a.even);
   }
   const long long T = s.T > 0 ? s.T : 1;

@@ -27,7 +27,7 @@ class LinearAttention:
             raise ValueError("log_decay is an fp32 vector with one entry for each state head")
         self.log_decay = log_decay.contiguous()
         self.Hs, self.r, self.Dk, self.Dv, self.T, self.N = log_decay.numel(), r, Dk, Dv, T, N
-        self.max_seqlen = (T // N if N else 0) if max_seqlen is None else max_seqlen
+        self.max_seqlen = (T // N if N else 0) if max_seqlen is None else min(max_seqlen, 0x7FFFFFFF)
         self.scale = Dk ** -0.5 if scale is None else scale
         dev = log_decay.device
         e = lambda *shape, dt=BF16: torch.empty(shape, dtype=dt, device=dev)  # noqa: E731

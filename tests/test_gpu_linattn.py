@@ -130,6 +130,15 @@ def test_empty_sequences_where_long_ones_were_expected(N, max_seqlen):
     _check(x, LinearAttention(x["ld"].cuda(), 0, 64, 128, r=2, N=N, max_seqlen=max_seqlen, scale=x["scale"]))
 
 
+@pytest.mark.parametrize("most", [2 ** 31 - 1, 2 ** 31 - 100, 2 ** 31 - 128, 10 ** 12])
+@pytest.mark.parametrize("lens,Hs", [([300, 0, 129], 2), ([2900], 3)], ids=str)
+def test_any_bound_of_the_lengths(lens, Hs, most):
+    """A bound that says nothing, up to the last number of its type."""
+    from sparse_moe_layer_topk_gb300.linattn import LinearAttention
+    x = _make(lens, Hs, 1, 64, 128, seed=Hs)
+    _check(x, LinearAttention(x["ld"].cuda(), sum(lens), 64, 128, N=len(lens), max_seqlen=most, scale=x["scale"]))
+
+
 def test_without_states():
     x = _make([200, 90], 2, 2, 64, 64, states=False)
     la = _check(x)
