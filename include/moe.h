@@ -495,8 +495,9 @@ int moe_adamw_plan(const moe_adamw_tensor* tensors, int n_tensors, int state_bit
  * ctl (device, MOE_ADAMW_CTL_BYTES, zeroed before the first step) holds the number
  * of steps taken (int64 at byte 0), the last gradient norm (fp32 at byte 8) and the
  * clip factor (byte 12), so a captured step counts by itself; lr_dev (device fp32,
- * nullable) takes the place of lr. With max_norm > 0 a gradient norm that is not
- * finite leaves every tensor and the count as they are and sets MOE_FLAG_NONFINITE;
+ * nullable) takes the place of lr. The norm is right to 2^-21 at any number of values (those
+ * under 1e-19, whose squares are below fp32's normal numbers, may count for less). With max_norm > 0 a norm that is not finite in
+ * fp32 leaves every tensor and the count as they are and sets MOE_FLAG_NONFINITE;
  * with max_norm <= 0 no norm is computed and such values pass into the tensors. Stochastic
  * rounding depends on (seed, t, tensor, index) alone; results do not depend on
  * timing. Workspace: moe_workspace_size(MOE_OP_ADAMW_STEP, 0, ...). */

@@ -228,10 +228,11 @@ __device__ __forceinline__ int find_tensor(const AdamwEntry* e, int n, long long
 constexpr int kNormRun = 4;  // blocks that a warp loads at a time
 static_assert(kChunkBlocks % kNormRun == 0, "a run lies in one tensor");
 
-// Squares of kNormRun blocks of a gradient from byte `at` (the lane's first) on, added to acc; `left`
-// values of the tensor are there from the lane's first on.
+// Sum of the squares of kNormRun blocks of a gradient from byte `at` (the lane's first) on; `left` values of
+// the tensor are there from the lane's first on. A lane's 32 squares are summed in fp32, in fp64 where
+// one of them is past fp32 (the sum is then infinite, or NaN).
 template <int BYTES>
-__device__ __forceinline__ void add_squares(const char* at, long long left, bool vec, f32x2 (&acc)[4]) {
+__device__ __forceinline__ double sum_squares(const char* at, long long left, bool vec) {
   uint32_t raw[kNormRun][2 * BYTES];
 #pragma unroll
   for (int u = 0; u < kNormRun; ++u) {
@@ -239,6 +240,7 @@ __device__ __forceinline__ void add_squares(const char* at, long long left, bool
     const int n = here > 0 ? static_cast<int>(here < 8 ? here : 8) : 0;
     load_raw(at + u * kBlock * BYTES, n, vec && n == 8, raw[u]);
   }
+  f32x2 acc[4] = {{0}, {0}, {0}, {0}};
 #pragma unroll
   for (int u = 0; u < kNormRun; ++u) {
     f32x2 g[4];
@@ -246,6 +248,25 @@ __device__ __forceinline__ void add_squares(const char* at, long long left, bool
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[i] = fma2(g[i], g[i], acc[i]);
   }
+  float x, y, sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    unpack2(acc[i], x, y);
+    sum += x + y;
+  }
+  if (sum < INFINITY) return sum;
+  double exact = 0.0;
+#pragma unroll
+  for (int u = 0; u < kNormRun; ++u) {
+    f32x2 g[4];
+    to_f32(raw[u], g);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      unpack2(g[i], x, y);
+      exact += static_cast<double>(x) * x + static_cast<double>(y) * y;
+    }
+  }
+  return exact;
 }
 
 // Sum of squares of all gradients, from the first to the last, each warp a run of blocks in turn. Each CTA
@@ -256,22 +277,15 @@ __global__ void __launch_bounds__(kThreads)
     grad_norm_kernel(const AdamwEntry* entries, int n_tensors, long long chunks, float max_norm, double* partial,
                      AdamwControl* ctl) {
   allow_next_kernel();
-  f32x2 acc[4] = {{0}, {0}, {0}, {0}};
+  double s = 0.0;
   const long long blocks = chunks * kChunkBlocks, step = static_cast<long long>(gridDim.x) * (kThreads / 32) * kNormRun;
   for (long long from = (static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5)) * kNormRun;
        from < blocks; from += step) {
     // (a tensor's blocks are a multiple of a run's: a run lies in one)
     const AdamwEntry& e = entries[find_tensor(entries, n_tensors, from / kChunkBlocks)];
     const long long at = (from - e.chunk0 * kChunkBlocks) * kBlock + (threadIdx.x & 31) * kPerLane;
-    if (e.g_dtype == MOE_DTYPE_F32) add_squares<4>(static_cast<const char*>(e.g) + at * 4, e.n - at, e.vec, acc);
-    else add_squares<2>(static_cast<const char*>(e.g) + at * 2, e.n - at, e.vec, acc);
-  }
-  double s = 0.0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float x, y;
-    unpack2(acc[i], x, y);
-    s += static_cast<double>(x) + static_cast<double>(y);
+    if (e.g_dtype == MOE_DTYPE_F32) s += sum_squares<4>(static_cast<const char*>(e.g) + at * 4, e.n - at, e.vec);
+    else s += sum_squares<2>(static_cast<const char*>(e.g) + at * 2, e.n - at, e.vec);
   }
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
@@ -299,7 +313,7 @@ __global__ void __launch_bounds__(kThreads)
   if (threadIdx.x == 0) {
     s = 0.0;
     for (int i = 0; i < kThreads / 32; ++i) s += warp_sum[i];
-    const float norm = __fsqrt_rn(static_cast<float>(s));
+    const float norm = static_cast<float>(__dsqrt_rn(s));
     ctl->grad_norm = norm;
     ctl->clip = fminf(1.0f, max_norm / (norm + 1e-6f));
     ctl->skip = norm < INFINITY ? 0 : 1;

@@ -141,6 +141,38 @@ def test_large_norm_is_one_sum():
     _check_steps(*_tensors([20_000_003, 17], F32, BF), 1, max_norm=1.0)
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("g_dtype", [F32, BF], ids=str)
+@pytest.mark.parametrize("big,max_norm", [(1e19, 1.0), (1e20, 1.0), (-3e25, 1e5), (3e38, 1e12)])
+def test_a_finite_norm_whose_squares_pass_fp32(big, max_norm, g_dtype, bits):
+    """The step is taken and clipped: a norm counts as not finite only where itself is past fp32."""
+    params, grads = _tensors([3000, 17], F32, g_dtype)
+    grads[0][1234] = big
+    grads[1][3] = big / 2
+    if bits == 32:
+        _check_steps(params, grads, 2, max_norm=max_norm)
+        return
+    # (clipped, the other values' v lies below fp32's normal numbers, and with it what 8-bit r can be held to)
+    opt = _adamw(params, grads, max_norm=max_norm, state_bits=8)
+    for step in (1, 2):
+        opt.step()
+        norm, clip = O.clip_factor([f64(g) for g in grads], max_norm)
+        assert abs(float(opt.grad_norm) - norm) <= 2.0 ** -21 * norm
+        assert int(opt.step_count) == step and int(opt.err) == 0
+    for i, at in ((0, 1234), (1, 3)):
+        want = (1 - HYPER["beta1"] ** 2) * clip * f64(grads[i])[at]  # two steps' m, rounded twice to E4M3
+        assert abs(_values8(opt.m[i], opt.m_scale[i])[at] - want) <= 2 * 2.0 ** -3 * abs(want)
+        assert bool(torch.isfinite(params[i]).all())
+
+
+def test_a_norm_past_fp32_is_not_finite():
+    params, grads = _tensors([3000], F32, F32)
+    grads[0][:2] = 3e38
+    opt, was = _adamw(params, grads, max_norm=1.0), params[0].clone()
+    opt.step()
+    assert int(opt.err) == M.MOE_FLAG_NONFINITE and int(opt.step_count) == 0 and torch.equal(params[0], was)
+
+
 def test_no_clipping_below_the_norm():
     params, grads = _tensors([1000], F32, F32)
     a = _check_steps([params[0].clone()], grads, 1, max_norm=1e6)
