@@ -496,9 +496,11 @@ int moe_adamw_plan(const moe_adamw_tensor* tensors, int n_tensors, int state_bit
  * of steps taken (int64 at byte 0), the last gradient norm (fp32 at byte 8) and the
  * clip factor (byte 12), so a captured step counts by itself; lr_dev (device fp32,
  * nullable) takes the place of lr. The norm is right to 2^-21 at any number of values (those
- * under 1e-19, whose squares are below fp32's normal numbers, may count for less). With max_norm > 0 a norm that is not finite in
- * fp32 leaves every tensor and the count as they are and sets MOE_FLAG_NONFINITE;
- * with max_norm <= 0 no norm is computed and such values pass into the tensors. Stochastic
+ * under 1e-19, whose squares are below fp32's normal numbers, may count for less). With
+ * max_norm > 0 a norm that is not finite in fp32 leaves every tensor and the count as they are and
+ * sets MOE_FLAG_NONFINITE; with max_norm <= 0 no norm is computed and such values pass into the tensors. Where v itself passes
+ * fp32 (|c g| above 1.8e19 / sqrt(1 - beta2)), 32-bit states hold infinity, after which the weight only decays;
+ * with 8-bit states that value's weight and states become NaN. Stochastic
  * rounding depends on (seed, t, tensor, index) alone; results do not depend on
  * timing. Workspace: moe_workspace_size(MOE_OP_ADAMW_STEP, 0, ...). */
 int moe_adamw_step(const void* plan, int n_tensors, long long chunks, int state_bits, float lr,

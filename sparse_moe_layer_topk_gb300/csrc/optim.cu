@@ -212,6 +212,15 @@ __device__ __forceinline__ f32x2 sqrt2(f32x2 v) {
   return fma2(d, mul2(y, pack2(0.5f, 0.5f)), g);
 }
 
+// The root where v is finite: sqrt2 makes NaN of an infinite v, which a finite gradient above 1.8e19 /
+// sqrt(1 - b2) leaves, and the weight would be lost. (8-bit states hold no infinity and lose the value anyway.)
+__device__ __forceinline__ f32x2 root_or_inf(f32x2 v, f32x2 root) {
+  float a, b, ra, rb;
+  unpack2(v, a, b);
+  unpack2(root, ra, rb);
+  return pack2(a == INFINITY ? a : ra, b == INFINITY ? b : rb);
+}
+
 // ------------------------------------------------------------------ the chunk's tensor
 
 __device__ __forceinline__ int find_tensor(const AdamwEntry* e, int n, long long chunk) {
@@ -421,6 +430,7 @@ struct Lane {
       mf[i] = sum2(mul2(b1, mf[i]), mul2(rate1, gi));
       vf[i] = sum2(mul2(b2, vf[i]), mul2(mul2(rate2, gi), gi));
       root[i] = sqrt2(vf[i]);
+      if constexpr (!Q8) root[i] = root_or_inf(vf[i], root[i]);
       float da, db, qa, qb;
       unpack2(fma2(root[i], isq, eps), da, db);
       asm("rcp.approx.f32 %0, %1;" : "=f"(qa) : "f"(da));

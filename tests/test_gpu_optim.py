@@ -173,6 +173,34 @@ def test_a_norm_past_fp32_is_not_finite():
     assert int(opt.err) == M.MOE_FLAG_NONFINITE and int(opt.step_count) == 0 and torch.equal(params[0], was)
 
 
+@pytest.mark.parametrize("p_dtype,master", [(F32, False), (BF, True), (BF, False)], ids=str)
+@pytest.mark.parametrize("n", [600, 603])
+def test_a_second_moment_past_fp32_leaves_the_weight_to_its_decay(n, p_dtype, master):
+    """v = inf takes the update to zero and not the weight to NaN, at this step and the next."""
+    params, grads = _tensors([n], p_dtype, F32)
+    grads[0][300], grads[0][n - 1] = 1e21, -3e25
+    opt = _adamw(params, grads, master=master, weight_decay=0.5)
+    keep = 1 - HYPER["lr"] * 0.5
+    for step in (1, 2):
+        before = f64(opt.master[0] if master else params[0])
+        opt.step()
+        got = f64(opt.master[0] if master else params[0])
+        for at in (300, n - 1):
+            assert float(opt.v[0][at]) == float("inf") and np.isfinite(float(opt.m[0][at]))
+            # one rounding of the weight, or one step of bf16
+            assert abs(got[at] - keep * before[at]) <= (2.0 ** -7 if p_dtype == BF and not master else 2.0 ** -22) * abs(before[at])
+        assert np.isfinite(got).all() and int(opt.step_count) == step
+
+
+def test_a_second_moment_past_fp32_in_8_bits_is_lost_alone():
+    params, grads = _tensors([600], F32, F32)
+    grads[0][300] = 1e21
+    opt = _adamw(params, grads, state_bits=8)
+    opt.step()
+    other = torch.arange(600, device="cuda") != 300
+    assert bool(torch.isnan(params[0][300])) and bool(torch.isfinite(params[0][other]).all())
+
+
 def test_no_clipping_below_the_norm():
     params, grads = _tensors([1000], F32, F32)
     a = _check_steps([params[0].clone()], grads, 1, max_norm=1e6)
