@@ -40,6 +40,8 @@ class AdamW:
                 raise ValueError("weights and gradients are fp32 or bf16")
             if p.numel() != g.numel() or p.device != g.device or not p.is_cuda:
                 raise ValueError("a weight and its gradient have the same size and GPU")
+            if p.device != params[0].device:
+                raise ValueError("all tensors of an optimizer are on one GPU")
             if not (p.is_contiguous() and g.is_contiguous()):
                 raise ValueError("weights and gradients are contiguous")
         self.params, self.grads, self.state_bits = params, grads, state_bits

@@ -6,6 +6,7 @@ import torch
 from sparse_moe_layer_topk_gb300 import _lib as M
 from sparse_moe_layer_topk_gb300 import build as B
 from sparse_moe_layer_topk_gb300.linattn import LinearAttention
+from sparse_moe_layer_topk_gb300.optim import AdamW
 
 BF = torch.bfloat16
 
@@ -56,3 +57,22 @@ def test_tokens_too_far_apart(stride):
     x = torch.empty_strided((2, 2, 64), (stride, 64, 1), dtype=BF, device="meta")
     with pytest.raises(ValueError, match="apart"):
         la._rows("q", x, 2, 64)
+
+
+class _OnGpu:
+    """A contiguous fp32 tensor of a GPU, as far as a constructor's checks look at one."""
+    dtype, is_cuda = torch.float32, True
+
+    def __init__(self, n=10, gpu=0):
+        self.n, self.device = n, torch.device("cuda", gpu)
+
+    def numel(self):
+        return self.n
+
+    def is_contiguous(self):
+        return True
+
+
+def test_an_optimizer_of_several_gpus():
+    with pytest.raises(ValueError, match="one GPU"):
+        AdamW([_OnGpu(), _OnGpu(gpu=1)], [_OnGpu(), _OnGpu(gpu=1)], 1e-3)
