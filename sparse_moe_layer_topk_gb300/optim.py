@@ -44,6 +44,9 @@ class AdamW:
                 raise ValueError("all tensors of an optimizer are on one GPU")
             if not (p.is_contiguous() and g.is_contiguous()):
                 raise ValueError("weights and gradients are contiguous")
+        held = sorted((p.data_ptr(), p.numel() * p.element_size()) for p in params if p.numel())
+        if any(a + size > b for (a, size), (b, _) in zip(held, held[1:])):
+            raise ValueError("two weights share memory: a step would update it twice")
         self.params, self.grads, self.state_bits = params, grads, state_bits
         self.lr, self.betas, self.eps, self.max_norm, self.seed = lr, betas, eps, max_norm, seed
         dev = params[0].device

@@ -63,8 +63,14 @@ class _OnGpu:
     """A contiguous fp32 tensor of a GPU, as far as a constructor's checks look at one."""
     dtype, is_cuda = torch.float32, True
 
-    def __init__(self, n=10, gpu=0):
-        self.n, self.device = n, torch.device("cuda", gpu)
+    def __init__(self, n=10, gpu=0, at=0):
+        self.n, self.device, self.at = n, torch.device("cuda", gpu), at
+
+    def data_ptr(self):
+        return self.at
+
+    def element_size(self):
+        return 4
 
     def numel(self):
         return self.n
@@ -76,3 +82,9 @@ class _OnGpu:
 def test_an_optimizer_of_several_gpus():
     with pytest.raises(ValueError, match="one GPU"):
         AdamW([_OnGpu(), _OnGpu(gpu=1)], [_OnGpu(), _OnGpu(gpu=1)], 1e-3)
+
+
+@pytest.mark.parametrize("at", [[4096, 4096], [4096, 8192, 4096 + 36], [4096, 4096 + 40, 4096 + 40]], ids=str)
+def test_an_optimizer_of_weights_that_share_memory(at):
+    with pytest.raises(ValueError, match="share memory"):
+        AdamW([_OnGpu(at=a) for a in at], [_OnGpu() for _ in at], 1e-3)

@@ -122,6 +122,13 @@ def test_views_with_any_alignment(offset, bits, p_dtype):
     _check_steps(*_tensors([5, 300, 3001], p_dtype, F32, offset=offset), 2, bits=bits, max_norm=0.5)
 
 
+def test_weights_that_lie_side_by_side():
+    """Slices of one buffer without a gap, an empty one between them, and one gradient for two of them."""
+    flat = torch.randn(1300, device="cuda")
+    g = 0.1 * torch.randn(500, device="cuda")
+    _check_steps([flat[:500], flat[500:500], flat[500:1000], flat[1000:]], [g, g[:0], g, g[:300]], 2, max_norm=1.0)
+
+
 def test_decay_for_each_tensor_and_shapes():
     params, grads = _tensors([600, 600], F32, F32)
     params, grads = [p.view(20, 30) for p in params], [g.view(20, 30) for g in grads]
