@@ -108,19 +108,25 @@ class AdamW:
 
     def load_state(self, step, m, v, m_scale=None, v_scale=None, master=None):
         """Takes over a state_dict's values (`load_state(**d)`); without a master copy given, it is
-        made from the weights."""
-        self.ctl.zero_()
-        self.ctl[0] = step
-        for mine, given in ((self.m, m), (self.v, v), (self.m_scale, m_scale), (self.v_scale, v_scale),
-                            (self.master, master)):
+        made from the weights. Nothing is taken over where an entry is missing or does not fit."""
+        pairs = []
+        for name, given in dict(m=m, v=v, m_scale=m_scale, v_scale=v_scale, master=master).items():
+            mine = getattr(self, name)
             if mine is None:
                 continue
             if given is None:
-                if mine is not self.master:
+                if name != "master":
                     raise ValueError("8-bit states come with their scales")
                 given = [None if x is None else p.float().flatten() for x, p in zip(mine, self.params)]
+            if len(given) != len(mine):
+                raise ValueError(f"{name}: one entry for each of {len(mine)} tensors, got {len(given)}")
             for dst, src in zip(mine, given):
-                if dst is not None:
-                    if dst.dtype != src.dtype or dst.numel() != src.numel():
-                        raise ValueError("the state has another type or size")
-                    dst.copy_(src.flatten())
+                if dst is None:
+                    continue
+                if src is None or dst.dtype != src.dtype or dst.numel() != src.numel():
+                    raise ValueError(f"{name}: the state has another type or size")
+                pairs.append((dst, src))
+        self.ctl.zero_()
+        self.ctl[0] = step
+        for dst, src in pairs:
+            dst.copy_(src.flatten())

@@ -331,6 +331,28 @@ def test_state_dict_round_trip():
         assert torch.equal(p, x)
 
 
+@pytest.mark.parametrize("change", [dict(m=-1), dict(v=-1), dict(m_scale=-1), dict(v_scale=-1), dict(master=-1),
+                                    dict(master=0), dict(v=1), dict(v_scale=1)], ids=str)
+def test_a_state_that_does_not_fit_is_not_taken_over_in_part(change):
+    """A list without its last entry (-1), an entry missing (0), one of another size (1)."""
+    params, grads = _tensors([3000, 11], BF, BF)
+    opt = _check_steps(params, grads, 2, bits=8, master=True)
+    (name, how), = change.items()
+    was, d = opt.state_dict(), opt.state_dict()
+    for xs in (d["m"], d["v"]):
+        for x in xs:
+            x.zero_()
+    d["step"] = 7
+    d[name] = d[name][:-1] if how == -1 else [d[name][0], None if how == 0 else d[name][1][:-1]]
+    with pytest.raises(ValueError, match=name):
+        opt.load_state(**d)
+    now = opt.state_dict()
+    assert now["step"] == was["step"] == 2
+    for n in ("m", "v", "m_scale", "v_scale", "master"):
+        for a, b in zip(now[n], was[n]):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
 def test_a_tensor_past_32_bits():
     """Indexes past 2^31 reach their own values (bf16, 8-bit states)."""
     n = (1 << 31) + 5000
