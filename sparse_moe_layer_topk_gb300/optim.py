@@ -60,7 +60,7 @@ class AdamW:
         self.m_scale = scales() if state_bits == 8 else None
         self.v_scale = scales() if state_bits == 8 else None
         wide = lambda p: p.dtype == torch.bfloat16  # noqa: E731
-        self.master = [p.float().flatten() if wide(p) else None for p in params] if master else None
+        self.master = [p.detach().float().flatten() if wide(p) else None for p in params] if master else None
         self.ctl = torch.zeros(M.MOE_ADAMW_CTL_BYTES // 8, dtype=torch.int64, device=dev)
         self.err = torch.zeros(1, dtype=torch.int32, device=dev)
         self.lr_dev = None
@@ -117,7 +117,7 @@ class AdamW:
             if given is None:
                 if name != "master":
                     raise ValueError("8-bit states come with their scales")
-                given = [None if x is None else p.float().flatten() for x, p in zip(mine, self.params)]
+                given = [None if x is None else p.detach().float().flatten() for x, p in zip(mine, self.params)]
             if len(given) != len(mine):
                 raise ValueError(f"{name}: one entry for each of {len(mine)} tensors, got {len(given)}")
             for dst, src in zip(mine, given):

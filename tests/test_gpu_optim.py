@@ -353,6 +353,18 @@ def test_a_state_that_does_not_fit_is_not_taken_over_in_part(change):
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
 
 
+def test_parameters_of_a_module():
+    """torch.nn.Parameter weights: the master copies stay out of autograd, and a state loads without no_grad."""
+    params, grads = _tensors([3000, 11], BF, F32)
+    params = [torch.nn.Parameter(p) for p in params]
+    opt = _adamw(params, grads, master=True, max_norm=1.0)
+    assert not any(x.requires_grad for x in opt.master)
+    opt.step()
+    opt.load_state(**opt.state_dict())
+    opt.load_state(1, opt.m, opt.v)
+    assert torch.equal(opt.master[0], params[0].detach().float())
+
+
 def test_a_tensor_past_32_bits():
     """Indexes past 2^31 reach their own values (bf16, 8-bit states)."""
     n = (1 << 31) + 5000
