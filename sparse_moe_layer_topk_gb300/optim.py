@@ -104,11 +104,12 @@ class AdamW:
     def state_dict(self):
         copy = lambda xs: None if xs is None else [None if x is None else x.clone() for x in xs]  # noqa: E731
         return dict(step=int(self.step_count), m=copy(self.m), v=copy(self.v), m_scale=copy(self.m_scale),
-                    v_scale=copy(self.v_scale), master=copy(self.master))
+                    v_scale=copy(self.v_scale), master=copy(self.master), seed=self.seed)
 
-    def load_state(self, step, m, v, m_scale=None, v_scale=None, master=None):
+    def load_state(self, step, m, v, m_scale=None, v_scale=None, master=None, seed=None):
         """Takes over a state_dict's values (`load_state(**d)`); without a master copy given, it is
-        made from the weights. Nothing is taken over where an entry is missing or does not fit."""
+        made from the weights. Nothing is taken over where an entry is missing or does not fit.
+        Without a seed the rounding goes on with this optimizer's own."""
         pairs = []
         for name, given in dict(m=m, v=v, m_scale=m_scale, v_scale=v_scale, master=master).items():
             mine = getattr(self, name)
@@ -128,5 +129,7 @@ class AdamW:
                 pairs.append((dst, src))
         self.ctl.zero_()
         self.ctl[0] = step
+        if seed is not None:
+            self.seed = seed
         for dst, src in pairs:
             dst.copy_(src.flatten())

@@ -365,6 +365,21 @@ def test_parameters_of_a_module():
     assert torch.equal(opt.master[0], params[0].detach().float())
 
 
+@pytest.mark.parametrize("bits,master", [(8, False), (8, True), (32, False)])
+def test_a_resumed_run_rounds_as_the_run_it_resumes(bits, master):
+    """The rounding numbers' seed is part of the state."""
+    params, grads = _tensors([3000], BF, F32)
+    opt = _adamw(params, grads, state_bits=bits, master=master, seed=12345)
+    opt.step()
+    twin, d = [params[0].clone()], opt.state_dict()
+    again = _adamw(twin, grads, state_bits=bits, master=master)
+    again.load_state(**d)
+    opt.step()
+    again.step()
+    assert torch.equal(params[0], twin[0])
+    assert torch.equal(opt.m[0].view(torch.uint8), again.m[0].view(torch.uint8))
+
+
 def test_a_tensor_past_32_bits():
     """Indexes past 2^31 reach their own values (bf16, 8-bit states)."""
     n = (1 << 31) + 5000
