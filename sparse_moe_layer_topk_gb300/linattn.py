@@ -110,7 +110,8 @@ class LinearAttention:
         first = state_in
         if self.trains and want_state and state_in is not None and state_in.data_ptr() == self.state_out.data_ptr():
             first = self._keep_first(state_in, stream)
-        self.saved = (q, k, v, cu_seqlens, first)
+        if self.trains:
+            self.saved = (q, k, v, cu_seqlens, first)
         M.moe_linattn_fwd(q, k, v, self.log_decay, cu_seqlens, state_in, self.N, self.T,
                           self.max_seqlen, self.Hs, self.r, self.Dk, self.Dv, *ld, Hq * self.Dv,
                           self.scale, self.o, self.state_out if want_state else None, self.ws,
@@ -121,6 +122,8 @@ class LinearAttention:
         """(dq, dk, dv) of the last forward call for dout = d loss / d o and d_state_out = d
         loss / d state_out; where the forward was given a state or d_state_out is given,
         d_state_in holds d loss / d state_in."""
+        if not self.trains:
+            raise ValueError("this instance was made without a backward")
         if self.saved is None:
             raise ValueError("backward needs a forward before it")
         q, k, v, cu_seqlens, state_in = self.saved

@@ -517,3 +517,16 @@ def test_class_refusals():
         la.forward(y["q"], y["k"], y["v"], state_in=y["S0"].double())
     with pytest.raises(M.MoEError):
         la.forward(y["q"].cpu(), y["k"], y["v"])
+
+
+def test_an_instance_without_a_backward():
+    """It says so, and keeps none of a prompt's operands alive."""
+    x = _make([10], 2, 1, 64, 64)
+    la, y = _layer(x, backward=False), _cuda(x)
+    held = torch.cuda.memory_allocated()
+    q = y["q"].clone()
+    la.forward(q, y["k"], y["v"], state_in=y["S0"])
+    del q
+    assert torch.cuda.memory_allocated() == held
+    with pytest.raises(ValueError, match="without a backward"):
+        la.backward(y["do"])
