@@ -143,6 +143,55 @@ def test_mixed_types_in_one_step():
     assert torch.equal(b[0][0], opt.master[1].to(BF))
 
 
+@pytest.mark.parametrize("max_norm", [0.0, 1.0])
+@pytest.mark.parametrize("master", [False, True])
+@pytest.mark.parametrize("bits", [32, 8])
+def test_mixed_types_against_the_oracle(bits, master, max_norm):
+    """Tensors of different types behind one another, long enough that a warp's run goes from one type's code
+    into another's (over 608 chunks of 2,048 values), with this file's bounds for each."""
+    kinds = [(700_001, F32, BF), (300, BF, F32), (500_017, BF, BF), (5, F32, F32), (4096, BF, BF), (600_000, F32, F32),
+             (257, BF, F32)]
+    params, grads = map(list, zip(*((p[0], g[0]) for p, g in (_tensors([n], pt, gt, seed=i)
+                                                              for i, (n, pt, gt) in enumerate(kinds)))))
+    seed = 11
+    opt = _adamw(params, grads, state_bits=bits, master=master, max_norm=max_norm, weight_decay=0.1, seed=seed)
+    for step in (1, 2):
+        wide = [x if master and x is not None else p for x, p in zip(opt.master or params, params)]
+        state = lambda x, sc, i: f64(x[i]) if bits == 32 else _values8(x[i], sc[i])  # noqa: E731
+        before = [(f64(wide[i]), state(opt.m, opt.m_scale, i), state(opt.v, opt.v_scale, i) ** (1 if bits == 32 else 2))
+                  for i in range(len(kinds))]
+        opt.step()
+        norm, clip = O.clip_factor([f64(g) for g in grads], max_norm) if max_norm else (0.0, 1.0)
+        extra = 2.0 ** -21 if max_norm else 0.0
+        if max_norm:
+            assert abs(float(opt.grad_norm) - norm) <= 2.0 ** -21 * norm
+        for i, (p0, m0, v0) in enumerate(before):
+            g = f64(grads[i])
+            p, m, v = O.adamw_update(p0, g, m0, v0, step, HYPER["lr"], HYPER["beta1"], HYPER["beta2"], HYPER["eps"], 0.1, clip)
+            mag = HYPER["beta1"] * np.abs(m0) + (1 - HYPER["beta1"]) * clip * np.abs(g)
+            u = O.rounding_numbers(seed, step, i, g.size)
+            if bits == 32:
+                _bounded("m", opt.m[i], m, (2.0 ** -22 + extra) * mag)
+                _bounded("v", opt.v[i], v, (2.0 ** -22 + 2 * extra) * v)
+            else:
+                for x, codes, scales, k in ((m, opt.m[i], opt.m_scale[i], 0), (np.sqrt(v), opt.v[i], opt.v_scale[i], 1)):
+                    y = x / np.repeat(O.block_scales(x), 256)[:x.size]
+                    picked = np.clip(O.round_stochastic(y, O.e4m3_unit(y), u[k]), -448, 448)
+                    assert np.mean(f64(codes.float()) != picked) <= 1e-4 + 1.0 / x.size * (x.size < 10000), i
+                    np.testing.assert_allclose(f64(scales), O.block_scales(x), rtol=2.0 ** -20 + 2 * extra)
+            size = np.abs(HYPER["lr"] * (mag / (1 - HYPER["beta1"] ** step))
+                          / (np.sqrt(v / (1 - HYPER["beta2"] ** step)) + HYPER["eps"]))
+            fine = 2.0 ** -22 * np.abs(p0) + (2.0 ** -20 + 2 * extra) * size
+            if params[i].dtype == F32:
+                _bounded("p", params[i], p, fine)
+            elif master:
+                _bounded("master", opt.master[i], p, fine)
+                assert torch.equal(params[i], opt.master[i].to(BF))
+            else:
+                _bounded("p", params[i], p, fine + 2.0 ** -7 * np.abs(p))
+    assert int(opt.step_count) == 2 and int(opt.err) == 0
+
+
 def test_large_norm_is_one_sum():
     """Twenty million gradients: the fp32 partial sums keep the norm to 2^-21."""
     _check_steps(*_tensors([20_000_003, 17], F32, BF), 1, max_norm=1.0)
