@@ -87,8 +87,8 @@ class AdamW:
     def schedule_on_device(self, lr_dev):
         """From now on the learning rate is read from lr_dev (device fp32 [1]) at each step:
         a captured step follows it."""
-        if lr_dev is not None and (lr_dev.dtype != torch.float32 or not lr_dev.is_cuda):
-            raise ValueError("lr_dev is a device fp32 tensor")
+        if lr_dev is not None and (lr_dev.dtype != torch.float32 or not lr_dev.is_cuda or lr_dev.numel() != 1):
+            raise ValueError("lr_dev is a device fp32 tensor of one value")
         self.lr_dev = lr_dev
 
     @property

@@ -88,3 +88,9 @@ def test_an_optimizer_of_several_gpus():
 def test_an_optimizer_of_weights_that_share_memory(at):
     with pytest.raises(ValueError, match="share memory"):
         AdamW([_OnGpu(at=a) for a in at], [_OnGpu() for _ in at], 1e-3)
+
+
+@pytest.mark.parametrize("n", [0, 2])
+def test_a_learning_rate_of_no_or_several_values(n):
+    with pytest.raises(ValueError, match="one value"):
+        AdamW.__new__(AdamW).schedule_on_device(_OnGpu(n))
