@@ -418,7 +418,13 @@ int moe_route_topk_bwd(const float* d_row_w, const int32_t* slot_of, const int32
  * state_in (nullable: zeros) is each sequence's state before its first token,
  * state_out (nullable) its state after the last; an empty sequence copies one to
  * the other. state_out may be state_in, but not overlap it in part; o shares no memory with
- * the inputs. Sums and states are fp32 throughout.
+ * the inputs. Rows of o that belong to no sequence keep what they hold; rows that two
+ * sequences claim (the second one's start lying before the first one's end) get either's values.
+ * Precision: states are held, carried and summed in fp32, but the tensor cores that make the sums take
+ * bf16. The decayed keys enter a state as two bf16 terms (16 bits): 3e-6 of the state (rms), where fp32
+ * throughout has 5e-7. The scores, and the copy of the state that a chunk's queries read, are one bf16
+ * term for Dk > 64: o is then 2.4e-3 off (rms), rounding o alone being 1.7e-3. For Dk <= 64 they are
+ * two terms and o has its own rounding's error. moe_linattn_step is fp32 throughout.
  * Workspace: moe_workspace_size(MOE_OP_LINATTN_FWD, max_seqlen, Dk, Dv, Hs, r, T, N). */
 int moe_linattn_fwd(const uint16_t* q, const uint16_t* k, const uint16_t* v,
                     const float* log_decay, const int32_t* cu_seqlens, const float* state_in,
@@ -435,6 +441,8 @@ int moe_linattn_fwd(const uint16_t* q, const uint16_t* k, const uint16_t* v,
  * dk and dv are the sums over the r query heads. d_state_in (nullable) is X before the
  * first token; it must not share memory with d_state_out or state_in. dq, dk, dv are bf16 with lddq,
  * lddk, lddv elements between tokens and share no memory with the inputs.
+ * Precision is the forward's: dv is as precise as its o, dq and dk are with Dv in Dk's place (2.4e-3 for
+ * Dv > 64), d_state_in is 3e-6 off.
  * Workspace: moe_workspace_size(MOE_OP_LINATTN_BWD, max_seqlen, Dk, Dv, Hs, r, T, N). */
 int moe_linattn_bwd(const uint16_t* dout, const uint16_t* q, const uint16_t* k, const uint16_t* v,
                     const float* log_decay, const int32_t* cu_seqlens, const float* state_in,

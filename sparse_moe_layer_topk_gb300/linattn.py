@@ -4,7 +4,10 @@ the one-token step of decoding.
 
     S_t = exp(log_decay[h]) S_{t-1} + k_t v_t^T;   o_t = scale S_t^T q_t
 
-Hs state heads, each read by r query heads. PyTorch only provides the device
+Hs state heads, each read by r query heads. The chunked passes hold and sum states in fp32 from
+products of bf16 terms: states are 3e-6 off (rms), outputs and gradients up to 2.4e-3, of which
+1.7e-3 is their own rounding to bf16; the step is fp32 throughout. Bounds, slots and decays that only
+the device can check set bits of `err` (MOE_FLAG_*). PyTorch only provides the device
 buffers and the stream. One instance holds the outputs, workspaces and gradients
 for a fixed number of packed tokens T, so a call allocates nothing.
 """
@@ -22,7 +25,7 @@ class LinearAttention:
                  max_seqlen: int | None = None, scale: float | None = None, backward: bool = True):
         """log_decay: fp32 [Hs] on the device, <= 0. T packed tokens of N sequences, none
         longer than max_seqlen (default: T / N where the sequences are of one length, else T
-        has to be given). scale: Dk ** -0.5 if not given."""
+        has to be given); a longer one is skipped and flagged. scale: Dk ** -0.5 if not given."""
         if log_decay.dtype != torch.float32 or log_decay.dim() != 1:
             raise ValueError("log_decay is an fp32 vector with one entry for each state head")
         self.log_decay = log_decay.contiguous()
