@@ -26,7 +26,8 @@ __device__ __forceinline__ float head_log_decay(const float* log_decay, int h, i
 // of whose loads are under way before the first is used; four CTAs an SM hold 128 KB in flight. The
 // partial sums of o over the rows are joined by shuffles and in shared memory, in a fixed order.
 // Measured: 256 rows x 32 heads, 128 x 128 (1.08 GB): 185 us, 5.8 TB/s, 0.86 of a plain copy's rate;
-// with 16-byte accesses and three CTAs an SM 246. One row: 10 us a call from Python, 2.5 in a graph.
+// with 16-byte accesses and three CTAs an SM 246. (Tiles of 64 columns spill 48 bytes a thread at the
+// 64 registers that four CTAs an SM allow.) One row: 10 us a call from Python, 2.5 in a graph.
 constexpr int kStepThreads = 256;
 constexpr int kStepHeads = 4;  // query heads whose partial sums share one exchange
 

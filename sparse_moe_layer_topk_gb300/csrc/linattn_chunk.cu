@@ -21,7 +21,7 @@
 //                bf16 copy as the B operand of QS
 // Rounding: P and the copy of S that QS reads are bf16 (their error is that of the output's own
 // rounding; with keys of up to 64 values, two bf16 terms). The state itself is summed in fp32 and K~
-// enters the product as two bf16 terms (16 bits and a sign: 2.7e-6 of the state, rms; one term 1.7e-3),
+// enters the product as two bf16 terms (16 bits and a sign: 2.5e-6 of the state, rms; one term 1.7e-3),
 // because the state is an output of the call and is carried over thousands of chunks. A chunk's sum
 // starts from zero and is added in fp32 registers, not in tensor memory, whose accumulation truncates.
 //

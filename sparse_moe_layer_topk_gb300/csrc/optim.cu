@@ -10,9 +10,11 @@
 // bf16, 8-byte of codes. A block is also what shares a scale in the 8-bit states: its largest magnitude
 // is one warp reduction. The 8-bit step moves 10 bytes a value (bf16 weights and gradients) with 73
 // instructions, which weigh more than its bytes: arithmetic runs two values to an instruction, and
-// types are told apart once a run.
-// Measured: 67 M values, bf16 weights with a master copy, fp32 gradients: 325 us, 6.2 TB/s (0.91 of a
-// plain copy's rate); 8-bit states, bf16 weights and gradients: 181 us, 3.7 TB/s, issue slots 73% taken.
+// types are told apart once a run. The 8-bit forms spill 24 - 76 bytes a thread at the 64 registers that four
+// CTAs an SM allow.
+// Measured (67 M values, no clip, in a graph): 32-bit states, bf16 weights with a master copy, fp32 gradients
+// 321 us, 6.3 TB/s (0.92 of a plain copy's rate); 8-bit states, bf16 weights and gradients 177 us, 3.8 TB/s,
+// issue slots 73% taken; 8-bit states, bf16 weights with a master copy, fp32 gradients 218 us, 5.5 TB/s.
 
 #include "common.cuh"
 #include "optim.h"
@@ -281,7 +283,7 @@ __device__ __forceinline__ double sum_squares(const char* at, long long left, bo
 // Sum of squares of all gradients, from the first to the last, each warp a run of blocks in turn. Each CTA
 // writes one partial; the last one to finish adds them in a fixed order, so the norm does not depend
 // on timing. Four blocks a warp are loaded at once, and a small step has few CTAs, whose tickets and partials
-// are its time: a clipped step of 1 M values in a graph 12.2 us, with two blocks and a CTA a chunk 17.0.
+// are its time: a clipped step of 1 M values in a graph 11.9 us, with two blocks and a CTA a chunk 17.0.
 __global__ void __launch_bounds__(kThreads)
     grad_norm_kernel(const AdamwEntry* entries, int n_tensors, long long chunks, float max_norm, double* partial,
                      AdamwControl* ctl) {
@@ -608,8 +610,8 @@ cudaError_t launch_adamw_step(const AdamwEntry* entries, int n, long long chunks
   const long long ctas = (state_bits == 8 ? 4ll : 3ll) * num_sms();
   const int grid = static_cast<int>(chunks < ctas ? chunks : ctas);
   // A warp's run: an equal share of all blocks with 8-bit states, whose instructions have to be spread
-  // evenly (67 M bf16 values: 175 us, in runs of 8 blocks 194); at most 8 blocks with 32-bit ones, which
-  // HBM bounds and which want neighbouring addresses (fp32: 291 us, equal shares 311).
+  // evenly (67 M bf16 values: 177 us, in runs of 8 blocks 10% more); at most 8 blocks with 32-bit ones, which
+  // HBM bounds and which want neighbouring addresses (fp32: 295 us, equal shares 7% more).
   const long long warps = static_cast<long long>(grid) * (kThreads / 32);
   long long run = (chunks * kChunkBlocks + warps - 1) / warps;
   if (state_bits == 32 && run > kChunkBlocks) run = kChunkBlocks;
