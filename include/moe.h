@@ -425,7 +425,8 @@ int moe_route_topk_bwd(const float* d_row_w, const int32_t* slot_of, const int32
  * throughout has 5e-7. The scores, and the copy of the state that a chunk's queries read, are one bf16
  * term for Dk > 64: o is then 2.4e-3 off (rms), rounding o alone being 1.7e-3. For Dk <= 64 they are
  * two terms and o has its own rounding's error. moe_linattn_step is fp32 throughout.
- * Workspace: moe_workspace_size(MOE_OP_LINATTN_FWD, max_seqlen, Dk, Dv, Hs, r, T, N). */
+ * Workspace: moe_workspace_size(MOE_OP_LINATTN_FWD, max_seqlen, Dk, Dv, Hs, r, T, N), 32-byte
+ * aligned. */
 int moe_linattn_fwd(const uint16_t* q, const uint16_t* k, const uint16_t* v,
                     const float* log_decay, const int32_t* cu_seqlens, const float* state_in,
                     int N, int T, int max_seqlen, int Hs, int r, int Dk, int Dv, int ldq, int ldk,
@@ -443,7 +444,8 @@ int moe_linattn_fwd(const uint16_t* q, const uint16_t* k, const uint16_t* v,
  * lddk, lddv elements between tokens and share no memory with the inputs.
  * Precision is the forward's: dv is as precise as its o, dq and dk are with Dv in Dk's place (2.4e-3 for
  * Dv > 64), d_state_in is 3e-6 off.
- * Workspace: moe_workspace_size(MOE_OP_LINATTN_BWD, max_seqlen, Dk, Dv, Hs, r, T, N). */
+ * Workspace: moe_workspace_size(MOE_OP_LINATTN_BWD, max_seqlen, Dk, Dv, Hs, r, T, N), 32-byte
+ * aligned. */
 int moe_linattn_bwd(const uint16_t* dout, const uint16_t* q, const uint16_t* k, const uint16_t* v,
                     const float* log_decay, const int32_t* cu_seqlens, const float* state_in,
                     const float* d_state_out, int N, int T, int max_seqlen, int Hs, int r, int Dk,

@@ -89,6 +89,7 @@ int moe_linattn_fwd(const uint16_t* q, const uint16_t* k, const uint16_t* v,
   if (N == 0) return MOE_OK;
   const size_t need = moe_workspace_size(MOE_OP_LINATTN_FWD, max_seqlen, Dk, Dv, Hs, r, T, N);
   MOE_REQUIRE(need == 0 || (ws != nullptr && ws_bytes >= need), MOE_ERR_WORKSPACE);
+  MOE_REQUIRE(need == 0 || aligned(ws, 32), MOE_ERR_ALIGN);  // (states: 32-byte accesses)
   const LinShape s{cu_seqlens, log_decay, N, T, max_seqlen, Hs, err_flag};
   const LinProblem p{q, k, v, ldq, ldk, ldv, ldo, o, r, 1, Dk, Dv, 0, 1.0f, scale, state_in, state_out, Dv, 1, -1};
   return linattn_run(&p, 1, s, ws, S(stream));
@@ -120,6 +121,7 @@ int moe_linattn_bwd(const uint16_t* dout, const uint16_t* q, const uint16_t* k, 
   if (N == 0) return MOE_OK;
   const size_t need = moe_workspace_size(MOE_OP_LINATTN_BWD, max_seqlen, Dk, Dv, Hs, r, T, N);
   MOE_REQUIRE(need == 0 || (ws != nullptr && ws_bytes >= need), MOE_ERR_WORKSPACE);
+  MOE_REQUIRE(need == 0 || aligned(ws, 32), MOE_ERR_ALIGN);  // (states: 32-byte accesses)
   const LinShape s{cu_seqlens, log_decay, N, T, max_seqlen, Hs, err_flag};
   // dq_t = scale S_t dout_t: the forward's recurrence with k and v exchanged
   const LinProblem pq{dout, v, k, lddo, ldv, ldk, lddq, dq, r, 1, Dv, Dk, 0, 1.0f, scale, state_in, nullptr, 1, Dv, -1};

@@ -88,6 +88,15 @@ def test_workspaces_are_asked_for(lib):
             assert _status(lib, name, base, **big, ws_bytes=need - 1) == M.MOE_ERR_WORKSPACE
 
 
+@pytest.mark.parametrize("by", [4, 16])
+def test_workspaces_of_another_alignment(lib, by):
+    """The states in them are read and written 32 bytes at a time."""
+    big = dict(N=1, T=65536, max_seqlen=65536)
+    for op, name, base in ((M.MOE_OP_LINATTN_FWD, "moe_linattn_fwd", FWD), (M.MOE_OP_LINATTN_BWD, "moe_linattn_bwd", BWD)):
+        assert M.moe_workspace_size(op, T=65536, d=64, l=64, E=2, k=1, f=65536, S=1) > 0
+        assert _status(lib, name, base, **big, ws=P + by) == M.MOE_ERR_ALIGN
+
+
 def _tensor(**change):
     x = dict(p=P, g=P, m=P, v=P, m_scale=None, v_scale=None, master=None, n=5000, weight_decay=0.0,
              p_dtype=M.MOE_DTYPE_F32, g_dtype=M.MOE_DTYPE_F32)
