@@ -80,6 +80,11 @@ extern "C" {
 /* element types (weight gradients, optimizer tensors) */
 #define MOE_DTYPE_F32 0
 #define MOE_DTYPE_BF16 1
+#define MOE_DTYPE_E4M3 2 /* outputs of moe_rmsnorm_fwd */
+
+/* scores of moe_route_scores */
+#define MOE_SCORE_SIGMOID 0
+#define MOE_SCORE_SOFTMAX 1
 
 /* operations with a workspace, for moe_workspace_size */
 #define MOE_OP_ROUTE_TOPK 1
@@ -92,6 +97,11 @@ extern "C" {
 #define MOE_OP_LINATTN_BWD 8
 #define MOE_OP_ADAMW_PLAN 9
 #define MOE_OP_ADAMW_STEP 10
+#define MOE_OP_RMSNORM_BWD 11
+#define MOE_OP_CONV_BWD 12
+#define MOE_OP_SCAN_FWD 13
+#define MOE_OP_SCAN_BWD 14
+#define MOE_OP_SCAN_TILE_STATES 15
 
 int moe_version(void);
 const char* moe_status_string(int status);
@@ -146,6 +156,66 @@ int moe_route_topk_latent(const uint16_t* x, const uint16_t* Wr, const float* bi
  * Its gradient is added by moe_route_topk_bwd (aux_* arguments). */
 int moe_router_aux_loss(const float* logits, const float* bias, int T, int E, float* p_mean,
                         float* loss, void* ws, size_t ws_bytes, void* stream);
+
+/* The router's logits and the latent z of moe_route_topk_latent without the selection. */
+int moe_router_logits_latent(const uint16_t* x, const uint16_t* Wr, const uint16_t* W_dn, int T, int d, int E, int l,
+                             float* logits, uint16_t* z, void* stream);
+
+/* Selection from fp32 logits with scores, a bias for balance and groups of experts:
+ *   s = sigmoid(logits) or softmax(logits) over the E experts (score)
+ *   c = s + bias   (bias fp32 [E] chooses only; without one the logits themselves take c's place)
+ * The experts are `groups` runs of E / groups; a group's value is the sum of its group_top (1 or 2) largest c
+ * (sums of scores without a bias), and the group_k groups with the largest values stay. Of their experts
+ * topk_idx[t][j] (int32) lists the k largest c, ordered by (c desc, id asc); groups of equal value go by their
+ * index. topk_s[t][j] = s; topk_w[t][j] = scale * s / (sum of the k scores), or scale * s without renorm.
+ * The choice is that of values in 64 bits, so it does not depend on how scores are rounded here.
+ * A logit or bias of -infinity takes the expert out: it adds nothing to its group's value, comes after all
+ * others, and its score and weight are 0 where there are too few others. A NaN or +infinity does the same and sets
+ * MOE_FLAG_NONFINITE. Renormalised weights stay right where the scores themselves leave fp32.
+ * groups divides E and is at most 32; group_k * (E / groups) >= k. err_flag nullable. */
+int moe_route_scores(const float* logits, const float* bias, int T, int E, int k, int score, int groups, int group_k,
+                     int group_top, int renorm, float scale, int32_t* topk_idx, float* topk_w, float* topk_s,
+                     int32_t* err_flag, void* stream);
+
+/* Gradient of moe_route_scores' logits, d_logits[T][E] (fp32 or bf16), for the weights' gradient g:
+ *   renorm            d_l = w_j (g_j - sum_i w_i g_i / scale), times (1 - s_j) for the sigmoid; 0 for the others
+ *   sigmoid           d_l = g_j w_j (1 - s_j); 0 for the others
+ *   softmax           d_l[e] = scale p_e (g_e [e chosen] - sum_j s_j g_j), p the softmax of `logits` (needed here alone)
+ * g_j = d_w[t][j], or, with slot_of (of moe_permute), d_w[slot_of[t][j]] of moe_grouped_swiglu_bwd's d_row_w (0 for a
+ * negative slot). d_topk_w (nullable) receives g. The choice is piecewise constant and the bias a constant: no
+ * gradient. An id outside [0, E), or one that its row has named before, has none either and sets
+ * MOE_FLAG_BAD_EXPERT. scale must not be 0. */
+int moe_route_scores_bwd(const float* d_w, const int32_t* slot_of, const float* logits, const int32_t* topk_idx,
+                         const float* topk_w, const float* topk_s, int T, int E, int k, int score, int renorm, float scale,
+                         void* d_logits, int dtype, float* d_topk_w, int32_t* err_flag, void* stream);
+
+/* The products of moe_route_topk_bwd for a given dL = d_logits (bf16 [T][E]): dx_accum += dL @ Wr^T, or, with dz,
+ * dx_accum = dz @ W_dn^T + dL @ Wr^T; dWr = x^T @ dL (fp32 or bf16). */
+int moe_router_grads(const uint16_t* d_logits, const uint16_t* x, const uint16_t* Wr, int T, int d, int E,
+                     uint16_t* dx_accum, void* dWr, int wgrad_dtype, const uint16_t* dz, const uint16_t* W_dn, int l,
+                     void* stream);
+
+/* ---------------------------------------------------------------- norm */
+
+/* Root-mean-square norm of x + residual:
+ *   u = x + residual (residual nullable: u = x);  rstd = 1 / sqrt(mean(u^2) + eps);  y = u rstd weight
+ * x bf16 [T][d], ldx elements between rows; residual and sum [T][d] of res_dtype (fp32 or bf16); weight fp32 [d]. sum
+ * receives u (given exactly when residual is, and may be residual); y is computed from u before it is rounded. y_dtype MOE_DTYPE_BF16:
+ * y bf16 [T][d]. MOE_DTYPE_E4M3: y holds E4M3 bytes of y / y_scale (rounded to nearest even), y_scale fp32 [T][ceil(d / block)] = each
+ * block's largest magnitude / 448, for blocks of 64 or 128 columns or of the whole row (block = d); a block
+ * whose largest magnitude is below 2^-100 has scale 0. Any
+ * finite u is handled, those whose squares pass fp32 too. d is a multiple of 8 up to 16384, ldx of 8; eps > 0. */
+int moe_rmsnorm_fwd(const uint16_t* x, const void* residual, const float* weight, int T, int d, int ldx, int res_dtype,
+                    float eps, void* sum, void* y, int y_dtype, float* y_scale, int block, void* stream);
+
+/* Backward of moe_rmsnorm_fwd for dy (bf16 [T][d]) and d_sum = d loss / d sum (res_dtype [T][d], nullable), from u (sum, or x where
+ * there was no residual; ldu elements between rows, res_dtype): with rstd of u, g = dy weight, n = u rstd,
+ *   du = rstd (g - n mean(g n)) + d_sum;  dw[d] = sum_t dy n   (fp32, nullable)
+ * du is the gradient of x and of residual alike: dx receives it in bf16, d_residual in res_dtype (either may be NULL).
+ * Deterministic. Workspace (for dw): moe_workspace_size(MOE_OP_RMSNORM_BWD, T, d, ...). */
+int moe_rmsnorm_bwd(const uint16_t* dy, const void* u, const float* weight, const void* d_sum, int T, int d,
+                    int ldu, int res_dtype, float eps, uint16_t* dx, void* d_residual, float* dw, void* ws,
+                    size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------- permute */
 
@@ -463,6 +533,74 @@ int moe_linattn_step(const uint16_t* q, const uint16_t* k, const uint16_t* v,
                      const float* log_decay, float* state, const int32_t* state_idx, int n_slots,
                      int B, int Hs, int r, int Dk, int Dv, int ldq, int ldk, int ldv, int ldo,
                      float scale, uint16_t* o, int32_t* err_flag, void* stream);
+
+/* Causal depthwise convolution of W taps (2 to 4) along the tokens of packed sequences (as in moe_linattn_fwd, of any
+ * length), with silu or without:
+ *   p_t[c] = bias[c] + sum_j weight[c][j] x_{t - (W-1) + j}[c];  y = p or p sigmoid(p)
+ * x, y bf16 [T][D], ld* elements between tokens; weight fp32 [D][W], bias fp32 [D] (nullable). state_in (bf16
+ * [N][W-1][D], nullable: zeros) holds the W - 1 inputs before each sequence, the oldest first; state_out (nullable) receives the
+ * last W - 1 of state_in and sequence. The two share no memory. A sequence that ends before it starts or past T, or starts
+ * before an earlier bound, sets MOE_FLAG_BAD_INDEX and is skipped. Rows that belong to no sequence keep what they hold. D and ld*
+ * are multiples of 8. */
+int moe_conv_fwd(const uint16_t* x, const float* weight, const float* bias, const int32_t* cu_seqlens,
+                 const uint16_t* state_in, int N, int T, int D, int W, int ldx, int ldy, int silu, uint16_t* y,
+                 uint16_t* state_out, int32_t* err_flag, void* stream);
+
+/* Backward of moe_conv_fwd for dy and d_state_out (bf16 [N][W-1][D], nullable), from the forward's inputs: dx (bf16), dw
+ * (fp32 [D][W], nullable), db (fp32 [D], nullable), d_state_in (bf16 [N][W-1][D], nullable; shares no memory with the states given). dw and db
+ * are sums over all sequences that were not skipped. Deterministic. Workspace (for dw, db):
+ * moe_workspace_size(MOE_OP_CONV_BWD, T, D, W, 0, 0, 0, N). */
+int moe_conv_bwd(const uint16_t* dy, const uint16_t* x, const float* weight, const float* bias, const int32_t* cu_seqlens,
+                 const uint16_t* state_in, const uint16_t* d_state_out, int N, int T, int D, int W, int lddy, int ldx,
+                 int lddx, int silu, uint16_t* dx, float* dw, float* db, uint16_t* d_state_in, void* ws, size_t ws_bytes,
+                 int32_t* err_flag, void* stream);
+
+/* One token for each of B rows: y[b] from x[b] and the W - 1 inputs at slot state_idx[b] of the cache state (bf16
+ * [n_slots][W-1][D]), which takes x[b] in. Slots as in moe_linattn_step: negative is an empty row (y = 0). */
+int moe_conv_step(const uint16_t* x, const float* weight, const float* bias, uint16_t* state, const int32_t* state_idx,
+                  int n_slots, int B, int D, int W, int ldx, int ldy, int silu, uint16_t* y, int32_t* err_flag,
+                  void* stream);
+
+/* Selective state space scan over packed sequences (as in moe_linattn_fwd): channel c has `states` states with
+ * decays of their own and a step that depends on the token,
+ *   dt_t[c] = softplus(delta_t[c] + dt_bias[c])   (without softplus: the sum itself; dt_bias fp32 [D], nullable)
+ *   h_t[c]  = exp(dt_t[c] A[c]) h_{t-1}[c] + dt_t[c] u_t[c] B_t[g]      (fp32, A fp32 [D][states])
+ *   y_t[c]  = (C_t[g] . h_t[c] + skip[c] u_t[c]) silu(z_t[c])          (skip fp32 [D], z: nullable)
+ * with B and C shared by the D / G channels of a group g. u, delta, z, y bf16 [T][D], B, C bf16 [T][G][states], ld*
+ * elements between tokens. state_in, state_out fp32 [N][D][states] (nullable; state_out may be state_in). tile_states (nullable,
+ * moe_workspace_size(MOE_OP_SCAN_TILE_STATES, 0, D, states, 0, 0, T, N) bytes) receives what moe_scan_bwd needs of this call. A
+ * sequence longer than max_seqlen, or out of place as in moe_conv_fwd, sets MOE_FLAG_BAD_INDEX and is skipped.
+ * Everything is fp32: states are within 1e-6 (rms) of their values, y has its own rounding to bf16. Time steps
+ * and decays are taken as they come: exp(dt A) that passes fp32 makes infinities. D is a multiple of 8 and D / G of 4; states is 4, 8, 12 or 16; ld* of u, delta, z, y are
+ * multiples of 8, of B and C of 4 (8-byte aligned). Workspace:
+ * moe_workspace_size(MOE_OP_SCAN_FWD, max_seqlen, D, states, G, 0, T, N). */
+int moe_scan_fwd(const uint16_t* u, const uint16_t* delta, const float* A, const uint16_t* B, const uint16_t* C,
+                 const float* skip, const uint16_t* z, const float* dt_bias, const int32_t* cu_seqlens,
+                 const float* state_in, int N, int T, int max_seqlen, int D, int states, int G, int ldu, int lddelta,
+                 int ldB, int ldC, int ldz, int ldy, int softplus, uint16_t* y, float* state_out, float* tile_states,
+                 void* ws, size_t ws_bytes, int32_t* err_flag, void* stream);
+
+/* Backward of moe_scan_fwd for dy (bf16 [T][D]) and d_state_out (fp32, nullable), from the forward's inputs and tile_states:
+ * du, ddelta, dz (bf16 [T][D]; dz nullable, unused without z), dB, dC (bf16 [T][G][states], contiguous), dA (fp32
+ * [D][states]), dskip, d_dt_bias (fp32 [D], nullable), d_state_in (fp32 [N][D][states], nullable; not over d_state_out). With X the gradient
+ * that reaches a state from the later tokens and g_t = dy_t silu(z_t):
+ *   R_t = X + g_t C_t;  q = R_t exp(dt A) h_{t-1};  dC_t = sum_c g_t h_t;  dB_t = sum_c dt u_t R_t
+ *   du_t = dt (R_t . B_t) + skip g_t;  d dt_t = A . q + u_t (R_t . B_t);  dA += dt q;  then X = exp(dt A) R_t
+ * Deterministic. Workspace: moe_workspace_size(MOE_OP_SCAN_BWD, max_seqlen, D, states, G, 0, T, N). */
+int moe_scan_bwd(const uint16_t* dy, const uint16_t* u, const uint16_t* delta, const float* A, const uint16_t* B,
+                 const uint16_t* C, const float* skip, const uint16_t* z, const float* dt_bias,
+                 const int32_t* cu_seqlens, const float* tile_states, const float* d_state_out, int N, int T,
+                 int max_seqlen, int D, int states, int G, int lddy, int ldu, int lddelta, int ldB, int ldC, int ldz,
+                 int softplus, uint16_t* du, uint16_t* ddelta, uint16_t* dB, uint16_t* dC, uint16_t* dz, int lddu,
+                 int ldddelta, int lddz, float* dA, float* dskip, float* d_dt_bias, float* d_state_in, void* ws,
+                 size_t ws_bytes, int32_t* err_flag, void* stream);
+
+/* One token for each of `rows` rows: updates the state cache (fp32 [n_slots][D][states]) in place at slot
+ * state_idx[row] and writes y[row]. Slots as in moe_linattn_step. */
+int moe_scan_step(const uint16_t* u, const uint16_t* delta, const float* A, const uint16_t* B, const uint16_t* C,
+                  const float* skip, const uint16_t* z, const float* dt_bias, float* state, const int32_t* state_idx,
+                  int n_slots, int rows, int D, int states, int G, int ldu, int lddelta, int ldB, int ldC, int ldz, int ldy,
+                  int softplus, uint16_t* y, int32_t* err_flag, void* stream);
 
 /* ---------------------------------------------------------------- optimizer */
 

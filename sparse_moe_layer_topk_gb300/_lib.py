@@ -26,6 +26,9 @@ MOE_FLAG_TIMEOUT = 4
 MOE_FLAG_BAD_INDEX = 8
 MOE_DTYPE_F32 = 0
 MOE_DTYPE_BF16 = 1
+MOE_DTYPE_E4M3 = 2
+MOE_SCORE_SIGMOID = 0
+MOE_SCORE_SOFTMAX = 1
 MOE_OP_ROUTE_TOPK = 1
 MOE_OP_PERMUTE = 2
 MOE_OP_GROUPED_SWIGLU_BWD = 3
@@ -36,6 +39,11 @@ MOE_OP_LINATTN_FWD = 7
 MOE_OP_LINATTN_BWD = 8
 MOE_OP_ADAMW_PLAN = 9
 MOE_OP_ADAMW_STEP = 10
+MOE_OP_RMSNORM_BWD = 11
+MOE_OP_CONV_BWD = 12
+MOE_OP_SCAN_FWD = 13
+MOE_OP_SCAN_BWD = 14
+MOE_OP_SCAN_TILE_STATES = 15
 MOE_ADAMW_CTL_BYTES = 64
 
 _P = ctypes.c_void_p
@@ -89,6 +97,18 @@ SIGNATURES = {
     "moe_linattn_step": ([_P] * 6 + [_I] * 10 + [_F, _P, _P, _P], _I),
     "moe_adamw_plan": ([_P, _I, _I, _P, _Z, _P], _I),
     "moe_adamw_step": ([_P, _I, _L, _I, _F, _P, _F, _F, _F, _F, _I, _P, _P, _Z, _P, _P], _I),
+    "moe_router_logits_latent": ([_P] * 3 + [_I] * 4 + [_P] * 3, _I),
+    "moe_route_scores": ([_P] * 2 + [_I] * 8 + [_F] + [_P] * 5, _I),
+    "moe_route_scores_bwd": ([_P] * 6 + [_I] * 5 + [_F] + [_P] + [_I] + [_P] * 3, _I),
+    "moe_router_grads": ([_P] * 3 + [_I] * 3 + [_P] * 2 + [_I] + [_P] * 2 + [_I] + [_P], _I),
+    "moe_rmsnorm_fwd": ([_P] * 3 + [_I] * 4 + [_F] + [_P] * 2 + [_I] + [_P] + [_I] + [_P], _I),
+    "moe_rmsnorm_bwd": ([_P] * 4 + [_I] * 4 + [_F] + [_P] * 4 + [_Z] + [_P], _I),
+    "moe_conv_fwd": ([_P] * 5 + [_I] * 7 + [_P] * 4, _I),
+    "moe_conv_bwd": ([_P] * 7 + [_I] * 8 + [_P] * 5 + [_Z] + [_P] * 2, _I),
+    "moe_conv_step": ([_P] * 5 + [_I] * 7 + [_P] * 3, _I),
+    "moe_scan_fwd": ([_P] * 10 + [_I] * 13 + [_P] * 4 + [_Z] + [_P] * 2, _I),
+    "moe_scan_bwd": ([_P] * 12 + [_I] * 13 + [_P] * 5 + [_I] * 3 + [_P] * 5 + [_Z] + [_P] * 2, _I),
+    "moe_scan_step": ([_P] * 10 + [_I] * 12 + [_P] * 3, _I),
     "moe_diag_wait_timeout": ([ctypes.c_longlong, _P, _P, _P], _I),
     "moe_timing_enable": ([_I], _I),
     "moe_timing_report": ([ctypes.c_char_p, _Z], _I),
@@ -347,6 +367,65 @@ def moe_adamw_step(plan, n_tensors, chunks, state_bits, lr, lr_dev, rate1, rate2
                    ctl, ws, ws_bytes, err_flag=None, stream=None):
     _call("moe_adamw_step", plan, n_tensors, chunks, state_bits, lr, lr_dev, rate1, rate2, eps,
           max_norm, seed, ctl, ws, ws_bytes, err_flag, stream)
+
+def moe_router_logits_latent(x, Wr, W_dn, T, d, E, l, logits, z, stream=None):
+    _call("moe_router_logits_latent", x, Wr, W_dn, T, d, E, l, logits, z, stream)
+
+def moe_route_scores(logits, bias, T, E, k, score, groups, group_k, group_top, renorm, scale, topk_idx, topk_w,
+                     topk_s, err_flag=None, stream=None):
+    _call("moe_route_scores", logits, bias, T, E, k, score, groups, group_k, group_top, renorm, scale, topk_idx,
+          topk_w, topk_s, err_flag, stream)
+
+def moe_route_scores_bwd(d_w, slot_of, logits, topk_idx, topk_w, topk_s, T, E, k, score, renorm, scale,
+                         d_logits, dtype, d_topk_w, err_flag=None, stream=None):
+    _call("moe_route_scores_bwd", d_w, slot_of, logits, topk_idx, topk_w, topk_s, T, E, k, score, renorm, scale,
+          d_logits, dtype, d_topk_w, err_flag, stream)
+
+def moe_router_grads(d_logits, x, Wr, T, d, E, dx_accum, dWr, wgrad_dtype, dz, W_dn, l, stream=None):
+    _call("moe_router_grads", d_logits, x, Wr, T, d, E, dx_accum, dWr, wgrad_dtype, dz, W_dn, l, stream)
+
+def moe_rmsnorm_fwd(x, residual, weight, T, d, ldx, res_dtype, eps, sum, y, y_dtype, y_scale, block, stream=None):
+    _call("moe_rmsnorm_fwd", x, residual, weight, T, d, ldx, res_dtype, eps, sum, y, y_dtype, y_scale, block, stream)
+
+
+def moe_rmsnorm_bwd(dy, u, weight, d_sum, T, d, ldu, res_dtype, eps, dx, d_residual, dw, ws, ws_bytes, stream=None):
+    _call("moe_rmsnorm_bwd", dy, u, weight, d_sum, T, d, ldu, res_dtype, eps, dx, d_residual, dw, ws, ws_bytes, stream)
+
+
+def moe_conv_fwd(x, weight, bias, cu_seqlens, state_in, N, T, D, W, ldx, ldy, silu, y, state_out, err_flag=None,
+                 stream=None):
+    _call("moe_conv_fwd", x, weight, bias, cu_seqlens, state_in, N, T, D, W, ldx, ldy, silu, y, state_out,
+          err_flag, stream)
+
+def moe_conv_bwd(dy, x, weight, bias, cu_seqlens, state_in, d_state_out, N, T, D, W, lddy, ldx, lddx, silu, dx,
+                 dw, db, d_state_in, ws, ws_bytes, err_flag=None, stream=None):
+    _call("moe_conv_bwd", dy, x, weight, bias, cu_seqlens, state_in, d_state_out, N, T, D, W, lddy, ldx, lddx,
+          silu, dx, dw, db, d_state_in, ws, ws_bytes, err_flag, stream)
+
+def moe_conv_step(x, weight, bias, state, state_idx, n_slots, B, D, W, ldx, ldy, silu, y, err_flag=None,
+                  stream=None):
+    _call("moe_conv_step", x, weight, bias, state, state_idx, n_slots, B, D, W, ldx, ldy, silu, y, err_flag,
+          stream)
+
+def moe_scan_fwd(u, delta, A, B, C, skip, z, dt_bias, cu_seqlens, state_in, N, T, max_seqlen, D, states, G, ldu,
+                 lddelta, ldB, ldC, ldz, ldy, softplus, y, state_out, tile_states, ws, ws_bytes, err_flag=None,
+                 stream=None):
+    _call("moe_scan_fwd", u, delta, A, B, C, skip, z, dt_bias, cu_seqlens, state_in, N, T, max_seqlen, D,
+          states, G, ldu, lddelta, ldB, ldC, ldz, ldy, softplus, y, state_out, tile_states, ws, ws_bytes,
+          err_flag, stream)
+
+def moe_scan_bwd(dy, u, delta, A, B, C, skip, z, dt_bias, cu_seqlens, tile_states, d_state_out, N, T,
+                 max_seqlen, D, states, G, lddy, ldu, lddelta, ldB, ldC, ldz, softplus, du, ddelta, dB, dC, dz,
+                 lddu, ldddelta, lddz, dA, dskip, d_dt_bias, d_state_in, ws, ws_bytes, err_flag=None,
+                 stream=None):
+    _call("moe_scan_bwd", dy, u, delta, A, B, C, skip, z, dt_bias, cu_seqlens, tile_states, d_state_out, N, T,
+          max_seqlen, D, states, G, lddy, ldu, lddelta, ldB, ldC, ldz, softplus, du, ddelta, dB, dC, dz, lddu,
+          ldddelta, lddz, dA, dskip, d_dt_bias, d_state_in, ws, ws_bytes, err_flag, stream)
+
+def moe_scan_step(u, delta, A, B, C, skip, z, dt_bias, state, state_idx, n_slots, rows, D, states, G, ldu,
+                  lddelta, ldB, ldC, ldz, ldy, softplus, y, err_flag=None, stream=None):
+    _call("moe_scan_step", u, delta, A, B, C, skip, z, dt_bias, state, state_idx, n_slots, rows, D, states, G,
+          ldu, lddelta, ldB, ldC, ldz, ldy, softplus, y, err_flag, stream)
 
 
 def moe_diag_wait_timeout(limit_ns, err_flag, waited_ns, stream=None):

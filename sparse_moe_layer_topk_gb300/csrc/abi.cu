@@ -9,7 +9,9 @@
 #include "gemm.h"
 #include "kernels.h"
 #include "linattn.h"
+#include "mixer.h"
 #include "optim.h"
+#include "scan.h"
 
 namespace moe {
 
@@ -142,6 +144,71 @@ size_t grouped_bwd_ws(long long R, int f) {
 
 }  // namespace
 
+namespace moe {
+
+// Router logits (fp32) and the latent z of the same x.
+int router_latent_gemm(const uint16_t* x, const uint16_t* Wr, const uint16_t* W_dn, int T, int d, int E, int l,
+                       float* logits, uint16_t* z, cudaStream_t st) {
+  if (T > 128 && E % 128 == 0 && pick_bn(E + l) == 256) {  // CTA pairs: two row blocks or more
+    // one GEMM over [Wr | W_dn]: x is read once; columns < E are the fp32 logits,
+    // the rest the bf16 latent z
+    GemmLaunch G;
+    G.name = "router_latent_gemm";
+    G.BN = 256;
+    G.sched = SCHED_DENSE;
+    G.M = T;
+    G.N = E + l;
+    G.K = d;
+    G.A = view(x, T, d, d);
+    G.B = view(Wr, d, E, E);
+    G.b_mn = 1;
+    G.B2 = view(W_dn, d, l, l);
+    G.ncat = E;
+    G.epi = EPI_STORE;
+    G.C = logits;
+    G.ldc = E;
+    G.c_bf16 = 0;
+    G.C2 = z;
+    G.ldc2 = l;
+    G.c2_bf16 = 1;
+    return gemm_launch(G, st);
+  }
+  MOE_CHECK(moe_router_logits(x, Wr, T, d, E, logits, st));
+  return moe_latent_proj(x, W_dn, T, d, l, z, st);
+}
+
+// Gradients of the router's input and weights from the logits' (bf16).
+int router_grads(const uint16_t* dL, const uint16_t* x, const uint16_t* Wr, int T, int d, int E, uint16_t* dx_accum,
+                 void* dWr, int wgrad_dtype, const uint16_t* dz, const uint16_t* W_dn, int l, cudaStream_t st) {
+  if (dx_accum && dz) {
+    // dx = dz @ W_dn^T + dL @ Wr^T as one GEMM over K = l + E (overwrites dx)
+    GemmLaunch L;
+    L.name = "down_proj_router_dgrad";
+    L.BN = pick_bn(d);
+    L.sched = SCHED_DENSE;
+    L.M = T;
+    L.N = d;
+    L.K = l + E;
+    L.A = view(dz, T, l, l);
+    L.B = view(W_dn, d, l, l);      // B[n = d][k = l], K-major
+    L.kcat = l;
+    L.A2 = view(dL, T, E, E);
+    L.B2 = view(Wr, d, E, E);       // B2[n = d][k = E], K-major
+    L.epi = EPI_STORE;
+    L.C = dx_accum;
+    L.ldc = d;
+    L.c_bf16 = 1;
+    MOE_CHECK(gemm_launch(L, st));
+  } else if (dx_accum) {
+    MOE_CHECK(dense_gemm("router_dgrad", dL, E, 0, Wr, E, 0, T, d, E, dx_accum, d, 1, 1, st));
+  }
+  if (dWr)
+    MOE_CHECK(dense_gemm("router_wgrad", x, d, 1, dL, E, 1, d, E, T, dWr, E, wgrad_dtype == MOE_DTYPE_BF16, 0, st));
+  return MOE_OK;
+}
+
+}  // namespace moe
+
 extern "C" {
 
 int moe_version(void) { return 1; }
@@ -173,6 +240,16 @@ size_t moe_workspace_size(int op, int T, int d, int l, int E, int k, int f, int 
     case MOE_OP_LINATTN_BWD: return linattn_workspace(T, d, l, E, k, f, S, true);
     case MOE_OP_ADAMW_PLAN: return up256(static_cast<size_t>(T) * sizeof(AdamwEntry));
     case MOE_OP_ADAMW_STEP: return up256(static_cast<size_t>(adamw_norm_ctas()) * 8);
+    case MOE_OP_RMSNORM_BWD:
+      return T > 0 && d > 0 ? up256(static_cast<size_t>(rmsnorm_bwd_parts(T, d)) * d * 4) : 0;
+    case MOE_OP_CONV_BWD:
+      return T >= 0 && d > 0 && l > 0 && S > 0 ? up256(static_cast<size_t>(conv_bwd_parts(S, T, d)) * (l + 1) * d * 4) : 0;
+    case MOE_OP_SCAN_FWD:
+    case MOE_OP_SCAN_BWD:
+      if (T < 0 || d <= 0 || l <= 0 || E <= 0 || E > d || f < 0 || S <= 0) return 0;
+      return scan_workspace(T, f, S, d, l, E, op == MOE_OP_SCAN_BWD);
+    case MOE_OP_SCAN_TILE_STATES:
+      return d > 0 && l > 0 && f >= 0 && S > 0 ? scan_tile_states_bytes(f, S, d, l) : 0;
     default: return 0;
   }
 }
@@ -228,34 +305,7 @@ int moe_route_topk_latent(const uint16_t* x, const uint16_t* Wr, const float* bi
   MOE_REQUIRE(ws_bytes >= moe_workspace_size(MOE_OP_ROUTE_TOPK, T, d, 0, E, k, 0, 0),
               MOE_ERR_WORKSPACE);
   float* L = reinterpret_cast<float*>(ws);
-  cudaStream_t st = S(stream);
-  if (T > 128 && E % 128 == 0 && pick_bn(E + l) == 256) {  // CTA pairs: two row blocks or more
-    // one GEMM over [Wr | W_dn]: x is read once; columns < E are the fp32 logits,
-    // the rest the bf16 latent z
-    GemmLaunch G;
-    G.name = "router_latent_gemm";
-    G.BN = 256;
-    G.sched = SCHED_DENSE;
-    G.M = T;
-    G.N = E + l;
-    G.K = d;
-    G.A = view(x, T, d, d);
-    G.B = view(Wr, d, E, E);
-    G.b_mn = 1;
-    G.B2 = view(W_dn, d, l, l);
-    G.ncat = E;
-    G.epi = EPI_STORE;
-    G.C = L;
-    G.ldc = E;
-    G.c_bf16 = 0;
-    G.C2 = z;
-    G.ldc2 = l;
-    G.c2_bf16 = 1;
-    MOE_CHECK(gemm_launch(G, st));
-  } else {
-    MOE_CHECK(moe_router_logits(x, Wr, T, d, E, L, stream));
-    MOE_CHECK(moe_latent_proj(x, W_dn, T, d, l, z, stream));
-  }
+  MOE_CHECK(router_latent_gemm(x, Wr, W_dn, T, d, E, l, L, z, S(stream)));
   return moe_topk_from_logits(L, bias, T, E, k, topk_idx, topk_w, topk_s, err_flag, stream);
 }
 
@@ -868,31 +918,7 @@ int moe_route_topk_bwd(const float* d_row_w, const int32_t* slot_of, const int32
   if (aux_logits) {
     MOE_CHECK(cuda_status(launch_aux_bwd(aux_logits, aux_bias, aux_p_mean, T, E, aux_scale, dL, st)));
   }
-  if (dx_accum && dz) {
-    // dx = dz @ W_dn^T + dL @ Wr^T as one GEMM over K = l + E (overwrites dx)
-    GemmLaunch L;
-    L.name = "down_proj_router_dgrad";
-    L.BN = pick_bn(d);
-    L.sched = SCHED_DENSE;
-    L.M = T;
-    L.N = d;
-    L.K = l + E;
-    L.A = view(dz, T, l, l);
-    L.B = view(W_dn, d, l, l);      // B[n = d][k = l], K-major
-    L.kcat = l;
-    L.A2 = view(dL, T, E, E);
-    L.B2 = view(Wr, d, E, E);       // B2[n = d][k = E], K-major
-    L.epi = EPI_STORE;
-    L.C = dx_accum;
-    L.ldc = d;
-    L.c_bf16 = 1;
-    MOE_CHECK(gemm_launch(L, st));
-  } else if (dx_accum) {
-    MOE_CHECK(dense_gemm("router_dgrad", dL, E, 0, Wr, E, 0, T, d, E, dx_accum, d, 1, 1, st));
-  }
-  if (dWr)
-    MOE_CHECK(dense_gemm("router_wgrad", x, d, 1, dL, E, 1, d, E, T, dWr, E, wgrad_dtype == MOE_DTYPE_BF16, 0, st));
-  return MOE_OK;
+  return router_grads(dL, x, Wr, T, d, E, dx_accum, dWr, wgrad_dtype, dz, W_dn, l, st);
 }
 
 }  // extern "C"

@@ -1,0 +1,971 @@
+// Selective state space scan over packed sequences, its backward, and its step.
+//
+//   dt_t = softplus(delta_t + dt_bias);  h_t = exp(dt_t A) h_{t-1} + dt_t u_t B_t;
+//   y_t = (C_t . h_t + skip u_t) silu(z_t)
+//
+// Every channel has S <= 16 states with decays of their own, so nothing of this is a matrix product: it is an
+// exponential, two products and two sums for each state and token. Four lanes share two channels, four states of each
+// in a lane's fp32 registers, so that a B and a C from shared memory serve both. (One channel a lane: shared memory bounds it. Four:
+// too few warps to hide the arithmetic's latency.) A CTA takes 32 tokens of its channels at a time: whole rows of 128 or 256 bytes
+// arrive by asynchronous copies a tile ahead (a warp fetching its own 16 channels touches four times the cache lines, which cost as
+// much time as the recurrence); (dt, dt u) of two neighbouring channels a thread go to shared memory; then each warp walks
+// the tokens with its 16 channels' states; then skip, gate and store, two neighbouring channels a thread again.
+#include "common.cuh"
+#include "mixer.h"
+#include "scan.h"
+#include "seq.cuh"
+#include "timing.h"
+
+namespace moe {
+
+int num_sms();
+
+namespace {
+
+constexpr unsigned kAll = 0xFFFFFFFFu;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kTile = kScanTile;
+constexpr int kBRow = 20;  // floats of a token's B or C: sixteen and four of padding (no bank conflicts)
+constexpr int kC = 2;           // channels of a lane in the recurrence
+constexpr int kCh = 16;         // channels of a warp
+constexpr int kFwdWarps = 4;
+constexpr int kBwdWarps = 8;
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float sigmoid(float x) { return rcp(1.0f + ex2(-x * kLog2e)); }
+
+// 1 / (1 + exp(-x)) of two values.
+__device__ __forceinline__ float2 sigmoid2(float2 x) {
+  float a, b;
+  unpack2(mul2(pack2(x.x, x.y), pack2(-kLog2e, -kLog2e)), a, b);
+  unpack2(add2(pack2(ex2(a), ex2(b)), pack2(1.0f, 1.0f)), a, b);
+  return make_float2(rcp(a), rcp(b));
+}
+
+// max(x, 0) + log(1 + e), e = exp(-|x|), of two values. The exponent's product is taken in two terms (it would lose |x| 2^-24
+// of e), and log(1 + e) / e is a polynomial of degree 9, fitted on [0, 1] with equal relative errors (5e-9; 1.5e-7 with its
+// roundings), so that small results keep their relative precision: dt multiplies all that reaches a state.
+__device__ __forceinline__ float2 softplus2(float2 x) {
+  const f32x2 n = pack2(fabsf(x.x), fabsf(x.y)), l2e = pack2(-kLog2e, -kLog2e);
+  const f32x2 m = mul2(n, l2e);
+  const f32x2 lost = fma2(n, pack2(kLog2e, kLog2e), m);
+  float a, b;
+  unpack2(m, a, b);
+  f32x2 e = pack2(ex2(a), ex2(b));
+  e = fma2(mul2(e, pack2(-kLn2, -kLn2)), lost, e);
+  constexpr float c[9] = {0.019851261749863625f, -0.056959159672260284f, 0.10603617131710052f, -0.15305569767951965f, 0.19675931334495544f,
+                          -0.24954132735729218f, 0.3332996368408203f,    -0.4999990165233612f, 1.0f};
+  f32x2 p = pack2(-0.003243980696424842f, -0.003243980696424842f);
+#pragma unroll
+  for (int i = 0; i < 9; ++i) p = fma2(p, e, pack2(c[i], c[i]));
+  float2 r;
+  unpack2(fma2(p, e, pack2(fmaxf(x.x, 0.0f), fmaxf(x.y, 0.0f))), r.x, r.y);
+  return r;
+}
+__device__ __forceinline__ float softplus(float x) { return softplus2(make_float2(x, x)).x; }
+
+// Shared-memory loads that the compiler may move over stores (it cannot tell that those go to other places, and would
+// otherwise begin no token before the one ahead of it has stored its results). They stay below the `after_sync` that
+// their address comes from, and above whatever uses their values.
+__device__ __forceinline__ uint32_t after_sync(const void* p) {
+  uint32_t a = smem_u32(p);
+  asm volatile("" : "+r"(a)::"memory");
+  return a;
+}
+__device__ __forceinline__ float4 lds4(uint32_t a) {
+  float4 v;
+  asm("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ float2 lds2(uint32_t a) {
+  float2 v;
+  asm("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a));
+  return v;
+}
+
+// The channels of a CTA: `c0` the first, `have` how many of them there are, all in `group`.
+struct Channels {
+  int c0, have, group;
+};
+
+// Blocks of `width` channels, none across a group's end.
+__device__ __forceinline__ Channels block_channels(int block, int D, int G, int width) {
+  const int per = D / G, blocks = (per + width - 1) / width;
+  const int g = block / blocks, at = (block - g * blocks) * width;
+  return Channels{g * per + at, min(width, per - at), g};
+}
+
+// Asynchronous copies of 16 or 8 bytes; `real` false: nothing is read and zeros are written.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(real ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t to, const void* from, bool real) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(from), "r"(real ? 8 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+// A CTA's channels of one tile after another into shared memory, [token][channel] (bf16). `wide`: rows start on 16 bytes
+// (pieces of eight channels), else on 8 (of four).
+template <int WARPS>
+struct RowStream {
+  static constexpr int kPieces = 2 * WARPS;  // of eight channels in a row
+  const bf16* at;                            // this thread's first piece of the next tile
+  long long ld;
+  bool mine;                                 // whether its channels exist
+  __device__ __forceinline__ RowStream(const void* rows, long long first_row, long long ld_, const Channels& ch, bool wide) {
+    ld = ld_;
+    const int i = threadIdx.x, c = wide ? 8 * (i % kPieces) : 4 * (i % (2 * kPieces)), t = wide ? i / kPieces : i / (2 * kPieces);
+    mine = c < ch.have;
+    at = static_cast<const bf16*>(rows) + (mine ? (first_row + t) * ld + ch.c0 + c : 0);
+  }
+  __device__ __forceinline__ void fetch(uint32_t to, int n, bool wide) const {  // the next tile's first n tokens
+    const int i = threadIdx.x;
+    if (wide) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const bool real = mine && i / kPieces + 16 * k < n;
+        copy16(to + 16 * (i + 32 * WARPS * k), real ? at + 16 * k * ld : at, real);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const bool real = mine && i / (2 * kPieces) + 8 * k < n;
+        copy8(to + 8 * (i + 32 * WARPS * k), real ? at + 8 * k * ld : at, real);
+      }
+    }
+  }
+  __device__ __forceinline__ void move(int tiles) { at += mine ? tiles * kTile * ld : 0; }
+};
+
+// B (and C) of one tile after another, S values a token (a multiple of 4 up to 16), through registers to shared memory, where they are
+// fp32: [token][16] with padding, C after B. A thread has four values of a token, of every WARPS * 4-th one.
+template <int WARPS>
+struct BcStream {
+  static constexpr int kEach = 8 / WARPS;
+  const bf16* at;
+  long long ld;
+  bool mine;
+  uint2 v[kEach];
+  __device__ __forceinline__ BcStream(const void* B, const void* C, long long first_row, long long ldb, long long ldc, const Channels& ch, int S) {
+    const int i = threadIdx.x, piece = i & 3;
+    const bool is_c = i & 4;
+    ld = is_c ? ldc : ldb;
+    mine = 4 * piece < S && (is_c ? C : B) != nullptr;
+    at = static_cast<const bf16*>(is_c ? C : B) + (mine ? (first_row + (i >> 3)) * ld + ch.group * S + 4 * piece : 0);
+  }
+  __device__ __forceinline__ void fetch(int n) {
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      v[k] = make_uint2(0, 0);
+      if (mine && static_cast<int>(threadIdx.x >> 3) + 4 * WARPS * k < n) v[k] = *reinterpret_cast<const uint2*>(at + 4 * WARPS * k * ld);
+    }
+  }
+  __device__ __forceinline__ void put(float* to) const {
+    const int i = threadIdx.x;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k)
+      *reinterpret_cast<float4*>(to + (i & 4 ? kTile * kBRow : 0) + ((i >> 3) + 4 * WARPS * k) * kBRow + 4 * (i & 3)) =
+          make_float4(bf16_lo(v[k].x), bf16_hi(v[k].x), bf16_lo(v[k].y), bf16_hi(v[k].y));
+  }
+  __device__ __forceinline__ void move(int tiles) { at += mine ? tiles * kTile * ld : 0; }
+};
+
+// Two neighbouring channels (bf16).
+__device__ __forceinline__ float2 pair_at(const bf16* p) {
+  const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
+  return make_float2(bf16_lo(w), bf16_hi(w));
+}
+__device__ __forceinline__ float2 vector_at(const float* p, int c, bool real) {  // of two channels of a weight
+  return p && real ? make_float2(__ldg(p + c), __ldg(p + c + 1)) : make_float2(0.0f, 0.0f);
+}
+
+struct State4 {
+  f32x2 a, b;
+};
+__device__ __forceinline__ State4 pack4(float4 v) { return State4{pack2(v.x, v.y), pack2(v.z, v.w)}; }
+__device__ __forceinline__ float4 unpack4(const State4& s) {
+  float4 v;
+  unpack2(s.a, v.x, v.y);
+  unpack2(s.b, v.z, v.w);
+  return v;
+}
+__device__ __forceinline__ State4 ex2(const State4& s) {
+  const float4 v = unpack4(s);
+  return pack4(make_float4(ex2(v.x), ex2(v.y), ex2(v.z), ex2(v.w)));
+}
+__device__ __forceinline__ State4 mul4(f32x2 x, const State4& s) { return State4{mul2(x, s.a), mul2(x, s.b)}; }
+__device__ __forceinline__ State4 mul4(const State4& x, const State4& s) { return State4{mul2(x.a, s.a), mul2(x.b, s.b)}; }
+__device__ __forceinline__ State4 fma4(const State4& x, const State4& s, const State4& c) {
+  return State4{fma2(x.a, s.a, c.a), fma2(x.b, s.b, c.b)};
+}
+__device__ __forceinline__ State4 fma4(f32x2 x, const State4& s, const State4& c) {
+  return State4{fma2(x, s.a, c.a), fma2(x, s.b, c.b)};
+}
+__device__ __forceinline__ float sum4(const State4& x, const State4& y) {  // x . y
+  float a, b;
+  unpack2(fma2(x.b, y.b, mul2(x.a, y.a)), a, b);
+  return a + b;
+}
+__device__ __forceinline__ State4 zero4() { return pack4(make_float4(0, 0, 0, 0)); }
+
+// v[0..3] of four lanes (lane bits 0 and 1) joined: lane q gets the sum over the four lanes of their v[q].
+__device__ __forceinline__ float join4(float v0, float v1, float v2, float v3, int q) {
+  const bool odd = q & 1, high = q & 2;
+  const float a = (odd ? v1 : v0) + __shfl_xor_sync(kAll, odd ? v0 : v1, 1);
+  const float b = (odd ? v3 : v2) + __shfl_xor_sync(kAll, odd ? v2 : v3, 1);
+  return (high ? b : a) + __shfl_xor_sync(kAll, high ? a : b, 2);
+}
+
+// Where a sequence's tile states begin: tiles of kTile tokens, so that all sequences' are at most T / kTile + N.
+__device__ __forceinline__ long long tile_base(const SeqPart& s) { return static_cast<long long>(s.start) / kTile + s.n; }
+
+constexpr int kFwdRow = kCh * kFwdWarps;      // channels of a CTA
+constexpr int kFwdTile = kTile * kFwdRow;     // values of a tile
+constexpr int kFwdPairs = kFwdRow / 2;        // a thread's place where it takes two neighbouring channels of every fourth token
+// Shared memory: two stages of u, delta and z; the pairs; two stages of B and C.
+constexpr int kFwdSmem = (2 * 3 * kFwdTile / 2 + 2 * kFwdTile + 2 * 2 * kTile * kBRow) * 4;
+
+// SUMS: only the state that a part leaves from a zero state and the sum of its dt, for parts of long sequences.
+template <bool SUMS>
+__global__ void __launch_bounds__(kFwdWarps * 32, 4) scan_fwd_kernel(ScanArgs a, int blocks, int length, const float* starts,
+                                                                     float* sums, float* dt_sums) {
+  extern __shared__ float pool[];
+  const int warp = threadIdx.x >> 5, lane = static_cast<int>(lane_id());
+  const int part = blockIdx.x / blocks;
+  SeqPart s;
+  if (!find_part(a.cu, a.N, a.T, a.max_seqlen, length, part, s, !SUMS && blockIdx.x % blocks == 0 && warp == 0 ? a.err_flag : nullptr)) return;
+  const Channels ch = block_channels(blockIdx.x % blocks, a.D, a.G, kFwdRow);
+  const int t0 = s.part * length, count = min(length, s.len - t0);  // (0 in an empty sequence)
+  if (SUMS && length >= s.len - t0) return;  // nothing reads the last part's
+  bf16* const raw = reinterpret_cast<bf16*>(pool);  // [stage][u, delta, z]
+  float* const s_dt = pool + 2 * 3 * kFwdTile / 2;  // [token][channel] (dt, dt u); then y in the first half of a warp's part
+  float* const s_bc = s_dt + 2 * kFwdTile;          // [stage][B, C]
+
+  const int q = lane & 3, first = warp * kCh + (lane >> 2) * kC;  // four states of two channels
+  const long long all = static_cast<long long>(a.D) * a.S;
+  const long long state_at = (static_cast<long long>(ch.c0) + first) * a.S + 4 * q;
+  State4 decay[kC], h[kC];
+  bool real[kC];
+#pragma unroll
+  for (int j = 0; j < kC; ++j) {
+    real[j] = first + j < ch.have && 4 * q < a.S;
+    decay[j] = h[j] = zero4();
+    if (real[j]) {
+      const float4 v = __ldg(reinterpret_cast<const float4*>(a.A + state_at + j * a.S));
+      decay[j] = pack4(make_float4(v.x * kLog2e, v.y * kLog2e, v.z * kLog2e, v.w * kLog2e));
+      const float* const from = SUMS ? nullptr : starts ? starts + part * all : a.state_in ? a.state_in + s.n * all : nullptr;
+      if (from) h[j] = pack4(*reinterpret_cast<const float4*>(from + state_at + j * a.S));
+    }
+  }
+  const bool wide = (a.D / a.G) % 8 == 0, gated = !SUMS && a.z != nullptr;
+  const long long row0 = s.start + t0;
+  RowStream<kFwdWarps> u(a.u, row0, a.ldu, ch, wide), delta(a.delta, row0, a.ldd, ch, wide),
+      z(gated ? a.z : a.u, row0, gated ? a.ldz : a.ldu, ch, wide);
+  BcStream<kFwdWarps> bc(a.B, SUMS ? nullptr : a.C, row0, a.ldb, a.ldc, ch, a.S);
+  const auto fetch = [&](int n, int stage) {
+    if (n > 0) {
+      const uint32_t to = smem_u32(raw + stage * 3 * kFwdTile);
+      u.fetch(to, n, wide), u.move(1);
+      delta.fetch(to + 2 * kFwdTile, n, wide), delta.move(1);
+      if (gated) z.fetch(to + 4 * kFwdTile, n, wide), z.move(1);
+      bc.fetch(n), bc.move(1);
+    }
+    copies_commit();
+  };
+  const int pair = threadIdx.x % kFwdPairs, pair_token = threadIdx.x / kFwdPairs;
+  const bool pair_real = 2 * pair < ch.have;
+  const float2 bias = vector_at(a.dt_bias, ch.c0 + 2 * pair, pair_real);
+  const float2 skip = vector_at(a.skip, ch.c0 + 2 * pair, pair_real);
+  float dt_sum[kC] = {0.0f, 0.0f};
+  float* tiles = !SUMS && a.tile_states ? a.tile_states + (tile_base(s) + t0 / kTile) * all + state_at : nullptr;
+  bf16* out = SUMS ? nullptr : static_cast<bf16*>(a.y) + (row0 + pair_token) * a.ldy + ch.c0 + 2 * pair;
+  fetch(count, 0);
+  int stage = 0;
+  for (int tile = 0; tile < count; tile += kTile, stage ^= 1) {
+    const int n = min(kTile, count - tile);
+    float* const s_b = s_bc + stage * 2 * kTile * kBRow;
+    bc.put(s_b);
+    copies_done();
+    __syncthreads();  // the tile is here, and nothing reads the one before it any more
+    fetch(count - tile - kTile, stage ^ 1);
+    const bf16* const now = raw + stage * 3 * kFwdTile + pair_token * kFwdRow + 2 * pair;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float2 d = pair_at(now + kFwdTile + 4 * k * kFwdRow), v = pair_at(now + 4 * k * kFwdRow);
+      float2 x = make_float2(d.x + bias.x, d.y + bias.y);
+      if (a.softplus) x = softplus2(x);
+      if (pair_token + 4 * k >= n) x = make_float2(0.0f, 0.0f);  // (a token that is none keeps the state)
+      *reinterpret_cast<float4*>(s_dt + 2 * ((pair_token + 4 * k) * kFwdRow + 2 * pair)) = make_float4(x.x, x.x * v.x, x.y, x.y * v.y);
+    }
+    if (tiles) {
+#pragma unroll
+      for (int j = 0; j < kC; ++j)
+        if (real[j]) *reinterpret_cast<float4*>(tiles + j * a.S) = unpack4(h[j]);
+      tiles += all;
+    }
+    __syncthreads();
+    const uint32_t at_dt = after_sync(s_dt + 2 * first), at_b = after_sync(s_b + 4 * q), at_c = at_b + 4 * kTile * kBRow;
+#pragma unroll 4
+    for (int t2 = 0; t2 < kTile; t2 += 2) {
+      float y[2][kC];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float4 d = lds4(at_dt + (t2 + i) * 8 * kFwdRow);
+        const State4 b = pack4(lds4(at_b + (t2 + i) * 4 * kBRow));
+        h[0] = fma4(ex2(mul4(pack2(d.x, d.x), decay[0])), h[0], mul4(pack2(d.y, d.y), b));
+        h[1] = fma4(ex2(mul4(pack2(d.z, d.z), decay[1])), h[1], mul4(pack2(d.w, d.w), b));
+        if (SUMS) {
+          dt_sum[0] += d.x, dt_sum[1] += d.z;
+        } else {
+          const State4 c = pack4(lds4(at_c + (t2 + i) * 4 * kBRow));
+          y[i][0] = sum4(c, h[0]), y[i][1] = sum4(c, h[1]);
+        }
+      }
+      // (over the pairs, of tokens that every lane of the warp has read by now)
+      if (!SUMS) s_dt[(t2 + (q >> 1)) * 2 * kFwdRow + warp * kCh + first + (q & 1)] = join4(y[0][0], y[0][1], y[1][0], y[1][1], q);
+    }
+    if (!SUMS) {
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (pair_token + 4 * k < n && pair_real) {
+          const float2 v = pair_at(now + 4 * k * kFwdRow);
+          float2 y = *reinterpret_cast<const float2*>(s_dt + (pair_token + 4 * k) * 2 * kFwdRow + (pair / 8) * kCh + 2 * pair);
+          y.x = fmaf(skip.x, v.x, y.x), y.y = fmaf(skip.y, v.y, y.y);
+          if (gated) {
+            const float2 g = pair_at(now + 2 * kFwdTile + 4 * k * kFwdRow), sg = sigmoid2(g);
+            y.x *= g.x * sg.x, y.y *= g.y * sg.y;
+          }
+          *reinterpret_cast<uint32_t*>(out + 4 * k * a.ldy) = pack_bf16(y.x, y.y);
+        }
+      }
+      out += kTile * a.ldy;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kC; ++j) {
+    if (SUMS) {
+      if (real[j]) *reinterpret_cast<float4*>(sums + part * all + state_at + j * a.S) = unpack4(h[j]);
+      if (first + j < ch.have && q == 0) dt_sums[static_cast<long long>(part) * a.D + ch.c0 + first + j] = dt_sum[j];
+    } else if (a.state_out && real[j] && t0 + count == s.len) {
+      *reinterpret_cast<float4*>(a.state_out + s.n * all + state_at + j * a.S) = unpack4(h[j]);
+    }
+  }
+}
+
+// The states at the parts' starts (REVERSE: the gradients at their ends) from what each part leaves from zero, in place:
+// a thread walks the parts of one sequence with four states.
+template <bool REVERSE>
+__global__ void __launch_bounds__(128) scan_join_kernel(ScanArgs a, int length, const float* first, float* sums,
+                                                        const float* dt_sums) {
+  const int blocks = (a.D * (a.S / 4) + 127) / 128;
+  const int part = blockIdx.x / blocks, i = blockIdx.x % blocks * 128 + threadIdx.x;
+  SeqPart s;
+  if (!find_part(a.cu, a.N, a.T, a.max_seqlen, length, part, s, nullptr) || s.part != 0) return;
+  if (i >= a.D * (a.S / 4)) return;
+  const int c = i / (a.S / 4);
+  const long long at = 4ll * i, all = static_cast<long long>(a.D) * a.S;
+  const int parts = parts_of(s.len, length);
+  const float4 A = __ldg(reinterpret_cast<const float4*>(a.A + at));
+  float4 h = make_float4(0, 0, 0, 0);
+  if (first) h = *reinterpret_cast<const float4*>(first + s.n * all + at);
+  for (int k = 0; k < parts; ++k) {
+    const long long p = part + (REVERSE ? parts - 1 - k : k);
+    float4* const place = reinterpret_cast<float4*>(sums + p * all + at);
+    // (the last part in the walk's direction has no sums: nothing follows it)
+    const bool more = k + 1 < parts;
+    float4 e = make_float4(0, 0, 0, 0);
+    float d = 0.0f;
+    if (more) e = *place, d = __ldg(dt_sums + p * a.D + c);
+    *place = h;
+    h.x = fmaf(ex2(A.x * d * kLog2e), h.x, e.x);
+    h.y = fmaf(ex2(A.y * d * kLog2e), h.y, e.y);
+    h.z = fmaf(ex2(A.z * d * kLog2e), h.z, e.z);
+    h.w = fmaf(ex2(A.w * d * kLog2e), h.w, e.w);
+  }
+}
+
+// ------------------------------------------------------------------ backward
+//
+// With X the gradient that reaches a state from the later tokens:
+//   g_t = dy_t silu(z_t);  R_t = X + g_t C_t;  dC_t = g_t h_t;  dB_t = dt_t u_t R_t;  (both summed over the channels)
+//   to_b = R_t . B_t;  q = R_t exp(dt_t A) h_{t-1};  ddt = A . q + to_b u_t;  dA += dt_t q;
+//   du_t = to_b dt_t + skip g_t;  X = exp(dt_t A) R_t
+// Tiles of 32 tokens from the last to the first. The forward kept the state before each; from it the tile's states
+// are made again, first all of them (the gate's gradient needs y; every fourth state is noted), then four at a
+// time in registers, which the four tokens' backward reads. dB and dC are summed over a warp's channels by exchanging
+// halves between lanes, over a CTA's warps in shared memory, and over the CTAs by a second kernel, always in one order.
+constexpr int kBwdRow = kCh * kBwdWarps;      // channels of a CTA
+constexpr int kBwdTile = kTile * kBwdRow;
+constexpr int kBwdPairs = kBwdRow / 2;
+// Shared memory: two stages of u, delta, dy and z; the pairs; y, then g; the warps' noted states; their dB and dC; two stages of B and C.
+constexpr int kNotes = (kTile / 4) * kC * 128;
+constexpr int kBwdSmem = (2 * 4 * kBwdTile / 2 + 2 * kBwdTile + kBwdTile + kBwdWarps * (kNotes + kTile * 32) + 2 * 2 * kTile * kBRow) * 4;
+
+struct BwdWs {
+  float* tails;     // [parts][D][S] gradients at the parts' ends, where sequences are cut
+  float* bc_part;   // [channel blocks][T][32]
+  float* dA_part;   // [parts][D][S]
+  float* d_part;    // [2][parts][D]: skip, dt_bias
+};
+
+__global__ void __launch_bounds__(kBwdWarps * 32, 1) scan_bwd_kernel(ScanBwdArgs a, int blocks, int parts, int length, bool cut, BwdWs ws) {
+  extern __shared__ float pool[];
+  const ScanArgs& f = a.f;
+  const int warp = threadIdx.x >> 5, lane = static_cast<int>(lane_id());
+  const int part = blockIdx.x / blocks, block = blockIdx.x % blocks;
+  const long long all = static_cast<long long>(f.D) * f.S;
+  const Channels ch = block_channels(block, f.D, f.G, kBwdRow);
+  SeqPart s;
+  if (!find_part(f.cu, f.N, f.T, f.max_seqlen, length, part, s, block == 0 && warp == 0 ? f.err_flag : nullptr)) {
+    // a part that does not exist adds nothing to the sums over the parts
+    for (int i = threadIdx.x; i < ch.have * f.S; i += kBwdWarps * 32) ws.dA_part[part * all + static_cast<long long>(ch.c0) * f.S + i] = 0.0f;
+    for (int i = threadIdx.x; i < ch.have; i += kBwdWarps * 32)
+      for (int j = 0; j < 2; ++j) ws.d_part[(static_cast<long long>(j) * parts + part) * f.D + ch.c0 + i] = 0.0f;
+    return;
+  }
+  const int t0 = s.part * length, count = min(length, s.len - t0);
+  bf16* const raw = reinterpret_cast<bf16*>(pool);  // [stage][u, delta, dy, z]
+  float* const s_dt = pool + 2 * 4 * kBwdTile / 2;  // [token][channel] (dt, dt u)
+  float* const s_g = s_dt + 2 * kBwdTile;           // [token][channel] y, then g
+  float* const s_notes = s_g + kBwdTile;            // [warp][token / 4][channel of a lane][lane] states; then (to_b, r)
+  float* const s_sums = s_notes + kBwdWarps * kNotes;  // [warp][token][dB, dC]
+  float* const s_bc = s_sums + kBwdWarps * kTile * 32;  // [stage][B, C]
+  float* const s_note = s_notes + warp * kNotes;
+  float* const s_sum = s_sums + warp * kTile * 32;
+
+  const int q = lane & 3, mine = lane >> 2, first = warp * kCh + mine * kC;
+  const long long state_at = (static_cast<long long>(ch.c0) + first) * f.S + 4 * q;
+  State4 decay[kC], X[kC], dA[kC], dA_rest[kC];
+  bool real[kC];
+#pragma unroll
+  for (int j = 0; j < kC; ++j) {
+    real[j] = first + j < ch.have && 4 * q < f.S;
+    decay[j] = X[j] = dA[j] = dA_rest[j] = zero4();
+    if (real[j]) {
+      const float4 v = __ldg(reinterpret_cast<const float4*>(f.A + state_at + j * f.S));
+      decay[j] = pack4(make_float4(v.x * kLog2e, v.y * kLog2e, v.z * kLog2e, v.w * kLog2e));
+      const float* const from = cut ? ws.tails + part * all : a.d_state_out ? a.d_state_out + s.n * all : nullptr;
+      if (from) X[j] = pack4(*reinterpret_cast<const float4*>(from + state_at + j * f.S));
+    }
+  }
+  const bool wide = (f.D / f.G) % 8 == 0, gated = f.z != nullptr;
+  const int last = count > 0 ? (count - 1) / kTile * kTile : -kTile;
+  const long long row0 = s.start + t0 + max(last, 0);  // of the tile in hand, walking back
+  RowStream<kBwdWarps> u(f.u, row0, f.ldu, ch, wide), delta(f.delta, row0, f.ldd, ch, wide), dy(a.dy, row0, a.lddy, ch, wide),
+      z(gated ? f.z : f.u, row0, gated ? f.ldz : f.ldu, ch, wide);
+  BcStream<kBwdWarps> bc(f.B, f.C, row0, f.ldb, f.ldc, ch, f.S);
+  const float* tiles = f.tile_states + (tile_base(s) + (t0 + max(last, 0)) / kTile) * all + state_at;
+  State4 next[kC];
+  const auto fetch = [&](int tile, int stage) {
+    if (tile >= 0) {
+      const int n = count - tile;
+      const uint32_t to = smem_u32(raw + stage * 4 * kBwdTile);
+      u.fetch(to, n, wide), u.move(-1);
+      delta.fetch(to + 2 * kBwdTile, n, wide), delta.move(-1);
+      dy.fetch(to + 4 * kBwdTile, n, wide), dy.move(-1);
+      if (gated) z.fetch(to + 6 * kBwdTile, n, wide), z.move(-1);
+      bc.fetch(n), bc.move(-1);
+#pragma unroll
+      for (int j = 0; j < kC; ++j) {
+        next[j] = zero4();
+        if (real[j]) next[j] = pack4(*reinterpret_cast<const float4*>(tiles + j * f.S));
+      }
+      tiles -= all;
+    }
+    copies_commit();
+  };
+  const int pair = threadIdx.x % kBwdPairs, pair_token = threadIdx.x / kBwdPairs;
+  const bool pair_real = 2 * pair < ch.have;
+  const float2 bias = vector_at(f.dt_bias, ch.c0 + 2 * pair, pair_real);
+  const float2 skip = vector_at(f.skip, ch.c0 + 2 * pair, pair_real);
+  float2 d_skip = make_float2(0.0f, 0.0f), d_bias = d_skip;
+  const long long pair_row = row0 + pair_token;
+  const int pair_at0 = pair_token * kBwdRow + 2 * pair;  // this thread's place in a tile
+  bf16* dz = a.dz ? static_cast<bf16*>(a.dz) + pair_row * a.lddz + ch.c0 + 2 * pair : nullptr;
+  bf16* du = static_cast<bf16*>(a.du) + pair_row * a.lddu + ch.c0 + 2 * pair;
+  bf16* dd = static_cast<bf16*>(a.dd) + pair_row * a.lddd + ch.c0 + 2 * pair;
+
+  fetch(last, 0);
+  float* bc_sum = ws.bc_part + (static_cast<long long>(block) * f.T + row0) * 32;
+  int stage = 0;
+  for (int tile = last; tile >= 0; tile -= kTile, stage ^= 1) {
+    const int n = min(kTile, count - tile);
+    State4 h[kC] = {next[0], next[1]};
+    float* const s_b = s_bc + stage * 2 * kTile * kBRow;
+    bc.put(s_b);
+    copies_done();
+    __syncthreads();  // the tile is here, and nothing reads the one before it any more
+    fetch(tile - kTile, stage ^ 1);
+    const bf16* const now = raw + stage * 4 * kBwdTile + pair_at0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float2 d = pair_at(now + kBwdTile + 4 * k * kBwdRow), v = pair_at(now + 4 * k * kBwdRow);
+      float2 x = make_float2(d.x + bias.x, d.y + bias.y);
+      if (f.softplus) x = softplus2(x);
+      if (pair_token + 4 * k >= n) x = make_float2(0.0f, 0.0f);
+      *reinterpret_cast<float4*>(s_dt + 2 * (pair_at0 + 4 * k * kBwdRow)) = make_float4(x.x, x.x * v.x, x.y, x.y * v.y);
+    }
+    __syncthreads();
+    const uint32_t at_dt = after_sync(s_dt + 2 * first), at_b = after_sync(s_b + 4 * q), at_c = at_b + 4 * kTile * kBRow;
+    // forward through the tile
+#pragma unroll 2
+    for (int t4 = 0; t4 < kTile; t4 += 4) {
+#pragma unroll
+      for (int j = 0; j < kC; ++j) *reinterpret_cast<float4*>(s_note + (t4 / 4 * kC + j) * 128 + 4 * lane) = unpack4(h[j]);
+      float y[4][kC];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 d = lds4(at_dt + (t4 + i) * 8 * kBwdRow);
+        const State4 b = pack4(lds4(at_b + (t4 + i) * 4 * kBRow));
+        h[0] = fma4(ex2(mul4(pack2(d.x, d.x), decay[0])), h[0], mul4(pack2(d.y, d.y), b));
+        h[1] = fma4(ex2(mul4(pack2(d.z, d.z), decay[1])), h[1], mul4(pack2(d.w, d.w), b));
+        if (gated) {
+          const State4 c = pack4(lds4(at_c + (t4 + i) * 4 * kBRow));
+          y[i][0] = sum4(c, h[0]), y[i][1] = sum4(c, h[1]);
+        }
+      }
+      if (gated) {
+#pragma unroll
+        for (int i = 0; i < 4; i += 2)
+          s_g[(t4 + i + (q >> 1)) * kBwdRow + first + (q & 1)] = join4(y[i][0], y[i][1], y[i + 1][0], y[i + 1][1], q);
+      }
+    }
+    if (gated) __syncthreads();
+    // the gate's gradient; g
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int at = 4 * k * kBwdRow;
+      const float2 v = pair_at(now + at);
+      float2 g = pair_at(now + 2 * kBwdTile + at);
+      if (gated) {
+        const float2 zz = pair_at(now + 3 * kBwdTile + at), y = *reinterpret_cast<const float2*>(s_g + pair_at0 + at);
+        const float2 sg = sigmoid2(zz), silu = make_float2(zz.x * sg.x, zz.y * sg.y);
+        if (dz && pair_token + 4 * k < n && pair_real)  // silu' = sg + silu (1 - sg)
+          *reinterpret_cast<uint32_t*>(dz + 4 * k * a.lddz) =
+              pack_bf16(g.x * fmaf(skip.x, v.x, y.x) * fmaf(silu.x, 1.0f - sg.x, sg.x),
+                        g.y * fmaf(skip.y, v.y, y.y) * fmaf(silu.y, 1.0f - sg.y, sg.y));
+        g.x *= silu.x, g.y *= silu.y;
+      }
+      *reinterpret_cast<float2*>(s_g + pair_at0 + at) = g;
+      d_skip.x = fmaf(g.x, v.x, d_skip.x), d_skip.y = fmaf(g.y, v.y, d_skip.y);
+    }
+    if (dz) dz -= kTile * a.lddz;
+    __syncthreads();
+    const uint32_t at_note = after_sync(s_note + 4 * lane), at_g = after_sync(s_g + first);
+    State4 dA_tile[kC] = {zero4(), zero4()};
+#pragma unroll 1
+    for (int t4 = kTile - 4; t4 >= 0; t4 -= 4) {
+      State4 hs[5][kC], es[4][kC];
+      float4 d[4];
+#pragma unroll
+      for (int j = 0; j < kC; ++j) hs[0][j] = pack4(lds4(at_note + (t4 / 4 * kC + j) * 512));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        d[i] = lds4(at_dt + (t4 + i) * 8 * kBwdRow);
+        const State4 b = pack4(lds4(at_b + (t4 + i) * 4 * kBRow));
+        es[i][0] = ex2(mul4(pack2(d[i].x, d[i].x), decay[0]));
+        es[i][1] = ex2(mul4(pack2(d[i].z, d[i].z), decay[1]));
+        hs[i + 1][0] = fma4(es[i][0], hs[i][0], mul4(pack2(d[i].y, d[i].y), b));
+        hs[i + 1][1] = fma4(es[i][1], hs[i][1], mul4(pack2(d[i].w, d[i].w), b));
+      }
+      float to_b[4][kC], r[4][kC];
+#pragma unroll
+      for (int i = 3; i >= 0; --i) {
+        const float2 g = lds2(at_g + (t4 + i) * 4 * kBwdRow);
+        const State4 c = pack4(lds4(at_c + (t4 + i) * 4 * kBRow));
+        const State4 b = pack4(lds4(at_b + (t4 + i) * 4 * kBRow));
+        State4 sum_b = zero4(), sum_c = zero4();
+#pragma unroll
+        for (int j = 0; j < kC; ++j) {
+          const float gj = j ? g.y : g.x, dt = j ? d[i].z : d[i].x, dtu = j ? d[i].w : d[i].y;
+          const f32x2 gg = pack2(gj, gj), uu = pack2(dtu, dtu);
+          X[j] = fma4(gg, c, X[j]);
+          sum_c = j ? fma4(gg, hs[i + 1][j], sum_c) : mul4(gg, hs[i + 1][j]);
+          sum_b = j ? fma4(uu, X[j], sum_b) : mul4(uu, X[j]);
+          to_b[i][j] = sum4(X[j], b);
+          X[j] = mul4(X[j], es[i][j]);
+          const State4 qq = mul4(X[j], hs[i][j]);
+          r[i][j] = sum4(decay[j], qq);
+          dA_tile[j] = fma4(pack2(dt, dt), qq, dA_tile[j]);
+        }
+        const float4 dc = unpack4(sum_c), db = unpack4(sum_b);
+        // eight values over the eight lanes of one q: lane (mine, q) ends with the sum of the mine-th
+        const bool k4 = mine & 4, k2 = mine & 2, k1 = mine & 1;
+        float v0 = (k4 ? dc.x : db.x) + __shfl_xor_sync(kAll, k4 ? db.x : dc.x, 16);
+        float v1 = (k4 ? dc.y : db.y) + __shfl_xor_sync(kAll, k4 ? db.y : dc.y, 16);
+        const float v2 = (k4 ? dc.z : db.z) + __shfl_xor_sync(kAll, k4 ? db.z : dc.z, 16);
+        const float v3 = (k4 ? dc.w : db.w) + __shfl_xor_sync(kAll, k4 ? db.w : dc.w, 16);
+        v0 = (k2 ? v2 : v0) + __shfl_xor_sync(kAll, k2 ? v0 : v2, 8);
+        v1 = (k2 ? v3 : v1) + __shfl_xor_sync(kAll, k2 ? v1 : v3, 8);
+        s_sum[(t4 + i) * 32 + (mine >> 2) * 16 + 4 * q + (mine & 3)] = (k1 ? v1 : v0) + __shfl_xor_sync(kAll, k1 ? v0 : v1, 4);
+        // (to_b, r) [token][channel] over the noted states of these four tokens, which every lane has read by now
+        s_note[t4 / 4 * kC * 128 + i * 2 * kCh + 2 * (mine * kC + (q & 1)) + (q >> 1)] =
+            join4(to_b[i][0], to_b[i][1], r[i][0] * kLn2, r[i][1] * kLn2, q);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kC; ++j) {  // dA: the tile's sum joins the others with what the addition before lost
+      const f32x2 neg = pack2(-1.0f, -1.0f);
+      const State4 add{fma2(dA_rest[j].a, neg, dA_tile[j].a), fma2(dA_rest[j].b, neg, dA_tile[j].b)};
+      const State4 sum{add2(add.a, dA[j].a), add2(add.b, dA[j].b)};
+      dA_rest[j] = State4{fma2(add.a, neg, fma2(dA[j].a, neg, sum.a)), fma2(add.b, neg, fma2(dA[j].b, neg, sum.b))};
+      dA[j] = sum;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (pair_token + 4 * k < n && pair_real) {
+        const int at = 4 * k * kBwdRow;
+        const float4 w = *reinterpret_cast<const float4*>(s_notes + pair / 8 * kNotes + k * kC * 128 + pair_token * 2 * kCh + pair % 8 * 4);
+        const float2 v = pair_at(now + at), x = pair_at(now + kBwdTile + at), g = *reinterpret_cast<const float2*>(s_g + pair_at0 + at);
+        const float4 dt = *reinterpret_cast<const float4*>(s_dt + 2 * (pair_at0 + at));
+        *reinterpret_cast<uint32_t*>(du + 4 * k * a.lddu) = pack_bf16(fmaf(w.x, dt.x, skip.x * g.x), fmaf(w.z, dt.z, skip.y * g.y));
+        float2 e = make_float2(fmaf(w.x, v.x, w.y), fmaf(w.z, v.y, w.w));
+        if (f.softplus) {
+          const float2 sg = sigmoid2(make_float2(x.x + bias.x, x.y + bias.y));
+          e.x *= sg.x, e.y *= sg.y;
+        }
+        *reinterpret_cast<uint32_t*>(dd + 4 * k * a.lddd) = pack_bf16(e.x, e.y);
+        d_bias.x += e.x, d_bias.y += e.y;
+      }
+    }
+    du -= kTile * a.lddu, dd -= kTile * a.lddd;
+    // dB and dC over the warps
+    for (int i = threadIdx.x; i < n * 32; i += kBwdWarps * 32) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kBwdWarps; ++w) sum += s_sums[w * kTile * 32 + i];
+      bc_sum[i] = sum;
+    }
+    bc_sum -= kTile * 32;
+  }
+#pragma unroll
+  for (int j = 0; j < kC; ++j)
+    if (real[j]) {
+      *reinterpret_cast<float4*>(ws.dA_part + part * all + state_at + j * f.S) = unpack4(dA[j]);
+      if (a.d_state_in && s.part == 0) *reinterpret_cast<float4*>(a.d_state_in + s.n * all + state_at + j * f.S) = unpack4(X[j]);
+    }
+  // the four threads that share two channels
+  __syncthreads();
+  float4* const join = reinterpret_cast<float4*>(pool);
+  join[threadIdx.x] = make_float4(d_skip.x, d_skip.y, d_bias.x, d_bias.y);
+  __syncthreads();
+  if (threadIdx.x < kBwdPairs && pair_real) {
+    float4 v = join[threadIdx.x];
+#pragma unroll
+    for (int i = 1; i < 4; ++i) {
+      const float4 w = join[threadIdx.x + i * kBwdPairs];
+      v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+    }
+    float* const to = ws.d_part + static_cast<long long>(part) * f.D + ch.c0 + 2 * pair;
+    to[0] = v.x, to[1] = v.y;
+    to[static_cast<long long>(parts) * f.D] = v.z, to[static_cast<long long>(parts) * f.D + 1] = v.w;
+  }
+}
+
+
+// The gradient that a part hands to the one before it, from zero at its end, and the sum of its dt.
+__global__ void __launch_bounds__(kFwdWarps * 32, 4) scan_bwd_sums_kernel(ScanBwdArgs a, int blocks, int length, float* sums, float* dt_sums) {
+  extern __shared__ float pool[];
+  const ScanArgs& f = a.f;
+  const int warp = threadIdx.x >> 5, lane = static_cast<int>(lane_id());
+  const int part = blockIdx.x / blocks;
+  SeqPart s;
+  if (!find_part(f.cu, f.N, f.T, f.max_seqlen, length, part, s, nullptr) || s.part == 0) return;  // (nothing comes before a first part)
+  const Channels ch = block_channels(blockIdx.x % blocks, f.D, f.G, kFwdRow);
+  const int t0 = s.part * length, count = min(length, s.len - t0);
+  bf16* const raw = reinterpret_cast<bf16*>(pool);  // [stage][delta, dy, z]
+  float* const s_dt = pool + 2 * 3 * kFwdTile / 2;  // [token][channel] (dt, g)
+  float* const s_bc = s_dt + 2 * kFwdTile;          // [stage][nothing, C]
+  const int q = lane & 3, first = warp * kCh + (lane >> 2) * kC;
+  const long long all = static_cast<long long>(f.D) * f.S;
+  const long long state_at = (static_cast<long long>(ch.c0) + first) * f.S + 4 * q;
+  State4 decay[kC], X[kC];
+  float dt_sum[kC] = {0.0f, 0.0f};
+#pragma unroll
+  for (int j = 0; j < kC; ++j) {
+    decay[j] = X[j] = zero4();
+    if (first + j < ch.have && 4 * q < f.S) {
+      const float4 v = __ldg(reinterpret_cast<const float4*>(f.A + state_at + j * f.S));
+      decay[j] = pack4(make_float4(v.x * kLog2e, v.y * kLog2e, v.z * kLog2e, v.w * kLog2e));
+    }
+  }
+  const bool wide = (f.D / f.G) % 8 == 0, gated = f.z != nullptr;
+  const int last = (count - 1) / kTile * kTile;
+  const long long row0 = s.start + t0 + last;
+  RowStream<kFwdWarps> delta(f.delta, row0, f.ldd, ch, wide), dy(a.dy, row0, a.lddy, ch, wide),
+      z(gated ? f.z : f.delta, row0, gated ? f.ldz : f.ldd, ch, wide);
+  BcStream<kFwdWarps> bc(nullptr, f.C, row0, f.ldb, f.ldc, ch, f.S);
+  const auto fetch = [&](int tile, int stage) {
+    if (tile >= 0) {
+      const int n = count - tile;
+      const uint32_t to = smem_u32(raw + stage * 3 * kFwdTile);
+      delta.fetch(to, n, wide), delta.move(-1);
+      dy.fetch(to + 2 * kFwdTile, n, wide), dy.move(-1);
+      if (gated) z.fetch(to + 4 * kFwdTile, n, wide), z.move(-1);
+      bc.fetch(n), bc.move(-1);
+    }
+    copies_commit();
+  };
+  const int pair = threadIdx.x % kFwdPairs, pair_token = threadIdx.x / kFwdPairs;
+  const float2 bias = vector_at(f.dt_bias, ch.c0 + 2 * pair, 2 * pair < ch.have);
+  fetch(last, 0);
+  int stage = 0;
+  for (int tile = last; tile >= 0; tile -= kTile, stage ^= 1) {
+    const int n = min(kTile, count - tile);
+    float* const s_b = s_bc + stage * 2 * kTile * kBRow;
+    bc.put(s_b);
+    copies_done();
+    __syncthreads();  // the tile is here, and nothing reads the one before it any more
+    fetch(tile - kTile, stage ^ 1);
+    const bf16* const now = raw + stage * 3 * kFwdTile + pair_token * kFwdRow + 2 * pair;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float2 d = pair_at(now + 4 * k * kFwdRow);
+      float2 g = pair_at(now + kFwdTile + 4 * k * kFwdRow), x = make_float2(d.x + bias.x, d.y + bias.y);
+      if (f.softplus) x = softplus2(x);
+      if (pair_token + 4 * k >= n) x = make_float2(0.0f, 0.0f);
+      if (gated) {
+        const float2 zz = pair_at(now + 2 * kFwdTile + 4 * k * kFwdRow), sg = sigmoid2(zz);
+        g.x *= zz.x * sg.x, g.y *= zz.y * sg.y;
+      }
+      *reinterpret_cast<float4*>(s_dt + 2 * ((pair_token + 4 * k) * kFwdRow + 2 * pair)) = make_float4(x.x, g.x, x.y, g.y);
+    }
+    __syncthreads();
+    const uint32_t at_dt = after_sync(s_dt + 2 * first), at_c = after_sync(s_b + kTile * kBRow + 4 * q);
+#pragma unroll 8
+    for (int t = kTile - 1; t >= 0; --t) {
+      const float4 d = lds4(at_dt + t * 8 * kFwdRow);
+      const State4 c = pack4(lds4(at_c + t * 4 * kBRow));
+      X[0] = mul4(fma4(pack2(d.y, d.y), c, X[0]), ex2(mul4(pack2(d.x, d.x), decay[0])));
+      X[1] = mul4(fma4(pack2(d.w, d.w), c, X[1]), ex2(mul4(pack2(d.z, d.z), decay[1])));
+      dt_sum[0] += d.x, dt_sum[1] += d.z;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kC; ++j) {
+    if (first + j >= ch.have) continue;
+    if (4 * q < f.S) *reinterpret_cast<float4*>(sums + part * all + state_at + j * f.S) = unpack4(X[j]);
+    if (q == 0) dt_sums[static_cast<long long>(part) * f.D + ch.c0 + first + j] = dt_sum[j];
+  }
+}
+
+// dB and dC [T][G][S] (bf16) from the channel blocks' sums [blocks][T][32]: 32 tokens of a sequence a CTA, four of a
+// token's 32 values a thread.
+__global__ void __launch_bounds__(256) scan_bc_sums_kernel(ScanArgs f, const float* __restrict__ part, int blocks, bf16* dB, bf16* dC) {
+  SeqPart s;
+  if (!find_part(f.cu, f.N, f.T, f.max_seqlen, kTile, blockIdx.x, s, nullptr)) return;
+  const int at = s.part * kTile + static_cast<int>(threadIdx.x >> 3), piece = threadIdx.x & 7, state = 4 * (piece & 3);
+  if (at >= s.len || state >= f.S) return;
+  const long long t = s.start + at;
+  const int per = blocks / f.G;
+  for (int g = 0; g < f.G; ++g) {
+    float4 sum = make_float4(0, 0, 0, 0);
+#pragma unroll 8
+    for (int b = g * per; b < (g + 1) * per; ++b) {
+      const float4 v = __ldg(reinterpret_cast<const float4*>(part + (static_cast<long long>(b) * f.T + t) * 32 + 4 * piece));
+      sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+    }
+    bf16* const to = (piece < 4 ? dB : dC) + (t * f.G + g) * f.S + state;
+    *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16(sum.x, sum.y), pack_bf16(sum.z, sum.w));
+  }
+}
+
+// ------------------------------------------------------------------ step
+
+constexpr int kStepWarps = 8;
+
+__global__ void __launch_bounds__(kStepWarps * 32) scan_step_kernel(ScanStepArgs a, int blocks) {
+  const int q = threadIdx.x & 3;
+  const int b = blockIdx.x / blocks;
+  const Channels ch = block_channels(blockIdx.x % blocks, a.D, a.G, 8 * kStepWarps);
+  const int place_in = static_cast<int>(threadIdx.x >> 2), c = ch.c0 + place_in;
+  int slot = a.state_idx ? __ldg(a.state_idx + b) : b;
+  if (slot >= a.n_slots) {
+    if (threadIdx.x == 0) set_flag(a.err_flag, MOE_FLAG_BAD_INDEX);
+    slot = -1;
+  }
+  const bool in = place_in < ch.have;
+  bf16* const y = static_cast<bf16*>(a.y) + b * a.ldy + c;
+  if (slot < 0) {
+    if (in && q == 0) *y = __float2bfloat16_rn(0.0f);
+    return;
+  }
+  const bool real = in && 4 * q < a.S;
+  float* const place = a.state + (static_cast<long long>(slot) * a.D + c) * a.S + 4 * q;
+  float4 h = make_float4(0, 0, 0, 0), A = h, Bv = h, Cv = h;
+  if (real) {
+    h = *reinterpret_cast<const float4*>(place);
+    A = __ldg(reinterpret_cast<const float4*>(a.A + static_cast<long long>(c) * a.S + 4 * q));
+    const uint2 rb = *reinterpret_cast<const uint2*>(static_cast<const bf16*>(a.B) + b * a.ldb + ch.group * a.S + 4 * q);
+    const uint2 rc = *reinterpret_cast<const uint2*>(static_cast<const bf16*>(a.C) + b * a.ldc + ch.group * a.S + 4 * q);
+    Bv = make_float4(bf16_lo(rb.x), bf16_hi(rb.x), bf16_lo(rb.y), bf16_hi(rb.y));
+    Cv = make_float4(bf16_lo(rc.x), bf16_hi(rc.x), bf16_lo(rc.y), bf16_hi(rc.y));
+  }
+  float u = 0.0f, dt = 0.0f, gate = 1.0f;
+  if (in) {
+    u = __bfloat162float(static_cast<const bf16*>(a.u)[b * a.ldu + c]);
+    dt = __bfloat162float(static_cast<const bf16*>(a.delta)[b * a.ldd + c]) + (a.dt_bias ? __ldg(a.dt_bias + c) : 0.0f);
+    if (a.softplus) dt = softplus(dt);
+    if (a.z) {
+      const float z = __bfloat162float(static_cast<const bf16*>(a.z)[b * a.ldz + c]);
+      gate = z * sigmoid(z);
+    }
+  }
+  const float k = dt * kLog2e, du = dt * u;
+  h.x = fmaf(ex2(k * A.x), h.x, du * Bv.x);
+  h.y = fmaf(ex2(k * A.y), h.y, du * Bv.y);
+  h.z = fmaf(ex2(k * A.z), h.z, du * Bv.z);
+  h.w = fmaf(ex2(k * A.w), h.w, du * Bv.w);
+  if (real) *reinterpret_cast<float4*>(place) = h;
+  float o = fmaf(Cv.x, h.x, Cv.y * h.y) + fmaf(Cv.z, h.z, Cv.w * h.w);
+  o += __shfl_xor_sync(kAll, o, 1);
+  o += __shfl_xor_sync(kAll, o, 2);
+  if (in && q == 0) *y = __float2bfloat16_rn((o + (a.skip ? __ldg(a.skip + c) * u : 0.0f)) * gate);
+}
+
+// Channel blocks of `channels` channels.
+int blocks_of(int D, int G, int channels) { return G * ((D / G + channels - 1) / channels); }
+size_t up256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
+
+// How a launch is divided: channel blocks, tokens of a part.
+struct Division {
+  int blocks, length;
+  long long parts;
+  bool cut;
+};
+
+// Cutting a sequence costs a second run over its tokens (the sums, two thirds of the main run), so it is done only
+// where whole sequences leave most of the GPU empty.
+Division divide(int max_seqlen, int T, int N, int D, int G, bool backward) {
+  const int warps = backward ? kBwdWarps : kFwdWarps;
+  Division d;
+  d.blocks = blocks_of(D, G, kCh * warps);
+  const long long want = 8ll * num_sms(), have = static_cast<long long>(N) * d.blocks * warps;
+  long long whole = max_seqlen > 0 ? (static_cast<long long>(max_seqlen) + kTile - 1) / kTile * kTile : kTile;
+  if (whole > 0x7FFFFFE0) whole = 0x7FFFFFE0;
+  d.length = static_cast<int>(whole);
+  long long pieces = want / have;
+  if (pieces > whole / 128) pieces = whole / 128;
+  if (pieces >= 3) d.length = static_cast<int>((whole / kTile + pieces - 1) / pieces * kTile);
+  d.parts = T / d.length + static_cast<long long>(N);
+  d.cut = max_seqlen > d.length;
+  return d;
+}
+
+template <typename F>
+cudaError_t prepare_kernel(F kernel, int smem) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+}
+
+}  // namespace
+
+size_t scan_tile_states_bytes(int T, int N, int D, int S) {
+  return up256((static_cast<size_t>(T) / kTile + N) * D * S * 4);
+}
+
+size_t scan_workspace(int max_seqlen, int T, int N, int D, int S, int G, bool backward) {
+  const Division d = divide(max_seqlen, T, N, D, G, backward);
+  const size_t parts = static_cast<size_t>(d.parts), all = static_cast<size_t>(D) * S;
+  size_t bytes = d.cut ? up256(parts * all * 4) + up256(parts * D * 4) : 0;
+  if (backward) bytes += up256(static_cast<size_t>(d.blocks) * T * 32 * 4) + up256(parts * all * 4) + up256(2 * parts * D * 4);
+  return bytes;
+}
+
+cudaError_t launch_scan_fwd(const ScanArgs& a, cudaStream_t st) {
+  const Division d = divide(a.max_seqlen, a.T, a.N, a.D, a.G, false);
+  const unsigned grid = static_cast<unsigned>(d.parts * d.blocks);
+  const int smem = kFwdSmem;
+  cudaError_t e = prepare_kernel(scan_fwd_kernel<false>, smem);
+  if (e != cudaSuccess) return e;
+  float* starts = nullptr;
+  if (d.cut) {
+    starts = a.ws;
+    float* const dt_sums = reinterpret_cast<float*>(reinterpret_cast<char*>(a.ws) + up256(static_cast<size_t>(d.parts) * a.D * a.S * 4));
+    e = prepare_kernel(scan_fwd_kernel<true>, smem);
+    if (e != cudaSuccess) return e;
+    {
+      LaunchTimer lt("scan_fwd_sums", st);
+      scan_fwd_kernel<true><<<grid, kFwdWarps * 32, smem, st>>>(a, d.blocks, d.length, nullptr, starts, dt_sums);
+    }
+    LaunchTimer lt("scan_join", st);
+    const unsigned join = static_cast<unsigned>(d.parts * ((a.D * (a.S / 4) + 127) / 128));
+    scan_join_kernel<false><<<join, 128, 0, st>>>(a, d.length, a.state_in, starts, dt_sums);
+  }
+  LaunchTimer lt("scan_fwd", st);
+  scan_fwd_kernel<false><<<grid, kFwdWarps * 32, smem, st>>>(a, d.blocks, d.length, starts, nullptr, nullptr);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_scan_bwd(const ScanBwdArgs& a, cudaStream_t st) {
+  const ScanArgs& f = a.f;
+  const Division d = divide(f.max_seqlen, f.T, f.N, f.D, f.G, true);
+  const size_t all = static_cast<size_t>(f.D) * f.S;
+  char* at = reinterpret_cast<char*>(f.ws);
+  const auto take = [&](size_t bytes) {
+    float* const p = reinterpret_cast<float*>(at);
+    at += up256(bytes);
+    return p;
+  };
+  BwdWs ws{};
+  float* dt_sums = nullptr;
+  if (d.cut) ws.tails = take(d.parts * all * 4), dt_sums = take(d.parts * static_cast<size_t>(f.D) * 4);
+  ws.bc_part = take(static_cast<size_t>(d.blocks) * f.T * 32 * 4);
+  ws.dA_part = take(d.parts * all * 4);
+  ws.d_part = take(2 * d.parts * static_cast<size_t>(f.D) * 4);
+  cudaError_t e = prepare_kernel(scan_bwd_kernel, kBwdSmem);
+  if (e != cudaSuccess) return e;
+  if (d.cut) {
+    const int b = blocks_of(f.D, f.G, kCh * kFwdWarps), smem = kFwdSmem;
+    e = prepare_kernel(scan_bwd_sums_kernel, smem);
+    if (e != cudaSuccess) return e;
+    {
+      LaunchTimer lt("scan_bwd_sums", st);
+      scan_bwd_sums_kernel<<<static_cast<unsigned>(d.parts * b), kFwdWarps * 32, smem, st>>>(a, b, d.length, ws.tails, dt_sums);
+    }
+    LaunchTimer lt("scan_join", st);
+    const unsigned join = static_cast<unsigned>(d.parts * ((f.D * (f.S / 4) + 127) / 128));
+    scan_join_kernel<true><<<join, 128, 0, st>>>(f, d.length, a.d_state_out, ws.tails, dt_sums);
+  }
+  {
+    LaunchTimer lt("scan_bwd", st);
+    scan_bwd_kernel<<<static_cast<unsigned>(d.parts * d.blocks), kBwdWarps * 32, kBwdSmem, st>>>(
+        a, d.blocks, static_cast<int>(d.parts), d.length, d.cut, ws);
+  }
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  if (f.T > 0) {
+    LaunchTimer lt("scan_bc_sums", st);
+    scan_bc_sums_kernel<<<static_cast<unsigned>(f.T / kTile + static_cast<long long>(f.N)), 256, 0, st>>>(
+        f, ws.bc_part, d.blocks, static_cast<bf16*>(a.dB), static_cast<bf16*>(a.dC));
+  }
+  e = launch_column_sums("scan_dA", ws.dA_part, static_cast<int>(d.parts), static_cast<long long>(all), a.dA, st);
+  if (e != cudaSuccess) return e;
+  if (a.dskip) {
+    e = launch_column_sums("scan_dskip", ws.d_part, static_cast<int>(d.parts), f.D, a.dskip, st);
+    if (e != cudaSuccess) return e;
+  }
+  if (a.d_dt_bias) e = launch_column_sums("scan_dbias", ws.d_part + d.parts * f.D, static_cast<int>(d.parts), f.D, a.d_dt_bias, st);
+  return e;
+}
+
+cudaError_t launch_scan_step(const ScanStepArgs& a, cudaStream_t st) {
+  LaunchTimer lt("scan_step", st);
+  const int blocks = blocks_of(a.D, a.G, 8 * kStepWarps);
+  scan_step_kernel<<<static_cast<unsigned>(a.B_rows * blocks), kStepWarps * 32, 0, st>>>(a, blocks);
+  return cudaGetLastError();
+}
+
+}  // namespace moe

@@ -20,6 +20,15 @@ from . import _lib as M
 BF16 = torch.bfloat16
 
 
+def on_stream(stream, device):
+    """A context in which torch uses the stream (or handle) that a call was given."""
+    if stream is not None and not isinstance(stream, torch.cuda.Stream):
+        # (ExternalStream takes a handle of 0, the default stream, for none and makes a new one)
+        stream = (torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else
+                  torch.cuda.default_stream(device))
+    return torch.cuda.stream(stream)  # (None: the current one)
+
+
 class LinearAttention:
     def __init__(self, log_decay, T: int, Dk: int, Dv: int, r: int = 1, N: int = 1,
                  max_seqlen: int | None = None, scale: float | None = None, backward: bool = True):
@@ -85,11 +94,7 @@ class LinearAttention:
 
     def _keep_first(self, state, stream):
         """A copy, made on the call's stream, of states that the call is about to overwrite."""
-        if stream is not None and not isinstance(stream, torch.cuda.Stream):
-            # (ExternalStream takes a handle of 0, the default stream, for none and makes a new one)
-            stream = (torch.cuda.ExternalStream(int(stream), device=state.device) if int(stream) else
-                      torch.cuda.default_stream(state.device))
-        with torch.cuda.stream(stream):  # (None: the current one)
+        with on_stream(stream, state.device):
             if self._state_first is None:
                 self._state_first = torch.empty_like(state)
             return self._state_first.copy_(state)
