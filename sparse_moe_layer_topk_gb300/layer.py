@@ -21,12 +21,19 @@ With fp8_cache the routed experts' GMM output [g|u] is kept for the backward
 as E4M3 with one scale per row and 64 features (moe_grouped_swiglu[_bwd]_fp8cache)
 instead of bf16: 1 + 1/16 bytes per value instead of 2, and the backward's
 SwiGLU derivative reads the dequantized values.
+
+With a weight "norm" (fp32 [d]) the layer starts with the root-mean-square norm of its input, to which
+a residual may be added (norm.RMSNorm): the layer runs on the norm's output, `norm.sum` is the block's
+residual stream, and the backward ends with the norm's. With `router` (a dict of route.Router's options) the
+experts are chosen with its scores, bias and groups instead of the plain sigmoid form.
 """
 from __future__ import annotations
 
 import torch
 
 from . import _lib as M
+from .norm import RMSNorm
+from .route import Router
 
 BF16 = torch.bfloat16
 
@@ -34,9 +41,14 @@ BF16 = torch.bfloat16
 class LatentMoELayer:
     def __init__(self, weights: dict, T: int, k: int, wgrad_dtype: int = M.MOE_DTYPE_F32,
                  device="cuda", fused_gather: bool = False, aux_scale: float = 0.0,
-                 fp8_cache: bool = False):
+                 fp8_cache: bool = False, router: dict | None = None, norm_eps: float = 1e-6,
+                 residual_dtype=None):
         if fp8_cache and fused_gather:
             raise ValueError("fp8_cache runs with the explicit permute")
+        if router is not None and aux_scale > 0:
+            raise ValueError("the auxiliary loss is that of the plain sigmoid router")
+        if residual_dtype is not None and weights.get("norm") is None:
+            raise ValueError('a residual is added by the norm: the weights have no "norm"')
         self.w = weights
         self.fused_gather = fused_gather
         self.fp8_cache = fp8_cache
@@ -100,20 +112,43 @@ class LatentMoELayer:
             "rbwd": ws(M.MOE_OP_ROUTE_TOPK_BWD, T=T_, E=E),
             "aux": ws(M.MOE_OP_ROUTER_AUX, T=T_, E=E),
         }
+        self.router = self.norm = None
+        if router is not None:
+            self.router = Router(T_, E, k_, grad_dtype=BF16, device=dev, **router)
+            self.router.err = self.err
+            self.topk_idx, self.topk_w, self.topk_s = self.router.topk_idx, self.router.topk_w, self.router.topk_s
+        if weights.get("norm") is not None:
+            if tuple(weights["norm"].shape) != (d,):
+                raise ValueError(f'the weight "norm" is fp32 [{d}]')
+            self.norm = RMSNorm(weights["norm"], T_, norm_eps, residual_dtype)
+            self.d_normed = e(T_, d)
+            self.grads["norm"] = self.norm.dw
         self.p_mean = e(E, dt=torch.float32)
         self.aux_loss = e(1, dt=torch.float32)
         self.ws = {n: torch.empty(max(b, 256), dtype=torch.uint8, device=dev)
                    for n, b in self.ws_sizes.items()}
 
     # ------------------------------------------------------------------ forward
-    def forward(self, x, stream=None):
+    def forward(self, x, stream=None, residual=None):
+        """out [T, d]. With a weight "norm", the layer's input is norm(x + residual) (residual only where
+        residual_dtype was given); x + residual is then in norm.sum."""
         w, T, k, d, l, f, E, S, R = (self.w, self.T, self.k, self.d, self.l, self.f, self.E,
                                      self.S, self.R)
+        if self.norm is not None:
+            x = self.norm.forward(x, residual, stream=stream)
+        elif residual is not None:
+            raise ValueError('a residual is added by the norm: the weights have no "norm"')
         self.x = x
-        # router logits, top-k and the latent z = x W_dn (one GEMM over [Wr | W_dn])
-        M.moe_route_topk_latent(x, w["Wr"], w.get("bias"), w["W_dn"], T, d, E, k, l,
-                                self.topk_idx, self.topk_w, self.topk_s, self.z, self.ws["route"],
-                                self.ws_sizes["route"], self.err, stream)
+        if self.router is not None:
+            # the same GEMM, then the selection with the router's scores, bias and groups
+            logits = self.ws["route"][:T * E * 4].view(torch.float32).view(T, E)
+            M.moe_router_logits_latent(x, w["Wr"], w["W_dn"], T, d, E, l, logits, self.z, stream)
+            self.router.forward(logits, w.get("bias"), stream)
+        else:
+            # router logits, top-k and the latent z = x W_dn (one GEMM over [Wr | W_dn])
+            M.moe_route_topk_latent(x, w["Wr"], w.get("bias"), w["W_dn"], T, d, E, k, l,
+                                    self.topk_idx, self.topk_w, self.topk_s, self.z, self.ws["route"],
+                                    self.ws_sizes["route"], self.err, stream)
         if self.aux_scale > 0:
             # the router logits stay in the route workspace until the backward
             M.moe_router_aux_loss(self.ws["route"], w.get("bias"), T, E, self.p_mean, self.aux_loss,
@@ -141,7 +176,9 @@ class LatentMoELayer:
         return self.out
 
     # ------------------------------------------------------------------ backward
-    def backward(self, dout, stream=None):
+    def backward(self, dout, stream=None, d_sum=None):
+        """dx [T, d] for dout = d loss / d out. With a norm, d_sum (the residual's type) is the gradient that
+        reaches norm.sum from elsewhere, and norm.d_residual holds the residual's."""
         w, T, k, d, l, f, E, S, R = (self.w, self.T, self.k, self.d, self.l, self.f, self.E,
                                      self.S, self.R)
         g = self.grads
@@ -174,11 +211,21 @@ class LatentMoELayer:
         # dW_dn here; dx = dz W_dn^T + dL Wr^T in the router backward's fused GEMM
         M.moe_latent_proj_bwd(self.dz, self.x, w["W_dn"], T, d, l, None, g["W_dn"], wd, stream)
         aux = self.aux_scale > 0
-        M.moe_route_topk_bwd(self.d_row_w, self.slot_of, self.topk_idx, self.topk_w, self.topk_s,
-                             self.x, w["Wr"], T, d, E, k, self.d_topk_w, self.dx, g["Wr"], wd,
-                             self.ws["route"] if aux else None, w.get("bias") if aux else None,
-                             self.p_mean if aux else None, self.aux_scale, self.dz, w["W_dn"], l,
-                             self.ws["rbwd"], self.ws_sizes["rbwd"], self.err, stream)
+        dx = self.dx if self.norm is None else self.d_normed
+        if self.router is not None:
+            dL = self.router.backward(self.d_row_w, self.slot_of, self.d_topk_w, stream)
+            M.moe_router_grads(dL, self.x, w["Wr"], T, d, E, dx, g["Wr"], wd, self.dz, w["W_dn"], l, stream)
+        else:
+            M.moe_route_topk_bwd(self.d_row_w, self.slot_of, self.topk_idx, self.topk_w, self.topk_s,
+                                 self.x, w["Wr"], T, d, E, k, self.d_topk_w, dx, g["Wr"], wd,
+                                 self.ws["route"] if aux else None, w.get("bias") if aux else None,
+                                 self.p_mean if aux else None, self.aux_scale, self.dz, w["W_dn"], l,
+                                 self.ws["rbwd"], self.ws_sizes["rbwd"], self.err, stream)
+        if self.norm is not None:
+            self.norm.dx = self.dx
+            self.norm.backward(dx, d_sum, stream)
+        elif d_sum is not None:
+            raise ValueError("without a norm there is no sum")
         return self.dx
 
     def step(self, x, dout, stream=None):
@@ -292,4 +339,6 @@ def weights_to_device(inp: dict, device="cuda") -> dict:
     names = ("Wr", "W_dn", "W13", "W2", "W13_sh", "W2_sh", "W_up")
     out = {n: inp[n].to(device) for n in names}
     out["bias"] = inp["bias"].to(device) if inp.get("bias") is not None else None
+    if inp.get("norm") is not None:
+        out["norm"] = inp["norm"].to(device)
     return out

@@ -1,0 +1,209 @@
+"""Routing with scores, bias and groups on the GPU against the fp64 oracle.
+
+Ids are exact: the choice is that of 64-bit values. Scores and weights are fp32 of a few operations on exact logits,
+the exponential's argument up to 100 in magnitude (2^-24 of it): within 2^-17 of their values.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import mixer_oracle as O
+from sparse_moe_layer_topk_gb300 import _lib as M
+from gpu_util import f64, need_gpu
+
+pytestmark = pytest.mark.gpu
+TOL = 2.0 ** -17
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    need_gpu()
+
+
+def _router(*a, **k):
+    from sparse_moe_layer_topk_gb300.route import Router
+    return Router(*a, **k)
+
+
+def _check(logits, bias, k, score="sigmoid", renorm=True, scale=1.0, flag=0, **groups):
+    T, E = logits.shape
+    r = _router(T, E, k, score=score, renorm=renorm, scale=scale, **groups)
+    idx, w = r.forward(logits.cuda(), None if bias is None else bias.cuda())
+    torch.cuda.synchronize()
+    want = O.route(f64(logits), None if bias is None else f64(bias), k, score, renorm=renorm, scale=scale, **groups)
+    np.testing.assert_array_equal(idx.cpu().numpy(), want[0])
+    np.testing.assert_allclose(f64(w), want[1], rtol=TOL, atol=1e-37)
+    np.testing.assert_allclose(f64(r.topk_s), want[2], rtol=TOL, atol=1e-37)
+    assert int(r.err) == flag
+    return r
+
+
+def _logits(T, E, seed=0, std=1.5):
+    return std * torch.randn(T, E, generator=torch.Generator().manual_seed(seed))
+
+
+def _bias(E, seed=0, std=0.05):
+    return std * torch.randn(E, generator=torch.Generator().manual_seed(seed + 1000))
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (3, 8, 3), (5, 8, 8), (2, 33, 32), (7, 64, 6), (9, 100, 7), (4, 255, 31), (33, 896, 16),
+                                   (5, 1024, 32), (3, 1023, 17), (2, 36, 32), (3, 896, 32)])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_without_groups(T, E, k, score, bias, renorm):
+    _check(_logits(T, E, E + k), _bias(E, k) if bias else None, k, score, renorm, 2.5 if renorm else 1.0)
+
+
+@pytest.mark.parametrize("E,groups,group_k,k", [(896, 8, 4, 16), (896, 8, 1, 32), (896, 7, 3, 9), (896, 14, 13, 16), (256, 8, 4, 8), (60, 4, 2, 6),
+                                                (1024, 32, 5, 32), (1024, 32, 31, 3), (1000, 5, 2, 32), (96, 32, 1, 3), (8, 2, 1, 4), (64, 4, 4, 8),
+                                                (35, 5, 2, 14), (32, 32, 8, 8), (1023, 3, 2, 20), (1020, 17, 9, 32)])
+@pytest.mark.parametrize("score,bias,group_top", [("sigmoid", True, 2), ("sigmoid", False, 2), ("softmax", True, 1),
+                                                  ("softmax", False, 2), ("sigmoid", False, 1), ("softmax", True, 2)])
+def test_groups(E, groups, group_k, k, score, bias, group_top):
+    _check(_logits(21, E, E + groups), _bias(E, k) if bias else None, k, score, groups=groups, group_k=group_k, group_top=group_top)
+
+
+@pytest.mark.parametrize("groups,group_k", [(1, 1), (8, 3), (7, 2)])
+@pytest.mark.parametrize("bias", [None, "zero", "some", "two"])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_rows_of_equal_logits(groups, group_k, bias, score):
+    """A padded batch: the same logit everywhere, so that only the bias and the order of the experts choose."""
+    l = torch.cat([torch.zeros(5, 896), torch.full((3, 896), -3.25), _logits(3, 896)])
+    b = {None: None, "zero": torch.zeros(896), "some": _bias(896), "two": (torch.arange(896) % 3 == 0).float() * 0.125}[bias]
+    _check(l, b, 16, score, groups=groups, group_k=group_k)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("groups,group_k", [(1, 1), (8, 4)])
+def test_values_nearer_than_32_bits_tell_apart(score, groups, group_k):
+    """Score and bias meet: bias = const - score up to a few 2^-24 of noise, so that the order lies below fp32's
+    rounding of the sums, and many pairs differ in logit and bias yet nearly not in their sum."""
+    g = torch.Generator().manual_seed(5)
+    l = torch.randn(40, 896, generator=g).repeat_interleave(3, 0)[:64]
+    s = torch.sigmoid(l.double()) if score == "sigmoid" else torch.softmax(l.double(), 1)
+    b = (0.75 - s[0] + 1e-8 * torch.randn(896, generator=g, dtype=torch.float64)).float()
+    _check(l, b, 16, score, groups=groups, group_k=group_k)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("groups,group_k", [(1, 1), (4, 2)])
+@pytest.mark.parametrize("by", ["logit", "bias"])
+def test_experts_out_of_service(score, groups, group_k, by):
+    """-infinity takes an expert out; where too few others are left, such experts fill the list with weight 0."""
+    l, b = _logits(12, 64, 3), _bias(64)
+    out = torch.rand(12, 64, generator=torch.Generator().manual_seed(8)) < torch.linspace(0.05, 1.0, 12)[:, None]
+    out[-1] = True
+    if by == "logit":
+        l[out] = -torch.inf
+    else:
+        b[out[6]] = -torch.inf
+    r = _check(l, b if by == "bias" else None, 8, score, groups=groups, group_k=group_k)
+    assert not r.topk_w.isnan().any()
+
+
+def test_values_that_are_no_numbers_are_flagged_and_taken_out():
+    for bad in (float("nan"), float("inf")):
+        l = _logits(4, 128)
+        l[2, 7] = bad
+        r = _check(l, None, 8, flag=M.MOE_FLAG_NONFINITE)
+        assert 7 not in r.topk_idx[2].tolist()
+        b = _bias(128)
+        b[9] = bad
+        r = _check(_logits(4, 128), b, 8, "softmax", flag=M.MOE_FLAG_NONFINITE)
+        assert 9 not in r.topk_idx.flatten().tolist()
+
+
+def test_extreme_logits():
+    l = torch.tensor([[-100.0, -101.0, -102.5, -90.0] * 16, [100.0, 99.0, 80.0, -3e38] * 16, [3e38, 1.0, -3e38, 0.0] * 16,
+                      [-300.0, -301.0, -302.0, -303.0] * 16])
+    for score in ("sigmoid", "softmax"):
+        _check(l[[0, 3]], None, 6, score)
+    r = _router(4, 64, 6)
+    idx, w = r.forward(l.cuda())
+    np.testing.assert_allclose(f64(w).sum(1), 1.0, rtol=1e-6)
+    assert idx[1].tolist() == [0, 4, 8, 12, 16, 20]
+
+
+@pytest.mark.parametrize("E", [64, 100, 896, 1023])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_gradient(E, score, renorm, dtype):
+    """fp32: within 2^-17 of the terms of each entry (g_j and the weighted sum of all g); bf16: a rounding more, 2^-8."""
+    T, k = 37, 7
+    l, g = _logits(T, E, E), torch.randn(T, k, generator=torch.Generator().manual_seed(1))
+    l[3, 5:9] = -torch.inf
+    r = _router(T, E, k, score=score, renorm=renorm, scale=2.5, grad_dtype=dtype)
+    r.forward(l.cuda(), _bias(E).cuda())
+    idx, w, s = r.topk_idx.cpu().numpy(), f64(r.topk_w), f64(r.topk_s)
+    got = f64(r.backward(g.cuda()))
+    args = f64(g), f64(l), idx, w, s, score, renorm, 2.5
+    want = O.route_backward(*args)
+    size = np.abs(want)
+    if renorm:
+        np.put_along_axis(size, idx.astype(np.int64), w * (np.abs(f64(g)) + (w * np.abs(f64(g))).sum(1, keepdims=True) / 2.5), 1)
+    elif score == "softmax":
+        size = size + 2.5 * O.scores(f64(l), score) * (s * np.abs(f64(g))).sum(1, keepdims=True)
+    bound = TOL * size + (2.0 ** -8 * np.abs(want) if dtype == torch.bfloat16 else 0) + 1e-37
+    assert (np.abs(got - want) <= bound).all()
+    assert int(r.err) == 0
+
+
+def test_gradient_from_permuted_rows():
+    T, E, k = 20, 64, 4
+    r = _router(T, E, k)
+    r.forward(_logits(T, E).cuda())
+    slot = torch.randperm(T * k, generator=torch.Generator().manual_seed(0)).to(torch.int32).view(T, k)
+    slot[3, 1] = -1
+    rows = torch.randn(T * k, generator=torch.Generator().manual_seed(2))
+    d_w = torch.empty(T, k, device="cuda")
+    got = r.backward(rows.cuda(), slot.cuda(), d_w).clone()
+    want = torch.where(slot >= 0, rows[slot.long().clamp(min=0)], 0.0)
+    assert torch.equal(d_w.cpu(), want)
+    assert torch.equal(r.backward(want.cuda()), got)
+
+
+@pytest.mark.parametrize("score,renorm", [("sigmoid", True), ("softmax", False)])
+def test_gradient_of_bad_and_repeated_ids(score, renorm):
+    """An id out of range and one that its row names twice are flagged, and nothing is written out of bounds."""
+    T, E, k = 6, 64, 4
+    r = _router(T, E, k, score=score, renorm=renorm)
+    r.forward(_logits(T, E).cuda())
+    d_w = torch.ones(T, k, device="cuda")
+    good = r.backward(d_w).clone()
+    assert int(r.err) == 0
+    r.topk_idx[1, 2] = E
+    r.topk_idx[2, 3] = -5
+    r.topk_idx[4, 3] = r.topk_idx[4, 0]
+    got = r.backward(d_w)
+    assert int(r.err) == M.MOE_FLAG_BAD_EXPERT
+    rows = [0, 3, 5]
+    assert torch.equal(got[rows], good[rows]) and bool(got.isfinite().all())
+
+
+def test_no_tokens():
+    r = _router(0, 64, 4)
+    idx, w = r.forward(torch.empty(0, 64, device="cuda"))
+    assert idx.shape == (0, 4) and r.backward(torch.empty(0, 4, device="cuda")).shape == (0, 64)
+
+
+def test_in_a_graph_and_on_another_stream():
+    T, E, k = 300, 896, 16
+    l, b, g = _logits(T, E).cuda(), _bias(E).cuda(), torch.randn(T, k, device="cuda")
+    kw = dict(score="softmax", renorm=False, groups=8, group_k=4)
+    r = _router(T, E, k, **kw)
+    r.forward(l, b), r.backward(g)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        r.forward(l, b), r.backward(g)
+    l.copy_(_logits(T, E, 7).cuda())
+    graph.replay()
+    side = torch.cuda.Stream()
+    other = _router(T, E, k, **kw)
+    torch.cuda.synchronize()
+    other.forward(l, b, stream=side), other.backward(g, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(r.topk_idx, other.topk_idx) and torch.equal(r.topk_w, other.topk_w)
+    assert torch.equal(r.d_logits, other.d_logits)
