@@ -12,6 +12,17 @@ constexpr unsigned kAll = 0xFFFFFFFFu;
 constexpr int kWarps = 8;      // tokens of a CTA, one for each warp
 constexpr float kLog2e = 1.4426950408889634f;
 
+__device__ __forceinline__ float exp2_quick(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_quick(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xFF800000); }
 
 // Order-preserving bits of a float (+0 and -0 are one value); 0 is below every number's.
@@ -21,18 +32,6 @@ __device__ __forceinline__ uint32_t order_bits(float v) {
 }
 __device__ __forceinline__ float bits_value(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
-}
-
-// How the experts of a token lie on the lanes: the groups side by side, `lanes` lanes each (a power of two), a
-// lane holding every lanes-th expert (or every lanes-th run of four) of its group.
-struct Layout {
-  int size, lanes, group, sub;
-  bool mine;  // whether this lane has a group
-};
-
-template <bool VEC>
-__device__ __forceinline__ int place_in_group(const Layout& g, int i) {
-  return VEC ? 4 * (g.sub + g.lanes * (i >> 2)) + (i & 3) : g.sub + g.lanes * i;
 }
 
 struct Params {
@@ -45,92 +44,6 @@ struct Params {
   float* s;
   int* err_flag;
 };
-
-// The same selection in 64 bits, for the rare tokens whose 32-bit values are too close to tell apart: lane j gets the
-// j-th expert. Values that are not numbers below infinity count as masked, as in the kernel.
-template <bool SOFTMAX, bool VEC>
-__device__ __noinline__ int select_exactly(const Params& p, const float* row, Layout g, int npl) {
-  const int lane = static_cast<int>(lane_id());
-  double c[64];
-  float top = neg_inf();
-  // A padded row (equal logits, equal biases): the first experts, without any arithmetic.
-  bool equal = row[0] < -neg_inf() && row[0] > neg_inf();
-  for (int i = lane; i < p.E; i += 32) equal &= row[i] == row[0] && (!p.bias || p.bias[i] == p.bias[0]);
-  if (__all_sync(kAll, equal && (!p.bias || fabsf(p.bias[0]) < -neg_inf()))) return lane;
-  for (int i = 0; i < npl; ++i) {
-    const int at = place_in_group<VEC>(g, i);
-    const float l = g.mine && at < g.size ? row[g.group * g.size + at] : neg_inf();
-    c[i] = l < -neg_inf() ? l : neg_inf();
-    top = fmaxf(top, static_cast<float>(c[i]));
-  }
-  double total = 1.0;
-  if (SOFTMAX) {
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
-    total = 0.0;
-    for (int i = 0; i < npl; ++i) total += c[i] > -1e300 ? exp(c[i] - top) : 0.0;
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
-  }
-  unsigned long long taken = 0;
-  for (int i = 0; i < npl; ++i) {
-    const int at = place_in_group<VEC>(g, i);
-    if (!g.mine || at >= g.size) {
-      taken |= 1ull << i;
-      continue;
-    }
-    const float b = p.bias ? p.bias[g.group * g.size + at] : 0.0f;
-    if (c[i] > -1e300 && b < -neg_inf() && b > neg_inf()) {
-      const double s = SOFTMAX ? exp(c[i] - top) / total : 1.0 / (1.0 + exp(-c[i]));
-      // (without a bias the logits order the experts, which scores near one no longer can)
-      c[i] = p.bias ? s + b : c[i];
-    } else {
-      c[i] = -INFINITY;
-    }
-  }
-  if (p.groups > 1) {
-    double t1 = -INFINITY, t2 = -INFINITY;
-    for (int i = 0; i < npl; ++i) {
-      if (taken >> i & 1) continue;
-      if (c[i] > t1) t2 = t1, t1 = c[i];
-      else if (c[i] > t2) t2 = c[i];
-    }
-    for (int o = 1; o < g.lanes; o <<= 1) {
-      const double a = __shfl_xor_sync(kAll, t1, o), b = __shfl_xor_sync(kAll, t2, o);
-      t2 = fmax(fmin(t1, a), fmax(t2, b));
-      t1 = fmax(t1, a);
-    }
-    if (!p.bias) {
-      const auto score = [&](double l) { return l < -1e300 ? l : SOFTMAX ? exp(l - top) / total : 1.0 / (1.0 + exp(-l)); };
-      t1 = p.group_top == 1 ? t1 : score(t1);
-      t2 = score(t2);
-    }
-    const double value = p.group_top > 1 && t2 > -1e300 ? t1 + t2 : t1;
-    int rank = 0;
-    for (int q = 0; q < p.groups; ++q) {
-      const double v = __shfl_sync(kAll, value, q * g.lanes);
-      rank += v > value || (v == value && q < g.group);
-    }
-    if (rank >= p.group_k) taken = ~0ull;
-  }
-  int mine = -1;
-  for (int j = 0; j < p.k; ++j) {
-    double best = -INFINITY;
-    int e = 0x7FFFFFFF, at = -1;
-    for (int i = 0; i < npl; ++i) {
-      const int id = g.group * g.size + place_in_group<VEC>(g, i);
-      if (!(taken >> i & 1) && (c[i] > best || (c[i] == best && id < e))) best = c[i], e = id, at = i;
-    }
-    double top_c = best;
-    int top_e = e;
-    for (int o = 16; o > 0; o >>= 1) {
-      const double oc = __shfl_xor_sync(kAll, top_c, o);
-      const int oe = __shfl_xor_sync(kAll, top_e, o);
-      if (oe != 0x7FFFFFFF && (top_e == 0x7FFFFFFF || oc > top_c || (oc == top_c && oe < top_e))) top_c = oc, top_e = oe;
-    }
-    if (e == top_e && at >= 0) taken |= 1ull << at;
-    if (lane == j) mine = top_e;
-  }
-  return mine;
-}
 
 // Bitonic sort of one value a lane, descending.
 template <typename V, typename Less>
@@ -147,52 +60,178 @@ __device__ __forceinline__ V sort_lanes(V x, int lane, Less less) {
   return x;
 }
 
+// A value and what tells it apart, for the sorts in 64 bits: larger values first, then lower ids.
+struct Exact {
+  double c;
+  int id;
+};
+__device__ __forceinline__ bool behind(const Exact& a, const Exact& b) { return a.c < b.c || (a.c == b.c && a.id > b.id); }
+__device__ __forceinline__ Exact sort_exact(Exact x, int lane) {
+#pragma unroll
+  for (int size = 2; size <= 32; size <<= 1) {
+#pragma unroll
+    for (int stride = size >> 1; stride > 0; stride >>= 1) {
+      const Exact o{__shfl_xor_sync(kAll, x.c, stride), __shfl_xor_sync(kAll, x.id, stride)};
+      const bool keep_larger = ((lane & size) == 0) == ((lane & stride) == 0);
+      if (keep_larger == behind(x, o)) x = o;
+    }
+  }
+  return x;
+}
+
+// Lanes that share a group where the groups lie side by side on a warp (a power of two).
+__device__ __forceinline__ int lanes_of_group(int groups) { return 1 << (31 - __clz(32 / groups)); }
+
+// The whole selection in 64 bits, for the very rare tokens that the steps before leave open: lane j gets the j-th
+// expert. A lane holds every lanes-th expert of one group. Values that are not numbers below infinity count as masked.
+template <bool SOFTMAX>
+__device__ __noinline__ int select_exactly(const Params& p, const float* row) {
+  const int lane = static_cast<int>(lane_id());
+  const int size = p.E / p.groups, lanes = lanes_of_group(p.groups), group = lane / lanes, sub = lane % lanes;
+  const int n = group < p.groups ? (size - sub + lanes - 1) / lanes : 0;  // (at most 61)
+  const auto id_of = [&](int i) { return group * size + sub + lanes * i; };
+  // A padded row (equal logits, equal biases): the first experts, without any arithmetic.
+  bool equal = row[0] < -neg_inf() && row[0] > neg_inf();
+  for (int i = lane; i < p.E; i += 32) equal &= row[i] == row[0] && (!p.bias || p.bias[i] == p.bias[0]);
+  if (__all_sync(kAll, equal && (!p.bias || fabsf(p.bias[0]) < -neg_inf()))) return lane;
+  double c[64];
+  float top = neg_inf();
+  for (int i = 0; i < n; ++i) {
+    const float l = row[id_of(i)];
+    c[i] = l < -neg_inf() ? l : neg_inf();
+    top = fmaxf(top, static_cast<float>(c[i]));
+  }
+  double total = 1.0;
+  if (SOFTMAX) {
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+    total = 0.0;
+    for (int i = 0; i < n; ++i) total += c[i] > -1e300 ? exp(c[i] - top) : 0.0;
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
+  }
+  const auto score = [&](double l) { return SOFTMAX ? exp(l - top) / total : 1.0 / (1.0 + exp(-l)); };
+  unsigned long long taken = 0;
+  for (int i = 0; i < n; ++i) {
+    const float b = p.bias ? p.bias[id_of(i)] : 0.0f;
+    if (!(c[i] > -1e300 && b < -neg_inf() && b > neg_inf())) c[i] = -INFINITY;
+    else if (p.bias) c[i] = score(c[i]) + b;  // (without a bias the logits order the experts, which scores near one no longer can)
+  }
+  if (p.groups > 1) {
+    double t1 = -INFINITY, t2 = -INFINITY;
+    for (int i = 0; i < n; ++i) {
+      if (c[i] > t1) t2 = t1, t1 = c[i];
+      else if (c[i] > t2) t2 = c[i];
+    }
+    for (int o = 1; o < lanes; o <<= 1) {
+      const double x = __shfl_xor_sync(kAll, t1, o), y = __shfl_xor_sync(kAll, t2, o);
+      t2 = fmax(fmin(t1, x), fmax(t2, y));
+      t1 = fmax(t1, x);
+    }
+    if (!p.bias && p.group_top > 1) {
+      t1 = t1 < -1e300 ? t1 : score(t1);
+      t2 = t2 < -1e300 ? t2 : score(t2);
+    }
+    const double value = p.group_top > 1 && t2 > -1e300 ? t1 + t2 : t1;
+    int rank = 0;
+    for (int q = 0; q < p.groups; ++q) {
+      const double v = __shfl_sync(kAll, value, q * lanes);
+      rank += v > value || (v == value && q < group);
+    }
+    if (rank >= p.group_k) taken = ~0ull;
+  }
+  int mine = -1;
+  for (int j = 0; j < p.k; ++j) {
+    Exact best{-INFINITY, 0x7FFFFFFF};
+    int at = -1;
+    for (int i = 0; i < n; ++i) {
+      const Exact x{c[i], id_of(i)};
+      if (!(taken >> i & 1) && (at < 0 || behind(best, x))) best = x, at = i;
+    }
+    const int own = best.id;
+    for (int o = 16; o > 0; o >>= 1) {
+      const Exact x{__shfl_xor_sync(kAll, best.c, o), __shfl_xor_sync(kAll, best.id, o)};
+      if (behind(best, x)) best = x;
+    }
+    if (at >= 0 && own == best.id) taken |= 1ull << at;
+    if (lane == j) mine = best.id;
+  }
+  return mine;
+}
+
+// What the groups' choice needs of one group's lanes, in 64 bits: the value of the group from its two largest members, found
+// again in `row_c` (the 32-bit values by expert). False where a third member is too close to the second.
+template <bool SOFTMAX>
+__device__ __noinline__ bool group_value_exactly(const Params& p, const float* row, const float* row_c, int size, int lanes, int group, int sub,
+                                                 float t1, float t2, float tol, float top, float inv, double& value, double& scores) {
+  int at1 = 0x7FFFFFFF, at2 = 0x7FFFFFFF, close = 0;
+  const bool mine = group < p.groups;
+  for (int i = sub; mine && i < size; i += lanes)
+    if (row_c[group * size + i] == t1) at1 = min(at1, i);
+  for (int o = 1; o < lanes; o <<= 1) at1 = min(at1, __shfl_xor_sync(kAll, at1, o));
+  for (int i = sub; mine && i < size; i += lanes) {
+    const float c = row_c[group * size + i];
+    if (c == t2 && i != at1) at2 = min(at2, i);
+    close += c > neg_inf() && c >= t2 - tol;
+  }
+  for (int o = 1; o < lanes; o <<= 1) {
+    at2 = min(at2, __shfl_xor_sync(kAll, at2, o));
+    close += __shfl_xor_sync(kAll, close, o);
+  }
+  const auto exactly = [&](int at, double& s) {
+    const int e = group * size + at;
+    const double l = row[e];
+    s = SOFTMAX ? exp(l - static_cast<double>(top)) * static_cast<double>(inv) : 1.0 / (1.0 + exp(-l));
+    return p.bias ? s + static_cast<double>(p.bias[e]) : s;
+  };
+  value = -INFINITY, scores = 0.0;
+  if (!mine || !(t1 > neg_inf())) return true;
+  double s1 = 0.0, s2 = 0.0;
+  value = exactly(at1, s1);
+  if (p.group_top > 1 && t2 > neg_inf()) value += exactly(at2, s2);
+  scores = s1 + s2;
+  return close <= 2 || p.group_top == 1;
+}
+
 // One warp routes one token; the logits are read once and HBM bounds it.
 //
 // The values that choose (score + bias, or the logits themselves without a bias) are held as order-preserving bits,
-// NPL a lane. Groups: a lane's two largest, joined over the group's lanes; each group is ranked by counting those
-// ahead of it; the experts of the groups that stay are spread over all lanes by way of shared memory. Of the lanes'
-// maxima the (k+1)-th is a bound tau that at least k + 1 values reach; those that do (some twenty of 896) are sorted
-// across the warp. More than 32 of them, or too few lanes for the bound: k rounds of a warp-wide maximum.
+// NPL a lane, runs of four (VEC) or single ones spread over all lanes. Groups: the values pass through shared memory to lanes that lie
+// by groups, which find each group's two largest and rank the groups by counting those ahead; the other groups' values
+// are cleared. Of the lanes' maxima the (k+1)-th is a bound tau that at least k + 1 values reach; those that do (some twenty
+// of 896) are sorted across the warp. More than 32 of them, or too few lanes for the bound: k rounds of a warp-wide maximum.
 //
-// Which experts are chosen does not depend on the rounding here: a 32-bit score is within
+// Which experts are chosen does not depend on the rounding here. A 32-bit score is within
 // tol = 2^-21 s (2 + |l - m|) + 2^-22 |c| of its value (the exponent's argument is rounded once, 2^-24 of it, the exponential and
-// the reciprocal are right to 2 ulp, the sum over the experts to 4; m is the row's maximum, 0 for the sigmoid), and where two
-// neighbours in the order are nearer than that, the candidates are sorted again by their values in 64 bits. Two
-// experts with the same logit and bias are equal in any precision and go by their index.
-template <int NPL, bool VEC, bool SOFTMAX>
+// the reciprocal are right to 2 ulp, the sum over the experts to 4; m is the row's maximum, 0 for the sigmoid). Where two
+// neighbours in the order, or two groups, are nearer than that, all that could be meant are compared by values in 64
+// bits. (A softmax keeps its 32-bit sum there, a common factor: only the scores' difference is uncertain by 2^-20 of itself,
+// and where that is not enough either the token starts over in 64 bits: 15 us.) Two experts with the same logit and bias are
+// equal in any precision and go by their index.
+template <int NPL, bool VEC, bool SOFTMAX, bool GROUPED>
 __global__ void __launch_bounds__(kWarps * 32) route_scores_kernel(Params p) {
-  extern __shared__ uint32_t pool[];
+  extern __shared__ float pool[];
   __shared__ unsigned long long cand_s[kWarps][32];
-  __shared__ int kept_s[kWarps][32];
   const int t = (blockIdx.x * kWarps * 32 + threadIdx.x) >> 5;
   const int lane = static_cast<int>(lane_id()), wib = threadIdx.x >> 5;
   if (t >= p.T) return;
-  const float* const row = p.logits + static_cast<size_t>(t) * p.E;
-  Layout g;
-  g.size = p.E / p.groups;
-  g.lanes = 1 << (31 - __clz(32 / p.groups));
-  g.group = lane / g.lanes;
-  g.sub = lane % g.lanes;
-  g.mine = g.group < p.groups;
-  const int k = p.k;
+  const int E = p.E, k = p.k;
+  const float* const row = p.logits + static_cast<size_t>(t) * E;
   const bool by_logit = p.bias == nullptr;
+  const auto expert_of = [&](int i) { return VEC ? 128 * (i >> 2) + 4 * lane + (i & 3) : lane + 32 * i; };
+  const auto here = [&](int i) { return VEC ? 128 * (i >> 2) + 4 * lane < E : lane + 32 * i < E; };
 
   float v[NPL];  // logits, then the values that choose
-  bool bad = false;
+  if (VEC) {
 #pragma unroll
-  for (int i = 0; i < NPL; i += VEC ? 4 : 1) {
-    const int at = place_in_group<VEC>(g, i);
-    const bool in = g.mine && at < g.size;
-    if (VEC) {
+    for (int i = 0; i < NPL / 4; ++i) {
       float4 x = make_float4(neg_inf(), neg_inf(), neg_inf(), neg_inf());
-      if (in) x = __ldg(reinterpret_cast<const float4*>(row + g.group * g.size + at));
-      v[i] = x.x;
-      if (i + 1 < NPL) v[i + 1] = x.y, v[i + 2] = x.z, v[i + 3] = x.w;
-    } else {
-      v[i] = in ? __ldg(row + g.group * g.size + at) : neg_inf();
+      if (here(4 * i)) x = __ldg(reinterpret_cast<const float4*>(row) + 32 * i + lane);
+      v[4 * i] = x.x, v[4 * i + 1] = x.y, v[4 * i + 2] = x.z, v[4 * i + 3] = x.w;
     }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) v[i] = here(i) ? __ldg(row + expert_of(i)) : neg_inf();
   }
+  bool bad = false;
   float top = neg_inf();
 #pragma unroll
   for (int i = 0; i < NPL; ++i) {
@@ -209,98 +248,149 @@ __global__ void __launch_bounds__(kWarps * 32) route_scores_kernel(Params p) {
     top = top > neg_inf() ? top : 0.0f;
     float sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) sum += exp2f((v[i] - top) * kLog2e);
+    for (int i = 0; i < NPL; ++i) sum += exp2_quick((v[i] - top) * kLog2e);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
     inv = sum > 0.0f ? 1.0f / sum : 0.0f;
   }
   const auto quick_score = [&](float l) {
-    return SOFTMAX ? exp2f((l - top) * kLog2e) * inv : __fdividef(1.0f, 1.0f + __expf(-l));
+    return SOFTMAX ? exp2_quick((l - top) * kLog2e) * inv : rcp_quick(1.0f + exp2_quick(-l * kLog2e));
   };
   uint32_t kv[NPL];  // 0: no expert of this lane
+  if (!by_logit) {
 #pragma unroll
-  for (int i = 0; i < NPL; ++i) {
-    const int at = place_in_group<VEC>(g, i);
-    const bool in = g.mine && at < g.size;
-    if (!by_logit && in) {
-      const float b = __ldg(p.bias + g.group * g.size + at);
-      bad |= !(b < -neg_inf());
-      const float s = quick_score(v[i]);
-      v[i] = v[i] > neg_inf() && b < -neg_inf() ? s + b : neg_inf();
+    for (int i = 0; i < NPL; i += VEC ? 4 : 1) {
+      float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (here(i)) {
+        if (VEC) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) b[j] = __ldg(p.bias + expert_of(i) + j);
+        } else {
+          b[0] = __ldg(p.bias + expert_of(i));
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < (VEC ? 4 : 1); ++j) {
+        bad |= !(b[j] < -neg_inf());
+        v[i + j] = v[i + j] > neg_inf() && b[j] < -neg_inf() ? quick_score(v[i + j]) + b[j] : neg_inf();
+      }
     }
-    kv[i] = in ? order_bits(v[i]) : 0u;
   }
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) kv[i] = here(i) ? order_bits(v[i]) : 0u;
   if (__any_sync(kAll, bad) && lane == 0) set_flag(p.err_flag, MOE_FLAG_NONFINITE);
 
-  bool exact = false;  // whether the order has to be found in 64 bits
-  const bool grouped = p.groups > 1 && p.group_k < p.groups;
-  if (grouped) {
-    float t1 = neg_inf(), t2 = neg_inf();
+  bool exact = false;  // whether the token starts over in 64 bits
+  if (GROUPED) {
+    const int size = E / p.groups, lanes = lanes_of_group(p.groups), group = lane / lanes, sub = lane % lanes;
+    float* const row_c = pool + static_cast<size_t>(wib) * E;
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-      const float x = kv[i] ? v[i] : neg_inf();
+    for (int i = 0; i < NPL; i += VEC ? 4 : 1) {
+      if (!here(i)) continue;
+      if (VEC) *reinterpret_cast<float4*>(row_c + expert_of(i)) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+      else row_c[expert_of(i)] = v[i];
+    }
+    __syncwarp();
+    float t1 = neg_inf(), t2 = neg_inf();
+    const auto meet = [&](float x) {
       t2 = fmaxf(t2, fminf(t1, x));
       t1 = fmaxf(t1, x);
+    };
+    if (group < p.groups) {
+      const float* const from = row_c + group * size;
+      if (VEC) {
+#pragma unroll 4
+        for (int i = 4 * sub; i < size; i += 4 * lanes) {
+          const float4 x = *reinterpret_cast<const float4*>(from + i);
+          meet(x.x), meet(x.y), meet(x.z), meet(x.w);
+        }
+      } else {
+#pragma unroll 4
+        for (int i = sub; i < size; i += lanes) meet(from[i]);
+      }
     }
-    for (int o = 1; o < g.lanes; o <<= 1) {
+    for (int o = 1; o < lanes; o <<= 1) {
       const float a = __shfl_xor_sync(kAll, t1, o), b = __shfl_xor_sync(kAll, t2, o);
       t2 = fmaxf(fminf(t1, a), fmaxf(t2, b));
       t1 = fmaxf(t1, a);
     }
     const bool sums = p.group_top > 1;
-    float value = t1, slack = 0.0f;
-    if (by_logit) {
-      const float s1 = t1 > neg_inf() ? quick_score(t1) : t1, s2 = t2 > neg_inf() ? quick_score(t2) : t2;
-      if (sums) value = s2 > neg_inf() ? s1 + s2 : s1;
+    float value = t1;
+    if (by_logit && sums && t1 > neg_inf()) {
+      value = quick_score(t1);
+      if (t2 > neg_inf()) value += quick_score(t2);
     } else if (sums && t2 > neg_inf()) {
       value = t1 + t2;
     }
-    // (a score is at most 1, with softmax at most the row's largest; two of them and the sum's rounding)
-    if (sums || !by_logit) slack = 0x1p-18f * (SOFTMAX ? fminf(1.0f, inv) : 1.0f);
+    // (scores are at most 1, with softmax at most the row's largest, and off by 2^-22 of that for every 2 of |l|: 2^-19 for two of them)
+    const float slack = sums || !by_logit ? 0x1p-19f * (SOFTMAX ? fminf(1.0f, inv) : 1.0f) : 0.0f;
     int rank = 0;
     unsigned near = 0;  // groups whose value is too close to this one's to tell apart
     for (int q = 0; q < p.groups; ++q) {
-      const float x = __shfl_sync(kAll, value, q * g.lanes), x1 = __shfl_sync(kAll, t1, q * g.lanes),
-                  x2 = __shfl_sync(kAll, t2, q * g.lanes);
-      rank += x > value || (x == value && q < g.group);
-      const bool same = by_logit && x1 == t1 && x2 == t2;
-      const float d = fabsf(x - value);  // (NaN where both are empty)
-      if (slack > 0.0f && !same && d <= 2.0f * slack + 0x1p-21f * (fabsf(x) + fabsf(value)) && d < -neg_inf()) near |= 1u << q;
+      const float x = __shfl_sync(kAll, value, q * lanes);
+      rank += x > value || (x == value && q < group);
+      // (values of empty groups give NaN or infinity here: not near)
+      if (slack > 0.0f && fabsf(x - value) <= slack + 0x1p-21f * (fabsf(x) + fabsf(value)) && fabsf(x) < -neg_inf()) near |= 1u << q;
     }
-    const bool keep = g.mine && rank < p.group_k;
-    const unsigned kept_lanes = __ballot_sync(kAll, keep);
-    unsigned kept = 0;  // by group
-    for (int q = 0; q < p.groups; ++q) kept |= (kept_lanes >> (q * g.lanes) & 1u) << q;
-    const unsigned groups_mask = p.groups < 32 ? (1u << p.groups) - 1u : kAll;
-    exact = __any_sync(kAll, g.mine && (near & (keep ? groups_mask & ~kept : kept)));
-    if (!exact) {
-      // the experts of the groups that stay, over all lanes
-      uint32_t* const mine = pool + static_cast<size_t>(wib) * p.group_k * g.size;
-      const int order = __popc(kept & ((1u << g.group) - 1u));
-      if (keep) {
-        if (g.sub == 0) kept_s[wib][order] = g.group;
-#pragma unroll
-        for (int i = 0; i < NPL; ++i) {
-          const int at = place_in_group<VEC>(g, i);
-          if (at < g.size) mine[order * g.size + at] = kv[i];
-        }
+    const unsigned all = p.groups < 32 ? (1u << p.groups) - 1u : kAll;
+    bool keep = group < p.groups && rank < p.group_k;
+    const auto by_group = [&](bool flag) {  // a flag of each group's lanes, as bits by group
+      const unsigned x = __ballot_sync(kAll, flag);
+      unsigned r = 0;
+      for (int q = 0; q < p.groups; ++q) r |= (x >> (q * lanes) & 1u) << q;
+      return r;
+    };
+    unsigned kept = by_group(keep);
+    if (__any_sync(kAll, group < p.groups && (near & (keep ? all & ~kept : kept)))) {
+      double value64, scores;
+      const float* const row_v = by_logit ? row : row_c;  // (where t1 and t2 were found)
+      const bool sure = group_value_exactly<SOFTMAX>(p, row, row_v, size, lanes, group, sub, t1, t2, by_logit ? fabsf(t2) * 0x1p-20f + 0x1p-20f : slack,
+                                                     top, inv, value64, scores);
+      int rank64 = 0;
+      bool open = !sure;
+      for (int q = 0; q < p.groups; ++q) {
+        const double x = __shfl_sync(kAll, value64, q * lanes), xs = __shfl_sync(kAll, scores, q * lanes);
+        rank64 += x > value64 || (x == value64 && q < group);
+        if (SOFTMAX && q != group && x > -1e300 && fabs(x - value64) <= 0x1p-20 * fabs(xs - scores) + 0x1p-45 * fabs(xs)) open = true;
       }
-      __syncwarp();
-      const int n = p.group_k * g.size;
+      exact = __any_sync(kAll, open && group < p.groups);
+      keep = group < p.groups && rank64 < p.group_k;
+      kept = by_group(keep);
+    }
+    const float per = 1.0f / static_cast<float>(size);
 #pragma unroll
-      for (int i = 0; i < NPL; ++i) kv[i] = 0u;
+    for (int i = 0; i < NPL; i += VEC ? 4 : 1) {  // (x + 1/2) / size is at least 2^-11 from a whole number, and x < 2^10: the cut is right
+      const bool stays = kept >> static_cast<int>((static_cast<float>(expert_of(i)) + 0.5f) * per) & 1u;
 #pragma unroll
-      for (int i = 0; i < (NPL < 32 ? NPL : 32); ++i)
-        if (lane + 32 * i < n) kv[i] = mine[lane + 32 * i];
+      for (int j = 0; j < (VEC ? 4 : 1); ++j) kv[i + j] = stays && here(i) ? kv[i + j] : 0u;
     }
   }
-  const auto expert_of = [&](int i) {
-    if (!grouped) return g.group * g.size + place_in_group<VEC>(g, i);
-    const int at = lane + 32 * i, o = at / g.size;
-    return kept_s[wib][o] * g.size + (at - o * g.size);
-  };
   const auto key_of = [&](int i) {
     return kv[i] ? (static_cast<unsigned long long>(kv[i]) << 32) | ~static_cast<uint32_t>(expert_of(i)) : 0ull;
+  };
+  // The experts whose bits reach `bound`, one a lane (0 past them); more than 32: none, and the count.
+  const auto collect = [&](uint32_t bound, unsigned long long& key) {
+    unsigned cand = 0u;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) cand |= kv[i] >= bound ? 1u << i : 0u;
+    const int count = __popc(cand);
+    int pos = count;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(kAll, pos, o);
+      if (lane >= o) pos += x;
+    }
+    const int total = __shfl_sync(kAll, pos, 31);
+    if (total <= 32) {
+      pos -= count;
+#pragma unroll
+      for (int i = 0; i < NPL; ++i)
+        if (cand >> i & 1u) cand_s[wib][pos++] = (static_cast<unsigned long long>(kv[i]) << 32) | ~static_cast<uint32_t>(expert_of(i));
+      __syncwarp();
+      key = lane < total ? cand_s[wib][lane] : 0ull;
+      __syncwarp();
+    }
+    return total;
   };
 
   unsigned long long mine = 0ull;  // lane j: the j-th expert's key
@@ -310,111 +400,76 @@ __global__ void __launch_bounds__(kWarps * 32) route_scores_kernel(Params p) {
     for (int i = 0; i < NPL; ++i) most = max(most, kv[i]);
     const uint32_t sorted = sort_lanes(most, lane, [](uint32_t a, uint32_t b) { return a < b; });
     const uint32_t tau = k < 32 ? __shfl_sync(kAll, sorted, k) : 0u;
-    unsigned cand = 0u;
-    unsigned cand_hi = 0u;
-    int count = 0, total = 33;
-    if (tau != 0u) {
-#pragma unroll
-      for (int i = 0; i < NPL; ++i)
-        if (kv[i] >= tau) (i < 32 ? cand : cand_hi) |= 1u << (i & 31);
-      count = __popc(cand) + __popc(cand_hi);
-      total = __reduce_add_sync(kAll, count);
-    }
-    bool listed = total <= 32;
+    const int total = tau != 0u ? collect(tau, mine) : 33;
+    const bool listed = total <= 32;
     if (listed) {
-      int pos = count;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(kAll, pos, o);
-        if (lane >= o) pos += x;
-      }
-      pos -= count;
-#pragma unroll
-      for (int i = 0; i < NPL; ++i)
-        if ((i < 32 ? cand : cand_hi) >> (i & 31) & 1u) cand_s[wib][pos++] = key_of(i);
-      __syncwarp();
-      mine = sort_lanes(lane < total ? cand_s[wib][lane] : 0ull, lane,
-                        [](unsigned long long a, unsigned long long b) { return a < b; });
+      mine = sort_lanes(mine, lane, [](unsigned long long a, unsigned long long b) { return a < b; });
     } else {
-      unsigned long long taken = 0ull;
+      unsigned taken = 0u;
       for (int j = 0; j < min(k + 1, 32); ++j) {
         unsigned long long best = 0ull;
         int at = 0;
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
-          const unsigned long long x = taken >> i & 1ull ? 0ull : key_of(i);
+          const unsigned long long x = taken >> i & 1u ? 0ull : key_of(i);
           if (x > best) best = x, at = i;
         }
         const uint32_t hi = __reduce_max_sync(kAll, static_cast<uint32_t>(best >> 32));
         const uint32_t lo = __reduce_max_sync(kAll, static_cast<uint32_t>(best >> 32) == hi ? static_cast<uint32_t>(best) : 0u);
         const unsigned long long m = static_cast<unsigned long long>(hi) << 32 | lo;
-        if (m != 0ull && best == m) taken |= 1ull << at;
+        if (m != 0ull && best == m) taken |= 1u << at;
         if (lane == j) mine = m;
       }
-      if (!by_logit) {  // anything left near the last one that differs from it?
-        const unsigned long long last = __shfl_sync(kAll, mine, k - 1);
-        const float c = bits_value(static_cast<uint32_t>(last >> 32));
-        const int e = static_cast<int>(~static_cast<uint32_t>(last));
-        if (c > neg_inf()) {
-          const float l = row[e], b = p.bias[e];
-          const float tol = 0x1p-18f * (SOFTMAX ? fminf(1.0f, inv) : 1.0f) + 0x1p-20f * fabsf(c);
-          bool near = false;
-          for (int i = 0; i < NPL; ++i) {
-            if (kv[i] == 0u || taken >> i & 1ull) continue;
-            if (bits_value(kv[i]) >= c - tol) {
-              const int o = expert_of(i);
-              near |= row[o] != l || p.bias[o] != b;
-            }
-          }
-          exact = __any_sync(kAll, near);
-        }
-      }
     }
-    if (!by_logit && !exact) {
+    if (!by_logit) {
       // neighbours in the order, the first that is left out among them
-      const int checked = min(k + 1, 32);
+      const int listed_n = listed ? total : min(k + 1, 32);
       const float c = bits_value(static_cast<uint32_t>(mine >> 32));
-      const bool real = mine != 0ull && c > neg_inf() && lane < (listed ? total : checked);
+      const bool real = mine != 0ull && c > neg_inf() && lane < listed_n;
       const int e = real ? static_cast<int>(~static_cast<uint32_t>(mine)) : 0;
       const float l = real ? __ldg(row + e) : 0.0f, b = real ? __ldg(p.bias + e) : 0.0f;
       const float tol = real ? 0x1p-21f * fabsf(c - b) * (2.0f + fabsf(l - (SOFTMAX ? top : 0.0f))) + 0x1p-22f * fabsf(c) : 0.0f;
       const float nc = __shfl_down_sync(kAll, c, 1), nl = __shfl_down_sync(kAll, l, 1), nb = __shfl_down_sync(kAll, b, 1),
                   nt = __shfl_down_sync(kAll, tol, 1);
-      const bool next_real = __shfl_down_sync(kAll, static_cast<int>(real), 1) != 0 && lane < 31;
+      const unsigned reals = __ballot_sync(kAll, real);
+      const bool pair = real && (reals >> lane >> 1 & 1u);
+      // what the last chosen one could be taken for: down to `reach`
       const float wide = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(tol)));
-      const float last = __shfl_sync(kAll, c, k - 1);
-      const bool counts = lane + 1 < checked || last - c <= 2.0f * wide;
-      const bool near = real && next_real && counts && (nl != l || nb != b) && c - nc <= tol + nt;
-      const bool beyond = listed && last - bits_value(tau) <= 2.0f * wide;  // something below tau may be as near
-      if (__any_sync(kAll, near) || beyond) {
+      const float last = __shfl_sync(kAll, c, k - 1), reach = last - 2.0f * wide;
+      bool near = pair && (lane + 1 < k || nc >= reach) && (nl != l || nb != b) && c - nc <= tol + nt;
+      if (listed) {
+        near |= last > neg_inf() && reach <= bits_value(tau);  // something below tau may be as near
+      } else if (last > neg_inf()) {  // anything behind the list that differs from the last?
+        const float ll = __shfl_sync(kAll, l, k - 1), lb = __shfl_sync(kAll, b, k - 1);
+        for (int i = 0; i < NPL; ++i)
+          if (kv[i] != 0u && bits_value(kv[i]) >= reach && bits_value(kv[i]) <= last) near |= row[expert_of(i)] != ll || p.bias[expert_of(i)] != lb;
+      }
+      if (__any_sync(kAll, near)) {
         exact = true;
-        if (listed && !SOFTMAX && !beyond) {
-          // every expert that could be among the first k is a candidate: sort these by their 64-bit values
-          const double c64 = real ? 1.0 / (1.0 + exp(-static_cast<double>(l))) + static_cast<double>(b) : -INFINITY;
-          unsigned long long u = static_cast<unsigned long long>(__double_as_longlong(c64 + 0.0));
-          u = u ^ (static_cast<unsigned long long>(static_cast<long long>(u) >> 63) | 0x8000000000000000ull);
-          int id = real ? e : 0x7FFFFFFF - lane;
-          if (!real && mine != 0ull) id = static_cast<int>(~static_cast<uint32_t>(mine));
-          if (mine == 0ull) u = 0ull;
-#pragma unroll
-          for (int size = 2; size <= 32; size <<= 1) {
-#pragma unroll
-            for (int stride = size >> 1; stride > 0; stride >>= 1) {
-              const unsigned long long ou = __shfl_xor_sync(kAll, u, stride);
-              const int oi = __shfl_xor_sync(kAll, id, stride);
-              const bool keep_larger = ((lane & size) == 0) == ((lane & stride) == 0);
-              const bool smaller = u < ou || (u == ou && id > oi);
-              if (keep_larger == smaller) u = ou, id = oi;
-            }
-          }
-          mine = (1ull << 32) | ~static_cast<uint32_t>(id);
+        unsigned long long key = 0ull;
+        const int n = last > neg_inf() ? collect(order_bits(last - 4.0f * wide), key) : 33;
+        if (n <= 32) {  // all that could be among the first k, by their 64-bit values
+          const bool some = lane < n;
+          const int id = some ? static_cast<int>(~static_cast<uint32_t>(key)) : 0x7FFFFFFF;
+          const double l64 = some ? row[id] : 0.0, b64 = some ? p.bias[id] : 0.0;
+          const double s64 = SOFTMAX ? exp(l64 - static_cast<double>(top)) * static_cast<double>(inv) : 1.0 / (1.0 + exp(-l64));
+          const Exact x = sort_exact(Exact{some ? s64 + b64 : -INFINITY, id}, lane);
           exact = false;
+          if (SOFTMAX) {  // the sum's rounding moves neighbours by 2^-20 of their scores' difference
+            const bool in = x.id != 0x7FFFFFFF;
+            const float xl = in ? row[x.id] : 0.0f, xb = in ? p.bias[x.id] : 0.0f;
+            const double y = __shfl_down_sync(kAll, x.c, 1);
+            const float yl = __shfl_down_sync(kAll, xl, 1), yb = __shfl_down_sync(kAll, xb, 1);
+            const bool open = lane + 1 < n && (xl != yl || xb != yb) && x.c - y <= 0x1p-20 * fabs(static_cast<double>(xb) - yb) + 0x1p-45 * fabs(x.c);
+            exact = __any_sync(kAll, open);
+          }
+          mine = (1ull << 32) | ~static_cast<uint32_t>(x.id);
         }
       }
     }
   }
   int e = static_cast<int>(~static_cast<uint32_t>(mine));
-  if (exact) e = select_exactly<SOFTMAX, VEC>(p, row, g, NPL);
+  if (exact) e = select_exactly<SOFTMAX>(p, row);
   const bool out = lane < k;
   const float l = out ? row[e] : neg_inf();
   const float b = out && p.bias ? p.bias[e] : 0.0f;
@@ -537,8 +592,8 @@ __global__ void __launch_bounds__(256) route_scores_bwd_kernel(RouteBwdArgs a) {
   float sum = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    x[i] = make_float4(exp2f((x[i].x - top) * kLog2e), exp2f((x[i].y - top) * kLog2e), exp2f((x[i].z - top) * kLog2e),
-                       exp2f((x[i].w - top) * kLog2e));
+    x[i] = make_float4(exp2_quick((x[i].x - top) * kLog2e), exp2_quick((x[i].y - top) * kLog2e), exp2_quick((x[i].z - top) * kLog2e),
+                       exp2_quick((x[i].w - top) * kLog2e));
     sum += (x[i].x + x[i].y) + (x[i].z + x[i].w);
   }
 #pragma unroll
@@ -565,20 +620,22 @@ __global__ void __launch_bounds__(256) route_scores_bwd_kernel(RouteBwdArgs a) {
 
 template <int NPL, bool VEC, bool SOFTMAX>
 cudaError_t route_launch(const Params& p, cudaStream_t st) {
-  const bool grouped = p.groups > 1 && p.group_k < p.groups;
-  const size_t smem = grouped ? static_cast<size_t>(kWarps) * p.group_k * (p.E / p.groups) * 4 : 0;
-  route_scores_kernel<NPL, VEC, SOFTMAX><<<(p.T + kWarps - 1) / kWarps, kWarps * 32, smem, st>>>(p);
+  const unsigned grid = static_cast<unsigned>((p.T + kWarps - 1) / kWarps);
+  if (p.groups > 1 && p.group_k < p.groups)
+    route_scores_kernel<NPL, VEC, SOFTMAX, true><<<grid, kWarps * 32, static_cast<size_t>(kWarps) * p.E * 4, st>>>(p);
+  else
+    route_scores_kernel<NPL, VEC, SOFTMAX, false><<<grid, kWarps * 32, 0, st>>>(p);
   return cudaGetLastError();
 }
 
 template <bool VEC, bool SOFTMAX>
-cudaError_t route_pick(const Params& p, int npl, cudaStream_t st) {
+cudaError_t route_pick(const Params& p, cudaStream_t st) {
+  const int npl = VEC ? (p.E + 127) / 128 * 4 : (p.E + 31) / 32;
   if (npl <= 4) return route_launch<4, VEC, SOFTMAX>(p, st);
   if (npl <= 8) return route_launch<8, VEC, SOFTMAX>(p, st);
   if (npl <= 16) return route_launch<16, VEC, SOFTMAX>(p, st);
   if (npl <= 28) return route_launch<28, VEC, SOFTMAX>(p, st);
-  if (npl <= 32) return route_launch<32, VEC, SOFTMAX>(p, st);
-  return route_launch<64, VEC, SOFTMAX>(p, st);
+  return route_launch<32, VEC, SOFTMAX>(p, st);
 }
 
 }  // namespace
@@ -586,13 +643,9 @@ cudaError_t route_pick(const Params& p, int npl, cudaStream_t st) {
 cudaError_t launch_route_scores(const RouteArgs& a, cudaStream_t st) {
   LaunchTimer lt("route_scores", st);
   const Params p{a.logits, a.bias, a.T, a.E, a.k, a.groups, a.group_k, a.group_top, a.renorm, a.scale, a.idx, a.w, a.s, a.err_flag};
-  const int size = a.E / a.groups;
-  int lanes = 32;
-  while (lanes * a.groups > 32) lanes >>= 1;
-  const bool vec = size % 4 == 0 && (reinterpret_cast<uintptr_t>(a.logits) & 15u) == 0;
-  const int npl = vec ? 4 * ((size / 4 + lanes - 1) / lanes) : (size + lanes - 1) / lanes;
-  if (a.softmax) return vec ? route_pick<true, true>(p, npl, st) : route_pick<false, true>(p, npl, st);
-  return vec ? route_pick<true, false>(p, npl, st) : route_pick<false, false>(p, npl, st);
+  const bool vec = a.E / a.groups % 4 == 0 && (reinterpret_cast<uintptr_t>(a.logits) & 15u) == 0;
+  if (a.softmax) return vec ? route_pick<true, true>(p, st) : route_pick<false, true>(p, st);
+  return vec ? route_pick<true, false>(p, st) : route_pick<false, false>(p, st);
 }
 
 cudaError_t launch_route_scores_bwd(const RouteBwdArgs& a, cudaStream_t st) {
