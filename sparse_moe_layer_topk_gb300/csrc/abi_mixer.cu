@@ -213,7 +213,7 @@ int moe_conv_fwd(const uint16_t* x, const float* weight, const float* bias, cons
   MOE_CHECK(check_sequences(cu_seqlens, N, T, T));
   MOE_CHECK(check_rows(x, D, ldx));
   MOE_CHECK(check_rows(y, D, ldy));
-  MOE_REQUIRE(aligned(weight, 4) && aligned(bias, 4) && aligned(state_in, 16) && aligned(state_out, 16), MOE_ERR_ALIGN);
+  MOE_REQUIRE(aligned(weight, 16) && aligned(bias, 4) && aligned(state_in, 16) && aligned(state_out, 16), MOE_ERR_ALIGN);
   // (a sequence's last state may be written before another CTA has read its first)
   const size_t state = static_cast<size_t>(N) * (W - 1) * D * 2;
   MOE_REQUIRE(!overlap(state_in, state, state_out, state), MOE_ERR_ARG);
@@ -233,7 +233,7 @@ int moe_conv_bwd(const uint16_t* dy, const uint16_t* x, const float* weight, con
   MOE_CHECK(check_rows(dy, D, lddy));
   MOE_CHECK(check_rows(x, D, ldx));
   MOE_CHECK(check_rows(dx, D, lddx));
-  MOE_REQUIRE(aligned(weight, 4) && aligned(bias, 4) && aligned(state_in, 16) && aligned(d_state_out, 16) &&
+  MOE_REQUIRE(aligned(weight, 16) && aligned(bias, 4) && aligned(state_in, 16) && aligned(d_state_out, 16) &&
                   aligned(d_state_in, 16) && aligned(dw, 4) && aligned(db, 4) && aligned(ws, 16),
               MOE_ERR_ALIGN);
   const size_t state = static_cast<size_t>(N) * (W - 1) * D * 2;
@@ -259,7 +259,7 @@ int moe_conv_step(const uint16_t* x, const float* weight, const float* bias, uin
   MOE_CHECK(check_conv(D, W));
   MOE_CHECK(check_rows(x, D, ldx));
   MOE_CHECK(check_rows(y, D, ldy));
-  MOE_REQUIRE(aligned(weight, 4) && aligned(bias, 4) && aligned(state, 16), MOE_ERR_ALIGN);
+  MOE_REQUIRE(aligned(weight, 16) && aligned(bias, 4) && aligned(state, 16), MOE_ERR_ALIGN);
   MOE_REQUIRE(grid_fits(B, D / 512 + 1), MOE_ERR_ARG);
   if (B == 0) return MOE_OK;
   const ConvStepArgs a{x, weight, bias, state, state_idx, n_slots, B, D, W, ldx, ldy, silu != 0, y, err_flag};

@@ -3,7 +3,8 @@
 //   p_t = bias + sum_j w[j] x_{t - (W-1) + j};  y_t = p_t or silu(p_t)
 //
 // A thread owns four channels (8-byte accesses, a warp's 256 bytes of a row) and walks tokens with the last W inputs
-// in registers, so every input is read once but for the W - 1 rows before a part. All three kernels are bound by HBM.
+// in registers, so every input is read once but for the W - 1 rows before a part. A group of tokens is on its way while the one
+// before it is computed, two values an instruction; HBM bounds all three kernels.
 #include "common.cuh"
 #include "mixer.h"
 #include "seq.cuh"
@@ -16,44 +17,76 @@ int num_sms();
 namespace {
 
 constexpr int kThreads = 128;       // 512 channels
-constexpr int kFwdTokens = 32;      // tokens of a part
+constexpr int kFwdTokens = 64;      // tokens of a part
 constexpr int kBwdTokens = 64;
-constexpr int kStep = 8;            // tokens whose loads are under way together
+constexpr float kLog2e = 1.4426950408889634f;
 
+// Four channels.
 struct F4 {
-  float v[4];
+  f32x2 a, b;
 };
 
-__device__ __forceinline__ F4 load4(const bf16* p) {
-  const uint2 w = *reinterpret_cast<const uint2*>(p);
-  return F4{{bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)}};
-}
-__device__ __forceinline__ void store4(bf16* p, const F4& x) {
-  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(x.v[0], x.v[1]), pack_bf16(x.v[2], x.v[3]));
-}
-__device__ __forceinline__ F4 zero4() { return F4{{0.0f, 0.0f, 0.0f, 0.0f}}; }
+__device__ __forceinline__ F4 make4(float x, float y, float z, float w) { return F4{pack2(x, y), pack2(z, w)}; }
+__device__ __forceinline__ F4 widen(uint2 w) { return make4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)); }
+__device__ __forceinline__ F4 zero4() { return make4(0.0f, 0.0f, 0.0f, 0.0f); }
+__device__ __forceinline__ F4 splat4(float x) { return make4(x, x, x, x); }
+__device__ __forceinline__ F4 fma4(const F4& x, const F4& y, const F4& z) { return F4{fma2(x.a, y.a, z.a), fma2(x.b, y.b, z.b)}; }
+__device__ __forceinline__ F4 mul4(const F4& x, const F4& y) { return F4{mul2(x.a, y.a), mul2(x.b, y.b)}; }
+__device__ __forceinline__ F4 add4(const F4& x, const F4& y) { return F4{add2(x.a, y.a), add2(x.b, y.b)}; }
+__device__ __forceinline__ uint2 load4(const bf16* p) { return *reinterpret_cast<const uint2*>(p); }
+__device__ __forceinline__ uint2 narrow(const F4& x) { return make_uint2(pack_bf16(x.a), pack_bf16(x.b)); }
+__device__ __forceinline__ void store4(bf16* p, uint2 x) { *reinterpret_cast<uint2*>(p) = x; }
 
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// 1 / (1 + exp(-x)).
+__device__ __forceinline__ f32x2 sigmoid2(f32x2 x) {
+  float a, b;
+  unpack2(mul2(x, pack2(-kLog2e, -kLog2e)), a, b);
+  unpack2(add2(pack2(ex2(a), ex2(b)), pack2(1.0f, 1.0f)), a, b);
+  return pack2(rcp(a), rcp(b));
+}
+__device__ __forceinline__ F4 sigmoid4(const F4& x) { return F4{sigmoid2(x.a), sigmoid2(x.b)}; }
 
-// The weights of four channels, tap by tap, from [D][W].
+// The weights of four channels from [D][W], 4 W values one behind the other.
+template <int W>
+__device__ __forceinline__ void load_taps(const float* w, int c, float (&v)[4 * W]) {
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    const float4 x = __ldg(reinterpret_cast<const float4*>(w + static_cast<long long>(c) * W) + i);
+    v[4 * i] = x.x, v[4 * i + 1] = x.y, v[4 * i + 2] = x.z, v[4 * i + 3] = x.w;
+  }
+}
 template <int W>
 __device__ __forceinline__ void load_taps(const float* w, int c, F4 (&tap)[W]) {
+  float v[4 * W];
+  load_taps<W>(w, c, v);
 #pragma unroll
-  for (int j = 0; j < W; ++j)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) tap[j].v[i] = __ldg(w + static_cast<long long>(c + i) * W + j);
+  for (int j = 0; j < W; ++j) tap[j] = make4(v[j], v[W + j], v[2 * W + j], v[3 * W + j]);
+}
+__device__ __forceinline__ F4 load_bias(const float* bias, int c) {
+  return bias ? make4(__ldg(bias + c), __ldg(bias + c + 1), __ldg(bias + c + 2), __ldg(bias + c + 3)) : zero4();
 }
 
 // Input `at` (from -(W-1)) of a sequence: its tokens, and before them its state.
 template <int W>
-__device__ __forceinline__ F4 input_at(const bf16* x, long long ldx, const bf16* state, int D, const SeqPart& s, int at, int c) {
+__device__ __forceinline__ uint2 input_at(const bf16* x, long long ldx, const bf16* state, int D, const SeqPart& s, int at, int c) {
   if (at >= 0) return load4(x + (s.start + at) * ldx + c);
-  if (state == nullptr) return zero4();
+  if (state == nullptr) return make_uint2(0, 0);
   return load4(state + (static_cast<long long>(s.n) * (W - 1) + (W - 1) + at) * D + c);
 }
 
 template <int W, bool SILU>
-__global__ void __launch_bounds__(kThreads) conv_fwd_kernel(ConvArgs a, int blocks) {
+__global__ void __launch_bounds__(kThreads, 5) conv_fwd_kernel(ConvArgs a, int blocks) {
+  constexpr int kStep = 8;
   const int block = blockIdx.x % blocks;  // of channels
   SeqPart s;
   if (!find_part(a.cu, a.N, a.T, a.T, kFwdTokens, blockIdx.x / blocks, s, block == 0 && threadIdx.x < 32 ? a.err_flag : nullptr)) return;
@@ -61,48 +94,45 @@ __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(ConvArgs a, int bloc
   if (c >= a.D) return;
   const bf16* const x = static_cast<const bf16*>(a.x);
   const bf16* const state = static_cast<const bf16*>(a.state_in);
-  bf16* const y = static_cast<bf16*>(a.y);
   const int t0 = s.part * kFwdTokens, t1 = min(s.len, t0 + kFwdTokens);
-  F4 tap[W], win[W];  // win[W - 1]: the newest input
-  load_taps<W>(a.weight, c, tap);
-  F4 bias = zero4();
-  if (a.bias) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) bias.v[i] = __ldg(a.bias + c + i);
-  }
-#pragma unroll
-  for (int j = 1; j < W; ++j) win[j] = input_at<W>(x, a.ldx, state, a.D, s, t0 - W + j, c);
-  for (int t = t0; t < t1; t += kStep) {
-    F4 in[kStep];
-#pragma unroll
-    for (int q = 0; q < kStep; ++q)
-      if (t + q < t1) in[q] = load4(x + static_cast<long long>(s.start + t + q) * a.ldx + c);
+  const bf16* from = x + static_cast<long long>(s.start + t0) * a.ldx + c;
+  bf16* to = static_cast<bf16*>(a.y) + static_cast<long long>(s.start + t0) * a.ldy + c;
+  uint2 next[kStep];
+  const auto fetch = [&](int left) {  // the next group of tokens
 #pragma unroll
     for (int q = 0; q < kStep; ++q) {
-      if (t + q >= t1) break;
+      next[q] = make_uint2(0, 0);
+      if (q < left) next[q] = load4(from + q * a.ldx);
+    }
+    from += kStep * a.ldx;
+  };
+  fetch(t1 - t0);
+  F4 tap[W], in[W - 1 + kStep];
+  load_taps<W>(a.weight, c, tap);
+  const F4 bias = load_bias(a.bias, c);
 #pragma unroll
-      for (int j = 0; j + 1 < W; ++j) win[j] = win[j + 1];
-      win[W - 1] = in[q];
+  for (int j = 0; j + 1 < W; ++j) in[j] = widen(input_at<W>(x, a.ldx, state, a.D, s, t0 - (W - 1) + j, c));
+  for (int t = t0; t < t1; t += kStep) {
+#pragma unroll
+    for (int q = 0; q < kStep; ++q) in[W - 1 + q] = widen(next[q]);
+    fetch(t1 - t - kStep);
+#pragma unroll
+    for (int q = 0; q < kStep; ++q) {
       F4 p = bias;
 #pragma unroll
-      for (int j = 0; j < W; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) p.v[i] = fmaf(tap[j].v[i], win[j].v[i], p.v[i]);
-      if (SILU) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) p.v[i] *= sigmoid(p.v[i]);
-      }
-      store4(y + static_cast<long long>(s.start + t + q) * a.ldy + c, p);
+      for (int j = 0; j < W; ++j) p = fma4(tap[j], in[q + j], p);
+      if (SILU) p = mul4(p, sigmoid4(p));
+      if (t + q < t1) store4(to + q * a.ldy, narrow(p));
     }
+    to += kStep * a.ldy;
+#pragma unroll
+    for (int j = 0; j + 1 < W; ++j) in[j] = in[kStep + j];
   }
   if (a.state_out && t1 == s.len) {
     bf16* const out = static_cast<bf16*>(a.state_out) + static_cast<long long>(s.n) * (W - 1) * a.D + c;
 #pragma unroll
-    for (int j = 0; j + 1 < W; ++j) {
-      // (read again: an empty sequence hands its state on)
-      const F4 v = input_at<W>(x, a.ldx, state, a.D, s, s.len - (W - 1) + j, c);
-      store4(out + static_cast<long long>(j) * a.D, v);
-    }
+    for (int j = 0; j + 1 < W; ++j)  // (read again: an empty sequence hands its state on)
+      store4(out + static_cast<long long>(j) * a.D, input_at<W>(x, a.ldx, state, a.D, s, s.len - (W - 1) + j, c));
   }
 }
 
@@ -110,25 +140,21 @@ __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(ConvArgs a, int bloc
 // tokens on either side for p and dp. A CTA takes every walkers-th part, so its sums of dw and dbias stay in
 // registers; they are joined in a fixed order afterwards.
 template <int W, bool SILU>
-__global__ void __launch_bounds__(kThreads) conv_bwd_kernel(ConvBwdArgs a, int blocks) {
+__global__ void __launch_bounds__(kThreads, 4) conv_bwd_kernel(ConvBwdArgs a, int blocks) {
+  constexpr int kStep = 4;
   const int block = blockIdx.x % blocks, walker = blockIdx.x / blocks, walkers = gridDim.x / blocks;
   const int c = 4 * (block * kThreads + threadIdx.x);
   const bool mine = c < a.D;
   const bf16* const x = static_cast<const bf16*>(a.x);
-  const bf16* const dy = static_cast<const bf16*>(a.dy);
   const bf16* const state = static_cast<const bf16*>(a.state_in);
   const bf16* const d_out = static_cast<const bf16*>(a.d_state_out);
-  bf16* const dx = static_cast<bf16*>(a.dx);
   bf16* const d_in = static_cast<bf16*>(a.d_state_in);
   F4 tap[W], dw[W], db = zero4(), bias = zero4();
 #pragma unroll
   for (int j = 0; j < W; ++j) dw[j] = tap[j] = zero4();
   if (mine) {
     load_taps<W>(a.weight, c, tap);
-    if (a.bias) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) bias.v[i] = __ldg(a.bias + c + i);
-    }
+    bias = load_bias(a.bias, c);
   }
   SeqPart s;
   for (int part = walker;
@@ -136,76 +162,72 @@ __global__ void __launch_bounds__(kThreads) conv_bwd_kernel(ConvBwdArgs a, int b
        part += walkers) {
     if (!mine) continue;
     const int t0 = s.part * kBwdTokens, t1 = min(s.len, t0 + kBwdTokens);
-    const bool first = s.part == 0;
     const int end = min(s.len, t1 + W - 1);  // dp is needed up to there
-    F4 win[W], dp[W];  // dp[W - 1]: the newest
-#pragma unroll
-    for (int j = 1; j < W; ++j) win[j] = input_at<W>(x, a.ldx, state, a.D, s, t0 - W + j, c), dp[j] = zero4();
-    // token t gives dx of t - (W - 1); a first part's first W - 1 are the state's
-    for (int t = t0; t < t1 + W - 1; t += kStep) {
-      F4 in[kStep], g[kStep];
+    const int first = s.part == 0 && d_in ? -(W - 1) : t0;  // the first dx of this part
+    const bf16* fx = x + static_cast<long long>(s.start + t0) * a.ldx + c;
+    const bf16* fg = static_cast<const bf16*>(a.dy) + static_cast<long long>(s.start + t0) * a.lddy + c;
+    bf16* to = static_cast<bf16*>(a.dx) + static_cast<long long>(s.start + t0 - (W - 1)) * a.lddx + c;
+    uint2 nx[kStep], ng[kStep];
+    const auto fetch = [&](int left) {
 #pragma unroll
       for (int q = 0; q < kStep; ++q) {
-        in[q] = g[q] = zero4();
-        if (t + q < end) {
-          in[q] = load4(x + static_cast<long long>(s.start + t + q) * a.ldx + c);
-          g[q] = load4(dy + static_cast<long long>(s.start + t + q) * a.lddy + c);
-        }
+        nx[q] = ng[q] = make_uint2(0, 0);
+        if (q < left) nx[q] = load4(fx + q * a.ldx), ng[q] = load4(fg + q * a.lddy);
       }
+      fx += kStep * a.ldx, fg += kStep * a.lddy;
+    };
+    fetch(end - t0);
+    F4 in[W - 1 + kStep], dp[W - 1 + kStep];  // the newest last
+#pragma unroll
+    for (int j = 0; j + 1 < W; ++j) in[j] = widen(input_at<W>(x, a.ldx, state, a.D, s, t0 - (W - 1) + j, c)), dp[j] = zero4();
+    // token t gives dx of t - (W - 1); a first part's first W - 1 are the state's
+    for (int t = t0; t < t1 + W - 1; t += kStep) {
+#pragma unroll
+      for (int q = 0; q < kStep; ++q) in[W - 1 + q] = widen(nx[q]), dp[W - 1 + q] = widen(ng[q]);  // (zero past the sequence's end)
+      fetch(end - t - kStep);
 #pragma unroll
       for (int q = 0; q < kStep; ++q) {
         const int at = t + q;
-        if (at >= t1 + W - 1) break;
-#pragma unroll
-        for (int j = 0; j + 1 < W; ++j) win[j] = win[j + 1], dp[j] = dp[j + 1];
-        win[W - 1] = in[q];
-        F4 d = g[q];  // (zero past the sequence's end)
+        F4& d = dp[W - 1 + q];
         if (SILU) {
           F4 p = bias;
 #pragma unroll
-          for (int j = 0; j < W; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) p.v[i] = fmaf(tap[j].v[i], win[j].v[i], p.v[i]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float sg = sigmoid(p.v[i]);
-            d.v[i] *= sg * fmaf(p.v[i], 1.0f - sg, 1.0f);
-          }
+          for (int j = 0; j < W; ++j) p = fma4(tap[j], in[q + j], p);
+          const F4 sg = sigmoid4(p);
+          // silu' = sg (1 + p (1 - sg))
+          d = mul4(mul4(d, sg), fma4(p, fma4(sg, splat4(-1.0f), splat4(1.0f)), splat4(1.0f)));
         }
-        if (at >= end) d = zero4();
-        dp[W - 1] = d;
         if (at < t1) {
+          db = add4(db, d);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) db.v[i] += d.v[i];
-#pragma unroll
-          for (int j = 0; j < W; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) dw[j].v[i] = fmaf(d.v[i], win[j].v[i], dw[j].v[i]);
+          for (int j = 0; j < W; ++j) dw[j] = fma4(d, in[q + j], dw[j]);
         }
-        const int to = at - (W - 1);  // dx_to = sum_i w[W-1-i] dp_{to+i}; dp[i] is dp_{to+i}
-        if (to < t0 && !(first && d_in)) continue;
+        const int out = at - (W - 1);  // dx_out = sum_i w[W-1-i] dp_{out+i}; dp[q + i] is dp_{out+i}
+        if (out < first || out >= t1) continue;
         F4 r = zero4();
 #pragma unroll
-        for (int j = 0; j < W; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) r.v[i] = fmaf(tap[W - 1 - j].v[i], dp[j].v[i], r.v[i]);
-        const int late = to - (s.len - (W - 1));  // inputs that are part of the last state
-        if (d_out && late >= 0) {
-          const F4 e = load4(d_out + (static_cast<long long>(s.n) * (W - 1) + late) * a.D + c);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) r.v[i] += e.v[i];
-        }
-        if (to >= 0) store4(dx + static_cast<long long>(s.start + to) * a.lddx + c, r);
-        else store4(d_in + (static_cast<long long>(s.n) * (W - 1) + (W - 1) + to) * a.D + c, r);
+        for (int j = 0; j < W; ++j) r = fma4(tap[W - 1 - j], dp[q + j], r);
+        const int late = out - (s.len - (W - 1));  // inputs that are part of the last state
+        if (d_out && late >= 0) r = add4(r, widen(load4(d_out + (static_cast<long long>(s.n) * (W - 1) + late) * a.D + c)));
+        if (out >= 0) store4(to + q * a.lddx, narrow(r));
+        else store4(d_in + (static_cast<long long>(s.n) * (W - 1) + (W - 1) + out) * a.D + c, narrow(r));
       }
+      to += kStep * a.lddx;
+#pragma unroll
+      for (int j = 0; j + 1 < W; ++j) in[j] = in[kStep + j], dp[j] = dp[kStep + j];
     }
   }
   if (!mine || a.part == nullptr) return;
   float* const out = a.part + static_cast<long long>(walker) * (W + 1) * a.D + c;
+  const auto put = [&](int j, const F4& v) {
+    float4 f;
+    unpack2(v.a, f.x, f.y);
+    unpack2(v.b, f.z, f.w);
+    *reinterpret_cast<float4*>(out + static_cast<long long>(j) * a.D) = f;
+  };
 #pragma unroll
-  for (int j = 0; j < W; ++j)
-    *reinterpret_cast<float4*>(out + static_cast<long long>(j) * a.D) = make_float4(dw[j].v[0], dw[j].v[1], dw[j].v[2], dw[j].v[3]);
-  *reinterpret_cast<float4*>(out + static_cast<long long>(W) * a.D) = make_float4(db.v[0], db.v[1], db.v[2], db.v[3]);
+  for (int j = 0; j < W; ++j) put(j, dw[j]);
+  put(W, db);
 }
 
 // dw [D][W] and db [D] from the parts' [parts][W + 1][D]: eight warps share 32 channels of one row.
@@ -242,27 +264,29 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(ConvStepArgs a, int
   }
   bf16* const y = static_cast<bf16*>(a.y) + b * a.ldy + c;
   if (slot < 0) {
-    store4(y, zero4());
+    store4(y, make_uint2(0, 0));
     return;
   }
   bf16* const state = static_cast<bf16*>(a.state) + static_cast<long long>(slot) * (W - 1) * a.D + c;
-  F4 in[W], tap[W];
+  uint2 in[W];
+  float tap[4 * W];
 #pragma unroll
   for (int j = 0; j + 1 < W; ++j) in[j] = load4(state + static_cast<long long>(j) * a.D);
   in[W - 1] = load4(static_cast<const bf16*>(a.x) + b * a.ldx + c);
   load_taps<W>(a.weight, c, tap);
   // Every operation is rounded by itself (no fused products, an exact quotient): the row's scan reads y as rounded to bf16, and a
   // neighbouring bf16 there would be 2^-8 of what it adds to the state. The cache bounds the time all the same.
-  F4 p;
+  float p[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    p.v[i] = __fmul_rn(tap[0].v[i], in[0].v[i]);
+    const auto value = [&](int j) { return i == 0 ? bf16_lo(in[j].x) : i == 1 ? bf16_hi(in[j].x) : i == 2 ? bf16_lo(in[j].y) : bf16_hi(in[j].y); };
+    p[i] = __fmul_rn(tap[i * W], value(0));
 #pragma unroll
-    for (int j = 1; j < W; ++j) p.v[i] = __fadd_rn(p.v[i], __fmul_rn(tap[j].v[i], in[j].v[i]));
-    if (a.bias) p.v[i] = __fadd_rn(__ldg(a.bias + c + i), p.v[i]);
-    if (SILU) p.v[i] = __fmul_rn(p.v[i], __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-p.v[i]))));
+    for (int j = 1; j < W; ++j) p[i] = __fadd_rn(p[i], __fmul_rn(tap[i * W + j], value(j)));
+    if (a.bias) p[i] = __fadd_rn(__ldg(a.bias + c + i), p[i]);
+    if (SILU) p[i] = __fmul_rn(p[i], __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-p[i]))));
   }
-  store4(y, p);
+  store4(y, make_uint2(pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3])));
 #pragma unroll
   for (int j = 0; j + 1 < W; ++j) store4(state + static_cast<long long>(j) * a.D, in[j + 1]);
 }

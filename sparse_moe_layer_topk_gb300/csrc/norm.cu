@@ -9,7 +9,8 @@ int num_sms();
 
 namespace {
 
-constexpr int kVec = 4;  // 16-byte vectors of a row that a thread holds
+constexpr int kVec = 4;     // 16-byte vectors (of bf16) of a row that a thread of the forward holds
+constexpr int kBwdVec = 2;  // and one of the backward, which holds four rows' worth of them and the next ones on their way
 
 // Eight consecutive values as fp32.
 __device__ __forceinline__ void load8(const bf16* p, float (&v)[8]) {
@@ -33,6 +34,34 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
   *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
   *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
 }
+
+// Eight values on their way.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<bf16> {
+  uint4 v;
+  __device__ __forceinline__ void clear() { v = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void load(const bf16* p) { v = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void floats(float (&f)[8]) const {
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[2 * j] = bf16_lo(u[j]), f[2 * j + 1] = bf16_hi(u[j]);
+  }
+};
+template <>
+struct Raw8<float> {
+  float v[8];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+  }
+  __device__ __forceinline__ void load(const float* p) { load8(p, v); }
+  __device__ __forceinline__ void floats(float (&f)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = v[j];
+  }
+};
 
 // Sum (or maximum) over the THREADS threads of a row, the same for all of them. `slot`: THREADS / 32 floats of
 // shared memory that nothing else uses until every thread has passed the next barrier.
@@ -68,12 +97,12 @@ __device__ __forceinline__ void row_sums(float& a, float& b, float (*slot)[THREA
 
 // 1 / sqrt(mean(u^2) + eps) of a row from its squares' sum. Squares past fp32 (values above 1e19 / sqrt(d)) are summed once
 // more, 2^-160 as large; eps is nothing beside them.
-template <int THREADS>
-__device__ __forceinline__ float row_rstd(const float (&u)[kVec][8], float ss, int d, float eps, float* slot) {
+template <int THREADS, int VEC>
+__device__ __forceinline__ float row_rstd(const float (&u)[VEC][8], float ss, int d, float eps, float* slot) {
   if (ss < 3e38f) return rsqrtf(ss / d + eps);
   float s2 = 0.0f;
 #pragma unroll
-  for (int i = 0; i < kVec; ++i)
+  for (int i = 0; i < VEC; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float v = u[i][j] * 0x1p-80f;
@@ -126,7 +155,7 @@ __global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS)
 #pragma unroll
     for (int j = 0; j < 8; ++j) ss = fmaf(u[i][j], u[i][j], ss);
   ss = row_reduce<THREADS, false>(ss, slots[0]);
-  const float scale = row_rstd<THREADS>(u, ss, d, eps, slots[1]);
+  const float scale = row_rstd<THREADS, kVec>(u, ss, d, eps, slots[1]);
   float top = 0.0f;
 #pragma unroll
   for (int i = 0; i < kVec; ++i) {
@@ -180,33 +209,46 @@ __global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS)
                        R* d_residual, float* part) {
   __shared__ float slots[3][2][THREADS / 32];
   constexpr int kRows = THREADS == 32 ? 4 : 1;
+  // (a row ahead where the registers allow it: 64 a thread at 1,024 threads do not)
+  constexpr bool kAhead = THREADS * (sizeof(R) == 4 ? 2 : 1) <= 512;
   const int tid = threadIdx.x % THREADS, vectors = d / 8;
-  const int first = blockIdx.x * kRows + (THREADS == 32 ? threadIdx.x >> 5 : 0);
-  float w[kVec][8], dw[kVec][8];
+  const int first = blockIdx.x * kRows + (THREADS == 32 ? threadIdx.x >> 5 : 0), stride = gridDim.x * kRows;
+  float w[kBwdVec][8], dw[kBwdVec][8];
 #pragma unroll
-  for (int i = 0; i < kVec; ++i) {
+  for (int i = 0; i < kBwdVec; ++i) {
     const int c = tid + i * THREADS;
 #pragma unroll
     for (int j = 0; j < 8; ++j) w[i][j] = dw[i][j] = 0.0f;
     if (c < vectors) load8(weight + 8 * c, w[i]);
   }
-  int turn = 0;
-  for (int t = first; t < T; t += gridDim.x * kRows) {
-    const long long at = static_cast<long long>(t) * d;
-    float u[kVec][8], g[kVec][8];
-    float ss = 0.0f, dot = 0.0f;
+  Raw8<U> nu[kBwdVec];
+  Raw8<bf16> ng[kBwdVec];
+  Raw8<R> ns[kBwdVec];
+  const auto fetch = [&](int t) {
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) {
+    for (int i = 0; i < kBwdVec; ++i) {
       const int c = tid + i * THREADS;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) u[i][j] = g[i][j] = 0.0f;
-      if (c < vectors) {
-        load8(from + t * ldu + 8 * c, u[i]);
-        load8(dy + at + 8 * c, g[i]);
+      nu[i].clear(), ng[i].clear(), ns[i].clear();
+      if (t < T && c < vectors) {
+        nu[i].load(from + t * ldu + 8 * c);
+        ng[i].load(dy + static_cast<long long>(t) * d + 8 * c);
+        if (d_sum != nullptr) ns[i].load(d_sum + static_cast<long long>(t) * d + 8 * c);
       }
     }
+  };
+  if (kAhead) fetch(first);
+  int turn = 0;
+  for (int t = first; t < T; t += stride) {
+    const long long at = static_cast<long long>(t) * d;
+    float u[kBwdVec][8], g[kBwdVec][8];
+    Raw8<R> s[kBwdVec];
+    float ss = 0.0f, dot = 0.0f;
+    if (!kAhead) fetch(t);
 #pragma unroll
-    for (int i = 0; i < kVec; ++i)
+    for (int i = 0; i < kBwdVec; ++i) nu[i].floats(u[i]), ng[i].floats(g[i]), s[i] = ns[i];
+    if (kAhead) fetch(t + stride);
+#pragma unroll
+    for (int i = 0; i < kBwdVec; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         ss = fmaf(u[i][j], u[i][j], ss);
@@ -214,31 +256,27 @@ __global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS)
       }
     row_sums<THREADS>(ss, dot, slots[turn]);  // (two slots in turn: one barrier a row)
     turn ^= 1;
-    const float r = row_rstd<THREADS>(u, ss, d, eps, slots[2][0]);
+    const float r = row_rstd<THREADS, kBwdVec>(u, ss, d, eps, slots[2][0]);
     dot = r * dot / d;  // mean(g n)
     if (!(ss < 3e38f)) {  // (u is too large for the sum above as well)
       dot = 0.0f;
 #pragma unroll
-      for (int i = 0; i < kVec; ++i)
+      for (int i = 0; i < kBwdVec; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j) dot = fmaf(g[i][j] * w[i][j], u[i][j] * r, dot);
       dot = row_reduce<THREADS, false>(dot, slots[2][1]) / d;
     }
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) {
+    for (int i = 0; i < kBwdVec; ++i) {
       const int c = tid + i * THREADS;
       if (c < vectors) {
+        float add[8];
+        s[i].floats(add);  // (zeros without d_sum)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float n = u[i][j] * r;
           dw[i][j] = fmaf(g[i][j], n, dw[i][j]);
-          g[i][j] = r * (g[i][j] * w[i][j] - n * dot);
-        }
-        if (d_sum != nullptr) {
-          float s[8];
-          load8(d_sum + at + 8 * c, s);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) g[i][j] += s[j];
+          g[i][j] = fmaf(r, g[i][j] * w[i][j] - n * dot, add[j]);
         }
         if (dx != nullptr) store8(dx + at + 8 * c, g[i]);
         if (d_residual != nullptr) store8(d_residual + at + 8 * c, g[i]);
@@ -246,15 +284,16 @@ __global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS)
     }
   }
   if (part == nullptr) return;
-  float* const mine = part + static_cast<long long>(blockIdx.x * kRows + (THREADS == 32 ? threadIdx.x >> 5 : 0)) * d;
+  float* const mine = part + static_cast<long long>(first) * d;
 #pragma unroll
-  for (int i = 0; i < kVec; ++i) {
+  for (int i = 0; i < kBwdVec; ++i) {
     const int c = tid + i * THREADS;
     if (c < vectors) store8(mine + 8 * c, dw[i]);
   }
 }
 
 int norm_threads(int d) { return d <= 1024 ? 32 : d <= 4096 ? 128 : d <= 8192 ? 256 : 512; }
+int bwd_threads(int d) { return d <= 512 ? 32 : d <= 2048 ? 128 : d <= 4096 ? 256 : d <= 8192 ? 512 : 1024; }
 
 }  // namespace
 
@@ -287,7 +326,7 @@ cudaError_t launch_column_sums(const char* name, const float* part, int parts, l
 
 // Rows of partial weight gradients that a backward writes.
 int rmsnorm_bwd_parts(int T, int d) {
-  const int th = norm_threads(d), rows = th == 32 ? 4 : 1;
+  const int th = bwd_threads(d), rows = th == 32 ? 4 : 1;
   const int ctas = (T + rows - 1) / rows, most = num_sms() * (th <= 128 ? 4 : th == 256 ? 2 : 1);
   return (ctas < most ? ctas : most) * rows;
 }
@@ -331,8 +370,18 @@ cudaError_t launch_rmsnorm_fwd(const NormArgs& a, cudaStream_t st) {
 cudaError_t launch_rmsnorm_bwd(const NormBwdArgs& a, cudaStream_t st) {
   {
     LaunchTimer lt("rmsnorm_bwd", st);
-    if (a.res_f32) { MOE_NORM_DISPATCH((norm_bwd<TH, float, float>(a, st))) }
-    else { MOE_NORM_DISPATCH((norm_bwd<TH, bf16, bf16>(a, st))) }
+    const auto run = [&](auto threads) {
+      constexpr int TH = decltype(threads)::value;
+      if (a.res_f32) norm_bwd<TH, float, float>(a, st);
+      else norm_bwd<TH, bf16, bf16>(a, st);
+    };
+    switch (bwd_threads(a.d)) {
+      case 32: run(std::integral_constant<int, 32>{}); break;
+      case 128: run(std::integral_constant<int, 128>{}); break;
+      case 256: run(std::integral_constant<int, 256>{}); break;
+      case 512: run(std::integral_constant<int, 512>{}); break;
+      default: run(std::integral_constant<int, 1024>{}); break;
+    }
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !a.dw) return e;
   }

@@ -42,7 +42,6 @@ __device__ __forceinline__ float rcp(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-__device__ __forceinline__ float sigmoid(float x) { return rcp(1.0f + ex2(-x * kLog2e)); }
 
 // 1 / (1 + exp(-x)) of two values.
 __device__ __forceinline__ float2 sigmoid2(float2 x) {
@@ -787,53 +786,75 @@ __global__ void __launch_bounds__(256) scan_bc_sums_kernel(ScanArgs f, const flo
 
 constexpr int kStepWarps = 8;
 
+// One token for each of ROWS rows: a thread has four states of a channel in each, whose loads are under way together, and A, dt_bias and
+// skip once for all of them. The states are read and written once, and HBM bounds it.
+template <int ROWS>
 __global__ void __launch_bounds__(kStepWarps * 32) scan_step_kernel(ScanStepArgs a, int blocks) {
   const int q = threadIdx.x & 3;
-  const int b = blockIdx.x / blocks;
   const Channels ch = block_channels(blockIdx.x % blocks, a.D, a.G, 8 * kStepWarps);
-  const int place_in = static_cast<int>(threadIdx.x >> 2), c = ch.c0 + place_in;
-  int slot = a.state_idx ? __ldg(a.state_idx + b) : b;
-  if (slot >= a.n_slots) {
-    if (threadIdx.x == 0) set_flag(a.err_flag, MOE_FLAG_BAD_INDEX);
-    slot = -1;
-  }
-  const bool in = place_in < ch.have;
-  bf16* const y = static_cast<bf16*>(a.y) + b * a.ldy + c;
-  if (slot < 0) {
-    if (in && q == 0) *y = __float2bfloat16_rn(0.0f);
-    return;
-  }
-  const bool real = in && 4 * q < a.S;
-  float* const place = a.state + (static_cast<long long>(slot) * a.D + c) * a.S + 4 * q;
-  float4 h = make_float4(0, 0, 0, 0), A = h, Bv = h, Cv = h;
-  if (real) {
-    h = *reinterpret_cast<const float4*>(place);
-    A = __ldg(reinterpret_cast<const float4*>(a.A + static_cast<long long>(c) * a.S + 4 * q));
-    const uint2 rb = *reinterpret_cast<const uint2*>(static_cast<const bf16*>(a.B) + b * a.ldb + ch.group * a.S + 4 * q);
-    const uint2 rc = *reinterpret_cast<const uint2*>(static_cast<const bf16*>(a.C) + b * a.ldc + ch.group * a.S + 4 * q);
-    Bv = make_float4(bf16_lo(rb.x), bf16_hi(rb.x), bf16_lo(rb.y), bf16_hi(rb.y));
-    Cv = make_float4(bf16_lo(rc.x), bf16_hi(rc.x), bf16_lo(rc.y), bf16_hi(rc.y));
-  }
-  float u = 0.0f, dt = 0.0f, gate = 1.0f;
-  if (in) {
-    u = __bfloat162float(static_cast<const bf16*>(a.u)[b * a.ldu + c]);
-    dt = __bfloat162float(static_cast<const bf16*>(a.delta)[b * a.ldd + c]) + (a.dt_bias ? __ldg(a.dt_bias + c) : 0.0f);
-    if (a.softplus) dt = softplus(dt);
-    if (a.z) {
-      const float z = __bfloat162float(static_cast<const bf16*>(a.z)[b * a.ldz + c]);
-      gate = z * sigmoid(z);
+  const int place = static_cast<int>(threadIdx.x >> 2), c = ch.c0 + place, b0 = blockIdx.x / blocks * ROWS;
+  const bool in = place < ch.have, real = in && 4 * q < a.S;
+  int slot[ROWS];
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) {
+    slot[r] = -1;
+    if (b0 + r >= a.B_rows) continue;
+    slot[r] = a.state_idx ? __ldg(a.state_idx + b0 + r) : b0 + r;
+    if (slot[r] >= a.n_slots) {
+      if (threadIdx.x == 0) set_flag(a.err_flag, MOE_FLAG_BAD_INDEX);
+      slot[r] = -1;
     }
   }
-  const float k = dt * kLog2e, du = dt * u;
-  h.x = fmaf(ex2(k * A.x), h.x, du * Bv.x);
-  h.y = fmaf(ex2(k * A.y), h.y, du * Bv.y);
-  h.z = fmaf(ex2(k * A.z), h.z, du * Bv.z);
-  h.w = fmaf(ex2(k * A.w), h.w, du * Bv.w);
-  if (real) *reinterpret_cast<float4*>(place) = h;
-  float o = fmaf(Cv.x, h.x, Cv.y * h.y) + fmaf(Cv.z, h.z, Cv.w * h.w);
-  o += __shfl_xor_sync(kAll, o, 1);
-  o += __shfl_xor_sync(kAll, o, 2);
-  if (in && q == 0) *y = __float2bfloat16_rn((o + (a.skip ? __ldg(a.skip + c) * u : 0.0f)) * gate);
+  float4 h[ROWS];
+  uint2 Bv[ROWS], Cv[ROWS];
+  float u[ROWS], dt[ROWS], z[ROWS];
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) {
+    h[r] = make_float4(0, 0, 0, 0);
+    Bv[r] = Cv[r] = make_uint2(0, 0);
+    u[r] = dt[r] = z[r] = 0.0f;
+    if (slot[r] < 0) continue;
+    const long long b = b0 + r;
+    if (real) {
+      h[r] = *reinterpret_cast<const float4*>(a.state + (static_cast<long long>(slot[r]) * a.D + c) * a.S + 4 * q);
+      Bv[r] = *reinterpret_cast<const uint2*>(static_cast<const bf16*>(a.B) + b * a.ldb + ch.group * a.S + 4 * q);
+      Cv[r] = *reinterpret_cast<const uint2*>(static_cast<const bf16*>(a.C) + b * a.ldc + ch.group * a.S + 4 * q);
+    }
+    if (in) {
+      u[r] = __bfloat162float(static_cast<const bf16*>(a.u)[b * a.ldu + c]);
+      dt[r] = __bfloat162float(static_cast<const bf16*>(a.delta)[b * a.ldd + c]);
+      if (a.z) z[r] = __bfloat162float(static_cast<const bf16*>(a.z)[b * a.ldz + c]);
+    }
+  }
+  float4 A = make_float4(0, 0, 0, 0);
+  if (real) A = __ldg(reinterpret_cast<const float4*>(a.A + static_cast<long long>(c) * a.S + 4 * q));
+  const float bias = in && a.dt_bias ? __ldg(a.dt_bias + c) : 0.0f, skip = in && a.skip ? __ldg(a.skip + c) : 0.0f;
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) {
+    if (b0 + r >= a.B_rows) break;
+    bf16* const y = static_cast<bf16*>(a.y) + (b0 + r) * a.ldy + c;
+    if (slot[r] < 0) {
+      if (in && q == 0) *y = __float2bfloat16_rn(0.0f);
+      continue;
+    }
+    float step = dt[r] + bias;
+    if (a.softplus) step = softplus(step);
+    const float k = step * kLog2e, du = step * u[r];
+    h[r].x = fmaf(ex2(k * A.x), h[r].x, du * bf16_lo(Bv[r].x));
+    h[r].y = fmaf(ex2(k * A.y), h[r].y, du * bf16_hi(Bv[r].x));
+    h[r].z = fmaf(ex2(k * A.z), h[r].z, du * bf16_lo(Bv[r].y));
+    h[r].w = fmaf(ex2(k * A.w), h[r].w, du * bf16_hi(Bv[r].y));
+    if (real) *reinterpret_cast<float4*>(a.state + (static_cast<long long>(slot[r]) * a.D + c) * a.S + 4 * q) = h[r];
+    float o = fmaf(bf16_lo(Cv[r].x), h[r].x, bf16_hi(Cv[r].x) * h[r].y) + fmaf(bf16_lo(Cv[r].y), h[r].z, bf16_hi(Cv[r].y) * h[r].w);
+    o += __shfl_xor_sync(kAll, o, 1);
+    o += __shfl_xor_sync(kAll, o, 2);
+    o = fmaf(skip, u[r], o);
+    if (a.z) {
+      const float g = z[r];
+      o *= g * rcp(1.0f + ex2(-g * kLog2e));
+    }
+    if (in && q == 0) *y = __float2bfloat16_rn(o);
+  }
 }
 
 // Channel blocks of `channels` channels.
@@ -964,7 +985,12 @@ cudaError_t launch_scan_bwd(const ScanBwdArgs& a, cudaStream_t st) {
 cudaError_t launch_scan_step(const ScanStepArgs& a, cudaStream_t st) {
   LaunchTimer lt("scan_step", st);
   const int blocks = blocks_of(a.D, a.G, 8 * kStepWarps);
-  scan_step_kernel<<<static_cast<unsigned>(a.B_rows * blocks), kStepWarps * 32, 0, st>>>(a, blocks);
+  // (four rows a CTA where that still fills the GPU's SMs twice)
+  const auto run = [&](auto kernel, int rows) {
+    kernel<<<static_cast<unsigned>((a.B_rows + rows - 1) / rows * blocks), kStepWarps * 32, 0, st>>>(a, blocks);
+  };
+  if (static_cast<long long>(a.B_rows) * blocks >= 8ll * num_sms()) run(scan_step_kernel<4>, 4);
+  else run(scan_step_kernel<1>, 1);
   return cudaGetLastError();
 }
 
