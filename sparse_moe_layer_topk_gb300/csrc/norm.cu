@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS)
 // 32 four warps, each its own rows) walks rows with a stride of the grid and keeps its columns' part of dw in
 // registers; the parts are summed in a fixed order afterwards.
 template <int THREADS, typename U, typename R>
-__global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS)
+__global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS, THREADS <= 128 ? 4 : THREADS <= 512 ? 512 / THREADS : 1)
     rmsnorm_bwd_kernel(const bf16* __restrict__ dy, const U* __restrict__ from, const float* __restrict__ weight,
                        const R* d_sum, int T, int d, long long ldu, float eps, bf16* dx,
                        R* d_residual, float* part) {

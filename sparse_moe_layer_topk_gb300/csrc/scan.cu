@@ -71,7 +71,7 @@ __device__ __forceinline__ float2 softplus2(float2 x) {
   unpack2(fma2(p, e, pack2(fmaxf(x.x, 0.0f), fmaxf(x.y, 0.0f))), r.x, r.y);
   return r;
 }
-__device__ __forceinline__ float softplus(float x) { return softplus2(make_float2(x, x)).x; }
+__device__ __forceinline__ float softplus(float x) { return softplus2(make_float2(x, 0.0f)).x; }
 
 // Shared-memory loads that the compiler may move over stores (it cannot tell that those go to other places, and would
 // otherwise begin no token before the one ahead of it has stored its results). They stay below the `after_sync` that
@@ -786,75 +786,69 @@ __global__ void __launch_bounds__(256) scan_bc_sums_kernel(ScanArgs f, const flo
 
 constexpr int kStepWarps = 8;
 
-// One token for each of ROWS rows: a thread has four states of a channel in each, whose loads are under way together, and A, dt_bias and
-// skip once for all of them. The states are read and written once, and HBM bounds it.
-template <int ROWS>
+// One token for each of four rows: a lane has four states of a channel in each, whose loads are under way together, and reads
+// A once for all of them. Time step, gate and output of a row are the work of one of the four lanes that share a channel.
+// The states are read and written once, and HBM bounds it.
 __global__ void __launch_bounds__(kStepWarps * 32) scan_step_kernel(ScanStepArgs a, int blocks) {
-  const int q = threadIdx.x & 3;
+  constexpr int kRows = 4;
+  const int lane = static_cast<int>(lane_id()), q = lane & 3;
   const Channels ch = block_channels(blockIdx.x % blocks, a.D, a.G, 8 * kStepWarps);
-  const int place = static_cast<int>(threadIdx.x >> 2), c = ch.c0 + place, b0 = blockIdx.x / blocks * ROWS;
+  const int place = static_cast<int>(threadIdx.x >> 2), c = ch.c0 + place, b0 = blockIdx.x / blocks * kRows;
   const bool in = place < ch.have, real = in && 4 * q < a.S;
-  int slot[ROWS];
+  const auto slot_of = [&](int r) {
+    if (b0 + r >= a.B_rows) return -1;
+    const int slot = a.state_idx ? __ldg(a.state_idx + b0 + r) : b0 + r;
+    if (slot < a.n_slots) return slot;
+    if (threadIdx.x == 0) set_flag(a.err_flag, MOE_FLAG_BAD_INDEX);
+    return -1;
+  };
+  float* state[kRows];  // null: an empty row
+  float4 h[kRows];
+  uint2 Bv[kRows], Cv[kRows];
+  bool own = false;  // whether this lane's row, b0 + q, is no empty one
 #pragma unroll
-  for (int r = 0; r < ROWS; ++r) {
-    slot[r] = -1;
-    if (b0 + r >= a.B_rows) continue;
-    slot[r] = a.state_idx ? __ldg(a.state_idx + b0 + r) : b0 + r;
-    if (slot[r] >= a.n_slots) {
-      if (threadIdx.x == 0) set_flag(a.err_flag, MOE_FLAG_BAD_INDEX);
-      slot[r] = -1;
-    }
+  for (int r = 0; r < kRows; ++r) {
+    const int slot = slot_of(r);
+    state[r] = slot >= 0 && real ? a.state + (static_cast<long long>(slot) * a.D + c) * a.S + 4 * q : nullptr;
+    if (r == q) own = slot >= 0;
   }
-  float4 h[ROWS];
-  uint2 Bv[ROWS], Cv[ROWS];
-  float u[ROWS], dt[ROWS], z[ROWS];
 #pragma unroll
-  for (int r = 0; r < ROWS; ++r) {
+  for (int r = 0; r < kRows; ++r) {
     h[r] = make_float4(0, 0, 0, 0);
     Bv[r] = Cv[r] = make_uint2(0, 0);
-    u[r] = dt[r] = z[r] = 0.0f;
-    if (slot[r] < 0) continue;
+    if (!state[r]) continue;
     const long long b = b0 + r;
-    if (real) {
-      h[r] = *reinterpret_cast<const float4*>(a.state + (static_cast<long long>(slot[r]) * a.D + c) * a.S + 4 * q);
-      Bv[r] = *reinterpret_cast<const uint2*>(static_cast<const bf16*>(a.B) + b * a.ldb + ch.group * a.S + 4 * q);
-      Cv[r] = *reinterpret_cast<const uint2*>(static_cast<const bf16*>(a.C) + b * a.ldc + ch.group * a.S + 4 * q);
-    }
-    if (in) {
-      u[r] = __bfloat162float(static_cast<const bf16*>(a.u)[b * a.ldu + c]);
-      dt[r] = __bfloat162float(static_cast<const bf16*>(a.delta)[b * a.ldd + c]);
-      if (a.z) z[r] = __bfloat162float(static_cast<const bf16*>(a.z)[b * a.ldz + c]);
-    }
+    h[r] = *reinterpret_cast<const float4*>(state[r]);
+    Bv[r] = *reinterpret_cast<const uint2*>(static_cast<const bf16*>(a.B) + b * a.ldb + ch.group * a.S + 4 * q);
+    Cv[r] = *reinterpret_cast<const uint2*>(static_cast<const bf16*>(a.C) + b * a.ldc + ch.group * a.S + 4 * q);
+  }
+  const long long row = b0 + q;
+  float u = 0.0f, dt = 0.0f, z = 0.0f;
+  if (own && in) {
+    u = __bfloat162float(static_cast<const bf16*>(a.u)[row * a.ldu + c]);
+    dt = __bfloat162float(static_cast<const bf16*>(a.delta)[row * a.ldd + c]) + (a.dt_bias ? __ldg(a.dt_bias + c) : 0.0f);
+    if (a.z) z = __bfloat162float(static_cast<const bf16*>(a.z)[row * a.ldz + c]);
   }
   float4 A = make_float4(0, 0, 0, 0);
   if (real) A = __ldg(reinterpret_cast<const float4*>(a.A + static_cast<long long>(c) * a.S + 4 * q));
-  const float bias = in && a.dt_bias ? __ldg(a.dt_bias + c) : 0.0f, skip = in && a.skip ? __ldg(a.skip + c) : 0.0f;
+  if (a.softplus) dt = softplus(dt);
+  const float step = dt * kLog2e, du = dt * u;
+  float o[kRows];
 #pragma unroll
-  for (int r = 0; r < ROWS; ++r) {
-    if (b0 + r >= a.B_rows) break;
-    bf16* const y = static_cast<bf16*>(a.y) + (b0 + r) * a.ldy + c;
-    if (slot[r] < 0) {
-      if (in && q == 0) *y = __float2bfloat16_rn(0.0f);
-      continue;
-    }
-    float step = dt[r] + bias;
-    if (a.softplus) step = softplus(step);
-    const float k = step * kLog2e, du = step * u[r];
-    h[r].x = fmaf(ex2(k * A.x), h[r].x, du * bf16_lo(Bv[r].x));
-    h[r].y = fmaf(ex2(k * A.y), h[r].y, du * bf16_hi(Bv[r].x));
-    h[r].z = fmaf(ex2(k * A.z), h[r].z, du * bf16_lo(Bv[r].y));
-    h[r].w = fmaf(ex2(k * A.w), h[r].w, du * bf16_hi(Bv[r].y));
-    if (real) *reinterpret_cast<float4*>(a.state + (static_cast<long long>(slot[r]) * a.D + c) * a.S + 4 * q) = h[r];
-    float o = fmaf(bf16_lo(Cv[r].x), h[r].x, bf16_hi(Cv[r].x) * h[r].y) + fmaf(bf16_lo(Cv[r].y), h[r].z, bf16_hi(Cv[r].y) * h[r].w);
-    o += __shfl_xor_sync(kAll, o, 1);
-    o += __shfl_xor_sync(kAll, o, 2);
-    o = fmaf(skip, u[r], o);
-    if (a.z) {
-      const float g = z[r];
-      o *= g * rcp(1.0f + ex2(-g * kLog2e));
-    }
-    if (in && q == 0) *y = __float2bfloat16_rn(o);
+  for (int r = 0; r < kRows; ++r) {
+    const float k = __shfl_sync(kAll, step, (lane & ~3) | r), d = __shfl_sync(kAll, du, (lane & ~3) | r);
+    h[r].x = fmaf(ex2(k * A.x), h[r].x, d * bf16_lo(Bv[r].x));
+    h[r].y = fmaf(ex2(k * A.y), h[r].y, d * bf16_hi(Bv[r].x));
+    h[r].z = fmaf(ex2(k * A.z), h[r].z, d * bf16_lo(Bv[r].y));
+    h[r].w = fmaf(ex2(k * A.w), h[r].w, d * bf16_hi(Bv[r].y));
+    if (state[r]) *reinterpret_cast<float4*>(state[r]) = h[r];
+    o[r] = fmaf(bf16_lo(Cv[r].x), h[r].x, bf16_hi(Cv[r].x) * h[r].y) + fmaf(bf16_lo(Cv[r].y), h[r].z, bf16_hi(Cv[r].y) * h[r].w);
   }
+  float y = join4(o[0], o[1], o[2], o[3], q);
+  if (!in || row >= a.B_rows) return;
+  if (a.skip) y = fmaf(__ldg(a.skip + c), u, y);
+  if (a.z) y *= z * rcp(1.0f + ex2(-z * kLog2e));
+  static_cast<bf16*>(a.y)[row * a.ldy + c] = __float2bfloat16_rn(own ? y : 0.0f);
 }
 
 // Channel blocks of `channels` channels.
@@ -985,12 +979,7 @@ cudaError_t launch_scan_bwd(const ScanBwdArgs& a, cudaStream_t st) {
 cudaError_t launch_scan_step(const ScanStepArgs& a, cudaStream_t st) {
   LaunchTimer lt("scan_step", st);
   const int blocks = blocks_of(a.D, a.G, 8 * kStepWarps);
-  // (four rows a CTA where that still fills the GPU's SMs twice)
-  const auto run = [&](auto kernel, int rows) {
-    kernel<<<static_cast<unsigned>((a.B_rows + rows - 1) / rows * blocks), kStepWarps * 32, 0, st>>>(a, blocks);
-  };
-  if (static_cast<long long>(a.B_rows) * blocks >= 8ll * num_sms()) run(scan_step_kernel<4>, 4);
-  else run(scan_step_kernel<1>, 1);
+  scan_step_kernel<<<static_cast<unsigned>((static_cast<long long>(a.B_rows) + 3) / 4 * blocks), kStepWarps * 32, 0, st>>>(a, blocks);
   return cudaGetLastError();
 }
 
