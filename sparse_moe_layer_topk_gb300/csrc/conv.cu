@@ -217,6 +217,7 @@ __global__ void __launch_bounds__(kThreads, 4) conv_bwd_kernel(ConvBwdArgs a, in
       for (int j = 0; j + 1 < W; ++j) in[j] = in[kStep + j], dp[j] = dp[kStep + j];
     }
   }
+  allow_next_kernel();
   if (!mine || a.part == nullptr) return;
   float* const out = a.part + static_cast<long long>(walker) * (W + 1) * a.D + c;
   const auto put = [&](int j, const F4& v) {
@@ -230,22 +231,23 @@ __global__ void __launch_bounds__(kThreads, 4) conv_bwd_kernel(ConvBwdArgs a, in
   put(W, db);
 }
 
-// dw [D][W] and db [D] from the parts' [parts][W + 1][D]: eight warps share 32 channels of one row.
-__global__ void __launch_bounds__(256) conv_weight_sums_kernel(const float* __restrict__ part, int parts, int D, int W,
+// dw [D][W] and db [D] from the walkers' [walkers][W + 1][D], in one order: 16 warps share 32 channels of one row.
+__global__ void __launch_bounds__(512) conv_weight_sums_kernel(const float* __restrict__ part, int parts, int D, int W,
                                                                float* __restrict__ dw, float* __restrict__ db) {
-  __shared__ float sums[8][33];
+  __shared__ float sums[16][33];
   const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane, j = blockIdx.y;
+  wait_for_last_kernel();
   float sum = 0.0f;
   if (c < D) {
-#pragma unroll 8
-    for (int p = g; p < parts; p += 8) sum += __ldg(part + (static_cast<long long>(p) * (W + 1) + j) * D + c);
+#pragma unroll 4
+    for (int p = g; p < parts; p += 16) sum += __ldg(part + (static_cast<long long>(p) * (W + 1) + j) * D + c);
   }
   sums[g][lane] = sum;
   __syncthreads();
   if (g != 0 || c >= D) return;
 #pragma unroll
-  for (int i = 1; i < 8; ++i) sum += sums[i][lane];
+  for (int i = 1; i < 16; ++i) sum += sums[i][lane];
   if (j < W) {
     if (dw) dw[static_cast<long long>(c) * W + j] = sum;
   } else if (db) {
@@ -328,8 +330,7 @@ cudaError_t launch_conv_bwd(const ConvBwdArgs& a, float* dw, float* db, cudaStre
     if (e != cudaSuccess || a.part == nullptr) return e;
   }
   LaunchTimer lt("conv_dw", st);
-  conv_weight_sums_kernel<<<dim3((a.D + 31) / 32, a.W + 1), 256, 0, st>>>(a.part, parts, a.D, a.W, dw, db);
-  return cudaGetLastError();
+  return launch_behind(conv_weight_sums_kernel, dim3((a.D + 31) / 32, a.W + 1), 512, 0, st, static_cast<const float*>(a.part), parts, a.D, a.W, dw, db);
 }
 
 cudaError_t launch_conv_step(const ConvStepArgs& a, cudaStream_t st) {

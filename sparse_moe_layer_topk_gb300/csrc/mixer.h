@@ -66,10 +66,6 @@ struct NormBwdArgs {
 int rmsnorm_bwd_parts(int T, int d);
 cudaError_t launch_rmsnorm_bwd(const NormBwdArgs& a, cudaStream_t st);
 
-// out[c] = sum of `parts` rows of `cols` values.
-cudaError_t launch_column_sums(const char* name, const float* part, int parts, long long cols, float* out,
-                               cudaStream_t st);
-
 struct ConvArgs {
   const void* x;
   const float* weight;

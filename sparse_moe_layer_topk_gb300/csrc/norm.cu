@@ -283,6 +283,7 @@ __global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS, THREADS <= 128 
       }
     }
   }
+  allow_next_kernel();
   if (part == nullptr) return;
   float* const mine = part + static_cast<long long>(first) * d;
 #pragma unroll
@@ -297,31 +298,23 @@ int bwd_threads(int d) { return d <= 512 ? 32 : d <= 2048 ? 128 : d <= 4096 ? 25
 
 }  // namespace
 
-// out[c] = sum over `parts` rows of part[.][c], in an order that depends on the sizes alone.
-__global__ void __launch_bounds__(256) column_sums_kernel(const float* __restrict__ part, int parts, long long cols,
-                                                          float* __restrict__ out) {
-  __shared__ float s[8][33];
-  const long long c = static_cast<long long>(blockIdx.x) * 32 + (threadIdx.x & 31);
-  const int g = threadIdx.x >> 5;
+// out[c] = sum over `parts` rows of part[.][c], in an order that depends on the sizes alone: 32 warps share 32 columns' rows.
+__global__ void __launch_bounds__(1024) column_sums_kernel(const float* __restrict__ part, int parts, int cols, float* __restrict__ out) {
+  __shared__ float s[32][33];
+  const int lane = threadIdx.x & 31, g = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+  wait_for_last_kernel();
   float sum = 0.0f;
   if (c < cols) {
 #pragma unroll 8
-    for (int p = g; p < parts; p += 8) sum += __ldg(part + p * cols + c);
+    for (int p = g; p < parts; p += 32) sum += __ldg(part + static_cast<long long>(p) * cols + c);
   }
-  s[g][threadIdx.x & 31] = sum;
+  s[g][lane] = sum;
   __syncthreads();
-  if (g == 0 && c < cols) {
+  sum = s[lane][g];  // (a warp has one column now)
 #pragma unroll
-    for (int i = 1; i < 8; ++i) sum += s[i][threadIdx.x];
-    out[c] = sum;
-  }
-}
-
-cudaError_t launch_column_sums(const char* name, const float* part, int parts, long long cols, float* out,
-                               cudaStream_t st) {
-  LaunchTimer lt(name, st);
-  column_sums_kernel<<<static_cast<unsigned>((cols + 31) / 32), 256, 0, st>>>(part, parts, cols, out);
-  return cudaGetLastError();
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+  const int mine = blockIdx.x * 32 + g;
+  if (lane == 0 && mine < cols) out[mine] = sum;
 }
 
 // Rows of partial weight gradients that a backward writes.
@@ -385,7 +378,8 @@ cudaError_t launch_rmsnorm_bwd(const NormBwdArgs& a, cudaStream_t st) {
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !a.dw) return e;
   }
-  return launch_column_sums("rmsnorm_dw", a.part, rmsnorm_bwd_parts(a.T, a.d), a.d, a.dw, st);
+  LaunchTimer lt("rmsnorm_dw", st);
+  return launch_behind(column_sums_kernel, dim3((a.d + 31) / 32), 1024, 0, st, static_cast<const float*>(a.part), rmsnorm_bwd_parts(a.T, a.d), a.d, a.dw);
 }
 
 }  // namespace moe

@@ -8,8 +8,11 @@
 // in a lane's fp32 registers, so that a B and a C from shared memory serve both. (One channel a lane: shared memory bounds it. Four:
 // too few warps to hide the arithmetic's latency.) A CTA takes 32 tokens of its channels at a time: whole rows of 128 or 256 bytes
 // arrive by asynchronous copies a tile ahead (a warp fetching its own 16 channels touches four times the cache lines, which cost as
-// much time as the recurrence); (dt, dt u) of two neighbouring channels a thread go to shared memory; then each warp walks
-// the tokens with its 16 channels' states; then skip, gate and store, two neighbouring channels a thread again.
+// much time as the recurrence); (dt, dt u) of four neighbouring channels a thread go to shared memory; then each warp walks
+// the tokens with its 16 channels' states; then skip, gate and store, four neighbouring channels a thread again.
+#include <algorithm>
+#include <cmath>
+
 #include "common.cuh"
 #include "mixer.h"
 #include "scan.h"
@@ -44,21 +47,22 @@ __device__ __forceinline__ float rcp(float x) {
 }
 
 // 1 / (1 + exp(-x)) of two values.
-__device__ __forceinline__ float2 sigmoid2(float2 x) {
+__device__ __forceinline__ f32x2 sigmoid2(f32x2 x) {
   float a, b;
-  unpack2(mul2(pack2(x.x, x.y), pack2(-kLog2e, -kLog2e)), a, b);
+  unpack2(mul2(x, pack2(-kLog2e, -kLog2e)), a, b);
   unpack2(add2(pack2(ex2(a), ex2(b)), pack2(1.0f, 1.0f)), a, b);
-  return make_float2(rcp(a), rcp(b));
+  return pack2(rcp(a), rcp(b));
 }
 
 // max(x, 0) + log(1 + e), e = exp(-|x|), of two values. The exponent's product is taken in two terms (it would lose |x| 2^-24
 // of e), and log(1 + e) / e is a polynomial of degree 9, fitted on [0, 1] with equal relative errors (5e-9; 1.5e-7 with its
 // roundings), so that small results keep their relative precision: dt multiplies all that reaches a state.
-__device__ __forceinline__ float2 softplus2(float2 x) {
-  const f32x2 n = pack2(fabsf(x.x), fabsf(x.y)), l2e = pack2(-kLog2e, -kLog2e);
+__device__ __forceinline__ f32x2 softplus2(f32x2 x) {
+  float a, b;
+  unpack2(x, a, b);
+  const f32x2 n = pack2(fabsf(a), fabsf(b)), above = pack2(fmaxf(a, 0.0f), fmaxf(b, 0.0f)), l2e = pack2(-kLog2e, -kLog2e);
   const f32x2 m = mul2(n, l2e);
   const f32x2 lost = fma2(n, pack2(kLog2e, kLog2e), m);
-  float a, b;
   unpack2(m, a, b);
   f32x2 e = pack2(ex2(a), ex2(b));
   e = fma2(mul2(e, pack2(-kLn2, -kLn2)), lost, e);
@@ -67,11 +71,13 @@ __device__ __forceinline__ float2 softplus2(float2 x) {
   f32x2 p = pack2(-0.003243980696424842f, -0.003243980696424842f);
 #pragma unroll
   for (int i = 0; i < 9; ++i) p = fma2(p, e, pack2(c[i], c[i]));
-  float2 r;
-  unpack2(fma2(p, e, pack2(fmaxf(x.x, 0.0f), fmaxf(x.y, 0.0f))), r.x, r.y);
-  return r;
+  return fma2(p, e, above);
 }
-__device__ __forceinline__ float softplus(float x) { return softplus2(make_float2(x, 0.0f)).x; }
+__device__ __forceinline__ float softplus(float x) {
+  float a, b;
+  unpack2(softplus2(pack2(x, 0.0f)), a, b);
+  return a;
+}
 
 // Shared-memory loads that the compiler may move over stores (it cannot tell that those go to other places, and would
 // otherwise begin no token before the one ahead of it has stored its results). They stay below the `after_sync` that
@@ -180,13 +186,42 @@ struct BcStream {
   __device__ __forceinline__ void move(int tiles) { at += mine ? tiles * kTile * ld : 0; }
 };
 
-// Two neighbouring channels (bf16).
-__device__ __forceinline__ float2 pair_at(const bf16* p) {
-  const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
-  return make_float2(bf16_lo(w), bf16_hi(w));
+// Four neighbouring channels.
+struct Quad {
+  f32x2 a, b;
+};
+__device__ __forceinline__ Quad quad(float x, float y, float z, float w) { return Quad{pack2(x, y), pack2(z, w)}; }
+__device__ __forceinline__ Quad quad(float4 v) { return quad(v.x, v.y, v.z, v.w); }
+__device__ __forceinline__ Quad zero_quad() { return quad(0.0f, 0.0f, 0.0f, 0.0f); }
+__device__ __forceinline__ float4 floats(const Quad& v) {
+  float4 f;
+  unpack2(v.a, f.x, f.y);
+  unpack2(v.b, f.z, f.w);
+  return f;
 }
-__device__ __forceinline__ float2 vector_at(const float* p, int c, bool real) {  // of two channels of a weight
-  return p && real ? make_float2(__ldg(p + c), __ldg(p + c + 1)) : make_float2(0.0f, 0.0f);
+__device__ __forceinline__ Quad quad_at(const bf16* p) {
+  const uint2 w = *reinterpret_cast<const uint2*>(p);
+  return quad(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
+}
+__device__ __forceinline__ Quad quad_at(const float* p) { return quad(*reinterpret_cast<const float4*>(p)); }
+__device__ __forceinline__ Quad weights_at(const float* p, int c, bool real) {  // of four channels
+  return p && real ? quad(__ldg(p + c), __ldg(p + c + 1), __ldg(p + c + 2), __ldg(p + c + 3)) : zero_quad();
+}
+__device__ __forceinline__ void put_quad(bf16* p, const Quad& v) { *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(v.a), pack_bf16(v.b)); }
+__device__ __forceinline__ Quad add(const Quad& x, const Quad& y) { return Quad{add2(x.a, y.a), add2(x.b, y.b)}; }
+__device__ __forceinline__ Quad mul(const Quad& x, const Quad& y) { return Quad{mul2(x.a, y.a), mul2(x.b, y.b)}; }
+__device__ __forceinline__ Quad fma(const Quad& x, const Quad& y, const Quad& z) { return Quad{fma2(x.a, y.a, z.a), fma2(x.b, y.b, z.b)}; }
+__device__ __forceinline__ Quad sigmoid(const Quad& x) { return Quad{sigmoid2(x.a), sigmoid2(x.b)}; }
+__device__ __forceinline__ Quad softplus(const Quad& x) { return Quad{softplus2(x.a), softplus2(x.b)}; }
+// (x, y) of four channels, one channel's pair behind the other.
+__device__ __forceinline__ void put_pairs(float* p, const Quad& x, const Quad& y) {
+  const float4 u = floats(x), v = floats(y);
+  *reinterpret_cast<float4*>(p) = make_float4(u.x, v.x, u.y, v.y);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(u.z, v.z, u.w, v.w);
+}
+__device__ __forceinline__ void get_pairs(const float* p, Quad& x, Quad& y) {
+  const float4 u = *reinterpret_cast<const float4*>(p), v = *reinterpret_cast<const float4*>(p + 4);
+  x = quad(u.x, u.z, v.x, v.z), y = quad(u.y, u.w, v.y, v.w);
 }
 
 struct State4 {
@@ -231,7 +266,7 @@ __device__ __forceinline__ long long tile_base(const SeqPart& s) { return static
 
 constexpr int kFwdRow = kCh * kFwdWarps;      // channels of a CTA
 constexpr int kFwdTile = kTile * kFwdRow;     // values of a tile
-constexpr int kFwdPairs = kFwdRow / 2;        // a thread's place where it takes two neighbouring channels of every fourth token
+constexpr int kFwdQuads = kFwdRow / 4;        // a thread's place where it takes four neighbouring channels of every eighth token
 // Shared memory: two stages of u, delta and z; the pairs; two stages of B and C.
 constexpr int kFwdSmem = (2 * 3 * kFwdTile / 2 + 2 * kFwdTile + 2 * 2 * kTile * kBRow) * 4;
 
@@ -251,6 +286,8 @@ __global__ void __launch_bounds__(kFwdWarps * 32, 4) scan_fwd_kernel(ScanArgs a,
   float* const s_dt = pool + 2 * 3 * kFwdTile / 2;  // [token][channel] (dt, dt u); then y in the first half of a warp's part
   float* const s_bc = s_dt + 2 * kFwdTile;          // [stage][B, C]
 
+  if (SUMS) allow_next_kernel();
+  else wait_for_last_kernel();  // (behind the join where the sequences are cut)
   const int q = lane & 3, first = warp * kCh + (lane >> 2) * kC;  // four states of two channels
   const long long all = static_cast<long long>(a.D) * a.S;
   const long long state_at = (static_cast<long long>(ch.c0) + first) * a.S + 4 * q;
@@ -282,13 +319,12 @@ __global__ void __launch_bounds__(kFwdWarps * 32, 4) scan_fwd_kernel(ScanArgs a,
     }
     copies_commit();
   };
-  const int pair = threadIdx.x % kFwdPairs, pair_token = threadIdx.x / kFwdPairs;
-  const bool pair_real = 2 * pair < ch.have;
-  const float2 bias = vector_at(a.dt_bias, ch.c0 + 2 * pair, pair_real);
-  const float2 skip = vector_at(a.skip, ch.c0 + 2 * pair, pair_real);
+  const int four = 4 * (threadIdx.x % kFwdQuads), token = threadIdx.x / kFwdQuads;
+  const bool four_real = four < ch.have;
+  const Quad bias = weights_at(a.dt_bias, ch.c0 + four, four_real), skip = weights_at(a.skip, ch.c0 + four, four_real);
   float dt_sum[kC] = {0.0f, 0.0f};
   float* tiles = !SUMS && a.tile_states ? a.tile_states + (tile_base(s) + t0 / kTile) * all + state_at : nullptr;
-  bf16* out = SUMS ? nullptr : static_cast<bf16*>(a.y) + (row0 + pair_token) * a.ldy + ch.c0 + 2 * pair;
+  bf16* out = SUMS ? nullptr : static_cast<bf16*>(a.y) + (row0 + token) * a.ldy + ch.c0 + four;
   fetch(count, 0);
   int stage = 0;
   for (int tile = 0; tile < count; tile += kTile, stage ^= 1) {
@@ -298,14 +334,15 @@ __global__ void __launch_bounds__(kFwdWarps * 32, 4) scan_fwd_kernel(ScanArgs a,
     copies_done();
     __syncthreads();  // the tile is here, and nothing reads the one before it any more
     fetch(count - tile - kTile, stage ^ 1);
-    const bf16* const now = raw + stage * 3 * kFwdTile + pair_token * kFwdRow + 2 * pair;
+    const bf16* const now = raw + stage * 3 * kFwdTile + token * kFwdRow + four;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float2 d = pair_at(now + kFwdTile + 4 * k * kFwdRow), v = pair_at(now + 4 * k * kFwdRow);
-      float2 x = make_float2(d.x + bias.x, d.y + bias.y);
-      if (a.softplus) x = softplus2(x);
-      if (pair_token + 4 * k >= n) x = make_float2(0.0f, 0.0f);  // (a token that is none keeps the state)
-      *reinterpret_cast<float4*>(s_dt + 2 * ((pair_token + 4 * k) * kFwdRow + 2 * pair)) = make_float4(x.x, x.x * v.x, x.y, x.y * v.y);
+    for (int k = 0; k < 4; ++k) {
+      const int at = 8 * k * kFwdRow;
+      const Quad v = quad_at(now + at);
+      Quad x = add(quad_at(now + kFwdTile + at), bias);
+      if (a.softplus) x = softplus(x);
+      if (token + 8 * k >= n) x = zero_quad();  // (a token that is none keeps the state)
+      put_pairs(s_dt + 2 * (at + token * kFwdRow + four), x, mul(x, v));
     }
     if (tiles) {
 #pragma unroll
@@ -315,38 +352,78 @@ __global__ void __launch_bounds__(kFwdWarps * 32, 4) scan_fwd_kernel(ScanArgs a,
     }
     __syncthreads();
     const uint32_t at_dt = after_sync(s_dt + 2 * first), at_b = after_sync(s_b + 4 * q), at_c = at_b + 4 * kTile * kBRow;
-#pragma unroll 4
-    for (int t2 = 0; t2 < kTile; t2 += 2) {
-      float y[2][kC];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float4 d = lds4(at_dt + (t2 + i) * 8 * kFwdRow);
-        const State4 b = pack4(lds4(at_b + (t2 + i) * 4 * kBRow));
+    if constexpr (SUMS) {
+#pragma unroll 8
+      for (int t = 0; t < kTile; ++t) {
+        const float4 d = lds4(at_dt + t * 8 * kFwdRow);
+        const State4 b = pack4(lds4(at_b + t * 4 * kBRow));
         h[0] = fma4(ex2(mul4(pack2(d.x, d.x), decay[0])), h[0], mul4(pack2(d.y, d.y), b));
         h[1] = fma4(ex2(mul4(pack2(d.z, d.z), decay[1])), h[1], mul4(pack2(d.w, d.w), b));
-        if (SUMS) {
-          dt_sum[0] += d.x, dt_sum[1] += d.z;
-        } else {
-          const State4 c = pack4(lds4(at_c + (t2 + i) * 4 * kBRow));
-          y[i][0] = sum4(c, h[0]), y[i][1] = sum4(c, h[1]);
-        }
+        dt_sum[0] += d.x, dt_sum[1] += d.z;
       }
+    } else {
+      // Two tokens at a time, in three stages one pair apart, so that a warp's own latencies overlap: shared memory to registers;
+      // decays and inputs; the recurrence and y.
+      float4 d[2];
+      State4 b[2], c[2], e[2][kC], in[2][kC], cc[2];
+      float y[2][kC];
+      const auto load = [&](int t) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          d[i] = lds4(at_dt + (t + i) * 8 * kFwdRow);
+          b[i] = pack4(lds4(at_b + (t + i) * 4 * kBRow));
+          c[i] = pack4(lds4(at_c + (t + i) * 4 * kBRow));
+        }
+      };
+      const auto prepare = [&]() {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          e[i][0] = ex2(mul4(pack2(d[i].x, d[i].x), decay[0])), in[i][0] = mul4(pack2(d[i].y, d[i].y), b[i]);
+          e[i][1] = ex2(mul4(pack2(d[i].z, d[i].z), decay[1])), in[i][1] = mul4(pack2(d[i].w, d[i].w), b[i]);
+          cc[i] = c[i];
+        }
+      };
       // (over the pairs, of tokens that every lane of the warp has read by now)
-      if (!SUMS) s_dt[(t2 + (q >> 1)) * 2 * kFwdRow + warp * kCh + first + (q & 1)] = join4(y[0][0], y[0][1], y[1][0], y[1][1], q);
+      const auto join = [&](int t) {
+        s_dt[(t + (q >> 1)) * 2 * kFwdRow + warp * kCh + first + (q & 1)] = join4(y[0][0], y[0][1], y[1][0], y[1][1], q);
+      };
+      load(0);
+      prepare();
+      load(2);
+#pragma unroll
+      for (int t = 0; t < kTile; t += 2) {
+        State4 e0[2][kC], in0[2][kC], c0[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          c0[i] = cc[i];
+#pragma unroll
+          for (int j = 0; j < kC; ++j) e0[i][j] = e[i][j], in0[i][j] = in[i][j];
+        }
+        if (t + 2 < kTile) prepare();
+        if (t + 4 < kTile) load(t + 4);
+        if (t > 0) join(t - 2);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < kC; ++j) {
+            h[j] = fma4(e0[i][j], h[j], in0[i][j]);
+            y[i][j] = sum4(c0[i], h[j]);
+          }
+      }
+      join(kTile - 2);
     }
     if (!SUMS) {
       __syncthreads();
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        if (pair_token + 4 * k < n && pair_real) {
-          const float2 v = pair_at(now + 4 * k * kFwdRow);
-          float2 y = *reinterpret_cast<const float2*>(s_dt + (pair_token + 4 * k) * 2 * kFwdRow + (pair / 8) * kCh + 2 * pair);
-          y.x = fmaf(skip.x, v.x, y.x), y.y = fmaf(skip.y, v.y, y.y);
+      for (int k = 0; k < 4; ++k) {
+        if (token + 8 * k < n && four_real) {
+          const int at = 8 * k * kFwdRow;
+          Quad y = fma(skip, quad_at(now + at), quad_at(s_dt + 2 * (at + token * kFwdRow) + four / kCh * kCh + four));
           if (gated) {
-            const float2 g = pair_at(now + 2 * kFwdTile + 4 * k * kFwdRow), sg = sigmoid2(g);
-            y.x *= g.x * sg.x, y.y *= g.y * sg.y;
+            const Quad g = quad_at(now + 2 * kFwdTile + at);
+            y = mul(y, mul(g, sigmoid(g)));
           }
-          *reinterpret_cast<uint32_t*>(out + 4 * k * a.ldy) = pack_bf16(y.x, y.y);
+          put_quad(out + 8 * k * a.ldy, y);
         }
       }
       out += kTile * a.ldy;
@@ -373,25 +450,35 @@ __global__ void __launch_bounds__(128) scan_join_kernel(ScanArgs a, int length, 
   SeqPart s;
   if (!find_part(a.cu, a.N, a.T, a.max_seqlen, length, part, s, nullptr) || s.part != 0) return;
   if (i >= a.D * (a.S / 4)) return;
+  allow_next_kernel();
+  wait_for_last_kernel();
   const int c = i / (a.S / 4);
   const long long at = 4ll * i, all = static_cast<long long>(a.D) * a.S;
   const int parts = parts_of(s.len, length);
   const float4 A = __ldg(reinterpret_cast<const float4*>(a.A + at));
   float4 h = make_float4(0, 0, 0, 0);
   if (first) h = *reinterpret_cast<const float4*>(first + s.n * all + at);
-  for (int k = 0; k < parts; ++k) {
-    const long long p = part + (REVERSE ? parts - 1 - k : k);
-    float4* const place = reinterpret_cast<float4*>(sums + p * all + at);
-    // (the last part in the walk's direction has no sums: nothing follows it)
-    const bool more = k + 1 < parts;
-    float4 e = make_float4(0, 0, 0, 0);
-    float d = 0.0f;
-    if (more) e = *place, d = __ldg(dt_sums + p * a.D + c);
-    *place = h;
-    h.x = fmaf(ex2(A.x * d * kLog2e), h.x, e.x);
-    h.y = fmaf(ex2(A.y * d * kLog2e), h.y, e.y);
-    h.z = fmaf(ex2(A.z * d * kLog2e), h.z, e.z);
-    h.w = fmaf(ex2(A.w * d * kLog2e), h.w, e.w);
+  constexpr int kBatch = 4;  // parts whose sums are on their way together
+  for (int k0 = 0; k0 < parts; k0 += kBatch) {
+    float4 e[kBatch];
+    float d[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const long long p = part + (REVERSE ? parts - 1 - (k0 + i) : k0 + i);
+      e[i] = make_float4(0, 0, 0, 0), d[i] = 0.0f;
+      // (the last part in the walk's direction has no sums: nothing follows it)
+      if (k0 + i + 1 < parts) e[i] = *reinterpret_cast<const float4*>(sums + p * all + at), d[i] = __ldg(dt_sums + p * a.D + c);
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (k0 + i >= parts) break;
+      const long long p = part + (REVERSE ? parts - 1 - (k0 + i) : k0 + i);
+      *reinterpret_cast<float4*>(sums + p * all + at) = h;
+      h.x = fmaf(ex2(A.x * d[i] * kLog2e), h.x, e[i].x);
+      h.y = fmaf(ex2(A.y * d[i] * kLog2e), h.y, e[i].y);
+      h.z = fmaf(ex2(A.z * d[i] * kLog2e), h.z, e[i].z);
+      h.w = fmaf(ex2(A.w * d[i] * kLog2e), h.w, e[i].w);
+    }
   }
 }
 
@@ -407,10 +494,10 @@ __global__ void __launch_bounds__(128) scan_join_kernel(ScanArgs a, int length, 
 // halves between lanes, over a CTA's warps in shared memory, and over the CTAs by a second kernel, always in one order.
 constexpr int kBwdRow = kCh * kBwdWarps;      // channels of a CTA
 constexpr int kBwdTile = kTile * kBwdRow;
-constexpr int kBwdPairs = kBwdRow / 2;
-// Shared memory: two stages of u, delta, dy and z; the pairs; y, then g; the warps' noted states; their dB and dC; two stages of B and C.
+constexpr int kBwdQuads = kBwdRow / 4;
+// Shared memory: two stages of u, delta, dy and z; the pairs; y, then g; the warps' noted states; their dB and dC; B and C.
 constexpr int kNotes = (kTile / 4) * kC * 128;
-constexpr int kBwdSmem = (2 * 4 * kBwdTile / 2 + 2 * kBwdTile + kBwdTile + kBwdWarps * (kNotes + kTile * 32) + 2 * 2 * kTile * kBRow) * 4;
+constexpr int kBwdSmem = (2 * 4 * kBwdTile / 2 + 2 * kBwdTile + kBwdTile + kBwdWarps * (kNotes + kTile * 32) + 2 * kTile * kBRow) * 4;
 
 struct BwdWs {
   float* tails;     // [parts][D][S] gradients at the parts' ends, where sequences are cut
@@ -440,10 +527,11 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 1) scan_bwd_kernel(ScanBwdArgs
   float* const s_g = s_dt + 2 * kBwdTile;           // [token][channel] y, then g
   float* const s_notes = s_g + kBwdTile;            // [warp][token / 4][channel of a lane][lane] states; then (to_b, r)
   float* const s_sums = s_notes + kBwdWarps * kNotes;  // [warp][token][dB, dC]
-  float* const s_bc = s_sums + kBwdWarps * kTile * 32;  // [stage][B, C]
+  float* const s_b = s_sums + kBwdWarps * kTile * 32;  // B, then C
   float* const s_note = s_notes + warp * kNotes;
   float* const s_sum = s_sums + warp * kTile * 32;
 
+  wait_for_last_kernel();  // (behind the join where the sequences are cut)
   const int q = lane & 3, mine = lane >> 2, first = warp * kCh + mine * kC;
   const long long state_at = (static_cast<long long>(ch.c0) + first) * f.S + 4 * q;
   State4 decay[kC], X[kC], dA[kC], dA_rest[kC];
@@ -485,36 +573,33 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 1) scan_bwd_kernel(ScanBwdArgs
     }
     copies_commit();
   };
-  const int pair = threadIdx.x % kBwdPairs, pair_token = threadIdx.x / kBwdPairs;
-  const bool pair_real = 2 * pair < ch.have;
-  const float2 bias = vector_at(f.dt_bias, ch.c0 + 2 * pair, pair_real);
-  const float2 skip = vector_at(f.skip, ch.c0 + 2 * pair, pair_real);
-  float2 d_skip = make_float2(0.0f, 0.0f), d_bias = d_skip;
-  const long long pair_row = row0 + pair_token;
-  const int pair_at0 = pair_token * kBwdRow + 2 * pair;  // this thread's place in a tile
-  bf16* dz = a.dz ? static_cast<bf16*>(a.dz) + pair_row * a.lddz + ch.c0 + 2 * pair : nullptr;
-  bf16* du = static_cast<bf16*>(a.du) + pair_row * a.lddu + ch.c0 + 2 * pair;
-  bf16* dd = static_cast<bf16*>(a.dd) + pair_row * a.lddd + ch.c0 + 2 * pair;
-
+  const int four = 4 * (threadIdx.x % kBwdQuads), token = threadIdx.x / kBwdQuads;
+  const bool four_real = four < ch.have;
+  const Quad bias = weights_at(f.dt_bias, ch.c0 + four, four_real), skip = weights_at(f.skip, ch.c0 + four, four_real);
+  Quad d_skip = zero_quad(), d_bias = zero_quad();
+  const int four_at = token * kBwdRow + four;  // this thread's place in a tile
+  bf16* dz = a.dz ? static_cast<bf16*>(a.dz) + (row0 + token) * a.lddz + ch.c0 + four : nullptr;
+  bf16* du = static_cast<bf16*>(a.du) + (row0 + token) * a.lddu + ch.c0 + four;
+  bf16* dd = static_cast<bf16*>(a.dd) + (row0 + token) * a.lddd + ch.c0 + four;
   fetch(last, 0);
   float* bc_sum = ws.bc_part + (static_cast<long long>(block) * f.T + row0) * 32;
   int stage = 0;
   for (int tile = last; tile >= 0; tile -= kTile, stage ^= 1) {
     const int n = min(kTile, count - tile);
     State4 h[kC] = {next[0], next[1]};
-    float* const s_b = s_bc + stage * 2 * kTile * kBRow;
     bc.put(s_b);
     copies_done();
     __syncthreads();  // the tile is here, and nothing reads the one before it any more
     fetch(tile - kTile, stage ^ 1);
-    const bf16* const now = raw + stage * 4 * kBwdTile + pair_at0;
+    const bf16* const now = raw + stage * 4 * kBwdTile + four_at;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float2 d = pair_at(now + kBwdTile + 4 * k * kBwdRow), v = pair_at(now + 4 * k * kBwdRow);
-      float2 x = make_float2(d.x + bias.x, d.y + bias.y);
-      if (f.softplus) x = softplus2(x);
-      if (pair_token + 4 * k >= n) x = make_float2(0.0f, 0.0f);
-      *reinterpret_cast<float4*>(s_dt + 2 * (pair_at0 + 4 * k * kBwdRow)) = make_float4(x.x, x.x * v.x, x.y, x.y * v.y);
+    for (int k = 0; k < 4; ++k) {
+      const int at = 8 * k * kBwdRow;
+      const Quad v = quad_at(now + at);
+      Quad x = add(quad_at(now + kBwdTile + at), bias);
+      if (f.softplus) x = softplus(x);
+      if (token + 8 * k >= n) x = zero_quad();
+      put_pairs(s_dt + 2 * (four_at + at), x, mul(x, v));
     }
     __syncthreads();
     const uint32_t at_dt = after_sync(s_dt + 2 * first), at_b = after_sync(s_b + 4 * q), at_c = at_b + 4 * kTile * kBRow;
@@ -544,21 +629,20 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 1) scan_bwd_kernel(ScanBwdArgs
     if (gated) __syncthreads();
     // the gate's gradient; g
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int at = 4 * k * kBwdRow;
-      const float2 v = pair_at(now + at);
-      float2 g = pair_at(now + 2 * kBwdTile + at);
+    for (int k = 0; k < 4; ++k) {
+      const int at = 8 * k * kBwdRow;
+      const Quad v = quad_at(now + at);
+      Quad g = quad_at(now + 2 * kBwdTile + at);
       if (gated) {
-        const float2 zz = pair_at(now + 3 * kBwdTile + at), y = *reinterpret_cast<const float2*>(s_g + pair_at0 + at);
-        const float2 sg = sigmoid2(zz), silu = make_float2(zz.x * sg.x, zz.y * sg.y);
-        if (dz && pair_token + 4 * k < n && pair_real)  // silu' = sg + silu (1 - sg)
-          *reinterpret_cast<uint32_t*>(dz + 4 * k * a.lddz) =
-              pack_bf16(g.x * fmaf(skip.x, v.x, y.x) * fmaf(silu.x, 1.0f - sg.x, sg.x),
-                        g.y * fmaf(skip.y, v.y, y.y) * fmaf(silu.y, 1.0f - sg.y, sg.y));
-        g.x *= silu.x, g.y *= silu.y;
+        const Quad zz = quad_at(now + 3 * kBwdTile + at), sg = sigmoid(zz), silu = mul(zz, sg);
+        if (dz && token + 8 * k < n && four_real) {  // silu' = sg + silu (1 - sg)
+          const Quad y = fma(skip, v, quad_at(s_g + four_at + at)), rest = fma(sg, quad(-1.0f, -1.0f, -1.0f, -1.0f), quad(1.0f, 1.0f, 1.0f, 1.0f));
+          put_quad(dz + 8 * k * a.lddz, mul(mul(g, y), fma(silu, rest, sg)));
+        }
+        g = mul(g, silu);
       }
-      *reinterpret_cast<float2*>(s_g + pair_at0 + at) = g;
-      d_skip.x = fmaf(g.x, v.x, d_skip.x), d_skip.y = fmaf(g.y, v.y, d_skip.y);
+      *reinterpret_cast<float4*>(s_g + four_at + at) = floats(g);
+      d_skip = fma(g, v, d_skip);
     }
     if (dz) dz -= kTile * a.lddz;
     __syncthreads();
@@ -566,25 +650,24 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 1) scan_bwd_kernel(ScanBwdArgs
     State4 dA_tile[kC] = {zero4(), zero4()};
 #pragma unroll 1
     for (int t4 = kTile - 4; t4 >= 0; t4 -= 4) {
-      State4 hs[5][kC], es[4][kC];
+      State4 hs[5][kC], es[4][kC], b[4];
       float4 d[4];
 #pragma unroll
       for (int j = 0; j < kC; ++j) hs[0][j] = pack4(lds4(at_note + (t4 / 4 * kC + j) * 512));
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         d[i] = lds4(at_dt + (t4 + i) * 8 * kBwdRow);
-        const State4 b = pack4(lds4(at_b + (t4 + i) * 4 * kBRow));
+        b[i] = pack4(lds4(at_b + (t4 + i) * 4 * kBRow));
         es[i][0] = ex2(mul4(pack2(d[i].x, d[i].x), decay[0]));
         es[i][1] = ex2(mul4(pack2(d[i].z, d[i].z), decay[1]));
-        hs[i + 1][0] = fma4(es[i][0], hs[i][0], mul4(pack2(d[i].y, d[i].y), b));
-        hs[i + 1][1] = fma4(es[i][1], hs[i][1], mul4(pack2(d[i].w, d[i].w), b));
+        hs[i + 1][0] = fma4(es[i][0], hs[i][0], mul4(pack2(d[i].y, d[i].y), b[i]));
+        hs[i + 1][1] = fma4(es[i][1], hs[i][1], mul4(pack2(d[i].w, d[i].w), b[i]));
       }
       float to_b[4][kC], r[4][kC];
 #pragma unroll
       for (int i = 3; i >= 0; --i) {
         const float2 g = lds2(at_g + (t4 + i) * 4 * kBwdRow);
         const State4 c = pack4(lds4(at_c + (t4 + i) * 4 * kBRow));
-        const State4 b = pack4(lds4(at_b + (t4 + i) * 4 * kBRow));
         State4 sum_b = zero4(), sum_c = zero4();
 #pragma unroll
         for (int j = 0; j < kC; ++j) {
@@ -593,7 +676,7 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 1) scan_bwd_kernel(ScanBwdArgs
           X[j] = fma4(gg, c, X[j]);
           sum_c = j ? fma4(gg, hs[i + 1][j], sum_c) : mul4(gg, hs[i + 1][j]);
           sum_b = j ? fma4(uu, X[j], sum_b) : mul4(uu, X[j]);
-          to_b[i][j] = sum4(X[j], b);
+          to_b[i][j] = sum4(X[j], b[i]);
           X[j] = mul4(X[j], es[i][j]);
           const State4 qq = mul4(X[j], hs[i][j]);
           r[i][j] = sum4(decay[j], qq);
@@ -611,7 +694,7 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 1) scan_bwd_kernel(ScanBwdArgs
         s_sum[(t4 + i) * 32 + (mine >> 2) * 16 + 4 * q + (mine & 3)] = (k1 ? v1 : v0) + __shfl_xor_sync(kAll, k1 ? v0 : v1, 4);
         // (to_b, r) [token][channel] over the noted states of these four tokens, which every lane has read by now
         s_note[t4 / 4 * kC * 128 + i * 2 * kCh + 2 * (mine * kC + (q & 1)) + (q >> 1)] =
-            join4(to_b[i][0], to_b[i][1], r[i][0] * kLn2, r[i][1] * kLn2, q);
+            join4(to_b[i][0], to_b[i][1], r[i][0], r[i][1], q);
       }
     }
 #pragma unroll
@@ -624,20 +707,18 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 1) scan_bwd_kernel(ScanBwdArgs
     }
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      if (pair_token + 4 * k < n && pair_real) {
-        const int at = 4 * k * kBwdRow;
-        const float4 w = *reinterpret_cast<const float4*>(s_notes + pair / 8 * kNotes + k * kC * 128 + pair_token * 2 * kCh + pair % 8 * 4);
-        const float2 v = pair_at(now + at), x = pair_at(now + kBwdTile + at), g = *reinterpret_cast<const float2*>(s_g + pair_at0 + at);
-        const float4 dt = *reinterpret_cast<const float4*>(s_dt + 2 * (pair_at0 + at));
-        *reinterpret_cast<uint32_t*>(du + 4 * k * a.lddu) = pack_bf16(fmaf(w.x, dt.x, skip.x * g.x), fmaf(w.z, dt.z, skip.y * g.y));
-        float2 e = make_float2(fmaf(w.x, v.x, w.y), fmaf(w.z, v.y, w.w));
-        if (f.softplus) {
-          const float2 sg = sigmoid2(make_float2(x.x + bias.x, x.y + bias.y));
-          e.x *= sg.x, e.y *= sg.y;
-        }
-        *reinterpret_cast<uint32_t*>(dd + 4 * k * a.lddd) = pack_bf16(e.x, e.y);
-        d_bias.x += e.x, d_bias.y += e.y;
+    for (int k = 0; k < 4; ++k) {
+      if (token + 8 * k < n && four_real) {
+        const int at = 8 * k * kBwdRow, t = token + 8 * k;
+        Quad to_b, r, dt, dtu;
+        get_pairs(s_notes + four / kCh * kNotes + t / 4 * kC * 128 + t % 4 * 2 * kCh + four % kCh * 2, to_b, r);
+        get_pairs(s_dt + 2 * (four_at + at), dt, dtu);
+        const Quad v = quad_at(now + at), g = quad_at(s_g + four_at + at);
+        put_quad(du + 8 * k * a.lddu, fma(to_b, dt, mul(skip, g)));
+        Quad e = fma(to_b, v, mul(r, quad(kLn2, kLn2, kLn2, kLn2)));
+        if (f.softplus) e = mul(e, sigmoid(add(quad_at(now + kBwdTile + at), bias)));
+        put_quad(dd + 8 * k * a.lddd, e);
+        d_bias = add(d_bias, e);
       }
     }
     du -= kTile * a.lddu, dd -= kTile * a.lddd;
@@ -656,24 +737,23 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 1) scan_bwd_kernel(ScanBwdArgs
       *reinterpret_cast<float4*>(ws.dA_part + part * all + state_at + j * f.S) = unpack4(dA[j]);
       if (a.d_state_in && s.part == 0) *reinterpret_cast<float4*>(a.d_state_in + s.n * all + state_at + j * f.S) = unpack4(X[j]);
     }
-  // the four threads that share two channels
+  // the eight threads that share four channels
+  allow_next_kernel();
   __syncthreads();
   float4* const join = reinterpret_cast<float4*>(pool);
-  join[threadIdx.x] = make_float4(d_skip.x, d_skip.y, d_bias.x, d_bias.y);
+  join[2 * threadIdx.x] = floats(d_skip), join[2 * threadIdx.x + 1] = floats(d_bias);
   __syncthreads();
-  if (threadIdx.x < kBwdPairs && pair_real) {
-    float4 v = join[threadIdx.x];
+  if (threadIdx.x < kBwdQuads && four_real) {
 #pragma unroll
-    for (int i = 1; i < 4; ++i) {
-      const float4 w = join[threadIdx.x + i * kBwdPairs];
-      v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+    for (int i = 1; i < 8; ++i) {
+      d_skip = add(d_skip, quad(join[2 * (threadIdx.x + i * kBwdQuads)]));
+      d_bias = add(d_bias, quad(join[2 * (threadIdx.x + i * kBwdQuads) + 1]));
     }
-    float* const to = ws.d_part + static_cast<long long>(part) * f.D + ch.c0 + 2 * pair;
-    to[0] = v.x, to[1] = v.y;
-    to[static_cast<long long>(parts) * f.D] = v.z, to[static_cast<long long>(parts) * f.D + 1] = v.w;
+    float* const to = ws.d_part + static_cast<long long>(part) * f.D + ch.c0 + four;
+    *reinterpret_cast<float4*>(to) = floats(d_skip);
+    *reinterpret_cast<float4*>(to + static_cast<long long>(parts) * f.D) = floats(d_bias);
   }
 }
-
 
 // The gradient that a part hands to the one before it, from zero at its end, and the sum of its dt.
 __global__ void __launch_bounds__(kFwdWarps * 32, 4) scan_bwd_sums_kernel(ScanBwdArgs a, int blocks, int length, float* sums, float* dt_sums) {
@@ -686,6 +766,7 @@ __global__ void __launch_bounds__(kFwdWarps * 32, 4) scan_bwd_sums_kernel(ScanBw
   const Channels ch = block_channels(blockIdx.x % blocks, f.D, f.G, kFwdRow);
   const int t0 = s.part * length, count = min(length, s.len - t0);
   bf16* const raw = reinterpret_cast<bf16*>(pool);  // [stage][delta, dy, z]
+  allow_next_kernel();
   float* const s_dt = pool + 2 * 3 * kFwdTile / 2;  // [token][channel] (dt, g)
   float* const s_bc = s_dt + 2 * kFwdTile;          // [stage][nothing, C]
   const int q = lane & 3, first = warp * kCh + (lane >> 2) * kC;
@@ -718,8 +799,8 @@ __global__ void __launch_bounds__(kFwdWarps * 32, 4) scan_bwd_sums_kernel(ScanBw
     }
     copies_commit();
   };
-  const int pair = threadIdx.x % kFwdPairs, pair_token = threadIdx.x / kFwdPairs;
-  const float2 bias = vector_at(f.dt_bias, ch.c0 + 2 * pair, 2 * pair < ch.have);
+  const int four = 4 * (threadIdx.x % kFwdQuads), token = threadIdx.x / kFwdQuads;
+  const Quad bias = weights_at(f.dt_bias, ch.c0 + four, four < ch.have);
   fetch(last, 0);
   int stage = 0;
   for (int tile = last; tile >= 0; tile -= kTile, stage ^= 1) {
@@ -729,18 +810,18 @@ __global__ void __launch_bounds__(kFwdWarps * 32, 4) scan_bwd_sums_kernel(ScanBw
     copies_done();
     __syncthreads();  // the tile is here, and nothing reads the one before it any more
     fetch(tile - kTile, stage ^ 1);
-    const bf16* const now = raw + stage * 3 * kFwdTile + pair_token * kFwdRow + 2 * pair;
+    const bf16* const now = raw + stage * 3 * kFwdTile + token * kFwdRow + four;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float2 d = pair_at(now + 4 * k * kFwdRow);
-      float2 g = pair_at(now + kFwdTile + 4 * k * kFwdRow), x = make_float2(d.x + bias.x, d.y + bias.y);
-      if (f.softplus) x = softplus2(x);
-      if (pair_token + 4 * k >= n) x = make_float2(0.0f, 0.0f);
+    for (int k = 0; k < 4; ++k) {
+      const int at = 8 * k * kFwdRow;
+      Quad g = quad_at(now + kFwdTile + at), x = add(quad_at(now + at), bias);
+      if (f.softplus) x = softplus(x);
+      if (token + 8 * k >= n) x = zero_quad();
       if (gated) {
-        const float2 zz = pair_at(now + 2 * kFwdTile + 4 * k * kFwdRow), sg = sigmoid2(zz);
-        g.x *= zz.x * sg.x, g.y *= zz.y * sg.y;
+        const Quad zz = quad_at(now + 2 * kFwdTile + at);
+        g = mul(g, mul(zz, sigmoid(zz)));
       }
-      *reinterpret_cast<float4*>(s_dt + 2 * ((pair_token + 4 * k) * kFwdRow + 2 * pair)) = make_float4(x.x, g.x, x.y, g.y);
+      put_pairs(s_dt + 2 * (at + token * kFwdRow + four), x, g);
     }
     __syncthreads();
     const uint32_t at_dt = after_sync(s_dt + 2 * first), at_c = after_sync(s_b + kTile * kBRow + 4 * q);
@@ -761,24 +842,71 @@ __global__ void __launch_bounds__(kFwdWarps * 32, 4) scan_bwd_sums_kernel(ScanBw
   }
 }
 
-// dB and dC [T][G][S] (bf16) from the channel blocks' sums [blocks][T][32]: 32 tokens of a sequence a CTA, four of a
-// token's 32 values a thread.
-__global__ void __launch_bounds__(256) scan_bc_sums_kernel(ScanArgs f, const float* __restrict__ part, int blocks, bf16* dB, bf16* dC) {
-  SeqPart s;
-  if (!find_part(f.cu, f.N, f.T, f.max_seqlen, kTile, blockIdx.x, s, nullptr)) return;
-  const int at = s.part * kTile + static_cast<int>(threadIdx.x >> 3), piece = threadIdx.x & 7, state = 4 * (piece & 3);
-  if (at >= s.len || state >= f.S) return;
-  const long long t = s.start + at;
-  const int per = blocks / f.G;
-  for (int g = 0; g < f.G; ++g) {
-    float4 sum = make_float4(0, 0, 0, 0);
-#pragma unroll 8
-    for (int b = g * per; b < (g + 1) * per; ++b) {
-      const float4 v = __ldg(reinterpret_cast<const float4*>(part + (static_cast<long long>(b) * f.T + t) * 32 + 4 * piece));
-      sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+// What is left to add up, in one launch, always in one order. dB and dC [T][G][S] (bf16) from the channel blocks' sums
+// [blocks][T][32]: a CTA has eight tokens of a sequence and 64 pieces of four values, each the sum of four threads' shares of the
+// blocks. dA, dskip and d_dt_bias from the parts' sums: a CTA has 32 columns, eight warps share the parts.
+__global__ void __launch_bounds__(256) scan_tail_kernel(ScanBwdArgs a, BwdWs ws, int blocks, int parts, int bc_ctas) {
+  __shared__ float4 share[4][64];
+  wait_for_last_kernel();
+  const ScanArgs& f = a.f;
+  if (static_cast<int>(blockIdx.x) < bc_ctas) {
+    SeqPart s;
+    if (!find_part(f.cu, f.N, f.T, f.max_seqlen, 8, blockIdx.x, s, nullptr)) return;
+    const int piece = threadIdx.x & 63, quarter = threadIdx.x >> 6, value = piece & 7, state = 4 * (value & 3);
+    const int at = s.part * 8 + (piece >> 3);
+    const bool real = at < s.len && state < f.S;
+    const long long t = s.start + at;
+    const int per = blocks / f.G;
+    for (int g = 0; g < f.G; ++g) {
+      float4 sum = make_float4(0, 0, 0, 0);
+      if (real) {
+#pragma unroll 4
+        for (int b = g * per + quarter; b < (g + 1) * per; b += 4) {
+          const float4 v = __ldg(reinterpret_cast<const float4*>(ws.bc_part + (static_cast<long long>(b) * f.T + t) * 32 + 4 * value));
+          sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+        }
+      }
+      share[quarter][piece] = sum;
+      __syncthreads();
+      if (quarter == 0 && real) {
+#pragma unroll
+        for (int i = 1; i < 4; ++i) {
+          const float4 v = share[i][piece];
+          sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+        }
+        bf16* const to = static_cast<bf16*>(value < 4 ? a.dB : a.dC) + (t * f.G + g) * f.S + state;
+        *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16(sum.x, sum.y), pack_bf16(sum.z, sum.w));
+      }
+      __syncthreads();
     }
-    bf16* const to = (piece < 4 ? dB : dC) + (t * f.G + g) * f.S + state;
-    *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16(sum.x, sum.y), pack_bf16(sum.z, sum.w));
+    return;
+  }
+  // columns: dA's, then dskip's, then d_dt_bias'
+  const long long all = static_cast<long long>(f.D) * f.S;
+  const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
+  const long long c = (static_cast<long long>(blockIdx.x) - bc_ctas) * 32 + lane;
+  const float* from = ws.dA_part + c;
+  float* to = a.dA + c;
+  long long ld = all;
+  if (c >= all) {
+    const long long i = c - all;
+    const bool second = i >= f.D;
+    from = ws.d_part + (second ? static_cast<long long>(parts) * f.D : 0) + (second ? i - f.D : i), ld = f.D;
+    float* const base = second ? a.d_dt_bias : a.dskip;
+    to = base && i < 2ll * f.D ? base + (second ? i - f.D : i) : nullptr;
+  }
+  float sum = 0.0f;
+  if (to) {
+#pragma unroll 4
+    for (int p = g; p < parts; p += 8) sum += __ldg(from + p * ld);
+  }
+  float* const sums = reinterpret_cast<float*>(share);
+  sums[g * 32 + lane] = sum;
+  __syncthreads();
+  if (g == 0 && to) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) sum += sums[i * 32 + lane];
+    *to = sum;
   }
 }
 
@@ -862,19 +990,38 @@ struct Division {
   bool cut;
 };
 
-// Cutting a sequence costs a second run over its tokens (the sums, two thirds of the main run), so it is done only
-// where whole sequences leave most of the GPU empty.
+// Cutting the sequences gives more CTAs but costs a second run over all parts but the last ones (the sums), so the
+// cheapest of some lengths is taken by an estimate from measured costs (nanoseconds; blocks of 64 channels in the forward and the
+// sums, of 128 in the backward). A CTA's chain of one token takes 150 in the forward and 140 in the sums, and a token of a block
+// 0.30 and 0.21 of the whole GPU's time; the larger of the two rules, and where they are near one another both count (fourth
+// powers). A backward CTA has an SM alone: 410 a token, in whole rounds. The launches and the join take 8 us and 0.5 us a part in a
+// row. The lengths are known by their bound and sum alone: the last parts are taken for half full. (7,864 tokens of prompts of 1 to 4,096 tokens
+// x 8,192 channels: 625 us in one piece, 541 in parts of 1,024, 485 of 512, 517 of 256.)
 Division divide(int max_seqlen, int T, int N, int D, int G, bool backward) {
-  const int warps = backward ? kBwdWarps : kFwdWarps;
   Division d;
-  d.blocks = blocks_of(D, G, kCh * warps);
-  const long long want = 8ll * num_sms(), have = static_cast<long long>(N) * d.blocks * warps;
+  d.blocks = blocks_of(D, G, kCh * (backward ? kBwdWarps : kFwdWarps));
+  const double sms = num_sms(), fwd_blocks = blocks_of(D, G, kCh * kFwdWarps);
   long long whole = max_seqlen > 0 ? (static_cast<long long>(max_seqlen) + kTile - 1) / kTile * kTile : kTile;
   if (whole > 0x7FFFFFE0) whole = 0x7FFFFFE0;
-  d.length = static_cast<int>(whole);
-  long long pieces = want / have;
-  if (pieces > whole / 128) pieces = whole / 128;
-  if (pieces >= 3) d.length = static_cast<int>((whole / kTile + pieces - 1) / pieces * kTile);
+  // (a bound above T says no more than T does)
+  const long long longest = whole < T ? whole : (static_cast<long long>(T) + kTile - 1) / kTile * kTile + kTile;
+  const auto both = [](double x, double y) { return std::sqrt(std::sqrt(x * x * x * x + y * y * y * y)); };
+  const auto cost = [&](long long length, int pieces) {
+    const double tokens = static_cast<double>(length), rest = std::max(0.0, T - 0.5 * N * tokens), share = fwd_blocks * 152.0 / sms;
+    double ns = backward ? std::ceil(std::max(1.0, T / tokens) * d.blocks / sms) * tokens * 410.0
+                         : both(tokens * 150.0, T * share * 0.30);
+    if (pieces > 1) ns += both(tokens * 140.0, rest * share * 0.21) + 8000.0 + 500.0 * pieces;
+    return ns;
+  };
+  long long best = whole;
+  double least = cost(longest, 1);
+  for (int pieces : {2, 3, 4, 5, 6, 7, 8, 10, 12, 16, 20, 24, 32, 48, 64, 96, 128}) {
+    const long long length = (longest / kTile + pieces - 1) / pieces * kTile;
+    if (length < 64) break;
+    const double ns = cost(length, pieces);
+    if (ns < 0.95 * least) least = ns, best = length;
+  }
+  d.length = static_cast<int>(best);
   d.parts = T / d.length + static_cast<long long>(N);
   d.cut = max_seqlen > d.length;
   return d;
@@ -917,10 +1064,14 @@ cudaError_t launch_scan_fwd(const ScanArgs& a, cudaStream_t st) {
     }
     LaunchTimer lt("scan_join", st);
     const unsigned join = static_cast<unsigned>(d.parts * ((a.D * (a.S / 4) + 127) / 128));
-    scan_join_kernel<false><<<join, 128, 0, st>>>(a, d.length, a.state_in, starts, dt_sums);
+    e = launch_behind(scan_join_kernel<false>, dim3(join), 128, 0, st, a, d.length, a.state_in, starts, static_cast<const float*>(dt_sums));
+    if (e != cudaSuccess) return e;
   }
   LaunchTimer lt("scan_fwd", st);
-  scan_fwd_kernel<false><<<grid, kFwdWarps * 32, smem, st>>>(a, d.blocks, d.length, starts, nullptr, nullptr);
+  if (d.cut)
+    return launch_behind(scan_fwd_kernel<false>, dim3(grid), kFwdWarps * 32, smem, st, a, d.blocks, d.length,
+                         static_cast<const float*>(starts), static_cast<float*>(nullptr), static_cast<float*>(nullptr));
+  scan_fwd_kernel<false><<<grid, kFwdWarps * 32, smem, st>>>(a, d.blocks, d.length, nullptr, nullptr, nullptr);
   return cudaGetLastError();
 }
 
@@ -952,28 +1103,23 @@ cudaError_t launch_scan_bwd(const ScanBwdArgs& a, cudaStream_t st) {
     }
     LaunchTimer lt("scan_join", st);
     const unsigned join = static_cast<unsigned>(d.parts * ((f.D * (f.S / 4) + 127) / 128));
-    scan_join_kernel<true><<<join, 128, 0, st>>>(f, d.length, a.d_state_out, ws.tails, dt_sums);
+    e = launch_behind(scan_join_kernel<true>, dim3(join), 128, 0, st, f, d.length, a.d_state_out, ws.tails, static_cast<const float*>(dt_sums));
+    if (e != cudaSuccess) return e;
   }
   {
     LaunchTimer lt("scan_bwd", st);
-    scan_bwd_kernel<<<static_cast<unsigned>(d.parts * d.blocks), kBwdWarps * 32, kBwdSmem, st>>>(
-        a, d.blocks, static_cast<int>(d.parts), d.length, d.cut, ws);
+    const unsigned grid = static_cast<unsigned>(d.parts * d.blocks);
+    const int parts = static_cast<int>(d.parts);
+    if (d.cut) e = launch_behind(scan_bwd_kernel, dim3(grid), kBwdWarps * 32, kBwdSmem, st, a, d.blocks, parts, d.length, true, ws);
+    else scan_bwd_kernel<<<grid, kBwdWarps * 32, kBwdSmem, st>>>(a, d.blocks, parts, d.length, false, ws);
+    if (e != cudaSuccess) return e;
   }
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  if (f.T > 0) {
-    LaunchTimer lt("scan_bc_sums", st);
-    scan_bc_sums_kernel<<<static_cast<unsigned>(f.T / kTile + static_cast<long long>(f.N)), 256, 0, st>>>(
-        f, ws.bc_part, d.blocks, static_cast<bf16*>(a.dB), static_cast<bf16*>(a.dC));
-  }
-  e = launch_column_sums("scan_dA", ws.dA_part, static_cast<int>(d.parts), static_cast<long long>(all), a.dA, st);
-  if (e != cudaSuccess) return e;
-  if (a.dskip) {
-    e = launch_column_sums("scan_dskip", ws.d_part, static_cast<int>(d.parts), f.D, a.dskip, st);
-    if (e != cudaSuccess) return e;
-  }
-  if (a.d_dt_bias) e = launch_column_sums("scan_dbias", ws.d_part + d.parts * f.D, static_cast<int>(d.parts), f.D, a.d_dt_bias, st);
-  return e;
+  LaunchTimer lt("scan_tail", st);
+  const long long bc_ctas = f.T / 8 + static_cast<long long>(f.N), columns = static_cast<long long>(all) + 2ll * f.D;
+  return launch_behind(scan_tail_kernel, dim3(static_cast<unsigned>(bc_ctas + (columns + 31) / 32)), 256, 0, st, a, ws, d.blocks,
+                       static_cast<int>(d.parts), static_cast<int>(bc_ctas));
 }
 
 cudaError_t launch_scan_step(const ScanStepArgs& a, cudaStream_t st) {
