@@ -28,6 +28,7 @@ namespace {
 constexpr unsigned kAll = 0xFFFFFFFFu;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kRaise = 2.2e-8f;
 constexpr int kTile = kScanTile;
 constexpr int kBRow = 20;  // floats of a token's B or C: sixteen and four of padding (no bank conflicts)
 constexpr int kC = 2;           // channels of a lane in the recurrence
@@ -246,6 +247,14 @@ __device__ __forceinline__ State4 fma4(const State4& x, const State4& s, const S
 __device__ __forceinline__ State4 fma4(f32x2 x, const State4& s, const State4& c) {
   return State4{fma2(x, s.a, c.a), fma2(x, s.b, c.b)};
 }
+// exp(dt A) of four states, `decay` being A / ln 2. The exponential unit's results just below one are 1e-8 too small on average (measured:
+// 0.6e-8 for arguments of 1e-4 to 1e-3, 1.2e-8 to 1e-2, 2.2e-8 to 0.1), which a state with a memory of a thousand tokens adds up to
+// 1e-5 of itself. The argument is raised by as much (log2 of it), in the product's own instruction; it still gives 1 for dt = 0. Gradients
+// of A over 3,000 tokens: 1.7e-6 off without, 0.7e-6 with it.
+__device__ __forceinline__ State4 decays(f32x2 dt, const State4& decay) {
+  const f32x2 raise = pack2(kRaise, kRaise);
+  return ex2(State4{fma2(dt, decay.a, raise), fma2(dt, decay.b, raise)});
+}
 __device__ __forceinline__ float sum4(const State4& x, const State4& y) {  // x . y
   float a, b;
   unpack2(fma2(x.b, y.b, mul2(x.a, y.a)), a, b);
@@ -357,8 +366,8 @@ __global__ void __launch_bounds__(kFwdWarps * 32, 4) scan_fwd_kernel(ScanArgs a,
       for (int t = 0; t < kTile; ++t) {
         const float4 d = lds4(at_dt + t * 8 * kFwdRow);
         const State4 b = pack4(lds4(at_b + t * 4 * kBRow));
-        h[0] = fma4(ex2(mul4(pack2(d.x, d.x), decay[0])), h[0], mul4(pack2(d.y, d.y), b));
-        h[1] = fma4(ex2(mul4(pack2(d.z, d.z), decay[1])), h[1], mul4(pack2(d.w, d.w), b));
+        h[0] = fma4(decays(pack2(d.x, d.x), decay[0]), h[0], mul4(pack2(d.y, d.y), b));
+        h[1] = fma4(decays(pack2(d.z, d.z), decay[1]), h[1], mul4(pack2(d.w, d.w), b));
         dt_sum[0] += d.x, dt_sum[1] += d.z;
       }
     } else {
@@ -366,7 +375,7 @@ __global__ void __launch_bounds__(kFwdWarps * 32, 4) scan_fwd_kernel(ScanArgs a,
       // decays and inputs; the recurrence and y.
       float4 d[2];
       State4 b[2], c[2], e[2][kC], in[2][kC], cc[2];
-      float y[2][kC];
+      float y[2][kC] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
       const auto load = [&](int t) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -378,8 +387,8 @@ __global__ void __launch_bounds__(kFwdWarps * 32, 4) scan_fwd_kernel(ScanArgs a,
       const auto prepare = [&]() {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          e[i][0] = ex2(mul4(pack2(d[i].x, d[i].x), decay[0])), in[i][0] = mul4(pack2(d[i].y, d[i].y), b[i]);
-          e[i][1] = ex2(mul4(pack2(d[i].z, d[i].z), decay[1])), in[i][1] = mul4(pack2(d[i].w, d[i].w), b[i]);
+          e[i][0] = decays(pack2(d[i].x, d[i].x), decay[0]), in[i][0] = mul4(pack2(d[i].y, d[i].y), b[i]);
+          e[i][1] = decays(pack2(d[i].z, d[i].z), decay[1]), in[i][1] = mul4(pack2(d[i].w, d[i].w), b[i]);
           cc[i] = c[i];
         }
       };
@@ -613,8 +622,8 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 1) scan_bwd_kernel(ScanBwdArgs
       for (int i = 0; i < 4; ++i) {
         const float4 d = lds4(at_dt + (t4 + i) * 8 * kBwdRow);
         const State4 b = pack4(lds4(at_b + (t4 + i) * 4 * kBRow));
-        h[0] = fma4(ex2(mul4(pack2(d.x, d.x), decay[0])), h[0], mul4(pack2(d.y, d.y), b));
-        h[1] = fma4(ex2(mul4(pack2(d.z, d.z), decay[1])), h[1], mul4(pack2(d.w, d.w), b));
+        h[0] = fma4(decays(pack2(d.x, d.x), decay[0]), h[0], mul4(pack2(d.y, d.y), b));
+        h[1] = fma4(decays(pack2(d.z, d.z), decay[1]), h[1], mul4(pack2(d.w, d.w), b));
         if (gated) {
           const State4 c = pack4(lds4(at_c + (t4 + i) * 4 * kBRow));
           y[i][0] = sum4(c, h[0]), y[i][1] = sum4(c, h[1]);
@@ -658,8 +667,8 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 1) scan_bwd_kernel(ScanBwdArgs
       for (int i = 0; i < 4; ++i) {
         d[i] = lds4(at_dt + (t4 + i) * 8 * kBwdRow);
         b[i] = pack4(lds4(at_b + (t4 + i) * 4 * kBRow));
-        es[i][0] = ex2(mul4(pack2(d[i].x, d[i].x), decay[0]));
-        es[i][1] = ex2(mul4(pack2(d[i].z, d[i].z), decay[1]));
+        es[i][0] = decays(pack2(d[i].x, d[i].x), decay[0]);
+        es[i][1] = decays(pack2(d[i].z, d[i].z), decay[1]);
         hs[i + 1][0] = fma4(es[i][0], hs[i][0], mul4(pack2(d[i].y, d[i].y), b[i]));
         hs[i + 1][1] = fma4(es[i][1], hs[i][1], mul4(pack2(d[i].w, d[i].w), b[i]));
       }
@@ -829,8 +838,8 @@ __global__ void __launch_bounds__(kFwdWarps * 32, 4) scan_bwd_sums_kernel(ScanBw
     for (int t = kTile - 1; t >= 0; --t) {
       const float4 d = lds4(at_dt + t * 8 * kFwdRow);
       const State4 c = pack4(lds4(at_c + t * 4 * kBRow));
-      X[0] = mul4(fma4(pack2(d.y, d.y), c, X[0]), ex2(mul4(pack2(d.x, d.x), decay[0])));
-      X[1] = mul4(fma4(pack2(d.w, d.w), c, X[1]), ex2(mul4(pack2(d.z, d.z), decay[1])));
+      X[0] = mul4(fma4(pack2(d.y, d.y), c, X[0]), decays(pack2(d.x, d.x), decay[0]));
+      X[1] = mul4(fma4(pack2(d.w, d.w), c, X[1]), decays(pack2(d.z, d.z), decay[1]));
       dt_sum[0] += d.x, dt_sum[1] += d.z;
     }
   }
@@ -965,10 +974,10 @@ __global__ void __launch_bounds__(kStepWarps * 32) scan_step_kernel(ScanStepArgs
 #pragma unroll
   for (int r = 0; r < kRows; ++r) {
     const float k = __shfl_sync(kAll, step, (lane & ~3) | r), d = __shfl_sync(kAll, du, (lane & ~3) | r);
-    h[r].x = fmaf(ex2(k * A.x), h[r].x, d * bf16_lo(Bv[r].x));
-    h[r].y = fmaf(ex2(k * A.y), h[r].y, d * bf16_hi(Bv[r].x));
-    h[r].z = fmaf(ex2(k * A.z), h[r].z, d * bf16_lo(Bv[r].y));
-    h[r].w = fmaf(ex2(k * A.w), h[r].w, d * bf16_hi(Bv[r].y));
+    h[r].x = fmaf(ex2(fmaf(k, A.x, kRaise)), h[r].x, d * bf16_lo(Bv[r].x));
+    h[r].y = fmaf(ex2(fmaf(k, A.y, kRaise)), h[r].y, d * bf16_hi(Bv[r].x));
+    h[r].z = fmaf(ex2(fmaf(k, A.z, kRaise)), h[r].z, d * bf16_lo(Bv[r].y));
+    h[r].w = fmaf(ex2(fmaf(k, A.w, kRaise)), h[r].w, d * bf16_hi(Bv[r].y));
     if (state[r]) *reinterpret_cast<float4*>(state[r]) = h[r];
     o[r] = fmaf(bf16_lo(Cv[r].x), h[r].x, bf16_hi(Cv[r].x) * h[r].y) + fmaf(bf16_lo(Cv[r].y), h[r].z, bf16_hi(Cv[r].y) * h[r].w);
   }
