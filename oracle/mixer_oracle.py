@@ -56,11 +56,11 @@ def route(logits, bias, k, kind="sigmoid", groups=1, group_k=None, group_top=2, 
     if not renorm:
         return idx, scale * sel, sel
     l = at(np.where(out, -np.inf, logits), idx.astype(np.int64), 1)
+    if kind == "sigmoid":  # log sigmoid(l) = min(l, 0) - log(1 + e^-|l|)
+        l = np.minimum(l, 0) - np.log1p(np.exp(-np.abs(l)))
     top = l.max(1, keepdims=True)
     with np.errstate(invalid="ignore"):
         rel = np.where(np.isfinite(l), np.exp(l - np.where(np.isfinite(top), top, 0.0)), 0.0)
-        if kind == "sigmoid":  # sigmoid(l) = e^l / (1 + e^l)
-            rel = np.where(np.isfinite(l), rel / (1 + np.exp(np.minimum(l, 700))), 0.0) * (1 + np.exp(np.minimum(np.where(np.isfinite(top), top, 0), 700)))
     total = rel.sum(1, keepdims=True)
     return idx, scale * rel / np.where(total > 0, total, 1.0), sel
 

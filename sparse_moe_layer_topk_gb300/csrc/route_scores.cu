@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_scores_kernel(Params p) {
       const bool real = mine != 0ull && c > neg_inf() && lane < listed_n;
       const int e = real ? static_cast<int>(~static_cast<uint32_t>(mine)) : 0;
       const float l = real ? __ldg(row + e) : 0.0f, b = real ? __ldg(p.bias + e) : 0.0f;
-      const float tol = real ? 0x1p-21f * fabsf(c - b) * (2.0f + fabsf(l - (SOFTMAX ? top : 0.0f))) + 0x1p-22f * fabsf(c) : 0.0f;
+      const float tol = real ? 0x1p-21f * fabsf(c - b) * (2.0f + fminf(fabsf(l - (SOFTMAX ? top : 0.0f)), 1e38f)) + 0x1p-22f * fabsf(c) : 0.0f;
       const float nc = __shfl_down_sync(kAll, c, 1), nl = __shfl_down_sync(kAll, l, 1), nb = __shfl_down_sync(kAll, b, 1),
                   nt = __shfl_down_sync(kAll, tol, 1);
       const unsigned reals = __ballot_sync(kAll, real);
@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_scores_kernel(Params p) {
         exact = true;
         unsigned long long key = 0ull;
         const int n = last > neg_inf() ? collect(order_bits(last - 4.0f * wide), key) : 33;
-        if (n <= 32) {  // all that could be among the first k, by their 64-bit values
+        if (n >= k && n <= 32) {  // all that could be among the first k, by their 64-bit values
           const bool some = lane < n;
           const int id = some ? static_cast<int>(~static_cast<uint32_t>(key)) : 0x7FFFFFFF;
           const double l64 = some ? row[id] : 0.0, b64 = some ? p.bias[id] : 0.0;

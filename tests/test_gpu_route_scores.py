@@ -207,3 +207,15 @@ def test_in_a_graph_and_on_another_stream():
     torch.cuda.synchronize()
     assert torch.equal(r.topk_idx, other.topk_idx) and torch.equal(r.topk_w, other.topk_w)
     assert torch.equal(r.d_logits, other.d_logits)
+
+
+@pytest.mark.parametrize("groups,group_k", [(1, 1), (8, 4)])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_logits_at_both_ends_of_the_range(score, groups, group_k):
+    """Differences of logits that pass the largest float, next to experts that only 64 bits tell apart."""
+    l = _logits(9, 256, 3)
+    l[:, ::5] = -3e38
+    l[3:6, 7] = 3e38
+    b = torch.full((256,), 0.25)
+    b[1::3] += 2.0 ** -24
+    _check(l, b, 12, score, groups=groups, group_k=group_k)
