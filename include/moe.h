@@ -596,7 +596,7 @@ int moe_scan_bwd(const uint16_t* dy, const uint16_t* u, const uint16_t* delta, c
                  size_t ws_bytes, int32_t* err_flag, void* stream);
 
 /* One token for each of `rows` rows: updates the state cache (fp32 [n_slots][D][states]) in place at slot
- * state_idx[row] and writes y[row]. Slots as in moe_linattn_step. */
+ * state_idx[row] and writes y[row]. Slots as in moe_linattn_step. At most 65,535 groups of 4,194,240 channels. */
 int moe_scan_step(const uint16_t* u, const uint16_t* delta, const float* A, const uint16_t* B, const uint16_t* C,
                   const float* skip, const uint16_t* z, const float* dt_bias, float* state, const int32_t* state_idx,
                   int n_slots, int rows, int D, int states, int G, int ldu, int lddelta, int ldB, int ldC, int ldz, int ldy,

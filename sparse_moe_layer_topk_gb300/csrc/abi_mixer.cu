@@ -354,7 +354,7 @@ int moe_scan_step(const uint16_t* u, const uint16_t* delta, const float* A, cons
   if (z) MOE_CHECK(check_rows(z, D, ldz));
   MOE_CHECK(check_rows(y, D, ldy));
   MOE_REQUIRE(aligned(A, 16) && aligned(skip, 4) && aligned(dt_bias, 4) && aligned(state, 16), MOE_ERR_ALIGN);
-  MOE_REQUIRE(grid_fits(rows, D / 32 + G), MOE_ERR_ARG);
+  MOE_REQUIRE(G <= 65535 && D / G <= 64 * 65535, MOE_ERR_ARG);
   if (rows == 0) return MOE_OK;
   const ScanStepArgs a{u, delta, A, B, C, skip, z, dt_bias, state, state_idx, n_slots, rows, D, states, G, ldu, lddelta, ldB,
                        ldC, ldz, ldy, softplus != 0, y, err_flag};

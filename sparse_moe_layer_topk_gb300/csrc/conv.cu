@@ -4,7 +4,10 @@
 //
 // A thread owns four channels (8-byte accesses, a warp's 256 bytes of a row) and walks tokens with the last W inputs
 // in registers, so every input is read once but for the W - 1 rows before a part. A group of tokens is on its way while the one
-// before it is computed, two values an instruction; HBM bounds all three kernels.
+// before it is computed, two values an instruction. HBM bounds the forward: 7,864 packed tokens x 8,192 channels in 46 us, 38 of them the
+// bytes (parts of 32 tokens in groups of 4: 60; parts of 128: 55).
+#include <type_traits>
+
 #include "common.cuh"
 #include "mixer.h"
 #include "seq.cuh"
@@ -138,7 +141,9 @@ __global__ void __launch_bounds__(kThreads, 5) conv_fwd_kernel(ConvArgs a, int b
 
 // With dp_t = dy_t silu'(p_t), p recomputed: dx_t = sum_i w[W-1-i] dp_{t+i}, dw[j] = sum_t dp_t x_{t-(W-1)+j}. A part reads W - 1
 // tokens on either side for p and dp. A CTA takes every walkers-th part, so its sums of dw and dbias stay in
-// registers; they are joined in a fixed order afterwards.
+// registers; they are joined in a fixed order afterwards. Latency bounds it: 40 registers of weights and sums and the two windows leave
+// room for 16 warps an SM, and two instructions issue a cycle. 16,384 tokens x 8,192 channels in 184 us, 119 of them the bytes;
+// a group of 2 tokens instead of 4 takes 226, of 8 217; three CTAs an SM 255, five spill (400).
 template <int W, bool SILU>
 __global__ void __launch_bounds__(kThreads, 4) conv_bwd_kernel(ConvBwdArgs a, int blocks) {
   constexpr int kStep = 4;
@@ -167,54 +172,58 @@ __global__ void __launch_bounds__(kThreads, 4) conv_bwd_kernel(ConvBwdArgs a, in
     const bf16* fx = x + static_cast<long long>(s.start + t0) * a.ldx + c;
     const bf16* fg = static_cast<const bf16*>(a.dy) + static_cast<long long>(s.start + t0) * a.lddy + c;
     bf16* to = static_cast<bf16*>(a.dx) + static_cast<long long>(s.start + t0 - (W - 1)) * a.lddx + c;
-    uint2 nx[kStep], ng[kStep];
-    const auto fetch = [&](int left) {
-#pragma unroll
-      for (int q = 0; q < kStep; ++q) {
-        nx[q] = ng[q] = make_uint2(0, 0);
-        if (q < left) nx[q] = load4(fx + q * a.ldx), ng[q] = load4(fg + q * a.lddy);
-      }
-      fx += kStep * a.ldx, fg += kStep * a.lddy;
+    uint2 nx[kStep], ng[kStep];  // the next tokens, each read anew as soon as it is taken
+    const auto fetch = [&](int q, bool some) {
+      nx[q] = ng[q] = make_uint2(0, 0);  // (zero past the sequence's end)
+      if (some) nx[q] = load4(fx + q * a.ldx), ng[q] = load4(fg + q * a.lddy);
     };
-    fetch(end - t0);
-    F4 in[W - 1 + kStep], dp[W - 1 + kStep];  // the newest last
+#pragma unroll
+    for (int q = 0; q < kStep; ++q) fetch(q, t0 + q < end);
+    F4 in[W], dp[W];  // the newest last
 #pragma unroll
     for (int j = 0; j + 1 < W; ++j) in[j] = widen(input_at<W>(x, a.ldx, state, a.D, s, t0 - (W - 1) + j, c)), dp[j] = zero4();
     // token t gives dx of t - (W - 1); a first part's first W - 1 are the state's
-    for (int t = t0; t < t1 + W - 1; t += kStep) {
-#pragma unroll
-      for (int q = 0; q < kStep; ++q) in[W - 1 + q] = widen(nx[q]), dp[W - 1 + q] = widen(ng[q]);  // (zero past the sequence's end)
-      fetch(end - t - kStep);
+    const auto group = [&](int t, auto inside) {
+      fx += kStep * a.ldx, fg += kStep * a.lddy;
 #pragma unroll
       for (int q = 0; q < kStep; ++q) {
         const int at = t + q;
-        F4& d = dp[W - 1 + q];
+        in[W - 1] = widen(nx[q]);
+        F4& d = dp[W - 1];
+        d = widen(ng[q]);
+        fetch(q, at + kStep < end);
         if (SILU) {
           F4 p = bias;
 #pragma unroll
-          for (int j = 0; j < W; ++j) p = fma4(tap[j], in[q + j], p);
+          for (int j = 0; j < W; ++j) p = fma4(tap[j], in[j], p);
           const F4 sg = sigmoid4(p);
           // silu' = sg (1 + p (1 - sg))
           d = mul4(mul4(d, sg), fma4(p, fma4(sg, splat4(-1.0f), splat4(1.0f)), splat4(1.0f)));
         }
-        if (at < t1) {
+        if (inside.value || at < t1) {
           db = add4(db, d);
 #pragma unroll
-          for (int j = 0; j < W; ++j) dw[j] = fma4(d, in[q + j], dw[j]);
+          for (int j = 0; j < W; ++j) dw[j] = fma4(d, in[j], dw[j]);
         }
-        const int out = at - (W - 1);  // dx_out = sum_i w[W-1-i] dp_{out+i}; dp[q + i] is dp_{out+i}
-        if (out < first || out >= t1) continue;
-        F4 r = zero4();
+        const int out = at - (W - 1);  // dx_out = sum_i w[W-1-i] dp_{out+i}; dp[i] is dp_{out+i}
+        if (inside.value || (out >= first && out < t1)) {
+          F4 r = zero4();
 #pragma unroll
-        for (int j = 0; j < W; ++j) r = fma4(tap[W - 1 - j], dp[q + j], r);
-        const int late = out - (s.len - (W - 1));  // inputs that are part of the last state
-        if (d_out && late >= 0) r = add4(r, widen(load4(d_out + (static_cast<long long>(s.n) * (W - 1) + late) * a.D + c)));
-        if (out >= 0) store4(to + q * a.lddx, narrow(r));
-        else store4(d_in + (static_cast<long long>(s.n) * (W - 1) + (W - 1) + out) * a.D + c, narrow(r));
+          for (int j = 0; j < W; ++j) r = fma4(tap[W - 1 - j], dp[j], r);
+          const int late = out - (s.len - (W - 1));  // inputs that are part of the last state
+          if (!inside.value && d_out && late >= 0) r = add4(r, widen(load4(d_out + (static_cast<long long>(s.n) * (W - 1) + late) * a.D + c)));
+          if (inside.value || out >= 0) store4(to + q * a.lddx, narrow(r));
+          else store4(d_in + (static_cast<long long>(s.n) * (W - 1) + (W - 1) + out) * a.D + c, narrow(r));
+        }
+#pragma unroll
+        for (int j = 0; j + 1 < W; ++j) in[j] = in[j + 1], dp[j] = dp[j + 1];
       }
       to += kStep * a.lddx;
-#pragma unroll
-      for (int j = 0; j + 1 < W; ++j) in[j] = in[kStep + j], dp[j] = dp[kStep + j];
+    };
+    for (int t = t0; t < t1 + W - 1; t += kStep) {
+      // inside: all of the group's tokens are the part's, and all of its dx too (none is late either: t + kStep <= s.len)
+      if (t - (W - 1) >= t0 && t + kStep <= t1) group(t, std::true_type{});
+      else group(t, std::false_type{});
     }
   }
   allow_next_kernel();
@@ -258,6 +267,7 @@ __global__ void __launch_bounds__(512) conv_weight_sums_kernel(const float* __re
 template <int W, bool SILU>
 __global__ void __launch_bounds__(kThreads) conv_step_kernel(ConvStepArgs a, int blocks) {
   const int b = blockIdx.x / blocks, c = 4 * (blockIdx.x % blocks * kThreads + threadIdx.x);
+  allow_next_kernel();  // (a scan's step, which waits for y before it reads anything that is written here)
   if (c >= a.D) return;
   int slot = a.state_idx ? __ldg(a.state_idx + b) : b;
   if (slot >= a.n_slots) {
