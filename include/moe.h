@@ -212,6 +212,7 @@ int moe_rmsnorm_fwd(const uint16_t* x, const void* residual, const float* weight
  * there was no residual; ldu elements between rows, res_dtype): with rstd of u, g = dy weight, n = u rstd,
  *   du = rstd (g - n mean(g n)) + d_sum;  dw[d] = sum_t dy n   (fp32, nullable)
  * du is the gradient of x and of residual alike: dx receives it in bf16, d_residual in res_dtype (either may be NULL).
+ * Either may take the place of dy, u or d_sum (of its type and row distance), and shares no other memory with them.
  * Deterministic. Workspace (for dw): moe_workspace_size(MOE_OP_RMSNORM_BWD, T, d, ...). */
 int moe_rmsnorm_bwd(const uint16_t* dy, const void* u, const float* weight, const void* d_sum, int T, int d,
                     int ldu, int res_dtype, float eps, uint16_t* dx, void* d_residual, float* dw, void* ws,
@@ -539,7 +540,7 @@ int moe_linattn_step(const uint16_t* q, const uint16_t* k, const uint16_t* v,
  *   p_t[c] = bias[c] + sum_j weight[c][j] x_{t - (W-1) + j}[c];  y = p or p sigmoid(p)
  * x, y bf16 [T][D], ld* elements between tokens; weight fp32 [D][W], bias fp32 [D] (nullable). state_in (bf16
  * [N][W-1][D], nullable: zeros) holds the W - 1 inputs before each sequence, the oldest first; state_out (nullable) receives the
- * last W - 1 of state_in and sequence. The two share no memory. A sequence that ends before it starts or past T, or starts
+ * last W - 1 of state_in and sequence. The two share no memory, and neither do x and y (which may be columns of one buffer). A sequence that ends before it starts or past T, or starts
  * before an earlier bound, sets MOE_FLAG_BAD_INDEX and is skipped. Rows that belong to no sequence keep what they hold. D and ld*
  * are multiples of 8. */
 int moe_conv_fwd(const uint16_t* x, const float* weight, const float* bias, const int32_t* cu_seqlens,
@@ -547,7 +548,7 @@ int moe_conv_fwd(const uint16_t* x, const float* weight, const float* bias, cons
                  uint16_t* state_out, int32_t* err_flag, void* stream);
 
 /* Backward of moe_conv_fwd for dy and d_state_out (bf16 [N][W-1][D], nullable), from the forward's inputs: dx (bf16), dw
- * (fp32 [D][W], nullable), db (fp32 [D], nullable), d_state_in (bf16 [N][W-1][D], nullable; shares no memory with the states given). dw and db
+ * (fp32 [D][W], nullable), db (fp32 [D], nullable), d_state_in (bf16 [N][W-1][D], nullable; shares no memory with the states given, nor dx with x and dy). dw and db
  * are sums over all sequences that were not skipped. Deterministic. Workspace (for dw, db):
  * moe_workspace_size(MOE_OP_CONV_BWD, T, D, W, 0, 0, 0, N). */
 int moe_conv_bwd(const uint16_t* dy, const uint16_t* x, const float* weight, const float* bias, const int32_t* cu_seqlens,
@@ -556,7 +557,7 @@ int moe_conv_bwd(const uint16_t* dy, const uint16_t* x, const float* weight, con
                  int32_t* err_flag, void* stream);
 
 /* One token for each of B rows: y[b] from x[b] and the W - 1 inputs at slot state_idx[b] of the cache state (bf16
- * [n_slots][W-1][D]), which takes x[b] in. Slots as in moe_linattn_step: negative is an empty row (y = 0). */
+ * [n_slots][W-1][D]), which takes x[b] in. Slots as in moe_linattn_step: negative is an empty row (y = 0). y may be x. */
 int moe_conv_step(const uint16_t* x, const float* weight, const float* bias, uint16_t* state, const int32_t* state_idx,
                   int n_slots, int B, int D, int W, int ldx, int ldy, int silu, uint16_t* y, int32_t* err_flag,
                   void* stream);
@@ -572,7 +573,7 @@ int moe_conv_step(const uint16_t* x, const float* weight, const float* bias, uin
  * sequence longer than max_seqlen, or out of place as in moe_conv_fwd, sets MOE_FLAG_BAD_INDEX and is skipped.
  * Everything is fp32: states are within 1e-6 (rms) of their values, y has its own rounding to bf16. Time steps
  * and decays are taken as they come: exp(dt A) that passes fp32 makes infinities. D is a multiple of 8 and D / G of 4; states is 4, 8, 12 or 16; ld* of u, delta, z, y are
- * multiples of 8, of B and C of 4 (8-byte aligned). Workspace:
+ * multiples of 8, of B and C of 4 (8-byte aligned). y shares no memory with what is read. Workspace:
  * moe_workspace_size(MOE_OP_SCAN_FWD, max_seqlen, D, states, G, 0, T, N). */
 int moe_scan_fwd(const uint16_t* u, const uint16_t* delta, const float* A, const uint16_t* B, const uint16_t* C,
                  const float* skip, const uint16_t* z, const float* dt_bias, const int32_t* cu_seqlens,
@@ -586,7 +587,7 @@ int moe_scan_fwd(const uint16_t* u, const uint16_t* delta, const float* A, const
  * that reaches a state from the later tokens and g_t = dy_t silu(z_t):
  *   R_t = X + g_t C_t;  q = R_t exp(dt A) h_{t-1};  dC_t = sum_c g_t h_t;  dB_t = sum_c dt u_t R_t
  *   du_t = dt (R_t . B_t) + skip g_t;  d dt_t = A . q + u_t (R_t . B_t);  dA += dt q;  then X = exp(dt A) R_t
- * Deterministic. Workspace: moe_workspace_size(MOE_OP_SCAN_BWD, max_seqlen, D, states, G, 0, T, N). */
+ * du, ddelta and dz share no memory with what is read. Deterministic. Workspace: moe_workspace_size(MOE_OP_SCAN_BWD, max_seqlen, D, states, G, 0, T, N). */
 int moe_scan_bwd(const uint16_t* dy, const uint16_t* u, const uint16_t* delta, const float* A, const uint16_t* B,
                  const uint16_t* C, const float* skip, const uint16_t* z, const float* dt_bias,
                  const int32_t* cu_seqlens, const float* tile_states, const float* d_state_out, int N, int T,
@@ -596,7 +597,7 @@ int moe_scan_bwd(const uint16_t* dy, const uint16_t* u, const uint16_t* delta, c
                  size_t ws_bytes, int32_t* err_flag, void* stream);
 
 /* One token for each of `rows` rows: updates the state cache (fp32 [n_slots][D][states]) in place at slot
- * state_idx[row] and writes y[row]. Slots as in moe_linattn_step. At most 65,535 groups of 4,194,240 channels. */
+ * state_idx[row] and writes y[row]. Slots as in moe_linattn_step. y may be u, delta or z. */
 int moe_scan_step(const uint16_t* u, const uint16_t* delta, const float* A, const uint16_t* B, const uint16_t* C,
                   const float* skip, const uint16_t* z, const float* dt_bias, float* state, const int32_t* state_idx,
                   int n_slots, int rows, int D, int states, int G, int ldu, int lddelta, int ldB, int ldC, int ldz, int ldy,

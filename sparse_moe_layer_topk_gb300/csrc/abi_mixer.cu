@@ -45,6 +45,24 @@ bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
   return x < y + b_bytes && y < x + a_bytes;
 }
 
+// Whether two [T][width] arrays with ld elements between rows share memory (rows of equal distance may lie between one another).
+struct Rows {
+  const void* p;
+  long long width, ld;
+  int size = 2;  // bytes of a value
+};
+bool meet(const Rows& a, const Rows& b, int T) {
+  if (a.p == nullptr || b.p == nullptr || T <= 0) return false;
+  const auto bytes = [&](const Rows& r) { return static_cast<size_t>((T - 1) * r.ld + r.width) * r.size; };
+  if (!overlap(a.p, bytes(a), b.p, bytes(b))) return false;
+  const long long step = a.ld * a.size;
+  if (T == 1 || step != b.ld * b.size) return true;
+  const long long apart = static_cast<long long>(reinterpret_cast<uintptr_t>(a.p) - reinterpret_cast<uintptr_t>(b.p));
+  const long long at = (apart % step + step) % step;  // where a's rows begin in b's
+  return at < b.width * b.size || at + a.width * a.size > step;
+}
+bool same(const Rows& a, const Rows& b) { return a.p == b.p && a.ld == b.ld && a.width == b.width && a.size == b.size; }
+
 // A [tokens][width] bf16 operand with ld elements between tokens, read `bytes` at a time.
 int check_rows(const void* p, long long width, int ld, int bytes = 16) {
   MOE_REQUIRE(p != nullptr && ld >= width, MOE_ERR_ARG);
@@ -198,6 +216,10 @@ int moe_rmsnorm_bwd(const uint16_t* dy, const void* u, const float* weight, cons
               MOE_ERR_ALIGN);
   MOE_REQUIRE(!dw || (ws && ws_bytes >= moe_workspace_size(MOE_OP_RMSNORM_BWD, T, d, 0, 0, 0, 0, 0)), MOE_ERR_WORKSPACE);
   if (T == 0) return dw ? cuda_status(cudaMemsetAsync(dw, 0, static_cast<size_t>(d) * 4, S(stream))) : MOE_OK;
+  const int res = res_dtype == MOE_DTYPE_F32 ? 4 : 2;
+  for (const Rows& out : {Rows{dx, d, d, 2}, Rows{d_residual, d, d, res}})  // (a row's own input may be written over)
+    for (const Rows& in : {Rows{dy, d, d, 2}, Rows{u, d, ldu, res}, Rows{d_sum, d, d, res}})
+      MOE_REQUIRE(same(out, in) || !meet(out, in, T), MOE_ERR_ARG);
   const NormBwdArgs a{dy, u, weight, d_sum, T, d, ldu, eps, res_dtype == MOE_DTYPE_F32, dx, d_residual, dw,
                       static_cast<float*>(ws)};
   return cuda_status(launch_rmsnorm_bwd(a, S(stream)));
@@ -219,6 +241,7 @@ int moe_conv_fwd(const uint16_t* x, const float* weight, const float* bias, cons
   MOE_REQUIRE(!overlap(state_in, state, state_out, state), MOE_ERR_ARG);
   MOE_REQUIRE(grid_fits(T / 32 + static_cast<long long>(N), D / 512 + 1), MOE_ERR_ARG);
   if (N == 0) return MOE_OK;
+  MOE_REQUIRE(!meet({y, D, ldy}, {x, D, ldx}, T), MOE_ERR_ARG);  // (tokens are read by their neighbours)
   const ConvArgs a{x, weight, bias, cu_seqlens, state_in, N, T, D, W, ldx, ldy, silu != 0, y, state_out, err_flag};
   return cuda_status(launch_conv_fwd(a, S(stream)));
 }
@@ -246,6 +269,7 @@ int moe_conv_bwd(const uint16_t* dy, const uint16_t* x, const float* weight, con
     if (db) MOE_CHECK(cuda_status(cudaMemsetAsync(db, 0, static_cast<size_t>(D) * 4, S(stream))));
     return MOE_OK;
   }
+  MOE_REQUIRE(!meet({dx, D, lddx}, {x, D, ldx}, T) && !meet({dx, D, lddx}, {dy, D, lddy}, T), MOE_ERR_ARG);
   const ConvBwdArgs a{dy, x, weight, bias, cu_seqlens, state_in, d_state_out, N, T, D, W, lddy, ldx, lddx, silu != 0, dx,
                       sums ? static_cast<float*>(ws) : nullptr, d_state_in, err_flag};
   return cuda_status(launch_conv_bwd(a, dw, db, S(stream)));
@@ -262,6 +286,8 @@ int moe_conv_step(const uint16_t* x, const float* weight, const float* bias, uin
   MOE_REQUIRE(aligned(weight, 16) && aligned(bias, 4) && aligned(state, 16), MOE_ERR_ALIGN);
   MOE_REQUIRE(grid_fits(B, D / 512 + 1), MOE_ERR_ARG);
   if (B == 0) return MOE_OK;
+  const Rows from{x, D, ldx}, to{y, D, ldy};
+  MOE_REQUIRE(same(from, to) || !meet(from, to, B), MOE_ERR_ARG);
   const ConvStepArgs a{x, weight, bias, state, state_idx, n_slots, B, D, W, ldx, ldy, silu != 0, y, err_flag};
   return cuda_status(launch_conv_step(a, S(stream)));
 }
@@ -291,6 +317,9 @@ int moe_scan_fwd(const uint16_t* u, const uint16_t* delta, const float* A, const
   if (N == 0) return MOE_OK;
   const size_t need = moe_workspace_size(MOE_OP_SCAN_FWD, max_seqlen, D, states, G, 0, T, N);
   MOE_REQUIRE(need == 0 || (ws && ws_bytes >= need), MOE_ERR_WORKSPACE);
+  const long long per_token = static_cast<long long>(G) * states;
+  for (const Rows& in : {Rows{u, D, ldu}, Rows{delta, D, lddelta}, Rows{z, D, ldz}, Rows{B, per_token, ldB}, Rows{C, per_token, ldC}})
+    MOE_REQUIRE(!meet({y, D, ldy}, in, T), MOE_ERR_ARG);
   const ScanArgs a{u, delta, A, B, C, skip, z, dt_bias, cu_seqlens, state_in, N, T, max_seqlen, D, states, G, ldu, lddelta,
                    ldB, ldC, ldz, ldy, softplus != 0, y, state_out, tile_states, static_cast<float*>(ws), err_flag};
   return cuda_status(launch_scan_fwd(a, S(stream)));
@@ -330,6 +359,10 @@ int moe_scan_bwd(const uint16_t* dy, const uint16_t* u, const uint16_t* delta, c
   }
   const size_t need = moe_workspace_size(MOE_OP_SCAN_BWD, max_seqlen, D, states, G, 0, T, N);
   MOE_REQUIRE(ws && ws_bytes >= need, MOE_ERR_WORKSPACE);
+  const long long per_token = static_cast<long long>(G) * states;
+  for (const Rows& in : {Rows{dy, D, lddy}, Rows{u, D, ldu}, Rows{delta, D, lddelta}, Rows{z, D, ldz}, Rows{B, per_token, ldB}, Rows{C, per_token, ldC}})
+    for (const Rows& out : {Rows{du, D, lddu}, Rows{ddelta, D, ldddelta}, Rows{z ? dz : nullptr, D, lddz}})
+      MOE_REQUIRE(!meet(out, in, T), MOE_ERR_ARG);
   ScanBwdArgs a{};
   a.f = ScanArgs{u, delta, A, B, C, skip, z, dt_bias, cu_seqlens, nullptr, N, T, max_seqlen, D, states, G, ldu, lddelta, ldB,
                  ldC, ldz, 0, softplus != 0, nullptr, nullptr, const_cast<float*>(tile_states), static_cast<float*>(ws), err_flag};
@@ -354,8 +387,13 @@ int moe_scan_step(const uint16_t* u, const uint16_t* delta, const float* A, cons
   if (z) MOE_CHECK(check_rows(z, D, ldz));
   MOE_CHECK(check_rows(y, D, ldy));
   MOE_REQUIRE(aligned(A, 16) && aligned(skip, 4) && aligned(dt_bias, 4) && aligned(state, 16), MOE_ERR_ALIGN);
-  MOE_REQUIRE(G <= 65535 && D / G <= 64 * 65535, MOE_ERR_ARG);
+  MOE_REQUIRE(grid_fits(rows / 4 + 1ll, G), MOE_ERR_ARG);
   if (rows == 0) return MOE_OK;
+  const Rows to{y, D, ldy};
+  for (const Rows& in : {Rows{u, D, ldu}, Rows{delta, D, lddelta}, Rows{z, D, ldz}})  // (read by the lane that writes there)
+    MOE_REQUIRE(same(to, in) || !meet(to, in, rows), MOE_ERR_ARG);
+  const long long per_token = static_cast<long long>(G) * states;
+  MOE_REQUIRE(!meet(to, {B, per_token, ldB}, rows) && !meet(to, {C, per_token, ldC}, rows), MOE_ERR_ARG);
   const ScanStepArgs a{u, delta, A, B, C, skip, z, dt_bias, state, state_idx, n_slots, rows, D, states, G, ldu, lddelta, ldB,
                        ldC, ldz, ldy, softplus != 0, y, err_flag};
   return cuda_status(launch_scan_step(a, S(stream)));

@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS, THREADS <= 128 
   // (a row ahead where the registers allow it: 64 a thread at 1,024 threads do not)
   constexpr bool kAhead = THREADS * (sizeof(R) == 4 ? 2 : 1) <= 512;
   const int tid = threadIdx.x % THREADS, vectors = d / 8;
-  const int first = blockIdx.x * kRows + (THREADS == 32 ? threadIdx.x >> 5 : 0), stride = gridDim.x * kRows;
+  const unsigned first = blockIdx.x * kRows + (THREADS == 32 ? threadIdx.x >> 5 : 0), stride = gridDim.x * kRows, rows = T;
   float w[kBwdVec][8], dw[kBwdVec][8];
 #pragma unroll
   for (int i = 0; i < kBwdVec; ++i) {
@@ -225,12 +225,12 @@ __global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS, THREADS <= 128 
   Raw8<U> nu[kBwdVec];
   Raw8<bf16> ng[kBwdVec];
   Raw8<R> ns[kBwdVec];
-  const auto fetch = [&](int t) {
+  const auto fetch = [&](unsigned t) {
 #pragma unroll
     for (int i = 0; i < kBwdVec; ++i) {
       const int c = tid + i * THREADS;
       nu[i].clear(), ng[i].clear(), ns[i].clear();
-      if (t < T && c < vectors) {
+      if (t < rows && c < vectors) {
         nu[i].load(from + t * ldu + 8 * c);
         ng[i].load(dy + static_cast<long long>(t) * d + 8 * c);
         if (d_sum != nullptr) ns[i].load(d_sum + static_cast<long long>(t) * d + 8 * c);
@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS, THREADS <= 128 
   };
   if (kAhead) fetch(first);
   int turn = 0;
-  for (int t = first; t < T; t += stride) {
+  for (unsigned t = first; t < rows; t += stride) {
     const long long at = static_cast<long long>(t) * d;
     float u[kBwdVec][8], g[kBwdVec][8];
     Raw8<R> s[kBwdVec];
@@ -320,14 +320,14 @@ __global__ void __launch_bounds__(1024) column_sums_kernel(const float* __restri
 // Rows of partial weight gradients that a backward writes.
 int rmsnorm_bwd_parts(int T, int d) {
   const int th = bwd_threads(d), rows = th == 32 ? 4 : 1;
-  const int ctas = (T + rows - 1) / rows, most = num_sms() * (th <= 128 ? 4 : th == 256 ? 2 : 1);
+  const int ctas = T / rows + (T % rows != 0), most = num_sms() * (th <= 128 ? 4 : th == 256 ? 2 : 1);
   return (ctas < most ? ctas : most) * rows;
 }
 
 template <int THREADS, int VEC, typename R>
 static void norm_fwd(const NormArgs& a, cudaStream_t st) {
   const int rows = THREADS == 32 ? 4 : 1, threads = THREADS == 32 ? 128 : THREADS;
-  const unsigned grid = static_cast<unsigned>((a.T + rows - 1) / rows);
+  const unsigned grid = (static_cast<unsigned>(a.T) + rows - 1) / rows;
   const auto run = [&](auto kernel) {
     kernel<<<grid, threads, 0, st>>>(static_cast<const bf16*>(a.x), static_cast<const R*>(a.residual), a.weight, a.T, a.d,
                                      a.ldx, a.eps, static_cast<R*>(a.sum), a.y, a.y_scale, a.block);

@@ -210,7 +210,7 @@ template <int NPL, bool VEC, bool SOFTMAX, bool GROUPED>
 __global__ void __launch_bounds__(kWarps * 32) route_scores_kernel(Params p) {
   extern __shared__ float pool[];
   __shared__ unsigned long long cand_s[kWarps][32];
-  const int t = (blockIdx.x * kWarps * 32 + threadIdx.x) >> 5;
+  const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
   const int lane = static_cast<int>(lane_id()), wib = threadIdx.x >> 5;
   if (t >= p.T) return;
   const int E = p.E, k = p.k;
@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_scores_kernel(Params p) {
 // The row is written whole by all lanes, then the chosen entries over it by theirs.
 template <bool DENSE, bool SOFTMAX, typename OUT>
 __global__ void __launch_bounds__(256) route_scores_bwd_kernel(RouteBwdArgs a) {
-  const int t = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  const int t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (t >= a.T) return;
   const size_t o = static_cast<size_t>(t) * a.k + lane;
@@ -620,7 +620,7 @@ __global__ void __launch_bounds__(256) route_scores_bwd_kernel(RouteBwdArgs a) {
 
 template <int NPL, bool VEC, bool SOFTMAX>
 cudaError_t route_launch(const Params& p, cudaStream_t st) {
-  const unsigned grid = static_cast<unsigned>((p.T + kWarps - 1) / kWarps);
+  const unsigned grid = (static_cast<unsigned>(p.T) + kWarps - 1) / kWarps;
   if (p.groups > 1 && p.group_k < p.groups)
     route_scores_kernel<NPL, VEC, SOFTMAX, true><<<grid, kWarps * 32, static_cast<size_t>(kWarps) * p.E * 4, st>>>(p);
   else
@@ -650,7 +650,7 @@ cudaError_t launch_route_scores(const RouteArgs& a, cudaStream_t st) {
 
 cudaError_t launch_route_scores_bwd(const RouteBwdArgs& a, cudaStream_t st) {
   LaunchTimer lt("route_scores_bwd", st);
-  const unsigned grid = static_cast<unsigned>((a.T + 7) / 8);
+  const unsigned grid = (static_cast<unsigned>(a.T) + 7) / 8;
   const bool dense = a.softmax && !a.renorm;
   const auto run = [&](auto f32, auto b16) {
     if (a.bf16_out) b16<<<grid, 256, 0, st>>>(a);

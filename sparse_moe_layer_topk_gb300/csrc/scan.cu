@@ -930,8 +930,9 @@ constexpr int kStepWarps = 8;
 __global__ void __launch_bounds__(kStepWarps * 32) scan_step_kernel(ScanStepArgs a, int per) {
   constexpr int kRows = 4;
   const int lane = static_cast<int>(lane_id()), q = lane & 3;
-  // grid: rows, a group's channels (`per` of them), groups
-  const int group = blockIdx.z, at = blockIdx.y * 8 * kStepWarps + static_cast<int>(threadIdx.x >> 2), c = group * per + at, b0 = blockIdx.x * kRows;
+  // grid: rows x groups, a group's channels (`per` of them); a division only where there are groups
+  const int part = a.G > 1 ? blockIdx.x / a.G : blockIdx.x, group = blockIdx.x - part * a.G;
+  const int at = blockIdx.y * 8 * kStepWarps + static_cast<int>(threadIdx.x >> 2), c = group * per + at, b0 = part * kRows;
   const bool in = at < per, real = in && 4 * q < a.S;
   wait_for_last_kernel();
   float4 A = make_float4(0, 0, 0, 0);
@@ -1136,7 +1137,7 @@ cudaError_t launch_scan_bwd(const ScanBwdArgs& a, cudaStream_t st) {
 cudaError_t launch_scan_step(const ScanStepArgs& a, cudaStream_t st) {
   LaunchTimer lt("scan_step", st);
   const int per = a.D / a.G;
-  const dim3 grid((static_cast<unsigned>(a.B_rows) + 3) / 4, (per + 8 * kStepWarps - 1) / (8 * kStepWarps), a.G);
+  const dim3 grid((static_cast<unsigned>(a.B_rows) + 3) / 4 * a.G, (per + 8 * kStepWarps - 1) / (8 * kStepWarps));
   return launch_behind(scan_step_kernel, grid, kStepWarps * 32, 0, st, a, per);
 }
 

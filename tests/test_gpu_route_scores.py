@@ -219,3 +219,18 @@ def test_logits_at_both_ends_of_the_range(score, groups, group_k):
     b = torch.full((256,), 0.25)
     b[1::3] += 2.0 ** -24
     _check(l, b, 12, score, groups=groups, group_k=group_k)
+
+
+def test_more_tokens_than_lanes_number_in_32_bits():
+    T = 2 ** 27 + 9  # (x 32 lanes is more than 2^32)
+    logits = torch.zeros(T, 2, device="cuda")
+    logits[::3, 1] = 1.0
+    r = _router(T, 2, 1, renorm=False, grad_dtype=torch.bfloat16)
+    idx, w = r.forward(logits)
+    assert torch.equal(idx[:, 0].long(), logits.argmax(1))
+    one = 1 / (1 + np.exp(-1.0))
+    assert float((w[::3] - one).abs().max()) < 1e-6 and float((w[1::3] - 0.5).abs().max()) < 1e-6
+    d = r.backward(torch.ones_like(w))
+    # d sigmoid: 0.25 at 0, 0.1966 at 1, rounded to 8 bits
+    assert bool((d[1::3, 0] == 0.25).all()) and float((d[::3, 1].float() - one * (1 - one)).abs().max()) < 2.0 ** -11
+    assert not d[1::3, 1].any() and not d[::3, 0].any()

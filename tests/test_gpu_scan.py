@@ -438,3 +438,22 @@ def test_in_a_graph_and_on_another_stream():
         assert torch.equal(getattr(s, name), getattr(s2, name)), name
     for name in ("y", "dx", "dw", "db", "state_out", "d_state_in"):
         assert torch.equal(getattr(c, name), getattr(c2, name)), name
+
+
+@pytest.mark.parametrize("at", [0, 64, 128])
+def test_results_between_the_rows_that_are_read(at):
+    """Inputs and outputs that are columns of one wide buffer share none of them."""
+    from sparse_moe_layer_topk_gb300 import _lib as M
+    T, D, W, wide = 70, 64, 4, 256
+    gen = torch.Generator().manual_seed(at)
+    buf = torch.randn(T, wide, generator=gen).to(torch.bfloat16).cuda()
+    w = torch.randn(D, W, generator=gen).cuda()
+    keep = buf.clone()
+    x, y = buf[:, 192:], buf[:, at:at + D]
+    want = torch.empty(T, D, dtype=torch.bfloat16, device="cuda")
+    call = lambda x, y, ldy: M.moe_conv_fwd(x, w, None, None, None, 1, T, D, W, wide, ldy, True, y, None, None)  # noqa: E731
+    call(x, want, D)
+    call(x, y, wide)
+    assert torch.equal(y, want)
+    keep[:, at:at + D] = want
+    assert torch.equal(buf, keep)

@@ -96,6 +96,41 @@ CASES = {
 }
 
 
+APART = {  # arguments that no two of share memory
+    "moe_rmsnorm_bwd": {**NORM_BWD, **_far("dy", "u", "weight", "d_sum", "dx", "d_residual", "dw", "ws")},
+    "moe_conv_fwd": {**CONV, **_far("x", "weight", "y")},
+    "moe_conv_bwd": {**CONV_BWD, **_far("dy", "x", "weight", "dx", "ws")},
+    "moe_conv_step": {**CONV_STEP, **_far("x", "weight", "state", "y")},
+    "moe_scan_fwd": {**SCAN, **_far("u", "delta", "B", "C", "z", "y", "ws")},
+    "moe_scan_bwd": {**SCAN_BWD, **_far("dy", "u", "delta", "B", "C", "z", "du", "ddelta", "dz", "ws")},
+    "moe_scan_step": {**SCAN_STEP, **_far("u", "delta", "B", "C", "z", "y")},
+}
+ROW = 64 * 2  # bytes of a row of the sizes above
+
+
+@pytest.mark.parametrize("name,out,others", [
+    ("moe_rmsnorm_bwd", "dx", ["dy", "u", "d_sum"]), ("moe_rmsnorm_bwd", "d_residual", ["dy", "u", "d_sum"]), ("moe_conv_fwd", "y", ["x"]),
+    ("moe_conv_bwd", "dx", ["dy", "x"]), ("moe_conv_step", "y", ["x"]), ("moe_scan_fwd", "y", ["u", "delta", "z", "B", "C"]),
+    ("moe_scan_bwd", "du", ["dy", "u", "delta", "z", "B", "C"]), ("moe_scan_bwd", "ddelta", ["dy", "u", "delta", "z", "B", "C"]),
+    ("moe_scan_bwd", "dz", ["dy", "u", "delta", "z", "B", "C"]), ("moe_scan_step", "y", ["u", "delta", "z", "B", "C"])], ids=str)
+def test_results_over_what_is_read(lib, name, out, others):
+    """A result that begins inside what other rows are still read from, at either end."""
+    base = APART[name]
+    for other in others:
+        for shift in (ROW // 2, -ROW // 2, ROW):
+            assert getattr(lib, name)(*{**base, out: base[other] + shift}.values()) == ARG, (other, shift)
+    if name in ("moe_conv_fwd", "moe_conv_bwd", "moe_scan_fwd", "moe_scan_bwd"):  # neighbours' rows are read: not in place either
+        assert getattr(lib, name)(*{**base, out: base[others[0]]}.values()) == ARG
+
+
+def test_results_among_the_columns_that_are_read(lib):
+    """Columns of one wide buffer of which some are both read and written."""
+    base = {**APART["moe_conv_fwd"], "ldx": 192, "ldy": 192}
+    at = base["x"]
+    for columns in (32, 136, -32, -184):  # a part of y's columns lies in x's
+        assert lib.moe_conv_fwd(*{**base, "y": at + 2 * columns}.values()) == ARG
+
+
 @pytest.mark.parametrize("name,change,want", [(n, c, w) for n, (_, rows) in CASES.items() for c, w in rows], ids=str)
 def test_refusals(lib, name, change, want):
     base = CASES[name][0]
