@@ -9,7 +9,7 @@ namespace moe {
 namespace {
 
 constexpr unsigned kAll = 0xFFFFFFFFu;
-constexpr int kWarps = 8;      // tokens of a CTA, one for each warp
+constexpr int kWarps = 4;      // tokens of a CTA, one for each warp
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float exp2_quick(float x) {
@@ -191,7 +191,9 @@ __device__ __noinline__ bool group_value_exactly(const Params& p, const float* r
   return close <= 2 || p.group_top == 1;
 }
 
-// One warp routes one token; the logits are read once and HBM bounds it.
+// One warp routes one token; the logits are read once. Instructions bound it, and what their order leaves idle at the 16 to 20 warps an SM that
+// the row's registers allow: 16,384 tokens x 896 experts, 16 chosen, take 35 us from the logits alone, 43 with a bias, 54 in 8 groups, where the
+// bytes would take 9. (Three CTAs of eight warps: 36, 45 and 61.)
 //
 // The values that choose (score + bias, or the logits themselves without a bias) are held as order-preserving bits,
 // NPL a lane, runs of four (VEC) or single ones spread over all lanes. Groups: the values pass through shared memory to lanes that lie
@@ -207,7 +209,7 @@ __device__ __noinline__ bool group_value_exactly(const Params& p, const float* r
 // and where that is not enough either the token starts over in 64 bits: 15 us.) Two experts with the same logit and bias are
 // equal in any precision and go by their index.
 template <int NPL, bool VEC, bool SOFTMAX, bool GROUPED>
-__global__ void __launch_bounds__(kWarps * 32) route_scores_kernel(Params p) {
+__global__ void __launch_bounds__(kWarps * 32, NPL < 28 ? 1 : GROUPED ? 4 : 5) route_scores_kernel(Params p) {
   extern __shared__ float pool[];
   __shared__ unsigned long long cand_s[kWarps][32];
   const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
@@ -219,27 +221,45 @@ __global__ void __launch_bounds__(kWarps * 32) route_scores_kernel(Params p) {
   const auto expert_of = [&](int i) { return VEC ? 128 * (i >> 2) + 4 * lane + (i & 3) : lane + 32 * i; };
   const auto here = [&](int i) { return VEC ? 128 * (i >> 2) + 4 * lane < E : lane + 32 * i < E; };
 
+  const auto spread = [&](const float* from, float (&to)[NPL]) {  // a row over the lanes, 0 where there is nothing
+    if (VEC) {
+#pragma unroll
+      for (int i = 0; i < NPL / 4; ++i) {
+        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (here(4 * i)) x = __ldg(reinterpret_cast<const float4*>(from) + 32 * i + lane);
+        to[4 * i] = x.x, to[4 * i + 1] = x.y, to[4 * i + 2] = x.z, to[4 * i + 3] = x.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) to[i] = here(i) ? __ldg(from + expert_of(i)) : 0.0f;
+    }
+  };
+  const auto any_odd = [&](const float (&x)[NPL]) {  // an infinity or NaN in the row: only then is it looked at value by value
+    uint32_t most = 0u;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) most = max(most, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+    return __any_sync(kAll, most >= 0x7F800000u) != 0;
+  };
+
   float v[NPL];  // logits, then the values that choose
-  if (VEC) {
+  spread(row, v);
+  bool bad = false, odd = any_odd(v);
+  if (odd) {
 #pragma unroll
-    for (int i = 0; i < NPL / 4; ++i) {
-      float4 x = make_float4(neg_inf(), neg_inf(), neg_inf(), neg_inf());
-      if (here(4 * i)) x = __ldg(reinterpret_cast<const float4*>(row) + 32 * i + lane);
-      v[4 * i] = x.x, v[4 * i + 1] = x.y, v[4 * i + 2] = x.z, v[4 * i + 3] = x.w;
+    for (int i = 0; i < NPL; ++i) {
+      if (!(v[i] < -neg_inf())) {  // NaN and infinity: flagged, and as if masked
+        bad = true;
+        v[i] = neg_inf();
+      }
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) v[i] = here(i) ? __ldg(row + expert_of(i)) : neg_inf();
   }
-  bool bad = false;
   float top = neg_inf();
+  if (SOFTMAX) {
 #pragma unroll
-  for (int i = 0; i < NPL; ++i) {
-    if (!(v[i] < -neg_inf())) {  // NaN and infinity: flagged, and as if masked
-      bad = true;
-      v[i] = neg_inf();
+    for (int i = 0; i < NPL; ++i) {
+      if (!here(i)) v[i] = neg_inf();
+      top = fmaxf(top, v[i]);
     }
-    if (SOFTMAX) top = fmaxf(top, v[i]);
   }
   float inv = 1.0f;
   if (SOFTMAX) {
@@ -258,27 +278,23 @@ __global__ void __launch_bounds__(kWarps * 32) route_scores_kernel(Params p) {
   };
   uint32_t kv[NPL];  // 0: no expert of this lane
   if (!by_logit) {
+    float b[NPL];
+    spread(p.bias, b);
+    if (any_odd(b)) odd = true;
+    if (odd) {
 #pragma unroll
-    for (int i = 0; i < NPL; i += VEC ? 4 : 1) {
-      float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      if (here(i)) {
-        if (VEC) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) b[j] = __ldg(p.bias + expert_of(i) + j);
-        } else {
-          b[0] = __ldg(p.bias + expert_of(i));
-        }
+      for (int i = 0; i < NPL; ++i) {
+        bad |= !(b[i] < -neg_inf());
+        v[i] = v[i] > neg_inf() && b[i] < -neg_inf() ? quick_score(v[i]) + b[i] : neg_inf();
       }
+    } else {
 #pragma unroll
-      for (int j = 0; j < (VEC ? 4 : 1); ++j) {
-        bad |= !(b[j] < -neg_inf());
-        v[i + j] = v[i + j] > neg_inf() && b[j] < -neg_inf() ? quick_score(v[i + j]) + b[j] : neg_inf();
-      }
+      for (int i = 0; i < NPL; ++i) v[i] = quick_score(v[i]) + b[i];
     }
   }
 #pragma unroll
   for (int i = 0; i < NPL; ++i) kv[i] = here(i) ? order_bits(v[i]) : 0u;
-  if (__any_sync(kAll, bad) && lane == 0) set_flag(p.err_flag, MOE_FLAG_NONFINITE);
+  if (odd && __any_sync(kAll, bad) && lane == 0) set_flag(p.err_flag, MOE_FLAG_NONFINITE);
 
   bool exact = false;  // whether the token starts over in 64 bits
   if (GROUPED) {
@@ -322,26 +338,24 @@ __global__ void __launch_bounds__(kWarps * 32) route_scores_kernel(Params p) {
     } else if (sums && t2 > neg_inf()) {
       value = t1 + t2;
     }
-    // (scores are at most 1, with softmax at most the row's largest, and off by 2^-22 of that for every 2 of |l|: 2^-19 for two of them)
-    const float slack = sums || !by_logit ? 0x1p-19f * (SOFTMAX ? fminf(1.0f, inv) : 1.0f) : 0.0f;
     int rank = 0;
-    unsigned near = 0;  // groups whose value is too close to this one's to tell apart
     for (int q = 0; q < p.groups; ++q) {
       const float x = __shfl_sync(kAll, value, q * lanes);
       rank += x > value || (x == value && q < group);
-      // (values of empty groups give NaN or infinity here: not near)
-      if (slack > 0.0f && fabsf(x - value) <= slack + 0x1p-21f * (fabsf(x) + fabsf(value)) && fabsf(x) < -neg_inf()) near |= 1u << q;
     }
-    const unsigned all = p.groups < 32 ? (1u << p.groups) - 1u : kAll;
-    bool keep = group < p.groups && rank < p.group_k;
-    const auto by_group = [&](bool flag) {  // a flag of each group's lanes, as bits by group
-      const unsigned x = __ballot_sync(kAll, flag);
-      unsigned r = 0;
-      for (int q = 0; q < p.groups; ++q) r |= (x >> (q * lanes) & 1u) << q;
-      return r;
-    };
-    unsigned kept = by_group(keep);
-    if (__any_sync(kAll, group < p.groups && (near & (keep ? all & ~kept : kept)))) {
+    const bool some = group < p.groups;
+    bool keep = some && rank < p.group_k;
+    unsigned kept = __ballot_sync(kAll, keep);  // a group's bit is that of its first lane
+    // (scores are at most 1, with softmax at most the row's largest, and off by 2^-22 of that for every 2 of |l|: 2^-19 for two of them)
+    const float slack = sums || !by_logit ? 0x1p-19f * (SOFTMAX ? fminf(1.0f, inv) : 1.0f) : 0.0f;
+    // The last group that stays and the first that goes: too close to tell apart? (Where one is all masked they are not, and where none
+    // goes `next` is NaN.)
+    const uint32_t bits = order_bits(value);
+    const float least = bits_value(__reduce_min_sync(kAll, keep ? bits : 0xFFFFFFFFu));
+    const float next = bits_value(__reduce_max_sync(kAll, some && !keep ? bits : 0u));
+    // (sums of two biases may pass fp32)
+    const bool close = least - next <= slack + 0x1p-21f * (fabsf(least) + fabsf(next)) || least == -neg_inf();
+    if (slack > 0.0f && close && least > neg_inf() && next > neg_inf()) {
       double value64, scores;
       const float* const row_v = by_logit ? row : row_c;  // (where t1 and t2 were found)
       const bool sure = group_value_exactly<SOFTMAX>(p, row, row_v, size, lanes, group, sub, t1, t2, by_logit ? fabsf(t2) * 0x1p-20f + 0x1p-20f : slack,
@@ -353,16 +367,16 @@ __global__ void __launch_bounds__(kWarps * 32) route_scores_kernel(Params p) {
         rank64 += x > value64 || (x == value64 && q < group);
         if (SOFTMAX && q != group && x > -1e300 && fabs(x - value64) <= 0x1p-20 * fabs(xs - scores) + 0x1p-45 * fabs(xs)) open = true;
       }
-      exact = __any_sync(kAll, open && group < p.groups);
-      keep = group < p.groups && rank64 < p.group_k;
-      kept = by_group(keep);
+      exact = __any_sync(kAll, open && some);
+      keep = some && rank64 < p.group_k;
+      kept = __ballot_sync(kAll, keep);
     }
     const float per = 1.0f / static_cast<float>(size);
 #pragma unroll
     for (int i = 0; i < NPL; i += VEC ? 4 : 1) {  // (x + 1/2) / size is at least 2^-11 from a whole number, and x < 2^10: the cut is right
-      const bool stays = kept >> static_cast<int>((static_cast<float>(expert_of(i)) + 0.5f) * per) & 1u;
+      const bool stays = here(i) && (kept >> (static_cast<int>((static_cast<float>(expert_of(i)) + 0.5f) * per) * lanes) & 1u);
 #pragma unroll
-      for (int j = 0; j < (VEC ? 4 : 1); ++j) kv[i + j] = stays && here(i) ? kv[i + j] : 0u;
+      for (int j = 0; j < (VEC ? 4 : 1); ++j) kv[i + j] = stays ? kv[i + j] : 0u;
     }
   }
   const auto key_of = [&](int i) {
@@ -643,7 +657,7 @@ cudaError_t route_pick(const Params& p, cudaStream_t st) {
 cudaError_t launch_route_scores(const RouteArgs& a, cudaStream_t st) {
   LaunchTimer lt("route_scores", st);
   const Params p{a.logits, a.bias, a.T, a.E, a.k, a.groups, a.group_k, a.group_top, a.renorm, a.scale, a.idx, a.w, a.s, a.err_flag};
-  const bool vec = a.E / a.groups % 4 == 0 && (reinterpret_cast<uintptr_t>(a.logits) & 15u) == 0;
+  const bool vec = a.E / a.groups % 4 == 0 && ((reinterpret_cast<uintptr_t>(a.logits) | reinterpret_cast<uintptr_t>(a.bias)) & 15u) == 0;
   if (a.softmax) return vec ? route_pick<true, true>(p, st) : route_pick<false, true>(p, st);
   return vec ? route_pick<true, false>(p, st) : route_pick<false, false>(p, st);
 }

@@ -234,3 +234,20 @@ def test_more_tokens_than_lanes_number_in_32_bits():
     # d sigmoid: 0.25 at 0, 0.1966 at 1, rounded to 8 bits
     assert bool((d[1::3, 0] == 0.25).all()) and float((d[::3, 1].float() - one * (1 - one)).abs().max()) < 2.0 ** -11
     assert not d[1::3, 1].any() and not d[::3, 0].any()
+
+
+@pytest.mark.parametrize("groups,group_k", [(1, 1), (8, 4)])
+def test_logits_and_biases_that_start_anywhere(groups, group_k):
+    """Rows and biases of a multiple of four values that begin on four bytes."""
+    logits, bias = _logits(9, 256, 5), _bias(256, 5)
+    for at_l, at_b in ((0, 1), (1, 0), (3, 2)):
+        l, b = torch.zeros(9 * 256 + at_l, device="cuda"), torch.zeros(256 + at_b, device="cuda")
+        l, b = l[at_l:].view(9, 256).copy_(logits), b[at_b:].copy_(bias)
+        _check(l, b, 8, groups=groups, group_k=group_k)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_biases_whose_sums_pass_32_bits(score):
+    """Groups whose two largest values add up to more than the largest float."""
+    b = torch.cat([torch.full((16,), v) for v in (2.0e38, 2.5e38, -3e38, 2.25e38)])
+    _check(_logits(6, 64, 8), b, 6, score, groups=4, group_k=2)
