@@ -21,7 +21,8 @@ namespace {
 
 constexpr int kThreads = 128;       // 512 channels
 constexpr int kFwdTokens = 64;      // tokens of a part
-constexpr int kBwdTokens = 64;
+constexpr int kBwdRing = 4;         // groups of tokens that the backward holds or has on their way
+constexpr int kBwdCtas = 4;         // an SM
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Four channels.
@@ -58,6 +59,11 @@ __device__ __forceinline__ f32x2 sigmoid2(f32x2 x) {
   return pack2(rcp(a), rcp(b));
 }
 __device__ __forceinline__ F4 sigmoid4(const F4& x) { return F4{sigmoid2(x.a), sigmoid2(x.b)}; }
+
+// An asynchronous copy of 8 bytes; `real` false: nothing is read and zeros are written.
+__device__ __forceinline__ void copy8(uint32_t to, const void* from, bool real) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(from), "r"(real ? 8 : 0) : "memory");
+}
 
 // The weights of four channels from [D][W], 4 W values one behind the other.
 template <int W>
@@ -141,12 +147,15 @@ __global__ void __launch_bounds__(kThreads, 5) conv_fwd_kernel(ConvArgs a, int b
 
 // With dp_t = dy_t silu'(p_t), p recomputed: dx_t = sum_i w[W-1-i] dp_{t+i}, dw[j] = sum_t dp_t x_{t-(W-1)+j}. A part reads W - 1
 // tokens on either side for p and dp. A CTA takes every walkers-th part, so its sums of dw and dbias stay in
-// registers; they are joined in a fixed order afterwards. Latency bounds it: 40 registers of weights and sums and the two windows leave
-// room for 16 warps an SM, and two instructions issue a cycle. 16,384 tokens x 8,192 channels in 184 us, 119 of them the bytes;
-// a group of 2 tokens instead of 4 takes 226, of 8 217; three CTAs an SM 255, five spill (400).
+// registers; they are joined in a fixed order afterwards. Tokens come by asynchronous copies three groups ahead, which a thread makes and
+// waits for by itself: in registers there is room for one group, and it waits for memory. 40 registers of weights and sums and the two
+// windows leave 16 warps an SM, whose arithmetic bounds it: 16,384 tokens x 8,192 channels in 149 us, 119 of them the bytes (with one group ahead in
+// registers 184; groups of 2 tokens instead of 4: 166, of 6: 153; three CTAs an SM: 165, five spill: 190 and more).
 template <int W, bool SILU>
-__global__ void __launch_bounds__(kThreads, 4) conv_bwd_kernel(ConvBwdArgs a, int blocks) {
+__global__ void __launch_bounds__(kThreads, kBwdCtas) conv_bwd_kernel(ConvBwdArgs a, int blocks, int length) {
   constexpr int kStep = 4;
+  __shared__ uint2 ring[kBwdRing][kStep][2][kThreads];  // (x, dy) of a thread's channels, its own to write and to read
+  const uint32_t to_ring = smem_u32(&ring[0][0][0][threadIdx.x]);
   const int block = blockIdx.x % blocks, walker = blockIdx.x / blocks, walkers = gridDim.x / blocks;
   const int c = 4 * (block * kThreads + threadIdx.x);
   const bool mine = c < a.D;
@@ -163,35 +172,46 @@ __global__ void __launch_bounds__(kThreads, 4) conv_bwd_kernel(ConvBwdArgs a, in
   }
   SeqPart s;
   for (int part = walker;
-       find_part(a.cu, a.N, a.T, a.T, kBwdTokens, part, s, block == 0 && threadIdx.x < 32 ? a.err_flag : nullptr);
+       find_part(a.cu, a.N, a.T, a.T, length, part, s, block == 0 && threadIdx.x < 32 ? a.err_flag : nullptr);
        part += walkers) {
     if (!mine) continue;
-    const int t0 = s.part * kBwdTokens, t1 = min(s.len, t0 + kBwdTokens);
+    const int t0 = s.part * length, t1 = min(s.len, t0 + length);
     const int end = min(s.len, t1 + W - 1);  // dp is needed up to there
     const int first = s.part == 0 && d_in ? -(W - 1) : t0;  // the first dx of this part
     const bf16* fx = x + static_cast<long long>(s.start + t0) * a.ldx + c;
     const bf16* fg = static_cast<const bf16*>(a.dy) + static_cast<long long>(s.start + t0) * a.lddy + c;
     bf16* to = static_cast<bf16*>(a.dx) + static_cast<long long>(s.start + t0 - (W - 1)) * a.lddx + c;
-    uint2 nx[kStep], ng[kStep];  // the next tokens, each read anew as soon as it is taken
-    const auto fetch = [&](int q, bool some) {
-      nx[q] = ng[q] = make_uint2(0, 0);  // (zero past the sequence's end)
-      if (some) nx[q] = load4(fx + q * a.ldx), ng[q] = load4(fg + q * a.lddy);
+    int ahead = t0, slot = 0;  // of the next group of tokens to be fetched
+    const auto fetch = [&] {
+#pragma unroll
+      for (int q = 0; q < kStep; ++q) {
+        const bool some = ahead + q < end;  // (zeros past the sequence's end)
+        const uint32_t to = to_ring + slot * (kStep * 2 * kThreads * 8) + q * (2 * kThreads * 8);
+        copy8(to, some ? fx + q * a.ldx : fx, some);
+        copy8(to + kThreads * 8, some ? fg + q * a.lddy : fg, some);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      if (ahead + kStep < end) fx += kStep * a.ldx, fg += kStep * a.lddy;  // (never past what there is)
+      ahead += kStep, slot = (slot + 1) % kBwdRing;
     };
 #pragma unroll
-    for (int q = 0; q < kStep; ++q) fetch(q, t0 + q < end);
+    for (int g = 0; g + 1 < kBwdRing; ++g) fetch();
+    int now = 0;  // the group in hand
     F4 in[W], dp[W];  // the newest last
 #pragma unroll
     for (int j = 0; j + 1 < W; ++j) in[j] = widen(input_at<W>(x, a.ldx, state, a.D, s, t0 - (W - 1) + j, c)), dp[j] = zero4();
     // token t gives dx of t - (W - 1); a first part's first W - 1 are the state's
     const auto group = [&](int t, auto inside) {
-      fx += kStep * a.ldx, fg += kStep * a.lddy;
+      asm volatile("cp.async.wait_group %0;" ::"n"(kBwdRing - 2) : "memory");
+      const uint2(*const own)[2][kThreads] = ring[now];
+      now = (now + 1) % kBwdRing;
+      fetch();  // into the place of the group before this one
 #pragma unroll
       for (int q = 0; q < kStep; ++q) {
         const int at = t + q;
-        in[W - 1] = widen(nx[q]);
+        in[W - 1] = widen(own[q][0][threadIdx.x]);
         F4& d = dp[W - 1];
-        d = widen(ng[q]);
-        fetch(q, at + kStep < end);
+        d = widen(own[q][1][threadIdx.x]);
         if (SILU) {
           F4 p = bias;
 #pragma unroll
@@ -225,6 +245,7 @@ __global__ void __launch_bounds__(kThreads, 4) conv_bwd_kernel(ConvBwdArgs a, in
       if (t - (W - 1) >= t0 && t + kStep <= t1) group(t, std::true_type{});
       else group(t, std::false_type{});
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
   }
   allow_next_kernel();
   if (!mine || a.part == nullptr) return;
@@ -308,11 +329,12 @@ int channel_blocks(int D) { return (D / 4 + kThreads - 1) / kThreads; }
 // Parts of `length` tokens that N sequences of T tokens can have at most.
 int most_parts(int N, int T, int length) { return T / length + N; }
 
-#define MOE_CONV_DISPATCH(KERNEL, GRID)                                                   \
-  do {                                                                                     \
-    if (a.W == 2) { if (a.silu) KERNEL<2, true><<<(GRID) * blocks, kThreads, 0, st>>>(a, blocks); else KERNEL<2, false><<<(GRID) * blocks, kThreads, 0, st>>>(a, blocks); } \
-    else if (a.W == 3) { if (a.silu) KERNEL<3, true><<<(GRID) * blocks, kThreads, 0, st>>>(a, blocks); else KERNEL<3, false><<<(GRID) * blocks, kThreads, 0, st>>>(a, blocks); } \
-    else { if (a.silu) KERNEL<4, true><<<(GRID) * blocks, kThreads, 0, st>>>(a, blocks); else KERNEL<4, false><<<(GRID) * blocks, kThreads, 0, st>>>(a, blocks); } \
+#define MOE_CONV_DISPATCH(KERNEL, GRID, ...)                                                   \
+  do {                                                                                          \
+    const auto run = [&](auto kernel) { kernel<<<(GRID) * blocks, kThreads, 0, st>>>(__VA_ARGS__); }; \
+    if (a.W == 2) a.silu ? run(KERNEL<2, true>) : run(KERNEL<2, false>);                        \
+    else if (a.W == 3) a.silu ? run(KERNEL<3, true>) : run(KERNEL<3, false>);                   \
+    else a.silu ? run(KERNEL<4, true>) : run(KERNEL<4, false>);                                 \
   } while (0)
 
 }  // namespace
@@ -320,22 +342,38 @@ int most_parts(int N, int T, int length) { return T / length + N; }
 cudaError_t launch_conv_fwd(const ConvArgs& a, cudaStream_t st) {
   LaunchTimer lt("conv_fwd", st);
   const int blocks = channel_blocks(a.D);
-  MOE_CONV_DISPATCH(conv_fwd_kernel, most_parts(a.N, a.T, kFwdTokens));
+  MOE_CONV_DISPATCH(conv_fwd_kernel, most_parts(a.N, a.T, kFwdTokens), a, blocks);
   return cudaGetLastError();
 }
 
-int conv_bwd_parts(int N, int T, int D) {
-  const int parts = most_parts(N, T, kBwdTokens), blocks = channel_blocks(D);
-  const int most = (num_sms() * 4 + blocks - 1) / blocks;
-  return parts < most ? parts : most;
+// The backward's division: CTAs that walk the parts of a channel block, and a part's tokens, of which there are enough that the last round of
+// parts is a full one, if the sequences are equally long (a part costs ten tokens more than it has: its start, its neighbours).
+struct BwdDivision {
+  int walkers, length;
+};
+static BwdDivision divide_bwd(int N, int T, int D) {
+  const int blocks = channel_blocks(D), most = (num_sms() * kBwdCtas + blocks - 1) / blocks;
+  const long long each = (static_cast<long long>(T) + N - 1) / N;
+  BwdDivision best{1, 16};
+  long long least = 1ll << 62;
+  for (int length = 16; length <= 256; length += 4) {
+    const long long parts = N * ((each + length - 1) / length), cost = (parts + most - 1) / most * (length + 10);
+    if (cost < least) least = cost, best.length = length;
+  }
+  const int parts = most_parts(N, T, best.length);
+  best.walkers = parts < most ? parts : most;
+  return best;
 }
 
+int conv_bwd_parts(int N, int T, int D) { return divide_bwd(N, T, D).walkers; }
+
 cudaError_t launch_conv_bwd(const ConvBwdArgs& a, float* dw, float* db, cudaStream_t st) {
-  const int parts = conv_bwd_parts(a.N, a.T, a.D);
+  const BwdDivision d = divide_bwd(a.N, a.T, a.D);
+  const int parts = d.walkers;
   {
     LaunchTimer lt("conv_bwd", st);
     const int blocks = channel_blocks(a.D);
-    MOE_CONV_DISPATCH(conv_bwd_kernel, parts);
+    MOE_CONV_DISPATCH(conv_bwd_kernel, parts, a, blocks, d.length);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || a.part == nullptr) return e;
   }
@@ -346,7 +384,7 @@ cudaError_t launch_conv_bwd(const ConvBwdArgs& a, float* dw, float* db, cudaStre
 cudaError_t launch_conv_step(const ConvStepArgs& a, cudaStream_t st) {
   LaunchTimer lt("conv_step", st);
   const int blocks = channel_blocks(a.D);
-  MOE_CONV_DISPATCH(conv_step_kernel, a.B);
+  MOE_CONV_DISPATCH(conv_step_kernel, a.B, a, blocks);
   return cudaGetLastError();
 }
 
