@@ -12,6 +12,7 @@
 // the tokens with its 16 channels' states; then skip, gate and store, four neighbouring channels a thread again.
 // 4 x 1,024 tokens x 8,192 channels take 187 us, 40 of them the bytes and 75 the exponentials: seven instructions a state and token bound it.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "common.cuh"
@@ -1043,9 +1044,16 @@ Division divide(int max_seqlen, int T, int N, int D, int G, bool backward) {
   return d;
 }
 
-template <typename F>
-cudaError_t prepare_kernel(F kernel, int smem) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+// A kernel's dynamic shared memory, allowed once a device.
+template <auto KERNEL>
+cudaError_t prepare_kernel(int smem) {
+  static std::atomic<bool> ready[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev >= 0 && dev < 64 && ready[dev].load())) return e;
+  e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess && dev >= 0 && dev < 64) ready[dev].store(true);
+  return e;
 }
 
 }  // namespace
@@ -1066,13 +1074,13 @@ cudaError_t launch_scan_fwd(const ScanArgs& a, cudaStream_t st) {
   const Division d = divide(a.max_seqlen, a.T, a.N, a.D, a.G, false);
   const unsigned grid = static_cast<unsigned>(d.parts * d.blocks);
   const int smem = kFwdSmem;
-  cudaError_t e = prepare_kernel(scan_fwd_kernel<false>, smem);
+  cudaError_t e = prepare_kernel<scan_fwd_kernel<false>>(smem);
   if (e != cudaSuccess) return e;
   float* starts = nullptr;
   if (d.cut) {
     starts = a.ws;
     float* const dt_sums = reinterpret_cast<float*>(reinterpret_cast<char*>(a.ws) + up256(static_cast<size_t>(d.parts) * a.D * a.S * 4));
-    e = prepare_kernel(scan_fwd_kernel<true>, smem);
+    e = prepare_kernel<scan_fwd_kernel<true>>(smem);
     if (e != cudaSuccess) return e;
     {
       LaunchTimer lt("scan_fwd_sums", st);
@@ -1107,11 +1115,11 @@ cudaError_t launch_scan_bwd(const ScanBwdArgs& a, cudaStream_t st) {
   ws.bc_part = take(static_cast<size_t>(d.blocks) * f.T * 32 * 4);
   ws.dA_part = take(d.parts * all * 4);
   ws.d_part = take(2 * d.parts * static_cast<size_t>(f.D) * 4);
-  cudaError_t e = prepare_kernel(scan_bwd_kernel, kBwdSmem);
+  cudaError_t e = prepare_kernel<scan_bwd_kernel>(kBwdSmem);
   if (e != cudaSuccess) return e;
   if (d.cut) {
     const int b = blocks_of(f.D, f.G, kCh * kFwdWarps), smem = kFwdSmem;
-    e = prepare_kernel(scan_bwd_sums_kernel, smem);
+    e = prepare_kernel<scan_bwd_sums_kernel>(smem);
     if (e != cudaSuccess) return e;
     {
       LaunchTimer lt("scan_bwd_sums", st);

@@ -56,7 +56,7 @@ class RMSNorm:
         return self.dx if self._d_residual is None else self._d_residual
 
     def _rows(self, name, x, dtype, strided=False):
-        if tuple(x.shape) != (self.T, self.d) or x.dtype != dtype:
+        if x.shape != (self.T, self.d) or x.dtype is not dtype:
             raise ValueError(f"{name} is {dtype} [{self.T}, {self.d}], got {x.dtype} {list(x.shape)}")
         if not strided:
             if not x.is_contiguous():

@@ -24,35 +24,50 @@ def _vector(name, x, n):
         raise ValueError(f"{name} is fp32 [{n}], contiguous")
 
 
-def _rows(name, x, T, *shape):
-    """Checks a bf16 [T, *shape] operand; returns the elements between tokens."""
-    if tuple(x.shape) != (T, *shape) or x.dtype != BF16:
-        raise ValueError(f"{name} is bf16 {[T, *shape]}, got {x.dtype} {list(x.shape)}")
-    width = 1
-    for n, stride in zip(reversed(shape), reversed(x.stride()[1:])):
-        if stride != width and n > 1 and x.numel():
-            raise ValueError(f"{name}: the values of a token have to be contiguous")
-        width *= n
-    if x.stride(0) > 0x7FFFFFFF and T > 1:
+# (a small call's time is the host's: each check asks a tensor as little as it can)
+def _rows(name, x, T, width):
+    """Checks a bf16 [T, width] operand; returns the elements between tokens."""
+    if x.shape != (T, width) or x.dtype is not BF16:
+        raise ValueError(f"{name} is bf16 {[T, width]}, got {x.dtype} {list(x.shape)}")
+    token, value = x.stride()
+    if value != 1 and width > 1 and x.numel():
+        raise ValueError(f"{name}: the values of a token have to be contiguous")
+    if T < 2:
+        return width  # (the stride of a single token means nothing)
+    if token > 0x7FFFFFFF:
         raise ValueError(f"{name}: tokens lie less than 2^31 values apart")
-    return x.stride(0) if T > 1 else width  # (the stride of a single token means nothing)
+    return token
+
+
+def _group_rows(name, x, T, groups, width):
+    """Checks a bf16 [T, groups, width] operand; returns the elements between tokens."""
+    if x.shape != (T, groups, width) or x.dtype is not BF16:
+        raise ValueError(f"{name} is bf16 {[T, groups, width]}, got {x.dtype} {list(x.shape)}")
+    token, group, value = x.stride()
+    if ((value != 1 and width > 1) or (group != width and groups > 1)) and x.numel():
+        raise ValueError(f"{name}: the values of a token have to be contiguous")
+    if T < 2:
+        return groups * width
+    if token > 0x7FFFFFFF:
+        raise ValueError(f"{name}: tokens lie less than 2^31 values apart")
+    return token
 
 
 def _bounds(cu_seqlens, N):
-    if cu_seqlens is not None and (cu_seqlens.dtype != torch.int32 or cu_seqlens.shape != (N + 1,)
+    if cu_seqlens is not None and (cu_seqlens.dtype is not torch.int32 or cu_seqlens.shape != (N + 1,)
                                    or not cu_seqlens.is_contiguous()):
         raise ValueError(f"cu_seqlens is int32 [{N + 1}], contiguous")
 
 
 def _like(name, x, shape, dtype):
-    if x is not None and (tuple(x.shape) != tuple(shape) or x.dtype != dtype or not x.is_contiguous()):
+    if x is not None and (x.shape != shape or x.dtype is not dtype or not x.is_contiguous()):
         raise ValueError(f"{name} is {dtype} {list(shape)}, contiguous")
 
 
 def _cache(state, state_idx, T, shape, dtype):
     slots = state.shape[0] if state.dim() else 0
     _like("state", state, (slots, *shape), dtype)
-    if state_idx is not None and (state_idx.dtype != torch.int32 or state_idx.shape != (T,) or not state_idx.is_contiguous()):
+    if state_idx is not None and (state_idx.dtype is not torch.int32 or state_idx.shape != (T,) or not state_idx.is_contiguous()):
         raise ValueError(f"state_idx is int32 [{T}], contiguous")
     return slots
 
@@ -195,9 +210,9 @@ class SelectiveScan:
         return self._dz
 
     def _operands(self, u, delta, B, C, z):
-        ld = [_rows("u", u, self.T, self.D), _rows("delta", delta, self.T, self.D),
-              _rows("B", B, self.T, self.G, self.S), _rows("C", C, self.T, self.G, self.S)]
-        return ld + [_rows("z", z, self.T, self.D) if z is not None else 0]
+        T, D, G, S = self.T, self.D, self.G, self.S
+        return (_rows("u", u, T, D), _rows("delta", delta, T, D), _group_rows("B", B, T, G, S), _group_rows("C", C, T, G, S),
+                0 if z is None else _rows("z", z, T, D))
 
     def forward(self, u, delta, B, C, z=None, cu_seqlens=None, state_in=None, want_state: bool = False, stream=None):
         """y [T, D] (bf16, this instance's buffer) for u, delta and the gate z [T, D], B and C [T, groups, S]: slices of wider rows will
