@@ -192,14 +192,16 @@ __device__ __noinline__ bool group_value_exactly(const Params& p, const float* r
 }
 
 // One warp routes one token; the logits are read once. Instructions bound it, and what their order leaves idle at the 16 to 20 warps an SM that
-// the row's registers allow: 16,384 tokens x 896 experts, 16 chosen, take 35 us from the logits alone, 43 with a bias, 54 in 8 groups, where the
-// bytes would take 9. (Three CTAs of eight warps: 36, 45 and 61.)
+// the row's registers allow: 16,384 tokens x 896 experts, 16 chosen, take 25 us from the logits alone, 33 with a bias, 45 in 8 groups, where the
+// bytes would take 9; 24 of 896 for 4,096 tokens 18.
 //
 // The values that choose (score + bias, or the logits themselves without a bias) are held as order-preserving bits,
 // NPL a lane, runs of four (VEC) or single ones spread over all lanes. Groups: the values pass through shared memory to lanes that lie
 // by groups, which find each group's two largest and rank the groups by counting those ahead; the other groups' values
 // are cleared. Of the lanes' maxima the (k+1)-th is a bound tau that at least k + 1 values reach; those that do (some twenty
-// of 896) are sorted across the warp. More than 32 of them, or too few lanes for the bound: k rounds of a warp-wide maximum.
+// of 896 for k = 16) are sorted across the warp. Where more than 32 reach it (k above 18 or so), a bound that fewer reach is found by
+// halving the distance to the largest value; where equal values leave none, k rounds of a warp-wide maximum (always in rounds: 34, 42 and 54 us,
+// and 66 for 24 of 896).
 //
 // Which experts are chosen does not depend on the rounding here. A 32-bit score is within
 // tol = 2^-21 s (2 + |l - m|) + 2^-22 |c| of its value (the exponent's argument is rounded once, 2^-24 of it, the exponential and
@@ -413,8 +415,25 @@ __global__ void __launch_bounds__(kWarps * 32, NPL < 28 ? 1 : GROUPED ? 4 : 5) r
 #pragma unroll
     for (int i = 0; i < NPL; ++i) most = max(most, kv[i]);
     const uint32_t sorted = sort_lanes(most, lane, [](uint32_t a, uint32_t b) { return a < b; });
-    const uint32_t tau = k < 32 ? __shfl_sync(kAll, sorted, k) : 0u;
-    const int total = tau != 0u ? collect(tau, mine) : 33;
+    uint32_t tau = max(__shfl_sync(kAll, sorted, min(k, 31)), 1u);
+    int total = collect(tau, mine);
+    if (total > 32) {  // a bound that k to 32 values reach lies between tau and the largest value, unless equal ones straddle it
+      uint32_t high = __shfl_sync(kAll, sorted, 0) + 1u;
+      while (high - tau > 1u) {
+        const uint32_t mid = tau + (high - tau) / 2u;
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) n += kv[i] >= mid;
+        n = __reduce_add_sync(kAll, n);
+        if (n < k) {
+          high = mid;
+        } else {
+          tau = mid;
+          if (n <= 32) break;
+        }
+      }
+      total = collect(tau, mine);
+    }
     const bool listed = total <= 32;
     if (listed) {
       mine = sort_lanes(mine, lane, [](unsigned long long a, unsigned long long b) { return a < b; });

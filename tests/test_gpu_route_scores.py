@@ -251,3 +251,19 @@ def test_biases_whose_sums_pass_32_bits(score):
     """Groups whose two largest values add up to more than the largest float."""
     b = torch.cat([torch.full((16,), v) for v in (2.0e38, 2.5e38, -3e38, 2.25e38)])
     _check(_logits(6, 64, 8), b, 6, score, groups=4, group_k=2)
+
+
+@pytest.mark.parametrize("k", [17, 20, 25, 31, 32])
+@pytest.mark.parametrize("E,groups,group_k", [(896, 1, 1), (1000, 5, 3), (64, 1, 1), (100, 1, 1), (256, 8, 4)])
+@pytest.mark.parametrize("score,bias", [("sigmoid", False), ("sigmoid", True), ("softmax", True)])
+def test_many_experts_a_token(E, groups, group_k, k, score, bias):
+    """More than 16, where the lanes' largest values alone do not bound them: values of their own, of few levels, all but some the
+    same, and masked."""
+    l = _logits(24, E, E + k)
+    l[6:12] = (l[6:12] * 4).round() / 4  # many equal values
+    l[12:18] = torch.where(torch.arange(E) % 7 == 0, l[12:18], torch.tensor(-0.5))
+    l[18:20, E // 3:] = -torch.inf
+    l[20:22] = 0.25
+    l[22:, ::2] = -torch.inf
+    b = (_bias(E, k) * 8).round() / 8 if bias else None
+    _check(l, b, k, score, groups=groups, group_k=group_k)
