@@ -205,7 +205,8 @@ __device__ __noinline__ bool group_value_exactly(const Params& p, const float* r
 //
 // Which experts are chosen does not depend on the rounding here. A 32-bit score is within
 // tol = 2^-21 s (2 + |l - m|) + 2^-22 |c| of its value (the exponent's argument is rounded once, 2^-24 of it, the exponential and
-// the reciprocal are right to 2 ulp, the sum over the experts to 4; m is the row's maximum, 0 for the sigmoid). Where two
+// the reciprocal are right to 2 ulp, the sum over the experts to 4; m is the row's maximum, 0 for the sigmoid, where of a positive l only
+// (1 - s) l counts, which is below 1). Where two
 // neighbours in the order, or two groups, are nearer than that, all that could be meant are compared by values in 64
 // bits. (A softmax keeps its 32-bit sum there, a common factor: only the scores' difference is uncertain by 2^-20 of itself,
 // and where that is not enough either the token starts over in 64 bits: 15 us.) Two experts with the same logit and bias are
@@ -461,7 +462,7 @@ __global__ void __launch_bounds__(kWarps * 32, NPL < 28 ? 1 : GROUPED ? 4 : 5) r
       const bool real = mine != 0ull && c > neg_inf() && lane < listed_n;
       const int e = real ? static_cast<int>(~static_cast<uint32_t>(mine)) : 0;
       const float l = real ? __ldg(row + e) : 0.0f, b = real ? __ldg(p.bias + e) : 0.0f;
-      const float tol = real ? 0x1p-21f * fabsf(c - b) * (2.0f + fminf(fabsf(l - (SOFTMAX ? top : 0.0f)), 1e38f)) + 0x1p-22f * fabsf(c) : 0.0f;
+      const float tol = real ? 0x1p-21f * fabsf(c - b) * (2.0f + fminf(SOFTMAX ? top - l : fmaxf(-l, fminf(l, 1.0f)), 1e38f)) + 0x1p-22f * fabsf(c) : 0.0f;
       const float nc = __shfl_down_sync(kAll, c, 1), nl = __shfl_down_sync(kAll, l, 1), nb = __shfl_down_sync(kAll, b, 1),
                   nt = __shfl_down_sync(kAll, tol, 1);
       const unsigned reals = __ballot_sync(kAll, real);
