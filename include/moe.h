@@ -182,7 +182,7 @@ int moe_route_scores(const float* logits, const float* bias, int T, int E, int k
  *   sigmoid           d_l = g_j w_j (1 - s_j); 0 for the others
  *   softmax           d_l[e] = scale p_e (g_e [e chosen] - sum_j s_j g_j), p the softmax of `logits` (needed here alone)
  * g_j = d_w[t][j], or, with slot_of (of moe_permute), d_w[slot_of[t][j]] of moe_grouped_swiglu_bwd's d_row_w (0 for a
- * negative slot). d_topk_w (nullable) receives g. The choice is piecewise constant and the bias a constant: no
+ * negative slot; one of T k or above sets MOE_FLAG_BAD_INDEX and counts as one). d_topk_w (nullable) receives g. The choice is piecewise constant and the bias a constant: no
  * gradient. An id outside [0, E), or one that its row has named before, has none either and sets
  * MOE_FLAG_BAD_EXPERT. scale must not be 0. */
 int moe_route_scores_bwd(const float* d_w, const int32_t* slot_of, const float* logits, const int32_t* topk_idx,

@@ -545,13 +545,36 @@ __global__ void __launch_bounds__(256) route_scores_bwd_kernel(RouteBwdArgs a) {
   const int t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (t >= a.T) return;
+  // the row's logits, on their way while the chosen ones are looked at
+  const float* const l = a.logits + static_cast<size_t>(t) * a.E;
+  // (1,024 experts at most: 8 runs of four a lane)
+  float4 x[8];
+  if (DENSE && a.E % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      x[i] = make_float4(neg_inf(), neg_inf(), neg_inf(), neg_inf());
+      if (4 * (lane + 32 * i) < a.E) x[i] = __ldg(reinterpret_cast<const float4*>(l) + lane + 32 * i);
+    }
+  } else if (DENSE) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float y[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int at = 4 * (lane + 32 * i) + j;
+        y[j] = at < a.E ? __ldg(l + at) : neg_inf();
+      }
+      x[i] = make_float4(y[0], y[1], y[2], y[3]);
+    }
+  }
   const size_t o = static_cast<size_t>(t) * a.k + lane;
   float gw = 0.0f, w = 0.0f, s = 0.0f;
   int e = -1 - lane;  // (different from one another)
   if (lane < a.k) {
     if (a.slot_of) {
       const int slot = __ldg(a.slot_of + o);
-      gw = slot >= 0 ? __ldg(a.d_w + slot) : 0.0f;
+      if (slot >= 0 && slot < static_cast<long long>(a.T) * a.k) gw = __ldg(a.d_w + slot);
+      else if (slot >= 0) set_flag(a.err_flag, MOE_FLAG_BAD_INDEX);
     } else {
       gw = __ldg(a.d_w + o);
     }
@@ -592,28 +615,7 @@ __global__ void __launch_bounds__(256) route_scores_bwd_kernel(RouteBwdArgs a) {
     if (e >= 0) row[e] = OUT(d);
     return;
   }
-  const float* const l = a.logits + static_cast<size_t>(t) * a.E;
-  // (1,024 experts at most: 8 runs of four a lane)
-  float4 x[8];
   float top = neg_inf();
-  if (a.E % 4 == 0) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      x[i] = make_float4(neg_inf(), neg_inf(), neg_inf(), neg_inf());
-      if (4 * (lane + 32 * i) < a.E) x[i] = __ldg(reinterpret_cast<const float4*>(l) + lane + 32 * i);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float y[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int at = 4 * (lane + 32 * i) + j;
-        y[j] = at < a.E ? __ldg(l + at) : neg_inf();
-      }
-      x[i] = make_float4(y[0], y[1], y[2], y[3]);
-    }
-  }
   const auto usable = [](float v) { return v < -neg_inf() ? v : neg_inf(); };  // as the forward reads them
 #pragma unroll
   for (int i = 0; i < 8; ++i) {

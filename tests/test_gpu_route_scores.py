@@ -267,3 +267,21 @@ def test_many_experts_a_token(E, groups, group_k, k, score, bias):
     l[22:, ::2] = -torch.inf
     b = (_bias(E, k) * 8).round() / 8 if bias else None
     _check(l, b, k, score, groups=groups, group_k=group_k)
+
+
+@pytest.mark.parametrize("score,renorm", [("sigmoid", True), ("softmax", True), ("softmax", False)])
+def test_slots_that_do_not_exist(score, renorm):
+    """A dropped row's slot is negative; one behind the last row is flagged. Both have no gradient of their own."""
+    T, E, k = 11, 60, 4
+    r = _router(T, E, k, score=score, renorm=renorm)
+    r.forward(_logits(T, E, 2).cuda())
+    g = torch.randn(T * k, generator=torch.Generator().manual_seed(3)).cuda()
+    slots = torch.randperm(T * k, generator=torch.Generator().manual_seed(4)).to(torch.int32).view(T, k)
+    slots[1, 2] = slots[5, 0] = -1
+    by_token = torch.where(slots >= 0, g.cpu()[slots.clamp(min=0).long()], torch.tensor(0.0)).cuda()
+    want = r.backward(by_token).clone()
+    seen = torch.empty(T, k, device="cuda")
+    assert torch.equal(r.backward(g, slots.cuda(), seen), want) and torch.equal(seen, by_token) and int(r.err) == 0
+    slots[5, 0] = T * k
+    assert torch.equal(r.backward(g, slots.cuda(), seen), want) and torch.equal(seen, by_token)
+    assert int(r.err) == M.MOE_FLAG_BAD_INDEX
