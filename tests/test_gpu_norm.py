@@ -154,3 +154,32 @@ def test_in_a_graph_and_on_another_stream():
     torch.cuda.synchronize()
     for a, b in ((n.y, m.y), (n.sum, m.sum), (n.dx, m.dx), (n.dw, m.dw), (n.d_residual, m.d_residual)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T,d", [(3, 64), (700, 1000), (2500, 4096), (40, 16384)])
+@pytest.mark.parametrize("place", ["dy", "u", "d_sum"])
+@pytest.mark.parametrize("dtype", [torch.float32, BF], ids=str)
+def test_gradients_in_place(T, d, place, dtype):
+    """A gradient over what its own row is read from, where the types are the same."""
+    from sparse_moe_layer_topk_gb300 import _lib as M
+    gen = torch.Generator().manual_seed(T + d)
+    make = lambda *s, dt: torch.randn(*s, generator=gen).to(dt).cuda()  # noqa: E731
+    ops = dict(dy=make(T, d, dt=BF), u=make(T, d, dt=dtype), d_sum=make(T, d, dt=dtype))
+    w = make(d, dt=torch.float32)
+    ws_bytes = M.moe_workspace_size(M.MOE_OP_RMSNORM_BWD, T=T, d=d)
+    ws = torch.empty(ws_bytes, dtype=torch.uint8, device="cuda")
+    code = M.MOE_DTYPE_F32 if dtype == torch.float32 else M.MOE_DTYPE_BF16
+
+    def run(dy, u, d_sum, dx, d_residual):
+        dw = torch.empty(d, device="cuda")
+        M.moe_rmsnorm_bwd(dy, u, w, d_sum, T, d, d, code, 1e-6, dx, d_residual, dw, ws, ws_bytes)
+        return dw
+
+    dx, d_residual = torch.empty(T, d, dtype=BF, device="cuda"), torch.empty(T, d, dtype=dtype, device="cuda")
+    want = run(**ops, dx=dx, d_residual=d_residual)
+    for name, result, other in (("dx", dx, "d_residual"), ("d_residual", d_residual, "dx")):
+        if ops[place].dtype != result.dtype:
+            continue
+        now = {n: t.clone() for n, t in ops.items()}
+        dw = run(**now, **{name: now[place], other: None})
+        assert torch.equal(now[place], result) and torch.equal(dw, want)

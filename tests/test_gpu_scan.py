@@ -457,3 +457,31 @@ def test_results_between_the_rows_that_are_read(at):
     assert torch.equal(y, want)
     keep[:, at:at + D] = want
     assert torch.equal(buf, keep)
+
+
+@pytest.mark.parametrize("B", [1, 5, 61])
+@pytest.mark.parametrize("place", ["u", "delta", "z"])
+def test_a_step_in_place(B, place):
+    """The outputs of the steps over what their own rows are read from."""
+    from sparse_moe_layer_topk_gb300 import _lib as M
+    D, S, W, G = 520, 16, 4, 2
+    gen = torch.Generator().manual_seed(B)
+    make = lambda *s, dt=torch.bfloat16: torch.randn(*s, generator=gen).to(dt).cuda()  # noqa: E731
+    f32 = torch.float32
+    u, delta, z, b, c = make(B, D), make(B, D), make(B, D), make(B, G * S), make(B, G * S)
+    A, skip, bias, state = -make(D, S, dt=f32).abs(), make(D, dt=f32), make(D, dt=f32), make(B, D, S, dt=f32)
+
+    def scan(u, delta, z, state, y):
+        M.moe_scan_step(u, delta, A, b, c, skip, z, bias, state, None, B, B, D, S, G, D, D, G * S, G * S, D, D, True, y)
+        return y
+
+    want, apart, over = torch.empty_like(u), state.clone(), state.clone()
+    scan(u, delta, z, apart, want)
+    ops = dict(u=u.clone(), delta=delta.clone(), z=z.clone())
+    assert torch.equal(scan(**ops, state=over, y=ops[place]), want) and torch.equal(over, apart)
+
+    w, inputs = make(D, W, dt=f32), make(B, W - 1, D)
+    apart, over, x = inputs.clone(), inputs.clone(), u.clone()
+    M.moe_conv_step(u, w, skip, apart, None, B, B, D, W, D, D, True, want)
+    M.moe_conv_step(x, w, skip, over, None, B, B, D, W, D, D, True, x)
+    assert torch.equal(x, want) and torch.equal(over, apart)
