@@ -926,12 +926,12 @@ __global__ void __launch_bounds__(256) scan_tail_kernel(ScanBwdArgs a, BwdWs ws,
 
 // ------------------------------------------------------------------ step
 
-constexpr int kStepWarps = 8;
+constexpr int kStepWarps = 4;
 
 // One token for each of four rows: a lane has four states of a channel in each, whose loads are under way together, and reads
 // A once for all of them. Time step, gate and output of a row are the work of one of the four lanes that share a channel.
-// 61 rows x 8,192 channels x 16 states in 15 us, 9.4 of them the states' bytes; the rest is arithmetic (some 520 instructions a warp).
-// A row a CTA: 24 us.
+// 61 rows x 8,192 channels x 16 states in 14.5 us, 9.4 of them the states' bytes; the rest is arithmetic (some 520 instructions a warp).
+// A row a CTA: 24 us; eight warps a CTA 15.4.
 __global__ void __launch_bounds__(kStepWarps * 32) scan_step_kernel(ScanStepArgs a, int per) {
   constexpr int kRows = 4;
   const int lane = static_cast<int>(lane_id()), q = lane & 3;
