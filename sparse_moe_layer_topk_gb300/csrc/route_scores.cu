@@ -157,13 +157,45 @@ __device__ __noinline__ int select_exactly(const Params& p, const float* row) {
   return mine;
 }
 
-// What the groups' choice needs of one group's lanes, in 64 bits: the value of the group from its two largest members, found
-// again in `row_c` (the 32-bit values by expert). False where a third member is too close to the second.
+// What the groups' choice needs of one group's lanes, in 64 bits: the value of the group from its largest member, or its two largest,
+// found again in `row_c` (the 32-bit values by expert; `tol`: how far apart those of members in the wrong order can be). False, on one of the
+// group's lanes at least, where that leaves open which members they are.
 template <bool SOFTMAX>
 __device__ __noinline__ bool group_value_exactly(const Params& p, const float* row, const float* row_c, int size, int lanes, int group, int sub,
                                                  float t1, float t2, float tol, float top, float inv, double& value, double& scores) {
+  const bool mine = group < p.groups && t1 > neg_inf();
+  const auto exactly = [&](int at, double& s) {
+    const int e = group * size + at;
+    const double l = row[e];
+    s = SOFTMAX ? exp(l - static_cast<double>(top)) * static_cast<double>(inv) : 1.0 / (1.0 + exp(-l));
+    return p.bias ? s + static_cast<double>(p.bias[e]) : s;
+  };
+  value = -INFINITY, scores = 0.0;
+  if (p.group_top == 1) {  // (only with a bias: logits need no rounding) the largest of all that could be
+    double v = 0.0, s = 0.0;
+    float seen_l = 0.0f, seen_b = 0.0f;  // (members of one logit and bias are computed once: padded rows)
+    bool some = false, again = false;
+    const auto meet = [&](auto use) {
+      some = false;
+      for (int i = sub; mine && i < size; i += lanes) {
+        const int e = group * size + i;
+        if (!(row_c[e] >= t1 - tol)) continue;
+        const float l = row[e], b = p.bias[e];
+        if (!some || l != seen_l || b != seen_b) v = exactly(i, s), seen_l = l, seen_b = b, some = true, use();
+      }
+    };
+    meet([&] {
+      if (v > value) value = v, scores = s;
+    });
+    for (int o = 1; o < lanes; o <<= 1) {
+      const double x = __shfl_xor_sync(kAll, value, o), xs = __shfl_xor_sync(kAll, scores, o);
+      if (x > value) value = x, scores = xs;
+    }
+    if (SOFTMAX)  // (the sum's rounding moves values by 2^-20 of their scores)
+      meet([&] { again |= (s != scores || v != value) && value - v <= 0x1p-20 * fabs(s - scores) + 0x1p-45 * fabs(scores); });
+    return !again;
+  }
   int at1 = 0x7FFFFFFF, at2 = 0x7FFFFFFF, close = 0;
-  const bool mine = group < p.groups;
   for (int i = sub; mine && i < size; i += lanes)
     if (row_c[group * size + i] == t1) at1 = min(at1, i);
   for (int o = 1; o < lanes; o <<= 1) at1 = min(at1, __shfl_xor_sync(kAll, at1, o));
@@ -176,19 +208,12 @@ __device__ __noinline__ bool group_value_exactly(const Params& p, const float* r
     at2 = min(at2, __shfl_xor_sync(kAll, at2, o));
     close += __shfl_xor_sync(kAll, close, o);
   }
-  const auto exactly = [&](int at, double& s) {
-    const int e = group * size + at;
-    const double l = row[e];
-    s = SOFTMAX ? exp(l - static_cast<double>(top)) * static_cast<double>(inv) : 1.0 / (1.0 + exp(-l));
-    return p.bias ? s + static_cast<double>(p.bias[e]) : s;
-  };
-  value = -INFINITY, scores = 0.0;
-  if (!mine || !(t1 > neg_inf())) return true;
+  if (!mine) return true;
   double s1 = 0.0, s2 = 0.0;
   value = exactly(at1, s1);
-  if (p.group_top > 1 && t2 > neg_inf()) value += exactly(at2, s2);
+  if (t2 > neg_inf()) value += exactly(at2, s2);
   scores = s1 + s2;
-  return close <= 2 || p.group_top == 1;
+  return close <= 2;
 }
 
 // One warp routes one token; the logits are read once. Instructions bound it, and what their order leaves idle at the 16 to 20 warps an SM that

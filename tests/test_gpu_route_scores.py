@@ -285,3 +285,35 @@ def test_slots_that_do_not_exist(score, renorm):
     slots[5, 0] = T * k
     assert torch.equal(r.backward(g, slots.cuda(), seen), want) and torch.equal(seen, by_token)
     assert int(r.err) == M.MOE_FLAG_BAD_INDEX
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("groups,group_k", [(8, 4), (7, 2), (32, 8)])
+def test_groups_by_one_value_that_32_bits_cannot_tell(score, groups, group_k):
+    """group_top = 1: a group's largest value is found in 64 bits where members lie within fp32's rounding of one another."""
+    g = torch.Generator().manual_seed(5)
+    l = torch.randn(40, 896, generator=g).repeat_interleave(3, 0)[:64]
+    s = torch.sigmoid(l.double()) if score == "sigmoid" else torch.softmax(l.double(), 1)
+    b = (0.75 - s[0] + 1e-8 * torch.randn(896, generator=g, dtype=torch.float64)).float()
+    _check(l, b, 16, score, groups=groups, group_k=group_k, group_top=1)
+
+
+@pytest.mark.parametrize("bias", [0.0, 64.0, -1000.0])
+@pytest.mark.parametrize("groups,group_k,group_top", [(8, 4, 1), (8, 4, 2), (5, 2, 1), (32, 7, 1), (1, 1, 1)])
+def test_scores_next_to_one_and_biases_that_quantise_them(bias, groups, group_k, group_top):
+    """Sigmoid scores that are all 1 in fp32, or equal once a large bias is added."""
+    l = 15 + 14 * torch.rand(48, 160, generator=torch.Generator().manual_seed(7))
+    l[40:] = l[40:, :1]  # padded rows: one logit everywhere
+    _check(l, torch.full((160,), bias), 5, groups=groups, group_k=group_k, group_top=group_top)
+    l = torch.tensor([[18.0, 30.0, 25.0, 20.0]])
+    if groups == 8:
+        _check(l, torch.full((4,), bias), 1, groups=2, group_k=1, group_top=group_top)
+
+
+@pytest.mark.parametrize("bias", ["zero", "some", "two"])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_rows_of_equal_logits_by_one_value(bias, score):
+    l = torch.cat([torch.zeros(5, 896), torch.full((3, 896), -3.25), _logits(3, 896)])
+    b = {"zero": torch.zeros(896), "some": _bias(896), "two": (torch.arange(896) % 3 == 0).float() * 0.125}[bias]
+    for groups, group_k in ((8, 3), (7, 2), (32, 20)):
+        _check(l, b, 16, score, groups=groups, group_k=group_k, group_top=1)
