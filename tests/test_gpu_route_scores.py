@@ -317,3 +317,67 @@ def test_rows_of_equal_logits_by_one_value(bias, score):
     b = {"zero": torch.zeros(896), "some": _bias(896), "two": (torch.arange(896) % 3 == 0).float() * 0.125}[bias]
     for groups, group_k in ((8, 3), (7, 2), (32, 20)):
         _check(l, b, 16, score, groups=groups, group_k=group_k, group_top=1)
+
+
+@pytest.mark.parametrize("group_top", [1, 2])
+@pytest.mark.parametrize("groups,group_k", [(8, 4), (16, 3)])
+def test_members_on_either_side_of_a_rounding(group_top, groups, group_k):
+    """Scores within a few 2^-24 of the middle between two sums of fp32: which of a group's members comes second is not what their
+    rounded sums say."""
+    g = torch.Generator().manual_seed(11)
+    size, T = 128 // groups, 400
+    middle = 0.5 + 2.0 ** -18  # (100.5 and 100.5 + 2^-17 are neighbours)
+    l = np.log(middle / (1 - middle)) + 4e-7 * torch.randn(T, groups, size, generator=g, dtype=torch.float64)
+    l = l + 8e-7 * (2 * torch.rand(T, 1, 1, generator=g, dtype=torch.float64) - 1)
+    if group_top == 2:
+        l[:, :, 0] = 2.0
+    l[:, :, 4:] = -5.0
+    _check(l.float().view(T, 128), torch.full((128,), 100.0), 8, groups=groups, group_k=group_k, group_top=group_top)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("group_top", [1, 2])
+def test_members_whose_scores_round_differently(score, group_top):
+    """As above, with scores of different sizes and biases that make up for it: each score has an error of its own."""
+    g = torch.Generator().manual_seed(14)
+    T, groups, size = 1500, 8, 8
+    rand = lambda *s: torch.rand(*s, generator=g, dtype=torch.float64)  # noqa: E731
+    noise = lambda *s: torch.randn(*s, generator=g, dtype=torch.float64)  # noqa: E731
+    unit = 2.0 ** -17 if score == "sigmoid" else 2.0 ** -24  # between two sums next to 100.5, or to 0.75
+    steps = torch.round((0.2 + 0.6 * rand(groups, size)) / unit if score == "sigmoid" else (0.003 + 0.006 * rand(groups, size)) / unit)
+    b = (100.5 if score == "sigmoid" else 0.75) - steps * unit
+    scatter = 1e-7 if score == "sigmoid" else 1e-9
+    s = (steps + 0.5) * unit + scatter * noise(T, groups, size) + 2 * scatter * (2 * rand(T, 1, 1) - 1)
+    if group_top == 2:
+        b[:, 0] = 101 if score == "sigmoid" else 1
+        s[:, :, 0] = 0.5 if score == "sigmoid" else 0.004
+    s[:, :, 4:] *= 0.01
+    if score == "sigmoid":
+        l = torch.log(s / (1 - s)).view(T, 64)
+    else:  # (an expert that is never chosen takes the rest of the row)
+        s = s.view(T, 64)
+        s[:, 63] = 0
+        s[:, 63] = 1 - s.sum(1)
+        b[-1, -1] = -10
+        l = torch.log(s)
+    _check(l.float(), b.float().view(64), 6, score, groups=groups, group_k=4, group_top=group_top)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_two_members_on_either_side_of_a_rounding(score):
+    """Two groups whose second member is one of two that differ by less than the error of their scores, while their sums with the bias
+    are neighbours in fp32, further apart than any score's error."""
+    g = torch.Generator().manual_seed(15)
+    T, E = 6000, 1024
+    rand = lambda *s: torch.rand(*s, generator=g, dtype=torch.float64)  # noqa: E731
+    unit, sums, scatter = (2.0 ** -17, 100.5, 5e-8) if score == "sigmoid" else (2.0 ** -24, 0.75, 1.5e-10)
+    span = 0.2 + 0.6 * rand(2, 2) if score == "sigmoid" else 0.0007 + 0.0004 * rand(2, 2)
+    steps = torch.round(span / unit)
+    b, s = torch.zeros(2, E // 2, dtype=torch.float64), torch.full((T, 2, E // 2), 0.01 if score == "sigmoid" else 0.0, dtype=torch.float64)
+    b[:, 1:3] = sums - steps * unit
+    s[:, :, 1:3] = (steps + 0.5) * unit + scatter * torch.randn(T, 2, 2, generator=g, dtype=torch.float64)
+    b[:, 0], s[:, :, 0] = sums + 0.25, 0.001
+    if score == "softmax":
+        s[:, :, 3:] = ((1 - s.sum((1, 2))) / (E - 6))[:, None, None]
+    l = torch.log(s / (1 - s)) if score == "sigmoid" else torch.log(s) + 7
+    _check(l.float().view(T, E), b.float().view(E), 2, score, groups=2, group_k=1, group_top=2)
