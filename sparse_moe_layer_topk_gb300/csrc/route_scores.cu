@@ -377,12 +377,13 @@ __global__ void __launch_bounds__(kWarps * 32, NPL < 28 ? 1 : GROUPED ? 4 : 5) r
     // (scores are at most 1, with softmax at most the row's largest, and off by 2^-22 of that for every 2 of |l|: 2^-19 for two of them)
     const float slack = sums || !by_logit ? 0x1p-19f * (SOFTMAX ? fminf(1.0f, inv) : 1.0f) : 0.0f;
     // The last group that stays and the first that goes: too close to tell apart? (Where one is all masked they are not, and where none
-    // goes `next` is NaN.)
-    const uint32_t bits = order_bits(value);
-    const float least = bits_value(__reduce_min_sync(kAll, keep ? bits : 0xFFFFFFFFu));
-    const float next = bits_value(__reduce_max_sync(kAll, some && !keep ? bits : 0u));
-    // (sums of two biases may pass fp32)
-    const bool close = least - next <= slack + 0x1p-21f * (fabsf(least) + fabsf(next)) || least == -neg_inf();
+    // goes `next` is NaN.) Each by as much as its roundings could have moved it: those of its terms, which may cancel; sums of two
+    // biases may pass fp32.
+    const float moved = 0x1p-21f * (by_logit ? value : sums && t2 > neg_inf() ? fmaxf(fabsf(t1), fabsf(t2)) : fabsf(t1));
+    const float low = value > neg_inf() ? fmaxf(value - moved, -3.4028235e38f) : value, high = value > neg_inf() ? value + moved : value;
+    const float least = bits_value(__reduce_min_sync(kAll, keep ? order_bits(low) : 0xFFFFFFFFu));
+    const float next = bits_value(__reduce_max_sync(kAll, some && !keep ? order_bits(high) : 0u));
+    const bool close = least - next <= slack || least == -neg_inf();
     if (slack > 0.0f && close && least > neg_inf() && next > neg_inf()) {
       double value64, scores;
       const float* const row_v = by_logit ? row : row_c;  // (where t1 and t2 were found)

@@ -381,3 +381,14 @@ def test_two_members_on_either_side_of_a_rounding(score):
         s[:, :, 3:] = ((1 - s.sum((1, 2))) / (E - 6))[:, None, None]
     l = torch.log(s / (1 - s)) if score == "sigmoid" else torch.log(s) + 7
     _check(l.float().view(T, E), b.float().view(E), 2, score, groups=2, group_k=1, group_top=2)
+
+
+def test_groups_of_opposite_biases():
+    """The two largest members of a group cancel: the sum is small, and its error that of its terms."""
+    g = torch.Generator().manual_seed(12)
+    T, groups, size = 400, 8, 8
+    middle = 0.5 + 2.0 ** -18
+    l = np.log(middle / (1 - middle)) + 4e-6 * torch.randn(T, groups, size, generator=g, dtype=torch.float64)
+    b = torch.full((groups, size), -100.0)
+    b[:, 0] = 100.0
+    _check(l.float().view(T, 64), b.view(64), 6, groups=groups, group_k=4)
