@@ -484,18 +484,21 @@ __global__ void __launch_bounds__(kWarps * 32, NPL < 28 ? 1 : GROUPED ? 4 : 5) r
     }
     if (!by_logit) {
       // neighbours in the order, the first that is left out among them
+      const auto tolerance = [&](float c, float l, float b) {
+        return 0x1p-21f * fabsf(c - b) * (2.0f + fminf(SOFTMAX ? top - l : fmaxf(-l, fminf(l, 1.0f)), 1e38f)) + 0x1p-22f * fabsf(c);
+      };
       const int listed_n = listed ? total : min(k + 1, 32);
       const float c = bits_value(static_cast<uint32_t>(mine >> 32));
       const bool real = mine != 0ull && c > neg_inf() && lane < listed_n;
       const int e = real ? static_cast<int>(~static_cast<uint32_t>(mine)) : 0;
       const float l = real ? __ldg(row + e) : 0.0f, b = real ? __ldg(p.bias + e) : 0.0f;
-      const float tol = real ? 0x1p-21f * fabsf(c - b) * (2.0f + fminf(SOFTMAX ? top - l : fmaxf(-l, fminf(l, 1.0f)), 1e38f)) + 0x1p-22f * fabsf(c) : 0.0f;
+      const float tol = real ? tolerance(c, l, b) : 0.0f;
       const float nc = __shfl_down_sync(kAll, c, 1), nl = __shfl_down_sync(kAll, l, 1), nb = __shfl_down_sync(kAll, b, 1),
                   nt = __shfl_down_sync(kAll, tol, 1);
       const unsigned reals = __ballot_sync(kAll, real);
       const bool pair = real && (reals >> lane >> 1 & 1u);
       // what the last chosen one could be taken for: down to `reach`
-      const float wide = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(tol)));
+      float wide = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(tol)));
       const float last = __shfl_sync(kAll, c, k - 1), reach = last - 2.0f * wide;
       bool near = pair && (lane + 1 < k || nc >= reach) && (nl != l || nb != b) && c - nc <= tol + nt;
       if (listed) {
@@ -504,6 +507,20 @@ __global__ void __launch_bounds__(kWarps * 32, NPL < 28 ? 1 : GROUPED ? 4 : 5) r
         const float ll = __shfl_sync(kAll, l, k - 1), lb = __shfl_sync(kAll, b, k - 1);
         for (int i = 0; i < NPL; ++i)
           if (kv[i] != 0u && bits_value(kv[i]) >= reach && bits_value(kv[i]) <= last) near |= row[expert_of(i)] != ll || p.bias[expert_of(i)] != lb;
+      }
+      // Below `reach` there may be one that is off by more than all that are listed: a large score and a bias that all but cancels it, beside
+      // small scores. s (2 + |l - m|) is below 3, and below twice the largest score of a softmax.
+      const float any = 3.0f * 0x1p-21f * (SOFTMAX ? fminf(1.0f, inv) : 1.0f) + 0x1p-22f * fabsf(last), deep = last - wide - any;
+      if (last > neg_inf() && any > wide && (!listed || deep <= bits_value(tau))) {
+        float most = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+          const float x = bits_value(kv[i]);
+          if (kv[i] == 0u || !(x >= deep) || x >= reach) continue;
+          const float t = tolerance(x, __ldg(row + expert_of(i)), __ldg(p.bias + expert_of(i)));
+          if (x + t >= last - wide) near = true, most = fmaxf(most, t);
+        }
+        wide = fmaxf(wide, __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(most))));
       }
       if (__any_sync(kAll, near)) {
         exact = true;

@@ -392,3 +392,46 @@ def test_groups_of_opposite_biases():
     b = torch.full((groups, size), -100.0)
     b[:, 0] = 100.0
     _check(l.float().view(T, 64), b.view(64), 6, groups=groups, group_k=4)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("k", [1, 3])
+@pytest.mark.parametrize("groups,group_k", [(1, 1), (2, 1)])
+def test_a_large_score_beside_small_ones(score, k, groups, group_k):
+    """An expert whose bias all but cancels its large score ends within that score's rounding of experts with small scores, which fp32
+    tells apart far more finely."""
+    rng, T, E = np.random.default_rng(13), 3000, 64
+    f32 = lambda x: np.asarray(x, dtype=np.float32).astype(np.float64)  # noqa: E731
+    sig = lambda x: 1 / (1 + np.exp(-x))  # noqa: E731
+    target = sig(-7.0)
+    cs = np.arange(8, 32, 4)
+    bias = np.zeros(E)
+    bias[cs] = f32(target - rng.uniform(0.55, 0.8, cs.size))
+    bias[30] = -10.0  # takes up the rest of a softmax, and is never chosen
+    l = np.full((T, E), -40.0)
+    c = rng.choice(cs, T)
+    rows = np.arange(T)
+    p = target - bias[c] + 3e-7 * rng.standard_normal(T)  # what the expert's score should be
+    near = 8e-9 * rng.standard_normal(T)
+    if score == "sigmoid":
+        l[rows, c] = f32(np.log(p / (1 - p)))
+        first = sig(l[rows, c]) + bias[c] + near
+        at = lambda v: f32(np.log(v / (1 - v)))  # noqa: E731
+    else:
+        l[rows, c] = 0.0
+        l[:, 30] = f32(np.log(1 / p - 1))
+        first = p + bias[c] + near
+        at = lambda v: f32(np.log(v / p))  # noqa: E731
+    wanted = p
+    for again in range(6):
+        l[:, 0] = at(first)
+        l[:, 4] = at(first - 1.8e-8)
+        for j in range(k - 1):
+            l[:, 1 + 8 * j] = at(first * (1.5 + j))
+        if score == "softmax":
+            small = np.exp(np.delete(l, 30, 1)).sum(1) - 1
+            l[:, 30] = f32(np.log(1 / wanted - 1 - small))
+            p = 1 / np.exp(l).sum(1)
+            first = p + bias[c] + near
+    assert np.isfinite(l).all()
+    _check(torch.from_numpy(l).float(), torch.from_numpy(bias).float(), k, score, groups=groups, group_k=group_k)
