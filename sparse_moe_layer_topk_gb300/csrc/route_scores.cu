@@ -387,8 +387,8 @@ __global__ void __launch_bounds__(kWarps * 32, NPL < 28 ? 1 : GROUPED ? 4 : 5) r
     if (slack > 0.0f && close && least > neg_inf() && next > neg_inf()) {
       double value64, scores;
       const float* const row_v = by_logit ? row : row_c;  // (where t1 and t2 were found)
-      // (of two members each is off by its score's error and the sum's rounding)
-      const float last = fabsf(sums ? t2 : t1), tol = by_logit ? last * 0x1p-20f + 0x1p-20f : 2.0f * slack + last * 0x1p-21f;
+      // (of two members each is off by its score's error, at most 5 x 2^-23 of the largest score, and the rounding of the sum with its bias)
+      const float last = fabsf(sums ? t2 : t1), tol = by_logit ? last * 0x1p-20f + 0x1p-20f : slack + last * 0x1p-21f;
       const bool sure = group_value_exactly<SOFTMAX>(p, row, row_v, size, lanes, group, sub, t1, t2, tol, top, inv, value64, scores);
       int rank64 = 0;
       bool open = !sure;
