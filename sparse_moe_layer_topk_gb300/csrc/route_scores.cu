@@ -229,7 +229,7 @@ __device__ __noinline__ bool group_value_exactly(const Params& p, const float* r
 // and 66 for 24 of 896).
 //
 // Which experts are chosen does not depend on the rounding here. A 32-bit score is within
-// tol = 2^-21 s (2 + |l - m|) + 2^-22 |c| of its value (the exponent's argument is rounded once, 2^-24 of it, the exponential and
+// tol = 2^-21 s (2 + |l - m|) + 2^-22 |c| + 2^-126 of its value (the exponent's argument is rounded once, 2^-24 of it, the exponential and
 // the reciprocal are right to 2 ulp, the sum over the experts to 4; m is the row's maximum, 0 for the sigmoid, where of a positive l only
 // (1 - s) l counts, which is below 1). Where two
 // neighbours in the order, or two groups, are nearer than that, all that could be meant are compared by values in 64
@@ -484,8 +484,8 @@ __global__ void __launch_bounds__(kWarps * 32, NPL < 28 ? 1 : GROUPED ? 4 : 5) r
     }
     if (!by_logit) {
       // neighbours in the order, the first that is left out among them
-      const auto tolerance = [&](float c, float l, float b) {
-        return 0x1p-21f * fabsf(c - b) * (2.0f + fminf(SOFTMAX ? top - l : fmaxf(-l, fminf(l, 1.0f)), 1e38f)) + 0x1p-22f * fabsf(c);
+      const auto tolerance = [&](float c, float l, float b) {  // (2^-126: scores below that are flushed to zero)
+        return 0x1p-21f * fabsf(c - b) * (2.0f + fminf(SOFTMAX ? top - l : fmaxf(-l, fminf(l, 1.0f)), 1e38f)) + (0x1p-22f * fabsf(c) + 0x1p-126f);
       };
       const int listed_n = listed ? total : min(k + 1, 32);
       const float c = bits_value(static_cast<uint32_t>(mine >> 32));

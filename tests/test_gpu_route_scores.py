@@ -435,3 +435,14 @@ def test_a_large_score_beside_small_ones(score, k, groups, group_k):
             first = p + bias[c] + near
     assert np.isfinite(l).all()
     _check(torch.from_numpy(l).float(), torch.from_numpy(bias).float(), k, score, groups=groups, group_k=group_k)
+
+
+def test_scores_below_the_smallest_normal_number():
+    """exp of them is flushed to zero in fp32, beside biases as small."""
+    l = torch.full((3, 64), -120.0)
+    l[0, 5], l[1, 9], l[2, 40] = -88.0, -88.5, -89.0
+    b = torch.zeros(64)
+    b[20], b[21] = 4e-39, 3e-39
+    for k in (1, 2, 3):
+        _check(l, b, k)
+        _check(torch.cat([l, torch.zeros(3, 64)], 1), torch.cat([b, torch.full((64,), -1.0)]), k, "softmax")
