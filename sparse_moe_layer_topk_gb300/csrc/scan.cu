@@ -57,13 +57,21 @@ __device__ __forceinline__ f32x2 sigmoid2(f32x2 x) {
   return pack2(rcp(a), rcp(b));
 }
 
+// The magnitude of x up to 128, where exp(-|x|) is 0 already: the product below may not pass fp32 for a token that is masked by the lowest
+// value of its type or by -infinity. NaN stays NaN.
+__device__ __forceinline__ float up_to_128(float x) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(x)), "f"(128.0f));
+  return r;
+}
+
 // max(x, 0) + log(1 + e), e = exp(-|x|), of two values. The exponent's product is taken in two terms (it would lose |x| 2^-24
 // of e), and log(1 + e) / e is a polynomial of degree 9, fitted on [0, 1] with equal relative errors (5e-9; 1.5e-7 with its
 // roundings), so that small results keep their relative precision: dt multiplies all that reaches a state.
 __device__ __forceinline__ f32x2 softplus2(f32x2 x) {
   float a, b;
   unpack2(x, a, b);
-  const f32x2 n = pack2(fabsf(a), fabsf(b)), above = pack2(fmaxf(a, 0.0f), fmaxf(b, 0.0f)), l2e = pack2(-kLog2e, -kLog2e);
+  const f32x2 n = pack2(up_to_128(a), up_to_128(b)), above = pack2(fmaxf(a, 0.0f), fmaxf(b, 0.0f)), l2e = pack2(-kLog2e, -kLog2e);
   const f32x2 m = mul2(n, l2e);
   const f32x2 lost = fma2(n, pack2(kLog2e, kLog2e), m);
   unpack2(m, a, b);

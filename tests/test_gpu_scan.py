@@ -485,3 +485,79 @@ def test_a_step_in_place(B, place):
     M.moe_conv_step(u, w, skip, apart, None, B, B, D, W, D, D, True, want)
     M.moe_conv_step(x, w, skip, over, None, B, B, D, W, D, D, True, x)
     assert torch.equal(x, want) and torch.equal(over, apart)
+
+
+@pytest.mark.parametrize("low", [float("-inf"), torch.finfo(BF).min, -2e38, -1e30, -130.0, -88.0])
+def test_tokens_masked_by_their_time_step(low):
+    """A token whose time step is softplus of -infinity, or of the type's lowest value, leaves the state as it is and has no gradient of
+    its own: the others get what they get without it. (softplus(-88) is 6e-39: nothing, in a state of fp32.)"""
+    from sparse_moe_layer_topk_gb300.scan import SelectiveScan
+    lens, D, S = [70, 200, 1, 900], 24, 16
+    T, g = sum(lens), torch.Generator().manual_seed(3)
+    n = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    u, z, dy, delta = (n(T, D).to(BF) for _ in range(4))
+    B, C, A, bias = n(T, 1, S).to(BF), n(T, 1, S).to(BF), -torch.exp(n(D, S)), n(D) - 2
+    out = torch.rand(T, generator=g) < 0.3
+    out[:2], out[70 + 199], out[270] = True, True, True
+    delta[out] = low
+    keep = ~out
+    at = np.concatenate([[0], np.cumsum(lens)])
+    kept = [int(keep[a:b].sum()) for a, b in zip(at[:-1], at[1:])]
+    cu, cu_kept = _cu(lens), _cu(kept)
+
+    def run(u, delta, B, C, z, dy, cu, longest):
+        s = SelectiveScan(A.cuda(), u.shape[0], n0.cuda(), bias.cuda(), N=len(lens), max_seqlen=longest)
+        y = s.forward(u.cuda(), delta.cuda(), B.cuda(), C.cuda(), z.cuda(), cu, want_state=True)
+        grads = s.backward(dy.cuda())
+        assert int(s.err) == 0
+        return s, y, grads
+
+    n0 = n(D)
+    dy[out] = 0  # (y of a masked token is C . h all the same; the loss does not see it)
+    s, y, grads = run(u, delta, B, C, z, dy, cu, max(lens))
+    want = O.scan(*(f64(t) for t in (u, delta.clamp(min=-1e4), A, B, C)), lens, f64(n0), f64(z), f64(bias))
+    size = O.scan(*(f64(t) for t in (u.abs(), delta.clamp(min=-1e4), A, B.abs(), C.abs())), lens, f64(n0.abs()), None, f64(bias))
+    gate = np.abs(f64(z) * O.sigmoid(f64(z)))
+    tol = (900 + 16) * 2.0 ** -21
+    _close("y", y, want[0], size[0] * gate, tol)
+    _close("state", s.state_out, want[1], size[1], tol, 0)
+    t, yk, gk = run(*(v[keep] for v in (u, delta, B, C, z, dy)), cu_kept, max(max(kept), 1))
+    rows = keep.cuda()
+    norm = torch.linalg.vector_norm
+    for name, a, b in zip(("du", "ddelta", "dB", "dC", "dz"), grads, gk):
+        a, b = a.float()[rows], b.float()
+        # (the tiles lie elsewhere, and sums go another way: a rounding to bf16 apart, 2^-8 of a value at most)
+        assert bool(a.isfinite().all()) and float(norm(a - b)) <= 2.0 ** -8 * float(norm(b)), name
+    assert not grads[1][out.cuda()].any() or low >= -88.0
+    for name in ("dA", "dskip", "d_dt_bias"):
+        a, b = getattr(s, name), getattr(t, name)
+        assert bool(a.isfinite().all()) and float(norm(a - b)) <= 2.0 ** -10 * float(norm(b)), name
+
+
+@pytest.mark.parametrize("low", [float("-inf"), torch.finfo(BF).min])
+def test_steps_masked_by_their_time_step(low):
+    from sparse_moe_layer_topk_gb300.scan import SelectiveScan
+    R, D, S, g = 7, 40, 16, torch.Generator().manual_seed(4)
+    n = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    u, delta, z = (n(R, D).to(BF).cuda() for _ in range(3))
+    B, C, state = n(R, 1, S).to(BF).cuda(), n(R, 1, S).to(BF).cuda(), n(R, D, S).cuda()
+    delta[[1, 4]] = low
+    s = SelectiveScan(-torch.exp(n(D, S)).cuda(), R, n(D).cuda(), n(D).cuda(), backward=False)
+    before = state.clone()
+    y = s.step(u, delta, B, C, z, state)
+    assert bool(y.isfinite().all()) and bool(state.isfinite().all())
+    # (a decay of no time at all is 1, to the bit that raising the exponential's argument by 2.2e-8 leaves it)
+    assert torch.equal(state[[1, 4]], before[[1, 4]]) and not torch.equal(state[0], before[0])
+
+
+def test_time_steps_that_are_no_numbers_stay_so():
+    """softplus(NaN) is NaN, and of +infinity infinite: neither is taken for a number."""
+    from sparse_moe_layer_topk_gb300.scan import SelectiveScan
+    D, S = 8, 16
+    one = torch.ones(4, D, dtype=BF, device="cuda")
+    b = torch.ones(4, 1, S, dtype=BF, device="cuda")
+    s = SelectiveScan(-torch.ones(D, S, device="cuda"), 4, N=4, backward=False)
+    delta = torch.zeros(4, D, dtype=BF, device="cuda")
+    delta[1], delta[2] = float("nan"), float("inf")
+    y = s.forward(one, delta, b, b)
+    assert bool(y[1].isnan().all()) and bool(y[2].isinf().all()) and bool(y[[0, 3]].isfinite().all())
