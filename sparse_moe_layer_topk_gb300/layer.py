@@ -179,6 +179,10 @@ class LatentMoELayer:
     def backward(self, dout, stream=None, d_sum=None):
         """dx [T, d] for dout = d loss / d out. With a norm, d_sum (the residual's type) is the gradient that
         reaches norm.sum from elsewhere, and norm.d_residual holds the residual's."""
+        if d_sum is not None:  # (before anything is computed)
+            if self.norm is None or self.norm.residual_dtype is None:
+                raise ValueError("without a residual there is no sum")
+            self.norm._rows("d_sum", d_sum, self.norm.residual_dtype)
         w, T, k, d, l, f, E, S, R = (self.w, self.T, self.k, self.d, self.l, self.f, self.E,
                                      self.S, self.R)
         g = self.grads
@@ -224,8 +228,6 @@ class LatentMoELayer:
         if self.norm is not None:
             self.norm.dx = self.dx
             self.norm.backward(dx, d_sum, stream)
-        elif d_sum is not None:
-            raise ValueError("without a norm there is no sum")
         return self.dx
 
     def step(self, x, dout, stream=None):

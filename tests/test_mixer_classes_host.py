@@ -142,3 +142,18 @@ def test_layer_options():
     layer = make({**w, "norm": torch.ones(w["Wr"].shape[0])}, router=dict(score="softmax", groups=2, group_k=1))
     assert layer.grads["norm"] is layer.norm.dw and layer.topk_idx is layer.router.topk_idx
     assert weights_to_device({**inp, "norm": torch.ones(4)}, "cpu")["norm"].tolist() == [1.0] * 4
+
+
+def test_a_layers_gradient_of_a_sum_that_is_not_there():
+    """Refused before anything is computed (a call of the library would refuse the host's tensors)."""
+    inp = I.make_layer_inputs(0)
+    w = weights_to_device(inp, "cpu")
+    normed = {**w, "norm": torch.ones(w["Wr"].shape[0])}
+    g = inp["g"][:4]
+    for layer in (LatentMoELayer(w, 4, 2, device="cpu"), LatentMoELayer(normed, 4, 2, device="cpu")):
+        with pytest.raises(ValueError, match="no sum"):
+            layer.backward(g, d_sum=g)
+    layer = LatentMoELayer(normed, 4, 2, device="cpu", residual_dtype=BF)
+    for d_sum in (g.float(), g[:3], torch.zeros(4, 2 * g.shape[1], dtype=BF)[:, ::2]):
+        with pytest.raises(ValueError, match="d_sum"):
+            layer.backward(g, d_sum=d_sum)
