@@ -230,63 +230,101 @@ class LatentMoELayer:
             self.norm.backward(dx, d_sum, stream)
         return self.dx
 
-    def step(self, x, dout, stream=None):
-        self.forward(x, stream)
-        return self.backward(dout, stream)
+    def step(self, x, dout, stream=None, residual=None, d_sum=None):
+        self.forward(x, stream, **_given(residual=residual))
+        return self.backward(dout, stream, **_given(d_sum=d_sum))
 
-    def capture_step(self, x, dout):
-        """Records one forward + backward on the fixed buffers x and dout as a
-        CUDA graph; graph.replay() reruns it on the current stream. A step
-        allocates nothing and never waits on the host, so it captures whole (run
-        one eager step first: the library sets its kernels' attributes then)."""
+    def capture_step(self, x, dout, residual=None, d_sum=None):
+        """Records one forward + backward on the fixed buffers x and dout (and, with a
+        residual, residual and d_sum) as a CUDA graph; graph.replay() reruns it on the
+        current stream. A step allocates nothing and never waits on the host, so it
+        captures whole (run one eager step first: the library sets its kernels'
+        attributes then)."""
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
-            self.step(x, dout)
+            self.step(x, dout, **_given(residual=residual, d_sum=d_sum))
         return g
 
-    def capture_halves(self, x, dout):
-        """The forward on x and the backward on dout as two CUDA graphs, so that
-        a step may start before its dout has arrived."""
+    def capture_halves(self, x, dout, residual=None, d_sum=None):
+        """The forward on x (and residual) and the backward on dout (and d_sum) as two
+        CUDA graphs, so that a step may start before its dout has arrived."""
         gf = torch.cuda.CUDAGraph()
         with torch.cuda.graph(gf):
-            self.forward(x)
+            self.forward(x, **_given(residual=residual))
         gb = torch.cuda.CUDAGraph()
         with torch.cuda.graph(gb):
-            self.backward(dout)
+            self.backward(dout, **_given(d_sum=d_sum))
         return gf, gb
 
-    def steps_from_host(self, x_host, g_host, dx_host, graphs: bool = True):
+    def steps_from_host(self, x_host, g_host, dx_host, graphs: bool = True, residual_host=None,
+                        d_sum_host=None, d_residual_host=None):
         """Forward + backward for each (x, dout) pair of pinned host tensors,
         writing each step's input gradient back to the pinned dx_host[i].
+
+        A layer with a residual takes residual_host as well, and d_sum_host where a
+        gradient reaches the sums from elsewhere; the residuals' gradients, which differ
+        from dx_host in their type alone, go to d_residual_host if it is given.
 
         The host->device copy of step i+1 and the device->host copy of step i-1
         run on their own streams (separate copy engines) while step i computes;
         device inputs and input gradients are double-buffered and ordered with
         events, so every step still copies its own inputs in and its gradient
-        out. A step's forward waits for its x alone and its backward for its
-        dout, which is copied in after x. With graphs, each slot's forward and
+        out. A step's forward waits for its x (and residual) alone and its backward for its
+        dout (and d_sum), which is copied in after x. With graphs, each slot's forward and
         backward are CUDA graphs captured on first use. Returns after the last copy has been enqueued; synchronise the
         current stream's device to wait for the results."""
         n = len(x_host)
         assert len(g_host) == n and len(dx_host) == n
+        norm = getattr(self, "norm", None)
+        res = None if norm is None else norm.residual_dtype
+        if (residual_host is None) != (res is None):
+            raise ValueError("residuals are given exactly where residual_dtype is")
+        if res is None and (d_sum_host is not None or d_residual_host is not None):
+            raise ValueError("without a residual there is no sum")
+        for name, host in (("residual_host", residual_host), ("d_sum_host", d_sum_host), ("d_residual_host", d_residual_host)):
+            if host is not None and (len(host) != n or any(t.shape != self.dx.shape or t.dtype != res for t in host)):
+                raise ValueError(f"{name} is {n} tensors of {res} {list(self.dx.shape)}")
+        if n == 0:
+            return
         dev = self.dx.device
         comp = torch.cuda.current_stream()
         h2d = torch.cuda.Stream(device=dev)
         d2h = torch.cuda.Stream(device=dev)
         if not hasattr(self, "_pipe"):
-            self._pipe = {
-                "x": [torch.empty_like(self.dx) for _ in range(2)],
-                "g": [torch.empty_like(self.dx) for _ in range(2)],
-                "dx": [torch.empty_like(self.dx) for _ in range(2)],
-            }
+            two = lambda dt=BF16: [torch.empty_like(self.dx, dtype=dt) for _ in range(2)]  # noqa: E731
+            self._pipe = {"x": two(self.dx.dtype), "g": two(self.dx.dtype), "dx": two(self.dx.dtype)}
+            if res is not None:
+                self._pipe |= {"residual": two(res), "d_sum": two(res)}
+                # (with a bf16 residual its gradient is dx itself)
+                self._pipe["d_residual"] = self._pipe["dx"] if norm._d_residual is None else two(res)
+            self._pipe_graphs = {}
         P = self._pipe
-        if graphs and not hasattr(self, "_pipe_graphs"):
-            keep = self.dx
-            self._pipe_graphs = []
-            for s in range(2):
-                self.dx = P["dx"][s]
-                self._pipe_graphs.append(self.capture_halves(P["x"][s], P["g"][s]))
-            self.dx = keep
+        keep = self.dx, None if norm is None else norm._d_residual
+
+        def into_slot(s):  # where a backward writes its gradients
+            self.dx = P["dx"][s]
+            if res is not None and norm._d_residual is not None:
+                norm._d_residual = P["d_residual"][s]
+
+        def restore():
+            self.dx = keep[0]
+            if norm is not None:
+                norm.dx, norm._d_residual = keep
+
+        def of_slot(name, s, host):
+            return {} if host is None else {name: P[name][s]}
+
+        with_sum = d_sum_host is not None
+        if graphs and with_sum not in self._pipe_graphs:
+            halves = []
+            try:
+                for s in range(2):
+                    into_slot(s)
+                    halves.append(self.capture_halves(P["x"][s], P["g"][s], **of_slot("residual", s, residual_host),
+                                                      **of_slot("d_sum", s, d_sum_host)))
+            finally:
+                restore()
+            self._pipe_graphs[with_sum] = halves
         ev = lambda: torch.cuda.Event()  # noqa: E731
         loaded_x = [None] * n
         loaded_g = [None] * n
@@ -299,13 +337,16 @@ class LatentMoELayer:
                 if i >= 2:
                     h2d.wait_event(computed[i - 2])  # slot s no longer read by step i-2
                 P["x"][s].copy_(x_host[i], non_blocking=True)
+                if residual_host is not None:
+                    P["residual"][s].copy_(residual_host[i], non_blocking=True)
                 loaded_x[i] = ev()
                 loaded_x[i].record(h2d)
                 P["g"][s].copy_(g_host[i], non_blocking=True)
+                if with_sum:
+                    P["d_sum"][s].copy_(d_sum_host[i], non_blocking=True)
                 loaded_g[i] = ev()
                 loaded_g[i].record(h2d)
 
-        keep = self.dx  # the eager steps write their input gradient into the slots
         load(0)
         try:
             for i in range(n):
@@ -314,27 +355,33 @@ class LatentMoELayer:
                     load(i + 1)
                 comp.wait_event(loaded_x[i])
                 if graphs:
-                    self._pipe_graphs[s][0].replay()
+                    self._pipe_graphs[with_sum][s][0].replay()
                 else:
-                    self.forward(P["x"][s])
+                    self.forward(P["x"][s], **of_slot("residual", s, residual_host))
                 comp.wait_event(loaded_g[i])
                 if i >= 2:
                     comp.wait_event(drained[i - 2])  # dx slot s copied out by step i-2
                 if graphs:
-                    self._pipe_graphs[s][1].replay()
+                    self._pipe_graphs[with_sum][s][1].replay()
                 else:
-                    self.dx = P["dx"][s]
-                    self.backward(P["g"][s])
+                    into_slot(s)
+                    self.backward(P["g"][s], **of_slot("d_sum", s, d_sum_host))
                 computed[i] = ev()
                 computed[i].record(comp)
                 with torch.cuda.stream(d2h):
                     d2h.wait_event(computed[i])
                     dx_host[i].copy_(P["dx"][s], non_blocking=True)
+                    if d_residual_host is not None:
+                        d_residual_host[i].copy_(P["d_residual"][s], non_blocking=True)
                     drained[i] = ev()
                     drained[i].record(d2h)
         finally:
-            self.dx = keep
+            restore()
         comp.wait_event(drained[n - 1])
+
+
+def _given(**options):
+    return {n: t for n, t in options.items() if t is not None}
 
 
 def weights_to_device(inp: dict, device="cuda") -> dict:

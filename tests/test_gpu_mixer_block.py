@@ -188,3 +188,75 @@ def test_the_example_decodes_as_the_packed_pass(example):
     block.forward(torch.cat(prompts), cu)
     _off(one.mixer.y, block.mixer.y[(cu[1:] - 1).long()], 2 * REL_FRO)
     assert int(one.mixer.err) == 0 and int(block.mixer.err) == 0
+
+
+@pytest.mark.parametrize("router", [None, dict(groups=2, group_k=1)], ids=str)
+@pytest.mark.parametrize("res", [BF, F32])
+@pytest.mark.parametrize("given", [False, True])
+def test_steps_with_a_residual(router, res, given):
+    """A step, its graph, its halves and the steps from the host give what forward and backward give one after the other."""
+    from sparse_moe_layer_topk_gb300.layer import LatentMoELayer, weights_to_device
+    inp = I.make_layer_inputs(0)
+    gen = torch.Generator().manual_seed(6)
+    inp["norm"] = 1 + 0.2 * torch.randn(inp["cfg"].d, generator=gen)
+    cfg, w, n = inp["cfg"], weights_to_device(inp), 3
+    make = lambda: LatentMoELayer(w, cfg.T, cfg.k, residual_dtype=res, router=router)  # noqa: E731
+    rows = lambda dt: [torch.randn(cfg.T, cfg.d, generator=gen).to(dt).pin_memory() for _ in range(n)]  # noqa: E731
+    xs, gs, rs, ds = rows(BF), rows(BF), rows(res), rows(res)
+    ref, want = make(), []
+    for i in range(n):
+        ref.forward(xs[i].cuda(), residual=rs[i].cuda())
+        dx = ref.backward(gs[i].cuda(), d_sum=ds[i].cuda() if given else None)
+        want.append([t.clone() for t in (dx, ref.norm.d_residual, ref.out, ref.norm.sum, *ref.grads.values())])
+
+    def same(layer, i):
+        got = (layer.dx, layer.norm.d_residual, layer.out, layer.norm.sum, *layer.grads.values())
+        assert all(torch.equal(a, b) for a, b in zip(got, want[i])) and int(layer.err) == 0
+
+    layer = make()
+    x, g, r = (v[0].cuda() for v in (xs, gs, rs))
+    kw = dict(d_sum=ds[0].cuda()) if given else {}
+    layer.step(x, g, residual=r, **kw)
+    same(layer, 0)
+    graphs = [layer.capture_step(x, g, residual=r, **kw)], layer.capture_halves(x, g, residual=r, **kw)
+    for parts in graphs:
+        for i in (1, 2):
+            x.copy_(xs[i]), g.copy_(gs[i]), r.copy_(rs[i])
+            if given:
+                kw["d_sum"].copy_(ds[i])
+            for part in parts:
+                part.replay()
+            same(layer, i)
+    for layer, host_graphs in ((layer, True), (layer, False), (make(), False)):
+        own = layer.dx, layer.norm.d_residual
+        for also in (True, False):
+            dx = [torch.empty_like(v).pin_memory() for v in xs]
+            dr = [torch.empty_like(v).pin_memory() for v in rs]
+            layer.steps_from_host(xs, gs, dx, graphs=host_graphs, residual_host=rs, d_sum_host=ds if given else None,
+                                  d_residual_host=dr if also else None)
+            torch.cuda.synchronize()
+            for i in range(n):
+                assert torch.equal(dx[i], want[i][0].cpu()) and (not also or torch.equal(dr[i], want[i][1].cpu())), i
+        assert layer.dx is own[0] and (res == BF or layer.norm.d_residual is own[1])
+        layer.step(xs[1].cuda(), gs[1].cuda(), residual=rs[1].cuda(), **(dict(d_sum=ds[1].cuda()) if given else {}))
+        same(layer, 1)
+
+
+def test_a_layer_whose_steps_take_a_sums_gradient_only_sometimes():
+    """Steps from the host with and without d_sum, in turn, have graphs of their own."""
+    from sparse_moe_layer_topk_gb300.layer import LatentMoELayer, weights_to_device
+    inp = I.make_layer_inputs(0)
+    inp["norm"] = torch.ones(inp["cfg"].d)
+    cfg, w, gen = inp["cfg"], weights_to_device(inp), torch.Generator().manual_seed(8)
+    layer = LatentMoELayer(w, cfg.T, cfg.k, residual_dtype=BF)
+    x, g, r, d = ([torch.randn(cfg.T, cfg.d, generator=gen).to(BF).pin_memory()] for _ in range(4))
+    want = []
+    for kw in ({}, dict(d_sum=d[0].cuda())):
+        layer.step(x[0].cuda(), g[0].cuda(), residual=r[0].cuda(), **kw)
+        want.append(layer.dx.cpu())
+    assert not torch.equal(*want)
+    for turn in (0, 1, 0, 1):
+        out = [torch.empty_like(x[0]).pin_memory()]
+        layer.steps_from_host(x, g, out, residual_host=r, d_sum_host=d if turn else None)
+        torch.cuda.synchronize()
+        assert torch.equal(out[0], want[turn])

@@ -157,3 +157,17 @@ def test_a_layers_gradient_of_a_sum_that_is_not_there():
     for d_sum in (g.float(), g[:3], torch.zeros(4, 2 * g.shape[1], dtype=BF)[:, ::2]):
         with pytest.raises(ValueError, match="d_sum"):
             layer.backward(g, d_sum=d_sum)
+
+
+def test_residuals_of_steps_from_the_host():
+    inp = I.make_layer_inputs(0)
+    w = weights_to_device(inp, "cpu")
+    normed = {**w, "norm": torch.ones(w["Wr"].shape[0])}
+    x = [inp["x"][:4].contiguous()]
+    plain, layer = LatentMoELayer(w, 4, 2, device="cpu"), LatentMoELayer(normed, 4, 2, device="cpu", residual_dtype=BF)
+    for make, kw, match in ((layer, {}, "residual"), (plain, dict(residual_host=x), "residual"), (plain, dict(d_sum_host=x), "no sum"),
+                            (plain, dict(d_residual_host=x), "no sum"), (layer, dict(residual_host=x * 2), "residual_host is 1"),
+                            (layer, dict(residual_host=[x[0].float()]), "residual_host"), (layer, dict(residual_host=x, d_sum_host=[x[0][:3]]), "d_sum_host"),
+                            (layer, dict(residual_host=x, d_residual_host=[x[0].float()]), "d_residual_host")):
+        with pytest.raises(ValueError, match=match):
+            make.steps_from_host(x, x, x, **kw)
