@@ -347,6 +347,9 @@ class LatentMoELayer:
                 loaded_g[i] = ev()
                 loaded_g[i].record(h2d)
 
+        called = ev()
+        called.record(comp)
+        h2d.wait_event(called)  # the slots' readers of an earlier call, or their memory's users before
         load(0)
         try:
             for i in range(n):

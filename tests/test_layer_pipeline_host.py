@@ -88,3 +88,30 @@ def test_each_step_gets_its_own_inputs_and_gradient(graphs, n):
         assert torch.equal(outs2[i], xs[n - 1 - i] + gs[n - 1 - i]), i
     assert layer.dx is own
     assert layer.captures == (2 if graphs else 0)
+
+
+def test_copies_wait_for_what_ran_before():
+    """The slots may still be read by an earlier call's steps, or be memory that earlier work used: the first copy into them comes behind
+    what the current stream holds at the call."""
+    log = []
+
+    class Stream(_Stream):
+        def wait_event(self, e):
+            super().wait_event(e)
+            log.append(("wait", self, e))
+
+    class Event(_Event):
+        def record(self, stream=None):
+            super().record(stream)
+            self.stream = stream
+
+    current = Stream()
+    layer = _Layer(4, 8)
+    x = [torch.ones(4, 8)] * 2
+    with mock.patch.object(torch.cuda, "current_stream", lambda *a: current), mock.patch.object(torch.cuda, "Stream", Stream), \
+            mock.patch.object(torch.cuda, "Event", Event), mock.patch.object(torch.cuda, "stream", lambda s: log.append(("on", s)) or _Ctx(s)):
+        layer.steps_from_host(x, x, [torch.zeros(4, 8) for _ in x], graphs=False)
+    first = next(i for i, entry in enumerate(log) if entry[0] == "on")
+    copies = log[first][1]
+    assert copies is not current
+    assert any(kind == "wait" and s is copies and e.stream is current for kind, s, e in log[:first])
