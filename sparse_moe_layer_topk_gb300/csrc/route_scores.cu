@@ -583,8 +583,9 @@ __global__ void __launch_bounds__(kWarps * 32, NPL < 28 ? 1 : GROUPED ? 4 : 5) r
 //   renormalised  dl_j = w_j (g_j - sum_i w_i g_i / scale) (1 - s_j for the sigmoid), 0 for the others
 //   sigmoid       dl_j = g_j w_j (1 - s_j), 0 for the others
 //   softmax       dl_e = scale p_e (g_e [chosen] - sum_j s_j g_j), for which the logits are read again
-// The row is written whole by all lanes, then the chosen entries over it by theirs.
-template <bool DENSE, bool SOFTMAX, typename OUT>
+// The row is written whole by all lanes, then the chosen entries over it by theirs. 1 - s of a sigmoid comes from the logit where the logits are
+// given: from s itself it has lost 4 % at a logit of 14, and all above 17.
+template <bool DENSE, bool SOFTMAX, bool FROM_LOGITS, typename OUT>
 __global__ void __launch_bounds__(256) route_scores_bwd_kernel(RouteBwdArgs a) {
   const int t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
@@ -612,7 +613,7 @@ __global__ void __launch_bounds__(256) route_scores_bwd_kernel(RouteBwdArgs a) {
     }
   }
   const size_t o = static_cast<size_t>(t) * a.k + lane;
-  float gw = 0.0f, w = 0.0f, s = 0.0f;
+  float gw = 0.0f, w = 0.0f, s = 0.0f, x_j = 0.0f;
   int e = -1 - lane;  // (different from one another)
   if (lane < a.k) {
     if (a.slot_of) {
@@ -628,6 +629,7 @@ __global__ void __launch_bounds__(256) route_scores_bwd_kernel(RouteBwdArgs a) {
     if (a.d_topk_w) a.d_topk_w[o] = gw;
     if (id >= 0 && id < a.E) {
       e = id;
+      if (FROM_LOGITS) x_j = __ldg(l + id);
     } else {
       set_flag(a.err_flag, MOE_FLAG_BAD_EXPERT);
       gw = 0.0f;
@@ -655,7 +657,7 @@ __global__ void __launch_bounds__(256) route_scores_bwd_kernel(RouteBwdArgs a) {
     __syncwarp();
     float d = gw * w;
     if (a.renorm) d = w * (gw - dot / a.scale);
-    if (!SOFTMAX) d *= 1.0f - s;
+    if (!SOFTMAX) d *= FROM_LOGITS && x_j < -neg_inf() ? 1.0f / (1.0f + expf(x_j)) : 1.0f - s;
     if (e >= 0) row[e] = OUT(d);
     return;
   }
@@ -736,9 +738,10 @@ cudaError_t launch_route_scores_bwd(const RouteBwdArgs& a, cudaStream_t st) {
     if (a.bf16_out) b16<<<grid, 256, 0, st>>>(a);
     else f32<<<grid, 256, 0, st>>>(a);
   };
-  if (dense) run(route_scores_bwd_kernel<true, true, float>, route_scores_bwd_kernel<true, true, bf16>);
-  else if (a.softmax) run(route_scores_bwd_kernel<false, true, float>, route_scores_bwd_kernel<false, true, bf16>);
-  else run(route_scores_bwd_kernel<false, false, float>, route_scores_bwd_kernel<false, false, bf16>);
+  if (dense) run(route_scores_bwd_kernel<true, true, false, float>, route_scores_bwd_kernel<true, true, false, bf16>);
+  else if (a.softmax) run(route_scores_bwd_kernel<false, true, false, float>, route_scores_bwd_kernel<false, true, false, bf16>);
+  else if (a.logits) run(route_scores_bwd_kernel<false, false, true, float>, route_scores_bwd_kernel<false, false, true, bf16>);
+  else run(route_scores_bwd_kernel<false, false, false, float>, route_scores_bwd_kernel<false, false, false, bf16>);
   return cudaGetLastError();
 }
 

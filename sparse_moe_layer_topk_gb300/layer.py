@@ -217,7 +217,7 @@ class LatentMoELayer:
         aux = self.aux_scale > 0
         dx = self.dx if self.norm is None else self.d_normed
         if self.router is not None:
-            dL = self.router.backward(self.d_row_w, self.slot_of, self.d_topk_w, stream)
+            dL = self.router.backward(self.d_row_w, self.slot_of, self.d_topk_w, stream, self.router.saved)
             M.moe_router_grads(dL, self.x, w["Wr"], T, d, E, dx, g["Wr"], wd, self.dz, w["W_dn"], l, stream)
         else:
             M.moe_route_topk_bwd(self.d_row_w, self.slot_of, self.topk_idx, self.topk_w, self.topk_s,

@@ -63,9 +63,11 @@ class Router:
                            self.renorm, self.scale, self.topk_idx, self.topk_w, self.topk_s, self.err, stream)
         return self.topk_idx, self.topk_w
 
-    def backward(self, d_w, slot_of=None, d_topk_w=None, stream=None):
+    def backward(self, d_w, slot_of=None, d_topk_w=None, stream=None, logits=None):
         """d_logits [T, E] of the last forward for d_w = d loss / d topk_w (fp32 [T, k]); with slot_of (int32 [T, k] of
-        moe_permute) d_w is that of the permuted rows, and d_topk_w (fp32 [T, k]), if given, receives it in the tokens' order."""
+        moe_permute) d_w is that of the permuted rows, and d_topk_w (fp32 [T, k]), if given, receives it in the tokens' order.
+        logits: the forward's, if they are still as they were. Sigmoid scores next to one then keep their gradient: from the
+        fp32 score alone 1 - s is off by 2^-23, and 0 for logits above 17."""
         if self.saved is None:
             raise ValueError("backward needs a forward before it")
         if slot_of is None:
@@ -75,7 +77,11 @@ class Router:
             self._check("d_w", d_w, (self.T * self.k,))
         if d_topk_w is not None:
             self._check("d_topk_w", d_topk_w, (self.T, self.k))
-        M.moe_route_scores_bwd(d_w, slot_of, self.saved, self.topk_idx, self.topk_w, self.topk_s, self.T, self.E, self.k,
+        if logits is not None:
+            self._check("logits", logits, (self.T, self.E))
+        elif self.score == M.MOE_SCORE_SOFTMAX and not self.renorm:
+            logits = self.saved
+        M.moe_route_scores_bwd(d_w, slot_of, logits, self.topk_idx, self.topk_w, self.topk_s, self.T, self.E, self.k,
                                self.score, self.renorm, self.scale, self.d_logits, _DTYPES[self.grad_dtype], d_topk_w,
                                self.err, stream)
         return self.d_logits

@@ -446,3 +446,30 @@ def test_scores_below_the_smallest_normal_number():
     for k in (1, 2, 3):
         _check(l, b, k)
         _check(torch.cat([l, torch.zeros(3, 64)], 1), torch.cat([b, torch.full((64,), -1.0)]), k, "softmax")
+
+
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_gradient_of_scores_next_to_one(renorm, dtype):
+    """With the logits, 1 - s keeps its relative precision where s itself is 1 in fp32. Against scores and weights in 64 bits from the logits:
+    w and s are off by 2^-17 of themselves and the sum of them by as much, 1 - s by 2^-21 (|l| < 32: the argument's rounding 2^-20)."""
+    T, E, k = 64, 64, 6
+    l = 2 + 24 * torch.rand(T, E, generator=torch.Generator().manual_seed(21))
+    l[9, 3:60], l[10, 4] = -torch.inf, -30.0
+    g = torch.randn(T, k, generator=torch.Generator().manual_seed(22))
+    r = _router(T, E, k, renorm=renorm, scale=2.5, grad_dtype=dtype)
+    r.forward(l.cuda(), _bias(E).cuda())
+    got = f64(r.backward(g.cuda(), logits=l.cuda()))
+    idx = r.topk_idx.cpu().numpy().astype(np.int64)
+    assert (np.take_along_axis(f64(l), idx, 1) > 17).mean() > 0.2
+    chosen = np.take_along_axis(f64(l), idx, 1)
+    s, rest = O.sigmoid(chosen), O.sigmoid(-chosen)
+    w = 2.5 * (s / s.sum(1, keepdims=True) if renorm else s)
+    v = w * (f64(g) - (w * f64(g)).sum(1, keepdims=True) / 2.5) if renorm else w * f64(g)
+    size = w * (np.abs(f64(g)) + ((w * np.abs(f64(g))).sum(1, keepdims=True) / 2.5 if renorm else 0))
+    want, bound = np.zeros((T, E)), np.zeros((T, E))
+    np.put_along_axis(want, idx, v * rest, 1)
+    np.put_along_axis(bound, idx, (4 * TOL + 2.0 ** -19) * size * rest, 1)
+    bound = bound + (2.0 ** -8 * np.abs(want) if dtype == torch.bfloat16 else 0) + 1e-37
+    assert (np.abs(got - want) <= bound).all()
+    assert int(r.err) == 0
