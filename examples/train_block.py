@@ -128,7 +128,7 @@ class ScanBlock:
         self.norm = RMSNorm(w.norm, T, backward=backward)
         self.conv = CausalConv(w.conv_w, w.conv_b, T, N=N, backward=backward)
         self.mixer = SelectiveScan(self.A, T, w.skip, w.dt_bias, N=N, max_seqlen=max_seqlen, backward=backward)
-        self.moe = LatentMoELayer(w.moe, T, w.cfg.k, residual_dtype=BF16, router=dict(groups=2, group_k=2, scale=1.0))
+        self.moe = LatentMoELayer(w.moe, T, w.cfg.k, residual_dtype=BF16, router=dict(groups=4, group_k=2))
         e = lambda *s: torch.empty(s, dtype=BF16, device="cuda")  # noqa: E731
         self.vz, self.bc, self.delta, self.att = e(T, 2 * D), e(T, 2 * R), e(T, D), e(T, self.d)
         if backward:

@@ -260,3 +260,16 @@ def test_a_layer_whose_steps_take_a_sums_gradient_only_sometimes():
         layer.steps_from_host(x, g, out, residual_host=r, d_sum_host=d if turn else None)
         torch.cuda.synchronize()
         assert torch.equal(out[0], want[turn])
+
+
+def test_the_example_chooses_experts_in_groups(example):
+    """Some groups of experts are left out for each token, others for other tokens."""
+    w = example.ScanWeights(0)
+    T = 96
+    block = example.ScanBlock(w, T, 1, T)
+    x = torch.randn(T, w.cfg.d, generator=torch.Generator().manual_seed(5)).to(BF)
+    block.forward(x.cuda(), torch.tensor([0, T], dtype=torch.int32, device="cuda"))
+    r = block.moe.router
+    assert 1 < r.group_k < r.groups
+    groups = block.moe.topk_idx.cpu() // (w.cfg.E // r.groups)
+    assert all(len(set(row)) <= r.group_k for row in groups.tolist()) and set(groups.flatten().tolist()) == set(range(r.groups))
