@@ -17,6 +17,7 @@ token before it, which only the mixer can carry over. PyTorch provides memory, s
 the residual sums and the loss.
 """
 import argparse
+import dataclasses
 import os
 import sys
 
@@ -36,11 +37,15 @@ BF16 = torch.bfloat16
 HS, R, DK, DV = 2, 2, 64, 128  # state heads, query heads for each, widths
 
 
+def _layer_inputs(seed):
+    return I.make_layer_inputs(dataclasses.replace(I.CONFIGS[0], seed=seed))
+
+
 class Weights:
     """A block's weights on the device: the mixer's two projections and the layer's."""
 
     def __init__(self, seed=0):
-        inp = I.make_layer_inputs(seed)
+        inp = _layer_inputs(seed)
         self.cfg = inp["cfg"]
         d = self.cfg.d
         g = torch.Generator().manual_seed(seed)
@@ -104,7 +109,7 @@ class ScanWeights:
     INNER, STATES, RANK, TAPS = 512, 16, 64, 4
 
     def __init__(self, seed=0):
-        inp = I.make_layer_inputs(seed)
+        inp = _layer_inputs(seed)
         self.cfg = inp["cfg"]
         d, D, S, R = self.cfg.d, self.INNER, self.STATES, self.RANK
         g = torch.Generator().manual_seed(seed)

@@ -41,3 +41,12 @@ def test_decoding_answers_as_the_packed_pass(example):
     ref, got = f64(block.mixer.o[last]), f64(one.mixer.o)
     assert np.linalg.norm(got - ref) <= 2 * REL_FRO * np.linalg.norm(ref)
     assert int(one.mixer.err) == 0 and int(block.mixer.err) == 0
+
+
+def test_seeds_make_other_weights_of_the_same_sizes(example):
+    for kind in (example.Weights, example.ScanWeights):
+        a, b, c = kind(0), kind(3), kind(3)
+        assert a.moe["Wr"].shape == b.moe["Wr"].shape and not torch.equal(a.moe["Wr"], b.moe["Wr"])
+        assert all(torch.equal(b.moe[n], c.moe[n]) for n in ("Wr", "W13", "W_up"))
+    losses, _ = example.train([20, 12], 2, seed=7)
+    assert len(losses) == 2
