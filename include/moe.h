@@ -181,6 +181,7 @@ int moe_route_scores(const float* logits, const float* bias, int T, int E, int k
  *   renorm            d_l = w_j (g_j - sum_i w_i g_i / scale), times (1 - s_j) for the sigmoid; 0 for the others
  *   sigmoid           d_l = g_j w_j (1 - s_j); 0 for the others
  *   softmax           d_l[e] = scale p_e (g_e [e chosen] - sum_j s_j g_j), p the softmax of `logits` (needed here)
+ *                     (16-byte aligned where E is a multiple of 4)
  * For the sigmoid `logits` may be NULL: 1 - s_j is then that of the fp32 score, off by 2^-23, which is 4 % of it at a logit of 14 and
  * all of it above 17; from the logits it is right to fp32. With renormalised softmax scores they are not read.
  * g_j = d_w[t][j], or, with slot_of (of moe_permute), d_w[slot_of[t][j]] of moe_grouped_swiglu_bwd's d_row_w (0 for a

@@ -142,7 +142,7 @@ int moe_route_scores_bwd(const float* d_w, const int32_t* slot_of, const float* 
   MOE_REQUIRE(std::isfinite(scale) && scale != 0.0f, MOE_ERR_ARG);
   const bool dense = score == MOE_SCORE_SOFTMAX && !renorm;
   MOE_REQUIRE(!dense || logits != nullptr, MOE_ERR_ARG);
-  MOE_REQUIRE(aligned(d_logits, 16) && aligned(logits, dense ? 16 : 4), MOE_ERR_ALIGN);
+  MOE_REQUIRE(aligned(d_logits, 16) && aligned(logits, dense && E % 4 == 0 ? 16 : 4), MOE_ERR_ALIGN);
   if (T == 0) return MOE_OK;
   const RouteBwdArgs a{d_w, slot_of, logits, topk_idx, topk_w, topk_s, T, E, k, score == MOE_SCORE_SOFTMAX, renorm != 0,
                        scale, d_logits, dtype == MOE_DTYPE_BF16, d_topk_w, err_flag};

@@ -54,7 +54,8 @@ class Router:
 
     def forward(self, logits, bias=None, stream=None):
         """(topk_idx, topk_w), this instance's buffers [T, k], for fp32 logits [T, E] and bias [E]; topk_s holds the scores.
-        The logits have to stay as they are until backward where its scores are softmax and not renormalised."""
+        The logits have to stay as they are until backward where its scores are softmax and not renormalised (and to lie on 16
+        bytes there, if E is a multiple of 4)."""
         self._check("logits", logits, (self.T, self.E))
         if bias is not None:
             self._check("bias", bias, (self.E,))

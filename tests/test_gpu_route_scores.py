@@ -473,3 +473,16 @@ def test_gradient_of_scores_next_to_one(renorm, dtype):
     bound = bound + (2.0 ** -8 * np.abs(want) if dtype == torch.bfloat16 else 0) + 1e-37
     assert (np.abs(got - want) <= bound).all()
     assert int(r.err) == 0
+
+
+@pytest.mark.parametrize("E", [62, 63, 65])
+def test_dense_gradient_of_logits_that_start_anywhere(E):
+    T, k = 9, 5
+    logits, g = _logits(T, E, 3), torch.randn(T, k, generator=torch.Generator().manual_seed(4)).cuda()
+    grads = []
+    for at in range(4):
+        l = torch.zeros(T * E + at, device="cuda")[at:].view(T, E).copy_(logits)
+        r = _router(T, E, k, score="softmax", renorm=False)
+        r.forward(l)
+        grads.append(r.backward(g).clone())
+    assert all(torch.equal(d, grads[0]) for d in grads) and bool(grads[0].any())

@@ -155,3 +155,11 @@ def test_tile_states_hold_every_tile(lib):
         taken += [at // 32 + n + k for k in range(-(-length // 32))]
         at += length
     assert at == 100 and len(set(taken)) == len(taken) and max(taken) < 100 // 32 + 5
+
+
+@pytest.mark.parametrize("E,logits,want", [(64, P + 4, ALIGN), (66, P + 4, OK), (63, P + 8, OK), (63, P + 2, ALIGN), (64, P, OK)])
+@pytest.mark.parametrize("renorm", [0, 1])
+def test_logits_that_the_dense_gradient_reads(lib, E, logits, want, renorm):
+    """Expert counts that are not a multiple of 4 are read one by one, from any place of a float; renormalised scores need no logits."""
+    got = lib.moe_route_scores_bwd(*{**ROUTE_BWD, "E": E, "logits": logits, "renorm": renorm, "T": 0}.values())
+    assert got == (OK if renorm and logits % 4 == 0 else want)
