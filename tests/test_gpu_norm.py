@@ -183,3 +183,35 @@ def test_gradients_in_place(T, d, place, dtype):
         now = {n: t.clone() for n, t in ops.items()}
         dw = run(**now, **{name: now[place], other: None})
         assert torch.equal(now[place], result) and torch.equal(dw, want)
+
+
+@pytest.mark.parametrize("size", [1e18, 1e25, 3e38, 1e-30])
+@pytest.mark.parametrize("res", [None, BF, F32])
+@pytest.mark.parametrize("given", [False, True])
+@pytest.mark.parametrize("d", [512, 2048, 5120])
+def test_gradients_of_values_whose_squares_leave_fp32(size, res, given, d):
+    """dx is as small as the values are large (rstd): d_sum, where it is given, is of its size. One row in three has ordinary values."""
+    if given and res is None:
+        return
+    x, r, w, dy, ds = _inputs(7, d, res, 5)
+    big = torch.tensor([1.0, 0.0, 0.0, 1.0, 1.0, 0.0, 1.0])[:, None] > 0
+    x = torch.where(big, x.float().clamp(-1, 1) * size, x.float()).to(BF)
+    if r is not None:
+        r = torch.where(big, torch.zeros_like(r), r)
+    n = _norm(w.cuda(), 7, EPS, res)
+    n.forward(x.cuda(), None if r is None else r.cuda())
+    u = f64(x) if r is None else f64(n.sum)
+    rstd = 1 / np.sqrt((u * u).mean(1, keepdims=True) + EPS)
+    ds = None
+    if given:
+        ds = (torch.randn(7, d, generator=torch.Generator().manual_seed(9)).double() * torch.from_numpy(rstd)).to(res)
+    dx = n.backward(dy.cuda(), None if ds is None else ds.cuda())
+    want, dw = O.rmsnorm_backward(f64(dy), u, f64(w), EPS, None if ds is None else f64(ds))
+    gw = np.abs(f64(dy) * f64(w))
+    bound = TOL * (rstd * (gw + np.abs(u * rstd) * (gw * np.abs(u * rstd)).mean(1, keepdims=True)) + (0 if ds is None else np.abs(f64(ds))))
+    # (2^-126 and below: what fp32 and bf16 leave of a gradient is a multiple of 2^-133 there)
+    assert (np.abs(f64(dx) - want) <= 2.0 ** -8 * np.abs(want) + bound + 2.0 ** -126).all()
+    if res is not None:
+        half = 2.0 ** -8 if res == BF else 2.0 ** -24
+        assert (np.abs(f64(n.d_residual) - want) <= half * np.abs(want) + bound + 2.0 ** -126).all()
+    assert (np.abs(f64(n.dw) - dw) <= 2 * TOL * (np.abs(f64(dy)) * np.abs(u * rstd)).sum(0) + 1e-37).all()

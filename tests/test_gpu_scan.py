@@ -561,3 +561,50 @@ def test_time_steps_that_are_no_numbers_stay_so():
     delta[1], delta[2] = float("nan"), float("inf")
     y = s.forward(one, delta, b, b)
     assert bool(y[1].isnan().all()) and bool(y[2].isinf().all()) and bool(y[[0, 3]].isfinite().all())
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_a_scan_step_directly_behind_its_convolution(captured):
+    """The scan's step reads what the convolution's has just written (their starts overlap), row after row and token after token, as a
+    decoding loop and as a graph that is replayed: the same bits as with a wait between them."""
+    from sparse_moe_layer_topk_gb300.scan import CausalConv, SelectiveScan
+    R, D, S, W, steps, g = 61, 1032, 16, 4, 12, torch.Generator().manual_seed(6)
+    n = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    taps, cb, A, skip, bias = n(D, W).cuda(), n(D).cuda(), -torch.exp(n(D, S)).cuda(), n(D).cuda(), (n(D) - 2).cuda()
+    xs = n(steps, R, D).to(BF).cuda()
+    delta, z = n(R, D).to(BF).cuda(), n(R, D).to(BF).cuda()
+    B, C = n(R, 1, S).to(BF).cuda(), n(R, 1, S).to(BF).cuda()
+    idx = torch.randperm(R + 3, generator=g)[:R].to(torch.int32).cuda()
+    idx[5] = -1
+    first = n(R + 3, W - 1, D).to(BF).cuda(), n(R + 3, D, S).cuda()
+
+    def run(wait):
+        conv, scan = CausalConv(taps, cb, R, backward=False), SelectiveScan(A, R, skip, bias, backward=False)
+        x, inputs, states, ys = torch.empty_like(xs[0]), first[0].clone(), first[1].clone(), []
+
+        def token():
+            v = conv.step(x, inputs, idx)
+            if wait:
+                torch.cuda.synchronize()
+            return scan.step(v, delta, B, C, z, states, idx)
+        if captured and not wait:
+            x.copy_(xs[0])
+            token()  # (kernels' attributes are set outside the capture)
+            inputs.copy_(first[0]), states.copy_(first[1])
+            torch.cuda.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                token()
+            inputs.copy_(first[0]), states.copy_(first[1])
+        for t in range(steps):
+            x.copy_(xs[t])
+            if captured and not wait:
+                graph.replay()
+            else:
+                token()
+            ys.append(scan.y.clone())
+        assert int(conv.err) == 0 and int(scan.err) == 0
+        return torch.stack(ys), inputs, states
+
+    for a, b in zip(run(False), run(True)):
+        assert torch.equal(a, b) and bool(a.isfinite().all())
