@@ -151,7 +151,8 @@ __global__ void __launch_bounds__(kThreads, 5) conv_fwd_kernel(ConvArgs a, int b
 // waits for by itself: in registers there is room for one group, and it waits for memory. 40 registers of weights and sums and the two
 // windows leave 16 warps an SM, whose arithmetic bounds it: 16,384 tokens x 8,192 channels in 149 us, 119 of them the bytes (with one group ahead in
 // registers 184; groups of 2 tokens instead of 4: 166, of 6: 153; three CTAs an SM: 165, five spill: 190 and more).
-template <int W, bool SILU>
+// FEW: less than 128 sequences, as find_part takes it. (Its walk over more of them in the parts' loop costs the tokens' loop registers: 157 us for 153.)
+template <int W, bool SILU, bool FEW>
 __global__ void __launch_bounds__(kThreads, kBwdCtas) conv_bwd_kernel(ConvBwdArgs a, int blocks, int length) {
   constexpr int kStep = 4;
   __shared__ uint2 ring[kBwdRing][kStep][2][kThreads];  // (x, dy) of a thread's channels, its own to write and to read
@@ -172,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) conv_bwd_kernel(ConvBwdArg
   }
   SeqPart s;
   for (int part = walker;
-       find_part(a.cu, a.N, a.T, a.T, length, part, s, block == 0 && threadIdx.x < 32 ? a.err_flag : nullptr);
+       find_part<FEW>(a.cu, a.N, a.T, a.T, length, part, s, block == 0 && threadIdx.x < 32 ? a.err_flag : nullptr);
        part += walkers) {
     if (!mine) continue;
     const int t0 = s.part * length, t1 = min(s.len, t0 + length);
@@ -332,17 +333,21 @@ int most_parts(int N, int T, int length) { return T / length + N; }
 #define MOE_CONV_DISPATCH(KERNEL, GRID, ...)                                                   \
   do {                                                                                          \
     const auto run = [&](auto kernel) { kernel<<<(GRID) * blocks, kThreads, 0, st>>>(__VA_ARGS__); }; \
-    if (a.W == 2) a.silu ? run(KERNEL<2, true>) : run(KERNEL<2, false>);                        \
-    else if (a.W == 3) a.silu ? run(KERNEL<3, true>) : run(KERNEL<3, false>);                   \
-    else a.silu ? run(KERNEL<4, true>) : run(KERNEL<4, false>);                                 \
+    if (a.W == 2) a.silu ? run(KERNEL(2, true)) : run(KERNEL(2, false));                        \
+    else if (a.W == 3) a.silu ? run(KERNEL(3, true)) : run(KERNEL(3, false));                   \
+    else a.silu ? run(KERNEL(4, true)) : run(KERNEL(4, false));                                 \
   } while (0)
+#define MOE_CONV_FWD(W, SILU) conv_fwd_kernel<W, SILU>
+#define MOE_CONV_BWD_FEW(W, SILU) conv_bwd_kernel<W, SILU, true>
+#define MOE_CONV_BWD_MANY(W, SILU) conv_bwd_kernel<W, SILU, false>
+#define MOE_CONV_STEP(W, SILU) conv_step_kernel<W, SILU>
 
 }  // namespace
 
 cudaError_t launch_conv_fwd(const ConvArgs& a, cudaStream_t st) {
   LaunchTimer lt("conv_fwd", st);
   const int blocks = channel_blocks(a.D);
-  MOE_CONV_DISPATCH(conv_fwd_kernel, most_parts(a.N, a.T, kFwdTokens), a, blocks);
+  MOE_CONV_DISPATCH(MOE_CONV_FWD, most_parts(a.N, a.T, kFwdTokens), a, blocks);
   return cudaGetLastError();
 }
 
@@ -373,7 +378,8 @@ cudaError_t launch_conv_bwd(const ConvBwdArgs& a, float* dw, float* db, cudaStre
   {
     LaunchTimer lt("conv_bwd", st);
     const int blocks = channel_blocks(a.D);
-    MOE_CONV_DISPATCH(conv_bwd_kernel, parts, a, blocks, d.length);
+    if (a.cu == nullptr || a.N < kWalk) MOE_CONV_DISPATCH(MOE_CONV_BWD_FEW, parts, a, blocks, d.length);
+    else MOE_CONV_DISPATCH(MOE_CONV_BWD_MANY, parts, a, blocks, d.length);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || a.part == nullptr) return e;
   }
@@ -384,7 +390,7 @@ cudaError_t launch_conv_bwd(const ConvBwdArgs& a, float* dw, float* db, cudaStre
 cudaError_t launch_conv_step(const ConvStepArgs& a, cudaStream_t st) {
   LaunchTimer lt("conv_step", st);
   const int blocks = channel_blocks(a.D);
-  MOE_CONV_DISPATCH(conv_step_kernel, a.B, a, blocks);
+  MOE_CONV_DISPATCH(MOE_CONV_STEP, a.B, a, blocks);
   return cudaGetLastError();
 }
 

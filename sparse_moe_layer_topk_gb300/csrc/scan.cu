@@ -289,15 +289,16 @@ constexpr int kFwdQuads = kFwdRow / 4;        // a thread's place where it takes
 // Shared memory: two stages of u, delta and z; the pairs; two stages of B and C.
 constexpr int kFwdSmem = (2 * 3 * kFwdTile / 2 + 2 * kFwdTile + 2 * 2 * kTile * kBRow) * 4;
 
-// SUMS: only the state that a part leaves from a zero state and the sum of its dt, for parts of long sequences.
-template <bool SUMS>
+// SUMS: only the state that a part leaves from a zero state and the sum of its dt, for parts of long sequences. FEW: less than 128 sequences, as
+// find_part takes it (its call for more of them costs 1 % in the registers that are left).
+template <bool SUMS, bool FEW>
 __global__ void __launch_bounds__(kFwdWarps * 32, 4) scan_fwd_kernel(ScanArgs a, int blocks, int length, const float* starts,
                                                                      float* sums, float* dt_sums) {
   extern __shared__ float pool[];
   const int warp = threadIdx.x >> 5, lane = static_cast<int>(lane_id());
   const int part = blockIdx.x / blocks;
   SeqPart s;
-  if (!find_part(a.cu, a.N, a.T, a.max_seqlen, length, part, s, !SUMS && blockIdx.x % blocks == 0 && warp == 0 ? a.err_flag : nullptr)) return;
+  if (!find_part<FEW>(a.cu, a.N, a.T, a.max_seqlen, length, part, s, !SUMS && blockIdx.x % blocks == 0 && warp == 0 ? a.err_flag : nullptr)) return;
   const Channels ch = block_channels(blockIdx.x % blocks, a.D, a.G, kFwdRow);
   const int t0 = s.part * length, count = min(length, s.len - t0);  // (0 in an empty sequence)
   if (SUMS && length >= s.len - t0) return;  // nothing reads the last part's
@@ -528,6 +529,7 @@ struct BwdWs {
   float* d_part;    // [2][parts][D]: skip, dt_bias
 };
 
+template <bool FEW>
 __global__ void __launch_bounds__(kBwdWarps * 32, 1) scan_bwd_kernel(ScanBwdArgs a, int blocks, int parts, int length, bool cut, BwdWs ws) {
   extern __shared__ float pool[];
   const ScanArgs& f = a.f;
@@ -536,7 +538,7 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 1) scan_bwd_kernel(ScanBwdArgs
   const long long all = static_cast<long long>(f.D) * f.S;
   const Channels ch = block_channels(block, f.D, f.G, kBwdRow);
   SeqPart s;
-  if (!find_part(f.cu, f.N, f.T, f.max_seqlen, length, part, s, block == 0 && warp == 0 ? f.err_flag : nullptr)) {
+  if (!find_part<FEW>(f.cu, f.N, f.T, f.max_seqlen, length, part, s, block == 0 && warp == 0 ? f.err_flag : nullptr)) {
     // a part that does not exist adds nothing to the sums over the parts
     for (int i = threadIdx.x; i < ch.have * f.S; i += kBwdWarps * 32) ws.dA_part[part * all + static_cast<long long>(ch.c0) * f.S + i] = 0.0f;
     for (int i = threadIdx.x; i < ch.have; i += kBwdWarps * 32)
@@ -1078,21 +1080,22 @@ size_t scan_workspace(int max_seqlen, int T, int N, int D, int S, int G, bool ba
   return bytes;
 }
 
-cudaError_t launch_scan_fwd(const ScanArgs& a, cudaStream_t st) {
+template <bool FEW>
+static cudaError_t scan_fwd(const ScanArgs& a, cudaStream_t st) {
   const Division d = divide(a.max_seqlen, a.T, a.N, a.D, a.G, false);
   const unsigned grid = static_cast<unsigned>(d.parts * d.blocks);
   const int smem = kFwdSmem;
-  cudaError_t e = prepare_kernel<scan_fwd_kernel<false>>(smem);
+  cudaError_t e = prepare_kernel<scan_fwd_kernel<false, FEW>>(smem);
   if (e != cudaSuccess) return e;
   float* starts = nullptr;
   if (d.cut) {
     starts = a.ws;
     float* const dt_sums = reinterpret_cast<float*>(reinterpret_cast<char*>(a.ws) + up256(static_cast<size_t>(d.parts) * a.D * a.S * 4));
-    e = prepare_kernel<scan_fwd_kernel<true>>(smem);
+    e = prepare_kernel<scan_fwd_kernel<true, FEW>>(smem);
     if (e != cudaSuccess) return e;
     {
       LaunchTimer lt("scan_fwd_sums", st);
-      scan_fwd_kernel<true><<<grid, kFwdWarps * 32, smem, st>>>(a, d.blocks, d.length, nullptr, starts, dt_sums);
+      scan_fwd_kernel<true, FEW><<<grid, kFwdWarps * 32, smem, st>>>(a, d.blocks, d.length, nullptr, starts, dt_sums);
     }
     LaunchTimer lt("scan_join", st);
     const unsigned join = static_cast<unsigned>(d.parts * ((a.D * (a.S / 4) + 127) / 128));
@@ -1101,11 +1104,15 @@ cudaError_t launch_scan_fwd(const ScanArgs& a, cudaStream_t st) {
   }
   LaunchTimer lt("scan_fwd", st);
   if (d.cut)
-    return launch_behind(scan_fwd_kernel<false>, dim3(grid), kFwdWarps * 32, smem, st, a, d.blocks, d.length,
+    return launch_behind(scan_fwd_kernel<false, FEW>, dim3(grid), kFwdWarps * 32, smem, st, a, d.blocks, d.length,
                          static_cast<const float*>(starts), static_cast<float*>(nullptr), static_cast<float*>(nullptr));
-  scan_fwd_kernel<false><<<grid, kFwdWarps * 32, smem, st>>>(a, d.blocks, d.length, nullptr, nullptr, nullptr);
+  scan_fwd_kernel<false, FEW><<<grid, kFwdWarps * 32, smem, st>>>(a, d.blocks, d.length, nullptr, nullptr, nullptr);
   return cudaGetLastError();
 }
+
+static bool few(const ScanArgs& a) { return a.cu == nullptr || a.N < kWalk; }
+
+cudaError_t launch_scan_fwd(const ScanArgs& a, cudaStream_t st) { return few(a) ? scan_fwd<true>(a, st) : scan_fwd<false>(a, st); }
 
 cudaError_t launch_scan_bwd(const ScanBwdArgs& a, cudaStream_t st) {
   const ScanArgs& f = a.f;
@@ -1123,7 +1130,8 @@ cudaError_t launch_scan_bwd(const ScanBwdArgs& a, cudaStream_t st) {
   ws.bc_part = take(static_cast<size_t>(d.blocks) * f.T * 32 * 4);
   ws.dA_part = take(d.parts * all * 4);
   ws.d_part = take(2 * d.parts * static_cast<size_t>(f.D) * 4);
-  cudaError_t e = prepare_kernel<scan_bwd_kernel>(kBwdSmem);
+  const bool is_few = few(f);
+  cudaError_t e = is_few ? prepare_kernel<scan_bwd_kernel<true>>(kBwdSmem) : prepare_kernel<scan_bwd_kernel<false>>(kBwdSmem);
   if (e != cudaSuccess) return e;
   if (d.cut) {
     const int b = blocks_of(f.D, f.G, kCh * kFwdWarps), smem = kFwdSmem;
@@ -1142,8 +1150,9 @@ cudaError_t launch_scan_bwd(const ScanBwdArgs& a, cudaStream_t st) {
     LaunchTimer lt("scan_bwd", st);
     const unsigned grid = static_cast<unsigned>(d.parts * d.blocks);
     const int parts = static_cast<int>(d.parts);
-    if (d.cut) e = launch_behind(scan_bwd_kernel, dim3(grid), kBwdWarps * 32, kBwdSmem, st, a, d.blocks, parts, d.length, true, ws);
-    else scan_bwd_kernel<<<grid, kBwdWarps * 32, kBwdSmem, st>>>(a, d.blocks, parts, d.length, false, ws);
+    const auto kernel = is_few ? scan_bwd_kernel<true> : scan_bwd_kernel<false>;
+    if (d.cut) e = launch_behind(kernel, dim3(grid), kBwdWarps * 32, kBwdSmem, st, a, d.blocks, parts, d.length, true, ws);
+    else kernel<<<grid, kBwdWarps * 32, kBwdSmem, st>>>(a, d.blocks, parts, d.length, false, ws);
     if (e != cudaSuccess) return e;
   }
   e = cudaGetLastError();

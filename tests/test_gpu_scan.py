@@ -608,3 +608,78 @@ def test_a_scan_step_directly_behind_its_convolution(captured):
 
     for a, b in zip(run(False), run(True)):
         assert torch.equal(a, b) and bool(a.isfinite().all())
+
+
+@pytest.mark.parametrize("bad", [[], [70], [3, 40, 255]], ids=str)
+@pytest.mark.parametrize("longest", [5, 90])
+def test_many_short_sequences(bad, longest):
+    """Hundreds of sequences, some empty and a few out of place: outputs, last states and gradients are those of the good ones alone."""
+    from sparse_moe_layer_topk_gb300.scan import CausalConv, SelectiveScan
+    g = torch.Generator().manual_seed(len(bad) + longest)
+    N, D = 300, 16
+    lens = torch.randint(0, 5, (N,), generator=g)
+    lens[torch.randint(0, N, (6,), generator=g)] = longest
+    bounds = [0, *lens.cumsum(0).tolist()]
+    T = bounds[-1] + 4
+    good = [True] * N
+    for n in bad:  # a bound behind the one before it: the sequences on either side of it are skipped
+        while n == 0 or bounds[n] == bounds[n - 1] or bounds[n] - bounds[n - 1] == bounds[n] + 1:
+            n += 1
+        bounds[n] = bounds[n - 1] - 1
+        good[n - 1] = good[n] = False
+    v, w = _scan_inputs([T], D, 16, 1, states=False), _conv_inputs([T], D, 4, False)
+    cu = torch.tensor(bounds, dtype=torch.int32, device="cuda")
+    s = SelectiveScan(v["A"].cuda(), T, v["skip"].cuda(), v["bias"].cuda(), N=N, max_seqlen=90)
+    c = CausalConv(w["w"].cuda(), w["b"].cuda(), T, N=N)
+    kept = [n for n in range(N) if good[n]]
+    rows = [t for n in kept for t in range(bounds[n], bounds[n + 1])]
+    left = [bounds[n + 1] - bounds[n] for n in kept]
+    other = sorted(set(range(T)) - set(rows))
+    for t in (s.y, s.du, s.ddelta, s.dB, s.dC, s.dz, c.y, c.dx, s.state_out, c.state_out):
+        t.fill_(7.0)
+    y, yc = s.forward(*_operands(v), cu, want_state=True), c.forward(w["x"].cuda(), cu, want_state=True)
+    flag = M.MOE_FLAG_BAD_INDEX if bad else 0
+    assert int(s.err) == flag and int(c.err) == flag
+    grads, gc = s.backward(v["dy"].cuda()), c.backward(w["dy"].cuda())
+    for t in (y, yc, gc, *grads):
+        assert bool((t[other] == 7.0).all())
+    pick = {k: t if k in ("A", "skip", "bias") or t is None else t[rows] for k, t in v.items()}
+    r, rc = _scan(pick, left), _conv({**w, "x": w["x"][rows]}, left, True)
+    assert torch.equal(r.forward(*_operands(pick), _cu(left), want_state=True), y[rows]) and torch.equal(r.state_out, s.state_out[kept])
+    assert torch.equal(rc.forward(w["x"][rows].cuda(), _cu(left), want_state=True), yc[rows]) and torch.equal(rc.state_out, c.state_out[kept])
+    for a, b in zip(r.backward(pick["dy"].cuda()), grads):
+        assert torch.equal(a, b[rows])
+    assert torch.equal(rc.backward(w["dy"][rows].cuda()), gc[rows])
+    for a, b in ((r.dA, s.dA), (r.d_dt_bias, s.d_dt_bias), (rc.dw, c.dw), (rc.db, c.db)):
+        np.testing.assert_allclose(f64(a), f64(b), rtol=1e-5, atol=1e-4)
+    skipped = [n for n in range(N) if not good[n]]
+    assert bool((s.state_out[skipped] == 7.0).all()) and bool((c.state_out[skipped] == 7.0).all())
+
+
+@pytest.mark.parametrize("N", [127, 128, 129, 400])
+def test_long_sequences_among_many(N):
+    """Sequences that are cut, their sums and joins, behind and between runs of 128 short ones."""
+    g = torch.Generator().manual_seed(N)
+    lens = torch.randint(0, 4, (N,), generator=g)
+    lens[torch.tensor([5, 126, N - 1])] = torch.tensor([900, 333, 1200])
+    lens = lens.tolist()
+    _check_scan(_scan_inputs(lens, 8, 8, 1), lens)
+
+
+@pytest.mark.parametrize("W,silu", [(2, True), (2, False), (3, True), (3, False), (4, True), (4, False)])
+def test_convolution_of_many_sequences(W, silu):
+    lens = [0, 1, 2, 3, 5, 70] * 50
+    v = _conv_inputs(lens, 24, W, True)
+    c = _conv(v, lens, silu)
+    y = c.forward(v["x"].cuda(), _cu(lens), _dev(v["st"]), want_state=True)
+    dx = c.backward(v["dy"].cuda(), _dev(v["ds"]))
+    args = f64(v["x"]), f64(v["w"]), f64(v["b"]), lens, silu, f64(v["st"])
+    size = O.conv(*(np.abs(a) for a in args[:3]), lens, False, np.abs(args[5]))[0]
+    want, last = O.conv(*args)
+    _close("y", y, want, size, 2.0 ** -18)
+    assert np.array_equal(f64(c.state_out), last)
+    want = O.conv_backward(f64(v["dy"]), *args, f64(v["ds"]))
+    norm = np.linalg.norm
+    for got, ref, tol in zip((dx, c.dw, c.db, c.d_state_in), want, (2.0 ** -8, 2.0 ** -16, 2.0 ** -16, 2.0 ** -8)):
+        assert norm(f64(got) - ref) <= tol * norm(ref)
+    assert int(c.err) == 0
