@@ -574,6 +574,7 @@ int moe_conv_step(const uint16_t* x, const float* weight, const float* bias, uin
  * elements between tokens. state_in, state_out fp32 [N][D][states] (nullable; state_out may be state_in). tile_states (nullable,
  * moe_workspace_size(MOE_OP_SCAN_TILE_STATES, 0, D, states, 0, 0, T, N) bytes) receives what moe_scan_bwd needs of this call. A
  * sequence longer than max_seqlen, or out of place as in moe_conv_fwd, sets MOE_FLAG_BAD_INDEX and is skipped.
+ * A time step of -infinity, or of its type's lowest value, is 0 after softplus: that token leaves the state as it is.
  * Everything is fp32: states are within 1e-6 (rms) of their values, y has its own rounding to bf16. Time steps
  * and decays are taken as they come: exp(dt A) that passes fp32 makes infinities. D is a multiple of 8 and D / G of 4; states is 4, 8, 12 or 16; ld* of u, delta, z, y are
  * multiples of 8, of B and C of 4 (8-byte aligned). y shares no memory with what is read. Workspace:

@@ -308,8 +308,9 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(ConvStepArgs a, int
   for (int j = 0; j + 1 < W; ++j) in[j] = load4(state + static_cast<long long>(j) * a.D);
   in[W - 1] = load4(static_cast<const bf16*>(a.x) + b * a.ldx + c);
   load_taps<W>(a.weight, c, tap);
-  // Every operation is rounded by itself (no fused products, an exact quotient): the row's scan reads y as rounded to bf16, and a
-  // neighbouring bf16 there would be 2^-8 of what it adds to the state. The cache bounds the time all the same.
+  // Every operation is rounded by itself (no fused products, an exact quotient), so that y is what the formula gives step by step in fp32: the
+  // row's scan reads it as rounded to bf16, and a neighbouring bf16 there is 2^-8 of what it adds to the state. The packed pass fuses its products
+  // and takes a quick reciprocal, so a few of its outputs are such neighbours of these. The cache bounds the time all the same.
   float p[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {

@@ -115,7 +115,7 @@ __device__ __forceinline__ float row_rstd(const float (&u)[VEC][8], float ss, in
 // stream rounded once. A row is held in the registers of THREADS threads (one warp up to 1024 columns, then a
 // CTA), VEC vectors each, so that HBM is read and written once and bounds it: 16,384 rows of 4,096 in 86 us, 79 of them the
 // bytes. Few vectors a thread, so that 1,536 threads fit an SM: 4,000 rows of 5,120 with a fp32 stream and E4M3 outputs in 48 us with three
-// vectors and 256 threads, 54 with four, 54 with two and 512 threads, 51 with five and 128.
+// vectors and 256 threads (43 in a graph, 33 of them the bytes: a CTA's one row is read, joined and written in turn), 54 with four, 54 with two and 512 threads, 51 with five and 128.
 template <int THREADS, int VEC, typename R, bool FP8>
 __global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS, THREADS * VEC <= 512 ? 1 : THREADS == 256 ? 6 : VEC <= 3 ? 3 : 2)
     rmsnorm_fwd_kernel(const bf16* __restrict__ x, const R* residual, const float* __restrict__ weight, int T, int d,
@@ -202,7 +202,8 @@ __global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS, THREADS * VEC <
 // du = rstd (g - n mean(g n)) + d_sum with g = dy w, n = u rstd; dw = sum_t dy n. The row's sums of u^2 and of g u, which
 // give rstd and the mean, are joined together, so nothing is kept from the forward but u. A CTA (THREADS threads; with
 // 32 four warps, each its own rows) walks rows with a stride of the grid and keeps its columns' part of dw in
-// registers; the parts are summed in a fixed order afterwards.
+// registers; the parts are summed in a fixed order afterwards. HBM bounds it: 16,384 rows of 4,096 in 85 us, 79 of them the bytes; with a fp32 stream
+// 165 and 158. 8,192 rows of 8,192 with a fp32 stream, where no row is ahead, 185 and 158.
 template <int THREADS, typename U, typename R>
 __global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS, THREADS <= 128 ? 4 : THREADS <= 512 ? 512 / THREADS : 1)
     rmsnorm_bwd_kernel(const bf16* __restrict__ dy, const U* __restrict__ from, const float* __restrict__ weight,

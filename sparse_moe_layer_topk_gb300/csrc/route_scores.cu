@@ -216,9 +216,9 @@ __device__ __noinline__ bool group_value_exactly(const Params& p, const float* r
   return close <= 2;
 }
 
-// One warp routes one token; the logits are read once. Instructions bound it, and what their order leaves idle at the 16 to 20 warps an SM that
-// the row's registers allow: 16,384 tokens x 896 experts, 16 chosen, take 25 us from the logits alone, 33 with a bias, 45 in 8 groups, where the
-// bytes would take 9; 24 of 896 for 4,096 tokens 18.
+// One warp routes one token; the logits are read once. Latency bounds it, at the 16 to 20 warps an SM that the row's registers allow, as much
+// as instructions (2.15 of 4 a clock in groups, warps waiting for one another's shuffles and for memory): 16,384 tokens x 896 experts, 16 chosen,
+// take 24 us from the logits alone, 32 with a bias, 44 in 8 groups, where the bytes would take 9; softmax 26 and 29; 24 of 896 for 4,096 tokens 18.
 //
 // The values that choose (score + bias, or the logits themselves without a bias) are held as order-preserving bits,
 // NPL a lane, runs of four (VEC) or single ones spread over all lanes. Groups: the values pass through shared memory to lanes that lie
@@ -228,13 +228,15 @@ __device__ __noinline__ bool group_value_exactly(const Params& p, const float* r
 // halving the distance to the largest value; where equal values leave none, k rounds of a warp-wide maximum (always in rounds: 34, 42 and 54 us,
 // and 66 for 24 of 896).
 //
-// Which experts are chosen does not depend on the rounding here. A 32-bit score is within
+// Which experts are chosen does not depend on the rounding here (65,000 random calls, half of them made to meet at fp32's rounding, against the
+// definition in 64 bits: no other choice). A 32-bit score is within
 // tol = 2^-21 s (2 + |l - m|) + 2^-22 |c| + 2^-126 of its value (the exponent's argument is rounded once, 2^-24 of it, the exponential and
 // the reciprocal are right to 2 ulp, the sum over the experts to 4; m is the row's maximum, 0 for the sigmoid, where of a positive l only
 // (1 - s) l counts, which is below 1). Where two
 // neighbours in the order, or two groups, are nearer than that, all that could be meant are compared by values in 64
 // bits. (A softmax keeps its 32-bit sum there, a common factor: only the scores' difference is uncertain by 2^-20 of itself,
-// and where that is not enough either the token starts over in 64 bits: 15 us.) Two experts with the same logit and bias are
+// and where that is not enough either the token starts over in 64 bits: its warp takes some 110 us. Of
+// random logits and biases one token in 100,000 does.) Two experts with the same logit and bias are
 // equal in any precision and go by their index.
 template <int NPL, bool VEC, bool SOFTMAX, bool GROUPED>
 __global__ void __launch_bounds__(kWarps * 32, NPL < 28 ? 1 : GROUPED ? 4 : 5) route_scores_kernel(Params p) {

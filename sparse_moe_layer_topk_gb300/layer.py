@@ -25,7 +25,9 @@ SwiGLU derivative reads the dequantized values.
 With a weight "norm" (fp32 [d]) the layer starts with the root-mean-square norm of its input, to which
 a residual may be added (norm.RMSNorm): the layer runs on the norm's output, `norm.sum` is the block's
 residual stream, and the backward ends with the norm's. With `router` (a dict of route.Router's options) the
-experts are chosen with its scores, bias and groups instead of the plain sigmoid form.
+experts are chosen with its scores, bias and groups instead of the plain sigmoid form. The weight "bias" then only
+chooses: it is added to the scores, and the experts are weighted by the scores without it. In the plain form it is
+added to the logits and is part of the weights. The auxiliary loss belongs to the plain form alone.
 """
 from __future__ import annotations
 
